@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define PKV_ABI_VERSION 6
+#define PKV_ABI_VERSION 7
 
 typedef enum {
   PKV_OK = 0,
@@ -48,7 +48,8 @@ typedef enum {
   PKV_ERR_UNSUPPORTED = 2,   /* valid but not implemented (e.g. head_dim 96) */
   PKV_ERR_OUT_OF_PAGES = 3,  /* host allocator: not enough free pages */
   PKV_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
-  PKV_ERR_WORKSPACE = 5      /* workspace too small */
+  PKV_ERR_WORKSPACE = 5,     /* workspace too small */
+  PKV_ERR_HOST_MEMORY = 6    /* host memory ran out; nothing was changed or launched */
 } pkv_status;
 
 /* Bits ORed into *dev_status by the kernels. */
@@ -57,6 +58,7 @@ typedef enum {
 #define PKV_DEV_BAD_POSITION 4  /* append slot beyond the block table / bad length */
 #define PKV_DEV_TIMEOUT 8       /* a bounded wait inside a kernel gave up */
 #define PKV_DEV_BAD_CONFIG 16   /* launch parameters a kernel refuses to run with */
+#define PKV_DEV_BAD_GROUP 32    /* prefix group outside [-1, num_groups), or a negative prefix length */
 
 /* PKV_U4: unsigned 4-bit codes, two per byte (the even channel in the low
  * nibble), for KV pools only. */
@@ -357,6 +359,85 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
                                               int32_t* dev_status, void* stream);
 
 /*
+ * shared_prefix_attention — decode attention for a batch whose rows share
+ * prefixes: out[b][h] = softmax(sm_scale * q[b][h] . K^T) V over tokens
+ * [0, seq_lens[b]) of row b, the same definition as paged_decode_attention in
+ * dense mode, where each prefix is read once for all rows of its group and
+ * multiplied with all their query heads together. The pages have no
+ * counterpart; it serves what pkv_alloc_fork makes (parallel samples, beams,
+ * one system prompt in front of many requests).
+ *   prefix_group : int32 [batch], the group of each row, in any order; -1: none.
+ *   prefix_lens  : int32 [num_groups], the tokens that the rows of a group have
+ *                  in common: tokens [0, prefix_lens[g]) hold the same values
+ *                  for each of them. They are read through one of the group's
+ *                  block-table rows or through the row's own, whichever suits
+ *                  the call; whole pages are normally the same pages, and a
+ *                  page in which the prefix ends may be a copy of each row's
+ *                  own. PER_GROUP64: only whole 64-token groups need to agree
+ *                  (the group in which the prefix ends depends on the tokens
+ *                  after it, which differ).
+ *                  A row shorter than its group's prefix attends over its own
+ *                  tokens on its own; a length of 0 shares nothing.
+ *   q            : [batch][num_q_heads][head_dim], F16 or BF16: for fp16/bf16
+ *                  caches the cache's type, for INT8 and 4-bit caches either.
+ *   out          : [batch][num_q_heads][head_dim] of out_dtype (F32/F16/BF16).
+ *                  With a 16-bit out_dtype the softmax weights enter the
+ *                  second product rounded to q's type (one rounding of the
+ *                  size of the output's own); with F32 they enter as a sum of
+ *                  two such values.
+ *   num_splits   : thread blocks that share the work; 0 = automatic.
+ *   workspace    : >= pkv_shared_prefix_workspace_bytes(...) bytes, 256-byte
+ *                  aligned, any contents. Two calls (two replays of captured
+ *                  calls as well) that share one must not run concurrently.
+ * num_q_heads / num_kv_heads is at most 128, batch and num_groups at most 1024.
+ * Two launches, in stream order with everything before and after them.
+ * A row with no tokens yields zeros.
+ * Device errors: PKV_DEV_BAD_PAGE (16 tokens skipped at a time),
+ * PKV_DEV_BAD_POSITION (length beyond the table or negative: clamped),
+ * PKV_DEV_BAD_GROUP (the row attends on its own), PKV_DEV_TIMEOUT.
+ */
+pkv_status pkv_shared_prefix_attention(const pkv_cache* cache, int32_t batch, int32_t num_q_heads,
+                                       const void* q, pkv_dtype q_dtype, float sm_scale,
+                                       const int32_t* block_table, int32_t max_pages,
+                                       const int32_t* seq_lens, const int32_t* prefix_group,
+                                       const int32_t* prefix_lens, int32_t num_groups, void* out,
+                                       pkv_dtype out_dtype, int32_t num_splits, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace bytes of pkv_shared_prefix_attention for these shapes on the
+ * current device (num_splits as in the call); 0 on bad input. */
+size_t pkv_shared_prefix_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t num_q_heads,
+                                         int32_t num_splits);
+
+/*
+ * copy_pages — page dst_pages[i] becomes a copy of page src_pages[i], in every
+ * part the cache keeps (K, V, scales, boxes), and row dst_rows[i] of `tail` a
+ * copy of row src_rows[i] (PER_GROUP64: the open group's originals, which a
+ * forked sequence needs in its own batch row before it appends).
+ *   src_pages, dst_pages, src_rows, dst_rows : HOST arrays, read before the call
+ *       returns. Within each pair of lists no destination may occur twice or
+ *       be a source too; a source may be copied to several places. A captured
+ *       call copies the same pages at every replay.
+ * Errors: PKV_ERR_INVALID_ARG for an id outside [0, num_pages) or
+ * [0, tail_rows), a list as above, or rows for a cache without `tail`; nothing
+ * is launched then.
+ */
+pkv_status pkv_copy_pages(const pkv_cache* cache, int32_t num_copies, const int32_t* src_pages,
+                          const int32_t* dst_pages, int32_t num_rows, const int32_t* src_rows,
+                          const int32_t* dst_rows, void* stream);
+
+/*
+ * remap_block_table — every entry of block_table that equals src_pages[i]
+ * becomes dst_pages[i]; all others stay (-1 and ids outside the pool too).
+ *   block_table : int32 [batch][max_pages], device memory, 4-byte aligned.
+ *   src_pages, dst_pages : HOST arrays of ids in [0, num_pages). No source may
+ *       occur twice or be a destination too.
+ */
+pkv_status pkv_remap_block_table(int32_t* block_table, int32_t batch, int32_t max_pages, int32_t num_pages,
+                                 int32_t num_moves, const int32_t* src_pages, const int32_t* dst_pages,
+                                 void* stream);
+
+/*
  * Host page allocator [HBM-layout page, section 三 allocate_blocks /
  * free_sequence]: a free list of physical page ids; a sequence needs
  * ceil(tokens / page_size) pages; an allocation that cannot be met fails
@@ -371,13 +452,39 @@ void pkv_alloc_destroy(pkv_allocator* a);
  * them. PKV_ERR_OUT_OF_PAGES leaves the allocator unchanged. */
 pkv_status pkv_alloc_reserve(pkv_allocator* a, int64_t seq_id, int32_t total_tokens,
                              int32_t page_size, int32_t* block_table_row, int32_t max_pages);
-/* Return every page of seq_id to the free list. */
+/* Sequence `child`, which must not exist, gets the first ceil(tokens / page_size)
+ * pages of `parent` as its own too; writes them into block_table_row as above.
+ * The pages are shared: before either sequence writes into one of them, it
+ * calls pkv_alloc_unshare. */
+pkv_status pkv_alloc_fork(pkv_allocator* a, int64_t parent, int64_t child, int32_t tokens, int32_t page_size,
+                          int32_t* block_table_row, int32_t max_pages);
+/* Give seq_id pages of its own in place of the shared ones from the page of
+ * first_token on: page src_pages[i] (still its other owners') is replaced by
+ * dst_pages[i], whose contents the caller copies (pkv_copy_pages) before it
+ * writes; *num_copies of them. More than max_copies is PKV_ERR_INVALID_ARG; too few
+ * free pages PKV_ERR_OUT_OF_PAGES; neither changes anything. */
+pkv_status pkv_alloc_unshare(pkv_allocator* a, int64_t seq_id, int32_t first_token, int32_t page_size,
+                             int32_t max_copies, int32_t* src_pages, int32_t* dst_pages, int32_t* num_copies,
+                             int32_t* block_table_row, int32_t max_pages);
+/* Move the pages in use to the lowest ids, the highest to the lowest free one
+ * first and at most max_moves: the allocator's sequences own dst_pages[i]
+ * instead of src_pages[i], *num_moves of them, and the caller moves the contents
+ * (pkv_copy_pages) and the block tables (pkv_remap_block_table). No destination is
+ * a source. */
+pkv_status pkv_alloc_compact(pkv_allocator* a, int32_t max_moves, int32_t* src_pages, int32_t* dst_pages,
+                             int32_t* num_moves);
+/* The pages of seq_id, -1 past them. */
+pkv_status pkv_alloc_table(const pkv_allocator* a, int64_t seq_id, int32_t* block_table_row, int32_t max_pages);
+/* Return every page of seq_id that no other sequence owns to the free list. */
 pkv_status pkv_alloc_free(pkv_allocator* a, int64_t seq_id);
 int32_t pkv_alloc_num_free(const pkv_allocator* a);
 /* Pages of seq_id (0 if unknown). */
 int32_t pkv_alloc_seq_pages(const pkv_allocator* a, int64_t seq_id);
-/* Consistency check: pages that are neither free nor owned by exactly one
- * sequence (leaked or double-owned) [Gemini page, section 2.3]. */
+/* Sequences that own `page`. */
+int32_t pkv_alloc_page_refs(const pkv_allocator* a, int32_t page);
+/* Consistency check: pages that are neither free nor owned (leaked), both, or
+ * owned by another number of sequences than recorded [Gemini page, section
+ * 2.3]; -1 if host memory ran out. */
 int32_t pkv_alloc_check(const pkv_allocator* a);
 
 #ifdef __cplusplus

@@ -18,14 +18,19 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "li
 F16, BF16, F32, I8, U4 = 0, 1, 2, 3, 4
 QUANT_NONE, QUANT_PER_TOKEN, QUANT_PER_GROUP64 = 0, 1, 2
 SELECT_PER_HEAD, SELECT_GROUP_SUM, SELECT_GROUP_MAX = 0, 1, 2
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OUT_OF_PAGES, ERR_CUDA, ERR_WORKSPACE = range(6)
+(OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OUT_OF_PAGES, ERR_CUDA, ERR_WORKSPACE,
+ ERR_HOST_MEMORY) = range(7)
 DEV_BAD_PAGE, DEV_BAD_SELECTED, DEV_BAD_POSITION, DEV_TIMEOUT, DEV_BAD_CONFIG = 1, 2, 4, 8, 16
+DEV_BAD_GROUP = 32
 
 EXPORTED = [
     "pkv_status_string", "pkv_abi_version", "pkv_tuning_reload", "pkv_kv_append", "pkv_page_score_topk",
     "pkv_attention_workspace_bytes", "pkv_paged_decode_attention", "pkv_append_decode_attention",
     "pkv_paged_decode_attention_noalloc",
+    "pkv_shared_prefix_attention", "pkv_shared_prefix_workspace_bytes", "pkv_copy_pages",
+    "pkv_remap_block_table",
     "pkv_alloc_create", "pkv_alloc_destroy", "pkv_alloc_reserve", "pkv_alloc_free",
+    "pkv_alloc_fork", "pkv_alloc_unshare", "pkv_alloc_compact", "pkv_alloc_table", "pkv_alloc_page_refs",
     "pkv_alloc_num_free", "pkv_alloc_seq_pages", "pkv_alloc_check",
 ]
 
@@ -77,10 +82,20 @@ def lib() -> ctypes.CDLL:
                                                 vp, c_int, i32, i32, vp, c_size_t, vp, vp]),
         "pkv_paged_decode_attention_noalloc": (c_int, [P, i32, i32, vp, c_int, c_float, vp, i32, vp, vp,
                                                        vp, i32, i32, vp, c_int, i32, vp, vp]),
+        "pkv_shared_prefix_attention": (c_int, [P, i32, i32, vp, c_int, c_float, vp, i32, vp, vp, vp, i32,
+                                                vp, c_int, i32, vp, c_size_t, vp, vp]),
+        "pkv_shared_prefix_workspace_bytes": (c_size_t, [P, i32, i32, i32]),
+        "pkv_copy_pages": (c_int, [P, i32, vp, vp, i32, vp, vp, vp]),
+        "pkv_remap_block_table": (c_int, [vp, i32, i32, i32, i32, vp, vp, vp]),
         "pkv_alloc_create": (c_int, [i32, POINTER(c_void_p)]),
         "pkv_alloc_destroy": (None, [vp]),
         "pkv_alloc_reserve": (c_int, [vp, i64, i32, i32, vp, i32]),
         "pkv_alloc_free": (c_int, [vp, i64]),
+        "pkv_alloc_fork": (c_int, [vp, i64, i64, i32, i32, vp, i32]),
+        "pkv_alloc_unshare": (c_int, [vp, i64, i32, i32, i32, vp, vp, POINTER(c_int32), vp, i32]),
+        "pkv_alloc_compact": (c_int, [vp, i32, vp, vp, POINTER(c_int32)]),
+        "pkv_alloc_table": (c_int, [vp, i64, vp, i32]),
+        "pkv_alloc_page_refs": (i32, [vp, i32]),
         "pkv_alloc_num_free": (i32, [vp]),
         "pkv_alloc_seq_pages": (i32, [vp, i64]),
         "pkv_alloc_check": (i32, [vp]),
@@ -183,6 +198,40 @@ def paged_decode_attention_noalloc(cache: PkvCache, batch: int, num_q_heads: int
         num_splits, dev_status or None, stream or None), "paged_decode_attention_noalloc")
 
 
+def shared_prefix_workspace_bytes(cache: PkvCache, batch: int, num_q_heads: int, num_splits: int) -> int:
+    n = lib().pkv_shared_prefix_workspace_bytes(ctypes.byref(cache), batch, num_q_heads, num_splits)
+    if n == 0:
+        raise PkvError(ERR_INVALID_ARG, "shared_prefix_workspace_bytes")
+    return n
+
+
+def shared_prefix_attention(cache: PkvCache, batch: int, num_q_heads: int, q: int, q_dtype: int,
+                            sm_scale: float, block_table: int, max_pages: int, seq_lens: int,
+                            prefix_group: int, prefix_lens: int, num_groups: int, out: int,
+                            out_dtype: int, num_splits: int, workspace: int, workspace_bytes: int,
+                            dev_status: int, stream: int) -> None:
+    _check(lib().pkv_shared_prefix_attention(ctypes.byref(cache), batch, num_q_heads, q, q_dtype, sm_scale,
+                                             block_table, max_pages, seq_lens, prefix_group,
+                                             prefix_lens or None, num_groups, out, out_dtype, num_splits,
+                                             workspace, workspace_bytes, dev_status or None, stream or None),
+           "shared_prefix_attention")
+
+
+def copy_pages(cache: PkvCache, num_copies: int, src_pages: int, dst_pages: int, num_rows: int,
+               src_rows: int, dst_rows: int, stream: int) -> None:
+    """The four lists are host addresses of int32 values."""
+    _check(lib().pkv_copy_pages(ctypes.byref(cache), num_copies, src_pages or None, dst_pages or None,
+                                num_rows, src_rows or None, dst_rows or None, stream or None), "copy_pages")
+
+
+def remap_block_table(block_table: int, batch: int, max_pages: int, num_pages: int, num_moves: int,
+                      src_pages: int, dst_pages: int, stream: int) -> None:
+    """src_pages and dst_pages are host addresses of int32 values."""
+    _check(lib().pkv_remap_block_table(block_table or None, batch, max_pages, num_pages, num_moves,
+                                       src_pages or None, dst_pages or None, stream or None),
+           "remap_block_table")
+
+
 def alloc_create(num_pages: int) -> int:
     h = c_void_p()
     _check(lib().pkv_alloc_create(num_pages, ctypes.byref(h)), "alloc_create")
@@ -213,3 +262,30 @@ def alloc_seq_pages(h: int, seq_id: int) -> int:
 
 def alloc_check(h: int) -> int:
     return lib().pkv_alloc_check(h)
+
+
+def alloc_fork(h: int, parent: int, child: int, tokens: int, page_size: int, row_ptr: int,
+               max_pages: int) -> None:
+    _check(lib().pkv_alloc_fork(h, parent, child, tokens, page_size, row_ptr, max_pages), "alloc_fork")
+
+
+def alloc_unshare(h: int, seq_id: int, first_token: int, page_size: int, max_copies: int, src_ptr: int,
+                  dst_ptr: int, row_ptr: int, max_pages: int) -> int:
+    n = c_int32()
+    _check(lib().pkv_alloc_unshare(h, seq_id, first_token, page_size, max_copies, src_ptr, dst_ptr,
+                                   ctypes.byref(n), row_ptr, max_pages), "alloc_unshare")
+    return n.value
+
+
+def alloc_compact(h: int, max_moves: int, src_ptr: int, dst_ptr: int) -> int:
+    n = c_int32()
+    _check(lib().pkv_alloc_compact(h, max_moves, src_ptr, dst_ptr, ctypes.byref(n)), "alloc_compact")
+    return n.value
+
+
+def alloc_table(h: int, seq_id: int, row_ptr: int, max_pages: int) -> None:
+    _check(lib().pkv_alloc_table(h, seq_id, row_ptr, max_pages), "alloc_table")
+
+
+def alloc_page_refs(h: int, page: int) -> int:
+    return lib().pkv_alloc_page_refs(h, page)

@@ -7,6 +7,7 @@ append, scoring, selection and attention runs in libpkv's kernels.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Dict, Optional, Tuple
 
 import numpy as np
@@ -44,6 +45,31 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None) -> None:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
+
+
+def _host_ids(ids, name: str) -> np.ndarray:
+    """Page or row ids on the host as contiguous int32 (a list, an array or a CPU tensor)."""
+    if isinstance(ids, torch.Tensor):
+        if ids.is_cuda:
+            raise ValueError(f"{name} must be on the host")
+        ids = ids.numpy()
+    a = np.asarray(ids)
+    if a.size == 0:
+        a = a.astype(np.int32)
+    if a.ndim != 1 or a.dtype.kind not in "iu":
+        raise TypeError(f"{name} must be a list of whole numbers")
+    if a.dtype != np.int32:
+        if a.size and (int(a.min()) < 0 or int(a.max()) > 0x7FFFFFFF):
+            raise ValueError(f"{name} holds an id out of range")
+        a = a.astype(np.int32)
+    return np.ascontiguousarray(a)
+
+
+def _pair_ids(src, dst, what: str) -> Tuple[np.ndarray, np.ndarray]:
+    s, d = _host_ids(src, f"src_{what}"), _host_ids(dst, f"dst_{what}")
+    if s.size != d.size:
+        raise ValueError(f"{s.size} source and {d.size} destination {what}")
+    return s, d
 
 
 class PagedKVCache:
@@ -85,11 +111,49 @@ class PagedKVCache:
                 self.v_pages.fill_(float("nan"))
             if self.page_meta is not None:
                 self.page_meta.fill_(float("nan"))
+        self._describe()
+
+    def _describe(self) -> None:
         self._desc = B.PkvCache(
-            num_pages, page_size, num_kv_heads, head_dim, self.kv_dtype, self.quant,
+            self.num_pages, self.page_size, self.num_kv_heads, self.head_dim, self.kv_dtype, self.quant,
             self.k_pages.data_ptr(), self.v_pages.data_ptr(), _ptr(self.kv_sz), _ptr(self.tail),
             0 if self.tail is None else self.tail.shape[0], _ptr(self.page_meta))
         self._ws: Dict[Tuple, torch.Tensor] = {}
+
+    @classmethod
+    def from_pools(cls, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_dtype: str = "bf16",
+                   quant: str = "none", kv_sz: Optional[torch.Tensor] = None,
+                   tail: Optional[torch.Tensor] = None,
+                   page_meta: Optional[torch.Tensor] = None) -> "PagedKVCache":
+        """A cache over pools that the caller has (layouts as in include/pkv.h); they are
+        kept alive, not copied."""
+        self = cls.__new__(cls)
+        self.kv_dtype, self.quant = _NAME_TO_PKV[kv_dtype], _QUANT[quant]
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [pages][kv heads][page size][row]")
+        self.num_pages, self.num_kv_heads, self.page_size, row = k_pages.shape
+        self.head_dim = 2 * row if self.kv_dtype == B.U4 else row
+        self.device = k_pages.device
+        N, H, ps, d = self.num_pages, self.num_kv_heads, self.page_size, self.head_dim
+        gran = 0 if quant == "none" else (1 if quant == "per_token" else 64)
+        want = [("k_pages", k_pages, _PKV_TO_TORCH[self.kv_dtype], (N, H, ps, row)),
+                ("v_pages", v_pages, _PKV_TO_TORCH[self.kv_dtype], (N, H, ps, row)),
+                ("kv_sz", kv_sz, torch.float32, (N, H, ps // gran, 4) if gran else None),
+                ("tail", tail, torch.float32, (-1, H, 2, 2, 64, d) if gran == 64 else None),
+                ("page_meta", page_meta, torch.float32, (N, H, 2, d))]
+        for name, t, dtype, shape in want:
+            if t is None:
+                if name == "kv_sz" and gran:
+                    raise ValueError(f"{quant} caches need kv_sz")
+                continue
+            if shape is None:
+                raise ValueError(f"a cache with quant={quant!r} has no {name}")
+            _need(t, name, dtype, self.device)
+            if t.dim() != len(shape) or any(s not in (-1, n) for s, n in zip(shape, t.shape)):
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        self.k_pages, self.v_pages, self.kv_sz, self.tail, self.page_meta = k_pages, v_pages, kv_sz, tail, page_meta
+        self._describe()
+        return self
 
     def descriptor(self) -> B.PkvCache:
         return self._desc
@@ -212,6 +276,90 @@ class PagedKVCache:
         return out
 
 
+    # --------------------------------------------------- sequences that share pages
+    def _launch_stream(self, stream: Optional[torch.cuda.Stream]) -> int:
+        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+
+    def copy_pages(self, src_pages, dst_pages, src_rows=None, dst_rows=None,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Page dst_pages[i] becomes a copy of page src_pages[i] (K, V, scales, boxes), and
+        tail row dst_rows[i] of row src_rows[i] (per-group caches). The ids are on the host:
+        lists, int32 arrays or CPU tensors, as PageAllocator.unshare and .compact give them."""
+        sp, dp = _pair_ids(src_pages, dst_pages, "pages")
+        sr, dr = _pair_ids(() if src_rows is None else src_rows, () if dst_rows is None else dst_rows, "rows")
+        with torch.cuda.device(self.device):
+            B.copy_pages(self._desc, sp.size, sp.ctypes.data, dp.ctypes.data, sr.size, sr.ctypes.data,
+                         dr.ctypes.data, self._launch_stream(stream))
+
+    def remap_table(self, block_table: torch.Tensor, src_pages, dst_pages,
+                    stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Entries of block_table equal to src_pages[i] become dst_pages[i] (in place)."""
+        _need(block_table, "block_table", torch.int32, self.device)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [batch][pages]")
+        sp, dp = _pair_ids(src_pages, dst_pages, "pages")
+        if block_table.numel() == 0:
+            return
+        with torch.cuda.device(self.device):
+            B.remap_block_table(block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
+                                self.num_pages, sp.size, sp.ctypes.data, dp.ctypes.data,
+                                self._launch_stream(stream))
+
+    def shared_workspace(self, batch: int, num_q_heads: int, num_splits: int = 0,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Workspace of shared_attention for these shapes, kept and reused by stream."""
+        key = ("shared", batch, num_q_heads, num_splits, self._launch_stream(stream))
+        ws = self._ws.get(key)
+        if ws is None:
+            with torch.cuda.device(self.device):
+                n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
+            ws = self._ws[key] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return ws
+
+    def shared_attention(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                         prefix_group: torch.Tensor, prefix_lens: torch.Tensor,
+                         sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.float32, num_splits: int = 0,
+                         dev_status: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Decode attention for q [B][Hq][d] where the rows of group g (prefix_group [B], -1:
+        none) have their first prefix_lens[g] tokens in common, which are then read once.
+        Results are those of attention(); see pkv_shared_prefix_attention in include/pkv.h.
+
+        workspace: memory of shared_workspace()'s size for this call alone. By default one
+        workspace per shape and stream is kept; graphs captured on one stream and replayed
+        at the same time on others need one each."""
+        for t, n, dt, shape in ((q, "q", None, None), (block_table, "block_table", torch.int32, None),
+                                (seq_lens, "seq_lens", torch.int32, (q.shape[0],)),
+                                (prefix_group, "prefix_group", torch.int32, (q.shape[0],)),
+                                (prefix_lens, "prefix_lens", torch.int32, None)):
+            _need(t, n, dt, self.device)
+            if shape is not None and t.shape != shape:
+                raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
+        if q.dim() != 3 or q.shape[2] != self.head_dim:
+            raise ValueError(f"q must be [batch][heads][{self.head_dim}], got {list(q.shape)}")
+        if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or prefix_lens.dim() != 1:
+            raise ValueError("block_table must be [batch][pages] and prefix_lens [groups]")
+        Bsz, Hq, d = q.shape
+        if out is None:
+            out = torch.empty((Bsz, Hq, d), dtype=out_dtype, device=self.device)
+        else:
+            _need(out, "out", None, self.device)
+            if out.shape != q.shape:
+                raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+        with torch.cuda.device(self.device):
+            ws = workspace if workspace is not None else self.shared_workspace(Bsz, Hq, num_splits, stream)
+            _need(ws, "workspace", None, self.device)
+            B.shared_prefix_attention(
+                self._desc, Bsz, Hq, q.data_ptr(), pkv_dtype(q),
+                1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(),
+                block_table.shape[1], seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(),
+                prefix_lens.shape[0], out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(),
+                ws.numel() * ws.element_size(), _ptr(dev_status), self._launch_stream(stream))
+        return out
+
+
 class PageAllocator:
     """Host free-list page allocator of libpkv (pkv_alloc_*)."""
 
@@ -227,6 +375,40 @@ class PageAllocator:
 
     def free(self, seq_id: int) -> None:
         B.alloc_free(self._h, seq_id)
+
+    def fork(self, parent: int, child: int, tokens: int, page_size: int, max_pages: int) -> np.ndarray:
+        """Sequence child shares the pages of parent's first `tokens` tokens; its table row."""
+        row = np.full(max_pages, -1, dtype=np.int32)
+        B.alloc_fork(self._h, parent, child, tokens, page_size, row.ctypes.data, max_pages)
+        return row
+
+    def unshare(self, seq_id: int, first_token: int, page_size: int,
+                max_pages: int) -> Tuple[np.ndarray, np.ndarray, np.ndarray]:
+        """Pages of its own for seq_id from first_token's page on: (source pages, destination
+        pages) for PagedKVCache.copy_pages, and the sequence's new table row."""
+        row = np.full(max_pages, -1, dtype=np.int32)
+        src, dst = np.empty(max_pages, dtype=np.int32), np.empty(max_pages, dtype=np.int32)
+        n = B.alloc_unshare(self._h, seq_id, first_token, page_size, max_pages, src.ctypes.data,
+                            dst.ctypes.data, row.ctypes.data, max_pages)
+        return src[:n], dst[:n], row
+
+    def compact(self, max_moves: Optional[int] = None) -> Tuple[np.ndarray, np.ndarray]:
+        """Move the pages in use to the lowest ids: (source pages, destination pages) for
+        PagedKVCache.copy_pages and .remap_table."""
+        m = self.num_pages if max_moves is None else max_moves
+        size = max(0, min(m, self.num_pages))
+        src, dst = np.empty(size, dtype=np.int32), np.empty(size, dtype=np.int32)
+        n = B.alloc_compact(self._h, m if m < 0 else size, src.ctypes.data, dst.ctypes.data)
+        return src[:n], dst[:n]
+
+    def table(self, seq_id: int, max_pages: int) -> np.ndarray:
+        row = np.full(max_pages, -1, dtype=np.int32)
+        B.alloc_table(self._h, seq_id, row.ctypes.data, max_pages)
+        return row
+
+    def page_refs(self, page: int) -> int:
+        """Sequences that own a page."""
+        return B.alloc_page_refs(self._h, page)
 
     @property
     def num_free(self) -> int:

@@ -469,6 +469,7 @@ const char* pkv_status_string(pkv_status s) {
     case PKV_ERR_OUT_OF_PAGES: return "out of pages";
     case PKV_ERR_CUDA: return "CUDA error";
     case PKV_ERR_WORKSPACE: return "workspace too small or misaligned";
+    case PKV_ERR_HOST_MEMORY: return "out of host memory";
   }
   return "unknown status";
 }
@@ -757,6 +758,90 @@ pkv_status pkv_page_score_topk(const pkv_cache* cache, int32_t batch, int32_t nu
   p.group_mode = group_mode;
   p.early = early_start;
   return launch_topk(p, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+pkv_status check_shared(const pkv_cache* cache, int32_t batch, int32_t num_q_heads, int32_t num_splits) {
+  if (batch < 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 || num_splits < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_q_heads / cache->num_kv_heads > 128 || batch > 1024 || num_splits > 65535) return PKV_ERR_UNSUPPORTED;
+  if (cache->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+
+}  // namespace
+
+size_t pkv_shared_prefix_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t num_q_heads,
+                                         int32_t num_splits) {
+  size_t n = 0;
+  if (check_cache(cache, false) != PKV_OK || check_shared(cache, batch, num_q_heads, num_splits) != PKV_OK) return 0;
+  return shared_workspace_bytes(cache, batch, num_q_heads, num_splits, n) == PKV_OK ? n : 0;
+}
+
+pkv_status pkv_shared_prefix_attention(const pkv_cache* cache, int32_t batch, int32_t num_q_heads, const void* q,
+                                       pkv_dtype q_dtype, float sm_scale, const int32_t* block_table,
+                                       int32_t max_pages, const int32_t* seq_lens, const int32_t* prefix_group,
+                                       const int32_t* prefix_lens, int32_t num_groups, void* out,
+                                       pkv_dtype out_dtype, int32_t num_splits, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  pkv_status st = check_cache(cache, true);
+  if (st == PKV_OK) st = check_shared(cache, batch, num_q_heads, num_splits);
+  if (st != PKV_OK) return st;
+  if (q_dtype != PKV_F16 && q_dtype != PKV_BF16 && q_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
+  if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
+  if (q_dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+  if ((cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) && q_dtype != cache->kv_dtype)
+    return PKV_ERR_UNSUPPORTED;
+  if (max_pages <= 0 || num_groups < 0) return PKV_ERR_INVALID_ARG;
+  if (num_groups > 1024) return PKV_ERR_UNSUPPORTED;
+  // token positions are 32-bit, and so are tensor-copy row coordinates
+  if ((long long)max_pages * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if ((long long)cache->num_pages * cache->num_kv_heads * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (!(sm_scale > 0.f) || !(sm_scale < 1e30f)) return PKV_ERR_INVALID_ARG;
+  if (batch == 0) return PKV_OK;
+  if (!q || !out || !block_table || !seq_lens || !prefix_group || (num_groups > 0 && !prefix_lens) ||
+      !aligned16(q) || !aligned16(out))
+    return PKV_ERR_INVALID_ARG;
+  SharedArgs a = {};
+  a.cache = cache;
+  a.batch = batch;
+  a.num_q_heads = num_q_heads;
+  a.max_pages = max_pages;
+  a.num_groups = num_groups;
+  a.num_splits = num_splits;
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.out_dtype = out_dtype;
+  a.sm_scale = sm_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.prefix_group = prefix_group;
+  a.prefix_lens = prefix_lens;
+  a.out = out;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.dev_status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_shared(a);
+}
+
+pkv_status pkv_copy_pages(const pkv_cache* cache, int32_t num_copies, const int32_t* src_pages,
+                          const int32_t* dst_pages, int32_t num_rows, const int32_t* src_rows,
+                          const int32_t* dst_rows, void* stream) {
+  const pkv_status st = check_cache(cache, true);
+  if (st != PKV_OK) return st;
+  return copy_pages(cache, num_copies, src_pages, dst_pages, num_rows, src_rows, dst_rows,
+                    static_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_remap_block_table(int32_t* block_table, int32_t batch, int32_t max_pages, int32_t num_pages,
+                                 int32_t num_moves, const int32_t* src_pages, const int32_t* dst_pages,
+                                 void* stream) {
+  if (batch < 0 || max_pages <= 0 || num_pages <= 0) return PKV_ERR_INVALID_ARG;
+  if (batch > 0 && (!block_table || (reinterpret_cast<uintptr_t>(block_table) & 3u))) return PKV_ERR_INVALID_ARG;
+  return remap_block_table(block_table, (long long)batch * max_pages, num_pages, num_moves, src_pages, dst_pages,
+                           static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

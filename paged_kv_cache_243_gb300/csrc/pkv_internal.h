@@ -42,6 +42,32 @@ struct TopkParams {
 pkv_status launch_append(const AppendParams& p, cudaStream_t st);
 pkv_status launch_topk(const TopkParams& p, cudaStream_t st);
 
+// Page copies and block-table renaming; the lists are host memory.
+pkv_status copy_pages(const pkv_cache* c, int32_t n, const int32_t* src, const int32_t* dst, int32_t n_rows,
+                      const int32_t* src_rows, const int32_t* dst_rows, cudaStream_t stream);
+pkv_status remap_block_table(int32_t* table, long long entries, int32_t num_pages, int32_t n, const int32_t* src,
+                             const int32_t* dst, cudaStream_t stream);
+
+// Attention over shared prefixes: what the entry point has checked.
+struct SharedArgs {
+  const pkv_cache* cache;
+  int batch, num_q_heads, max_pages, num_groups, num_splits;
+  const void* q;
+  int q_dtype, out_dtype;
+  float sm_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* prefix_group;
+  const int32_t* prefix_lens;
+  void* out;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* dev_status;
+  cudaStream_t stream;
+};
+pkv_status launch_shared(const SharedArgs& a);
+pkv_status shared_workspace_bytes(const pkv_cache* c, int batch, int num_q_heads, int num_splits, size_t& bytes);
+
 // Attention kernels, one getter per KV kind (each in its own translation unit).
 // mma: the tensor-core variant (query-head groups of 2, 4 or 8); self_fed:
 // its form without a producer warp (head_dim 128; NULL otherwise).

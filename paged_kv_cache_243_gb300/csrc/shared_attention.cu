@@ -1,112 +1,179 @@
-// Decode attention over shared prefixes, in its plainest form: one warp per
-// query row walks the row's tokens through the block table, 32 lanes over the
-// channels, with a running maximum and sum.
-#include "pkv_internal.h"
-#include "quant.cuh"
+// Shared-prefix attention: launch plan of the kernels in shared_kernel.cuh.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "shared_kernel.cuh"
 
 namespace pkv {
+
+const void* shared_kernel_f16(int D);
+const void* shared_kernel_bf16(int D);
+const void* shared_kernel_i8t(int D, bool bf);
+const void* shared_kernel_i8g(int D, bool bf);
+const void* shared_kernel_u4t(int D, bool bf);
+
 namespace {
 
-struct SharedParams {
-  const uint8_t* k_pages;
-  const uint8_t* v_pages;
-  const float* kv_sz;
-  const void* q;
-  void* out;
-  const int32_t* block_table;
-  const int32_t* seq_lens;
-  const int32_t* prefix_group;
-  const int32_t* prefix_lens;
-  int32_t* dev_status;
-  int num_pages, page_size, num_kv_heads, num_q_heads, head_dim, max_pages, num_groups;
-  int kind, q_dtype, out_dtype;
-  float scale;
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Device {
+  int sms, smem;
 };
 
-__device__ float restored(const SharedParams& p, const uint8_t* pool, int which, size_t row, size_t szrow, int i) {
-  const int D = p.head_dim;
-  if (p.kind == KV_F16) return __half2float(reinterpret_cast<const __half*>(pool)[row * D + i]);
-  if (p.kind == KV_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[row * D + i]);
-  const float s = p.kv_sz[szrow * 4 + which], z = p.kv_sz[szrow * 4 + which + 1];
-  const uint32_t u = p.kind == KV_U4T ? pool[(row * D + i) / 2] >> (4 * (i & 1)) & 15u : pool[row * D + i];
-  return fmaf((float)u, s, z);
+pkv_status device(Device& d) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&d.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  return PKV_OK;
 }
 
-__global__ void shared_plain_kernel(const SharedParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x, D = p.head_dim;
-  const int kvh = h / (p.num_q_heads / p.num_kv_heads);
-  const long long cap = (long long)p.max_pages * p.page_size;
-  int L = p.seq_lens[b];
-  if (L < 0 || L > cap) {
-    if (lane == 0 && h == 0) flag_status(p.dev_status, PKV_DEV_BAD_POSITION);
-    L = L < 0 ? 0 : (int)cap;
-  }
-  const int g = p.prefix_group[b];
-  if (h == 0 && lane == 0 && (g < -1 || g >= p.num_groups || (g >= 0 && p.prefix_lens[g] < 0)))
-    flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
-  const size_t qo = ((size_t)b * p.num_q_heads + h) * D;
-  float m = -INFINITY, l = 0.f, acc[4] = {}, q[4] = {};
-  for (int j = 0; j * 32 < D; ++j) q[j] = load_q_elem(p.q, p.q_dtype, qo + j * 32 + lane) * p.scale;
-  for (int t = 0; t < L; ++t) {
-    const int page = p.block_table[(size_t)b * p.max_pages + t / p.page_size];
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) flag_status(p.dev_status, PKV_DEV_BAD_PAGE);
-      continue;
-    }
-    const size_t row = ((size_t)page * p.num_kv_heads + kvh) * p.page_size + t % p.page_size;
-    const size_t szrow = p.kind == KV_I8G ? row / 64 : row;
-    float s = 0.f;
-    for (int j = 0; j * 32 < D; ++j) s = fmaf(q[j], restored(p, p.k_pages, 0, row, szrow, j * 32 + lane), s);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    const float mn = fmaxf(m, s), a = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - mn);
-    l = fmaf(l, a, w);
-    for (int j = 0; j * 32 < D; ++j)
-      acc[j] = fmaf(acc[j], a, w * restored(p, p.v_pages, 2, row, szrow, j * 32 + lane));
-    m = mn;
-  }
-  for (int j = 0; j * 32 < D; ++j)
-    store_out_elem(p.out, p.out_dtype, qo + j * 32 + lane, l > 0.f ? acc[j] / l : 0.f);
+// Workspace: each row's place in the plan, (m, l) by record row, accumulators.
+// Record rows: one per query row and segment kind for the block where the segment
+// begins, and 256 per block for the segment that it continues.
+struct Work {
+  size_t ml, acc, total;
+};
+Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
+  const size_t rows = 2 * (size_t)batch * hq + (size_t)ctas * 2 * kTile;
+  Work w;
+  w.ml = align256((size_t)batch * 2 * sizeof(int4));
+  w.acc = w.ml + align256(rows * sizeof(float2));
+  w.total = w.acc + align256(rows * c->head_dim * sizeof(float)) + 256;
+  return w;
+}
+
+using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// A 16-bit pool as [rows][d], copied in boxes of 16 rows x 64 channels.
+bool pool_map(void* base, uint64_t rows, int d, bool bf, CUtensorMap& m) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, rows}, strides[1] = {(cuuint64_t)d * 2};
+  const cuuint32_t box[2] = {64, 16}, step[2] = {1, 1};
+  return enc(&m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int KV>
+void sizes(int& threads, int& smem, int& entries, int avail, int batch, int groups) {
+  using G = SharedGeom<D, KV, true>;   // operand types have the same sizes
+  threads = G::THREADS;
+  entries = kMaxEntries;
+  while (entries > 2 && 1024 + shared_layout<G>(entries, batch, groups).total > avail) entries -= 2;
+  smem = 1024 + shared_layout<G>(entries, batch, groups).total;
+}
+
+template <int D>
+const void* merge_kernel(int warps) {
+  return warps == 4 ? reinterpret_cast<const void*>(&shared_merge_kernel<D, 4>)
+                    : reinterpret_cast<const void*>(&shared_merge_kernel<D, 1>);
 }
 
 }  // namespace
 
-pkv_status shared_workspace_bytes(const pkv_cache*, int, int, int, size_t& bytes) {
-  bytes = 256;
+pkv_status shared_workspace_bytes(const pkv_cache* c, int batch, int num_q_heads, int num_splits, size_t& bytes) {
+  Device dev = {0, 0};
+  if (num_splits == 0) {
+    const pkv_status st = device(dev);
+    if (st != PKV_OK) return st;
+  }
+  bytes = layout(c, batch, num_q_heads, num_splits ? num_splits : dev.sms).total;
   return PKV_OK;
 }
 
 pkv_status launch_shared(const SharedArgs& a) {
   const pkv_cache* c = a.cache;
-  if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < 256)
+  Device dev;
+  pkv_status st = device(dev);
+  if (st != PKV_OK) return st;
+  const int D = c->head_dim, group = a.num_q_heads / c->num_kv_heads;
+  const int kind = c->kv_dtype == PKV_F16 ? KV_F16 : c->kv_dtype == PKV_BF16 ? KV_BF16 : c->kv_dtype == PKV_U4 ? KV_U4T
+                   : c->quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G;
+  // visits are counted in 32 bits: rows and prefixes at the table's full width
+  const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
+  if (c->num_kv_heads * tiles * (2ll * a.batch + (long long)a.batch * group / (2 * kTile)) >= (1ll << 31) ||
+      2ll * a.batch * a.num_q_heads >= (1ll << 30))
+    return PKV_ERR_UNSUPPORTED;
+  const int ctas = a.num_splits ? a.num_splits : dev.sms;
+  const Work w = layout(c, a.batch, a.num_q_heads, ctas);
+  if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < w.total)
     return PKV_ERR_WORKSPACE;
+
   SharedParams p = {};
+  const bool bf = a.q_dtype == PKV_BF16;
+  const void* fn = kind == KV_F16    ? shared_kernel_f16(D)
+                   : kind == KV_BF16 ? shared_kernel_bf16(D)
+                   : kind == KV_I8T  ? shared_kernel_i8t(D, bf)
+                   : kind == KV_I8G  ? shared_kernel_i8g(D, bf)
+                                     : shared_kernel_u4t(D, bf);
+  int threads = 0, smem = 0, entries = 0;
+#define PKV_SIZES(d, kv) \
+  if (D == d && kind == kv) sizes<d, kv>(threads, smem, entries, dev.smem, a.batch, a.num_groups);
+  PKV_SIZES(64, KV_F16) PKV_SIZES(64, KV_BF16) PKV_SIZES(64, KV_I8T) PKV_SIZES(64, KV_I8G) PKV_SIZES(64, KV_U4T)
+  PKV_SIZES(128, KV_F16) PKV_SIZES(128, KV_BF16) PKV_SIZES(128, KV_I8T) PKV_SIZES(128, KV_I8G) PKV_SIZES(128, KV_U4T)
+#undef PKV_SIZES
+  if (smem > dev.smem) return PKV_ERR_UNSUPPORTED;
+  // the limit is set to the device's, once and for all sizes
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  if (kind == KV_F16 || kind == KV_BF16) {
+    const uint64_t rows = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
+    if (!pool_map(c->k_pages, rows, D, bf, p.tmap_k) || !pool_map(c->v_pages, rows, D, bf, p.tmap_v))
+      return PKV_ERR_CUDA;
+  }
   p.k_pages = static_cast<const uint8_t*>(c->k_pages);
   p.v_pages = static_cast<const uint8_t*>(c->v_pages);
   p.kv_sz = c->kv_sz;
-  p.q = a.q;
+  p.q = static_cast<const uint8_t*>(a.q);
   p.out = a.out;
   p.block_table = a.block_table;
   p.seq_lens = a.seq_lens;
   p.prefix_group = a.prefix_group;
   p.prefix_lens = a.prefix_lens;
   p.dev_status = a.dev_status;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.ws_info = reinterpret_cast<int4*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.ws_acc = reinterpret_cast<float*>(ws + w.acc);
   p.num_pages = c->num_pages;
   p.page_size = c->page_size;
   p.num_kv_heads = c->num_kv_heads;
   p.num_q_heads = a.num_q_heads;
-  p.head_dim = c->head_dim;
+  p.group = group;
+  p.batch = a.batch;
   p.max_pages = a.max_pages;
   p.num_groups = a.num_groups;
-  p.kind = c->kv_dtype == PKV_F16 ? KV_F16 : c->kv_dtype == PKV_BF16 ? KV_BF16 : c->kv_dtype == PKV_U4 ? KV_U4T
-           : c->quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G;
+  p.num_ctas = ctas;
+  p.entries = entries;
+  p.round_to = kind == KV_I8G ? 64 : 16;
   p.q_dtype = a.q_dtype;
   p.out_dtype = a.out_dtype;
+  p.two_terms = a.out_dtype == PKV_F32;
   p.scale = a.sm_scale * 1.4426950408889634f;
   void* args[] = {&p};
-  return launch_pdl(reinterpret_cast<const void*>(&shared_plain_kernel), dim3(a.num_q_heads, a.batch), dim3(32), 0,
-                    a.stream, args) == cudaSuccess
+  if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
+  const int rows = a.batch * a.num_q_heads;
+  // few rows have many records each
+  const int wpr = rows < 16 * dev.sms ? 4 : 1;
+  const void* merge = D == 64 ? merge_kernel<64>(wpr) : merge_kernel<128>(wpr);
+  const int per = 4 / wpr;
+  return launch_pdl(merge, dim3((rows + per - 1) / per), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

@@ -64,7 +64,7 @@ class SharedBatch:
             return bits, val
 
         pre = [(tokens(p, k_scale), tokens(p, v_scale)) for p, _ in groups]
-        self.bits, self.k, self.v, self.kmid = [], [], [], []
+        self.bits, self.k, self.v, self.kmid, self.vmid = [], [], [], [], []
         for g, n in rows:
             own = (tokens(n, k_scale), tokens(n, v_scale))
             parts = [pre[g], own] if g >= 0 else [own]
@@ -73,8 +73,10 @@ class SharedBatch:
             self.bits.append((kb, vb))
             k, mid = restore(kind, kf)
             self.k.append(k)
-            self.v.append(restore(kind, vf)[0])
+            v, vmid = restore(kind, vf)
+            self.v.append(v)
             self.kmid.append(mid)
+            self.vmid.append(vmid)
         self.lens = np.array([k.shape[0] for k in self.k], dtype=np.int32)
         # tables: the prefix's whole pages are the same pages, everything else a row's own
         whole = [p // ps for p, _ in groups]
@@ -127,7 +129,7 @@ class SharedBatch:
 
     def expected(self, q, g, sm_scale=None, lens=None):
         """Oracle outputs [B][Hq][d] and the bound on each output's error before its own rounding,
-        without the rounding of the weights: (out, bound without weights, sum p |v|)."""
+        without the rounding of the weights: (out, bound without weights, what their roundings meet)."""
         sm = 1.0 / np.sqrt(self.d) if sm_scale is None else sm_scale
         out = np.zeros(q.shape)
         bound = np.zeros(q.shape)
@@ -143,7 +145,10 @@ class SharedBatch:
                 p = np.exp(s - s.max())
                 p /= p.sum()
                 out[b, h] = p @ v
-                mass[b, h] = p @ np.abs(v)
+                # a weight meets a quantised value in two parts, sum p vs (u - c) and sum p mid with
+                # mid = vz + c vs: |vs (u - c)| = |v - mid| <= |v| + |mid|, so that is what the
+                # weights' roundings are multiplied with
+                mass[b, h] = p @ np.abs(v) + self.vmid[b]
                 # scores: fp32 sums of d products (each |q_i k_i|; quantised keys as code and
                 # midpoint parts, |code part| <= |k| + |mid|), each step at most 2^-23 off
                 a = (np.abs(k) @ np.abs(qq)).max() + 2 * np.abs(qq).sum() * self.kmid[b]

@@ -31,13 +31,13 @@ pkv_status device(Device& d) {
 }
 
 // Workspace: each row's place in the plan, (m, l) by record row, accumulators.
-// Record rows: one per query row and segment kind for the block where the segment
-// begins, and 256 per block for the segment that it continues.
+// Record rows: one per query row, segment kind and stream for the block where the
+// segment begins, and 256 per block for the segment that it continues.
 struct Work {
   size_t ml, acc, total;
 };
 Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
-  const size_t rows = 2 * (size_t)batch * hq + (size_t)ctas * 2 * kTile;
+  const size_t rows = 4 * (size_t)batch * hq + (size_t)ctas * 2 * kTile;
   Work w;
   w.ml = align256((size_t)batch * 2 * sizeof(int4));
   w.acc = w.ml + align256(rows * sizeof(float2));
@@ -75,7 +75,7 @@ void sizes(int& threads, int& smem, int& entries, int avail, int batch, int grou
   using G = SharedGeom<D, KV, true>;   // operand types have the same sizes
   threads = G::THREADS;
   entries = kMaxEntries;
-  while (entries > 2 && 1024 + shared_layout<G>(entries, batch, groups).total > avail) entries -= 2;
+  while (entries > 1 && 1024 + shared_layout<G>(entries, batch, groups).total > avail) --entries;
   smem = 1024 + shared_layout<G>(entries, batch, groups).total;
 }
 
@@ -108,7 +108,7 @@ pkv_status launch_shared(const SharedArgs& a) {
   // visits are counted in 32 bits: rows and prefixes at the table's full width
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   if (c->num_kv_heads * tiles * (2ll * a.batch + (long long)a.batch * group / (2 * kTile)) >= (1ll << 31) ||
-      2ll * a.batch * a.num_q_heads >= (1ll << 30))
+      2ll * a.batch * a.num_q_heads >= (1ll << 29))
     return PKV_ERR_UNSUPPORTED;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
   const Work w = layout(c, a.batch, a.num_q_heads, ctas);
@@ -165,6 +165,7 @@ pkv_status launch_shared(const SharedArgs& a) {
   p.q_dtype = a.q_dtype;
   p.out_dtype = a.out_dtype;
   p.two_terms = a.out_dtype == PKV_F32;
+  p.few_rows = p.two_terms ? 16 : 32;
   p.scale = a.sm_scale * 1.4426950408889634f;
   void* args[] = {&p};
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;

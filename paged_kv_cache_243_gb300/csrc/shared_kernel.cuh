@@ -43,16 +43,31 @@
 // fp16's range; the accumulator is rescaled when a later tile's scales outgrow it.
 #pragma once
 
+#include <type_traits>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 
 namespace pkv {
 
+// A place in a ring, and the parity of its use.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 constexpr int kTile = 128;        // tokens of a visit, query rows of a tile
 constexpr int kHdrs = 8;          // visit headers kept (more than the visits the ring holds)
 constexpr int kScaleSlots = 4;    // visits whose scales are kept for the softmax
 constexpr int kQSums = 8;
-constexpr int kMaxEntries = 12;   // ring entries: at most 2 (kHdrs - 2)
+constexpr int kMaxEntries = 6;    // ring entries of K, and of V: at most kHdrs - 2
+constexpr int kPtBytes = 8192;    // transposed weights of a stream: 16 rows in two terms, or 32 in one
 
 struct SharedParams {
   CUtensorMap tmap_k, tmap_v;   // 16-bit pools as [rows][d], boxes of 16 rows x 64 channels
@@ -71,7 +86,7 @@ struct SharedParams {
   float* ws_acc;
   int4* ws_info;
   int num_pages, page_size, num_kv_heads, num_q_heads, group, batch, max_pages, num_groups;
-  int num_ctas, entries, round_to, q_dtype, out_dtype, two_terms, rows_per_warp_group;
+  int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms, few_rows;
   float scale;   // sm_scale * log2(e)
 };
 
@@ -90,13 +105,14 @@ struct SharedGeom {
 
 // Shared memory by offset from a 1024-byte boundary.
 struct SharedLayout {
-  int q, kop, vop, ring, raw, scales, bars, hdr, ml, qsum, vmax, misc, lens, skip, bpre, gpre, gp, moff, members, rank;
+  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, lens, skip, bpre, gpre, gp, moff, members, rank;
   int total;
 };
 enum SharedBars {   // mbarriers, 8 bytes each
-  kBarFull = 0, kBarEmpty = kMaxEntries, kBarHdr = 2 * kMaxEntries, kBarQFull = kBarHdr + kHdrs,
-  kBarQEmpty = kBarQFull + 2, kBarS = kBarQEmpty + 2, kBarP = kBarS + 2, kBarO = kBarP + 2,
-  kBarKop = kBarO + 2, kBarVop = kBarKop + 2, kBarPair = kBarVop + 2, kBarEnd = kBarPair + 4, kBarCount = kBarEnd + 1
+  kBarKFull = 0, kBarVFull = kMaxEntries, kBarKEmpty = 2 * kMaxEntries, kBarVEmpty = 3 * kMaxEntries,
+  kBarHdr = 4 * kMaxEntries, kBarQFull = kBarHdr + kHdrs, kBarQEmpty = kBarQFull + 2, kBarS = kBarQEmpty + 2,
+  kBarP = kBarS + 2, kBarO = kBarP + 2, kBarX = kBarO + 2, kBarKop = kBarX + 2, kBarVop = kBarKop + 2,
+  kBarPair = kBarVop + 2, kBarEnd = kBarPair + 4, kBarCount = kBarEnd + 1
 };
 
 template <class G>
@@ -111,8 +127,10 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.q = put(2 * G::OPERAND);
   o.kop = put(G::QUANT ? G::OPERAND : 0);
   o.vop = put(G::QUANT ? G::OPERAND : 0);
-  o.ring = put(entries * G::ENTRY);
-  o.raw = put(entries / 2 * G::RAW_SCALES);
+  o.ring = put(2 * entries * G::ENTRY);
+  o.raw = put(entries * G::RAW_SCALES);
+  o.pt = put(2 * kPtBytes);
+  o.xch = put(2 * 2 * 4 * 64 * 4);
   o.scales = put(kScaleSlots * G::SCALES);
   o.bars = put(kBarCount * 8);
   o.hdr = put(kHdrs * 8);
@@ -133,7 +151,11 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
 }
 
 // Blocks' shares of W visits.
-__device__ __forceinline__ int share_lo(long long c, long long W, long long N) { return (int)(c * W / N); }
+// floor(c W / N) with c <= N < 2^16, in 32 bits
+__device__ __forceinline__ int share_lo(int c, int W, int N) {
+  const uint32_t q = (uint32_t)W / (uint32_t)N, r = (uint32_t)W - q * (uint32_t)N;
+  return (int)((uint32_t)c * q + (uint32_t)c * r / (uint32_t)N);
+}
 // The block that holds visit x: the largest c with floor(c W / N) <= x.
 __device__ __forceinline__ int share_of(long long x, long long W, long long N) {
   return (int)(((x + 1) * N + W - 1) / W - 1);
@@ -144,8 +166,20 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// The instructions below are issued by the one lane with `on` set, in code that the
+// whole warp runs: their operands then live in uniform registers (issued from
+// code of a single lane, each took about 110 cycles to set up).
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
+  return r;
 }
 
 // Shared-memory operand descriptor, 128-byte swizzle: start address, leading and
@@ -156,51 +190,61 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo, ui
 }
 
 // D[tmem] (+)= A[smem] B[smem], or A in TMEM.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t on) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t on) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
       : "memory");
 }
 
-// 32 columns of this warp's 32 TMEM lanes: lane i of the warp holds row i.
-__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t));
+// N columns of this warp's 32 TMEM lanes: lane i of the warp holds row i.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* r);
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_ld<8>(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(t));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+template <>
+__device__ __forceinline__ void tmem_ld<32>(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(t));
+}
+template <>
+__device__ __forceinline__ void tmem_st<8>(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<16>(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<32>(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
 }
 
 template <bool BF>
@@ -294,30 +338,29 @@ __device__ __forceinline__ Seg locate(const SharedPlan& p, int x, int hi) {
   return s;
 }
 
-// Exclusive prefix sums of val(i), i < n, into pre[0 .. n]; every thread of the block.
-template <class F>
-__device__ __forceinline__ void block_scan(int* pre, int n, int base, int threads, int* scratch, F&& val) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (n + threads - 1) / threads;
-  const int a = min(n, tid * per), b = min(n, a + per);
-  int sum = 0;
-  for (int i = a; i < b; ++i) sum += val(i);
-  int incl = sum;
+// Exclusive prefix sums over the block's threads of two values, and their totals.
+__device__ __forceinline__ void block_scan2(int a, int b, int& pa, int& pb, int& ta, int& tb, int threads,
+                                            int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = threads / 32;
+  int ia = a, ib = b;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
+    const int ya = __shfl_up_sync(0xffffffffu, ia, off), yb = __shfl_up_sync(0xffffffffu, ib, off);
+    if (lane >= off) {
+      ia += ya;
+      ib += yb;
+    }
   }
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  int run = base + incl - sum;
-  for (int w = 0; w < warp; ++w) run += scratch[w];
-  for (int i = a; i < b; ++i) {
-    pre[i] = run;
-    run += val(i);
+  if (lane == 31) {
+    scratch[warp] = ia;
+    scratch[16 + warp] = ib;
   }
-  if (tid == threads - 1) pre[n] = run;
   __syncthreads();
+  int va = lane < warps ? scratch[lane] : 0, vb = lane < warps ? scratch[16 + lane] : 0;
+  pa = ia - a + __reduce_add_sync(0xffffffffu, lane < warp ? va : 0);
+  pb = ib - b + __reduce_add_sync(0xffffffffu, lane < warp ? vb : 0);
+  ta = __reduce_add_sync(0xffffffffu, va);
+  tb = __reduce_add_sync(0xffffffffu, vb);
 }
 
 // --------------------------------------------------------------- code -> value
@@ -389,6 +432,35 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
 }
 
 // ------------------------------------------------------------------ the kernel
+// Sum of v[j] over the warp, for each j: lane (32 / R) j' + anything ends with the
+// total of one j (returned in `j`), by exchanging halves.
+template <int R>
+__device__ __forceinline__ float scatter_sum(float (&v)[R], int lane, int& j) {
+  j = 0;
+#pragma unroll
+  for (int n = R, off = 16; off > 0; off >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & off;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+      }
+      j += up ? n : 0;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <int D, int KV, bool BF>
 __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
@@ -415,8 +487,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kMaxEntries; ++i) {
-      mbar_init(bar(kBarFull + i), 1);
-      mbar_init(bar(kBarEmpty + i), QUANT ? 4 : 1);
+      mbar_init(bar(kBarKFull + i), 1);
+      mbar_init(bar(kBarVFull + i), 1);
+      mbar_init(bar(kBarKEmpty + i), QUANT ? 4 : 1);
+      mbar_init(bar(kBarVEmpty + i), QUANT ? 4 : 1);
     }
     for (int i = 0; i < kHdrs; ++i) mbar_init(bar(kBarHdr + i), QUANT ? 4 : 1);
     for (int i = 0; i < 2; ++i) {
@@ -425,6 +499,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), 4);
       mbar_init(bar(kBarO + i), 1);
+      mbar_init(bar(kBarX + i), 4);
     }
     mbar_init(bar(kBarKop), 4);        // converted K ready / free again
     mbar_init(bar(kBarKop + 1), 1);
@@ -435,6 +510,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     misc[1] = 0;
   }
   fence_mbar_init();
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(smem + lay.misc))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  for (int g = tid; g < NG; g += NT) moff[g] = 0;
   pdl_wait();
   pdl_launch_dependents();
 
@@ -443,10 +524,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   for (int g = tid; g < NG; g += NT) {
     const int P = p.prefix_lens[g];
     if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
-    gp[g] = P < 0 ? 0 : P;
-    moff[g] = 0;
+    gp[g] = max(P, 0) / p.round_to * p.round_to;
   }
-  __syncthreads();
   for (int b = tid; b < B; b += NT) {
     int L = p.seq_lens[b], g = p.prefix_group[b];
     if (L < 0 || L > cap) {
@@ -458,14 +537,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       g = -1;
     }
     // a row shares its group's prefix if it has all of it
-    const int P = g >= 0 ? gp[g] / p.round_to * p.round_to : 0;
-    if (g >= 0 && (P == 0 || L < gp[g])) g = -1;
+    const int P = g >= 0 ? p.prefix_lens[g] : 0;
+    if (P < p.round_to || L < P) g = -1;
     lens[b] = L;
-    skip[b] = g >= 0 ? P : 0;
+    skip[b] = g >= 0 ? P / p.round_to * p.round_to : 0;
     members[b] = (uint16_t)g;   // the group for now
   }
   __syncthreads();
-  if (warp == 0) {   // each row's place among its group's rows
+  if (warp == 0 && NG > 0) {   // each row's place among its group's rows
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int b = b0 + lane;
       const int g = b < B ? (int)(int16_t)members[b] : -1;
@@ -478,85 +557,88 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
   }
   __syncthreads();
-  // visits of a group's prefix: kv heads x pairs of row tiles x tiles of tokens
-  for (int g = tid; g < NG; g += NT) gp[g] = gp[g] / p.round_to * p.round_to;
-  __syncthreads();
-  block_scan(gpre, NG, 0, NT, scratch, [&](int g) {
-    const int rows = moff[g] * Gq;
-    return rows == 0 ? 0 : p.num_kv_heads * ((rows + 2 * kTile - 1) / (2 * kTile)) * ((gp[g] + kTile - 1) / kTile);
-  });
-  {   // members before each group, in place of their counts
+  // visits of a group's prefix: kv heads x pairs of row tiles x tiles of tokens;
+  // members before each group, in place of their counts
+  {
     const int per = (NG + NT - 1) / NT;   // <= 3: up to 1024 groups, 384 threads and more
     const int a = min(NG, tid * per), e = min(NG, a + per);
-    int c[3], sum = 0;
+    int c[3], w[3], sum = 0, wsum = 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       c[i] = a + i < e ? moff[a + i] : 0;
+      w[i] = c[i] == 0 ? 0
+                       : p.num_kv_heads * ((c[i] * Gq + 2 * kTile - 1) / (2 * kTile)) * ((gp[a + i] + kTile - 1) / kTile);
       sum += c[i];
+      wsum += w[i];
     }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += scratch[w];
+    int run, wrun, rt = 0, wt;
+    block_scan2(sum, wsum, run, wrun, rt, wt, NT, scratch);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      if (a + i < e) moff[a + i] = run;
-      run += c[i];
-    }
-    if (tid == NT - 1) moff[NG] = run;
-    __syncthreads();
-  }
-  const int Wp = gpre[NG];
-  block_scan(bpre, B, Wp, NT, scratch,
-             [&](int b) { return p.num_kv_heads * ((lens[b] - skip[b] + kTile - 1) / kTile); });
-  const int W = bpre[B];
-  // members by group; the group of row b is still in members[b], so each thread reads its rows' first
-  {
-    int16_t mine[4];
-    constexpr int PER = (1024 + NT - 1) / NT;
-    static_assert(PER <= 4, "rows per thread");
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = tid + i * NT;
-      mine[i] = b < B ? (int16_t)members[b] : (int16_t)-1;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = tid + i * NT;
-      if (b >= B) continue;
-      const int g = mine[i];
-      if (g >= 0) members[moff[g] + rank[b]] = (uint16_t)b;
-      if (b % (int)gridDim.x == (int)blockIdx.x) {   // for the merge: where row b's segments are
-        const int rows = g >= 0 ? (moff[g + 1] - moff[g]) * Gq : 0;
-        p.ws_info[2 * b] = make_int4(g >= 0 ? moff[g] * Gq : 0, g >= 0 ? rank[b] : 0, g >= 0 ? gpre[g] : 0,
-                                     (rows + 2 * kTile - 1) / (2 * kTile));
-        p.ws_info[2 * b + 1] = make_int4(g >= 0 ? (gp[g] + kTile - 1) / kTile : 0, bpre[b],
-                                         (lens[b] - skip[b] + kTile - 1) / kTile, W);
+      if (a + i < e) {
+        moff[a + i] = run;
+        gpre[a + i] = wrun;
       }
+      run += c[i];
+      wrun += w[i];
+    }
+    if (tid == NT - 1) {
+      moff[NG] = rt;
+      gpre[NG] = wt;
+    }
+    // and the rows' own tokens behind them
+    const int per_b = (B + NT - 1) / NT;
+    const int ba = min(B, tid * per_b), be = min(B, ba + per_b);
+    int bsum = 0;
+    for (int b = ba; b < be; ++b) bsum += p.num_kv_heads * ((lens[b] - skip[b] + kTile - 1) / kTile);
+    int brun, dummy, bt, dt;
+    __syncthreads();
+    block_scan2(bsum, 0, brun, dummy, bt, dt, NT, scratch);
+    brun += wt;
+    for (int b = ba; b < be; ++b) {
+      bpre[b] = brun;
+      brun += p.num_kv_heads * ((lens[b] - skip[b] + kTile - 1) / kTile);
+    }
+    if (tid == NT - 1) bpre[B] = wt + bt;
+  }
+  // the group of row b is still in members[b]: each thread reads its rows' first
+  int16_t mine[4];
+  constexpr int PER = (1024 + NT - 1) / NT;
+  static_assert(PER <= 4, "rows per thread");
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid + i * NT;
+    mine[i] = b < B ? (int16_t)members[b] : (int16_t)-1;
+  }
+  __syncthreads();
+  const int Wp = gpre[NG], W = bpre[B];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid + i * NT;
+    if (b >= B) continue;
+    const int g = mine[i];
+    if (g >= 0) members[moff[g] + rank[b]] = (uint16_t)b;
+    if (b % (int)gridDim.x == (int)blockIdx.x) {   // for the merge: where row b's segments are
+      const int rows = g >= 0 ? (moff[g + 1] - moff[g]) * Gq : 0;
+      p.ws_info[2 * b] = make_int4(g >= 0 ? moff[g] * Gq : 0, g >= 0 ? rank[b] : 0, g >= 0 ? gpre[g] : 0, rows);
+      p.ws_info[2 * b + 1] = make_int4(g >= 0 ? (gp[g] + kTile - 1) / kTile : 0, bpre[b],
+                                       (lens[b] - skip[b] + kTile - 1) / kTile, W);
     }
   }
   const SharedPlan plan = {lens, skip, bpre, gpre, gp, moff, members, B, NG, p.num_kv_heads, Gq, W, Wp};
   const int lo = W > 0 ? share_lo(blockIdx.x, W, p.num_ctas) : 0;
   const int hi = W > 0 ? share_lo(blockIdx.x + 1, W, p.num_ctas) : 0;
-  if (lo >= hi) return;   // uniform over the block
-
-  if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(smem + lay.misc))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = (uint32_t)misc[0];
-  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + D};
+  const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
+  if (lo >= hi) {   // uniform over the block
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    return;
+  }
+  // a stream's scores (and weights over them), and its accumulator
+  auto tm_s = [&](int st) { return tmem + 128u * (uint32_t)st; };
+  auto tm_o = [&](int st) { return tmem + 256u + (uint32_t)(D * st); };
 
   // Bounded wait; the first warp to give up reports it and everyone stops.
   auto wait = [&](int i, uint32_t parity) -> bool {
@@ -572,74 +654,129 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
     return true;
   };
-
   // for a whole warp: every lane goes on, or none does
   auto wait_warp = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(i, parity)); };
+  // queries of tile u of a segment into operand slot qs, by `warps` warps
+  auto gather_q = [&](const Seg& s, int u, int qs, int w, int warps) {
+    constexpr int CH = D / 8, RPI = 32 / CH;   // 16-byte pieces of a row, rows an instruction
+    uint8_t* dst = smem + lay.q + (size_t)qs * G::OPERAND;
+    const int rows = min(kTile, s.rows - u * kTile);
+    for (int r0 = 32 * w; r0 < rows; r0 += 32 * warps) {
+      // lane i finds row r0 + i
+      const int R = s.q0 + u * kTile + r0 + lane;
+      int b = s.row, gq = R;
+      if (s.mem0 >= 0) {
+        const int m = R / Gq;
+        b = r0 + lane < rows ? members[s.mem0 + m] : 0;
+        gq = R - m * Gq;
+      }
+      const int qrow = b * p.num_q_heads + s.head * Gq + gq;
+      const int n = min(32, rows - r0), c = lane % CH;
+#pragma unroll 4
+      for (int i = 0; i < n; i += RPI) {
+        const int r = i + lane / CH;
+        const int from = __shfl_sync(0xffffffffu, qrow, r & 31);
+        if (r < n)
+          cp_async16(smem_u32(dst + (c >> 3) * 16384 + (r0 + r) * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                     p.q + ((size_t)from * D + c * 8) * 2);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  };
+  // sums of the queries of a gathered tile, for the zero points
+  auto sum_q = [&](const Seg& s, int u, int qs, int slot) {
+    const uint8_t* src = smem + lay.q + (size_t)qs * G::OPERAND;
+    float* qsum = reinterpret_cast<float*>(smem + lay.qsum) + slot * kTile;
+    const int rows = min(kTile, s.rows - u * kTile);
+    for (int r = lane; r < rows; r += 32) {
+      float t = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        t += (low16<BF>(w.x) + high16<BF>(w.x)) + (low16<BF>(w.y) + high16<BF>(w.y)) +
+             ((low16<BF>(w.z) + high16<BF>(w.z)) + (low16<BF>(w.w) + high16<BF>(w.w)));
+      }
+      qsum[r] = t;
+    }
+  };
 
-  if (warp == 8) {
-    // ================================================================ loader
+  // the first segment's queries, by the warps that have nothing else to do yet
+  const Seg first = locate(plan, lo, hi);
+  const int first_tiles = first.rows > kTile ? 2 : 1;
+  if (warp < 8) {
+    for (int u = 0; u < first_tiles; ++u) gather_q(first, u, u, warp, 8);
+    fence_proxy_async_smem();
+    named_bar_sync(1, 288);
+  } else if (warp == 10) {
+    named_bar_sync(1, 288);
+    if constexpr (QUANT) {
+      for (int u = 0; u < first_tiles; ++u) sum_q(first, u, u, u);
+      __syncwarp();
+    }
+    if (lane == 0)
+      for (int u = 0; u < first_tiles; ++u) mbar_arrive(bar(kBarQFull + u));
+  }
+
+  if (warp == 8 || warp == 11) {
+    // =============================================== loaders: K (8) and V (11)
+    const bool isv = warp == 11;
     const uint64_t pol = policy_evict_first();
-    // lanes 0-15 copy K, 16-31 V; within them piece (16 tokens) and half of the channels
-    constexpr int PARTS = QUANT ? 1 : G::HALVES;
-    const int isv = lane >> 4, piece = (lane & 15) / PARTS, half = (lane & 15) % PARTS;
-    const bool lane_on = piece < 8;
+    constexpr int PARTS = QUANT ? 1 : G::HALVES;   // boxes side by side in a row
+    const int piece = lane / PARTS, half = lane % PARTS;
+    const int fulls = isv ? kBarVFull : kBarKFull, empties = isv ? kBarVEmpty : kBarKEmpty;
+    uint8_t* ring = smem + lay.ring + (isv ? (size_t)S * G::ENTRY : 0);
+    const uint8_t* pool = isv ? p.v_pages : p.k_pages;
+    const void* map = isv ? &p.tmap_v : &p.tmap_k;
     int v = 0;
     bool ok = true;
+    Seg s = first;
     // page of this lane's piece, one visit ahead
-    Seg s = locate(plan, lo, hi);
     auto lookup = [&](const Seg& sg, int x) -> int {
       const int tok = sg.first_tok + (sg.tile0 + x - sg.begin) * kTile + 16 * piece;
-      if (!lane_on || tok >= sg.end_tok) return -2;   // nothing to copy
+      if (piece >= 8 || tok >= sg.end_tok) return -2;   // nothing to copy
       return p.block_table[(size_t)sg.row * p.max_pages + tok / p.page_size];
     };
     int page = lookup(s, lo);
-    for (int x = lo; x < hi && ok; ++x, ++v) {
-      const Seg cs = s;
-      const int tok = cs.first_tok + (cs.tile0 + x - cs.begin) * kTile + 16 * piece;
-      const int pg = page;
+    RingPos pos;
+    for (int x = lo; x < hi && ok; ++x, ++v, pos.next(S)) {
+      const int head = s.head, tok0 = s.first_tok + (s.tile0 + x - s.begin) * kTile;
+      const int ntok = min(kTile, s.end_tok - tok0), pg = page;
       if (x + 1 < hi) {
         if (x + 1 == s.end) s = locate(plan, x + 1, hi);
         page = lookup(s, x + 1);
       }
       const bool bad = pg != -2 && (pg < 0 || pg >= p.num_pages);
-      if (bad && isv == 0 && half == 0) flag_status(p.dev_status, PKV_DEV_BAD_PAGE);
+      if (bad && !isv && half == 0) flag_status(p.dev_status, PKV_DEV_BAD_PAGE);
       const bool copy = pg != -2 && !bad;
       const unsigned has = __ballot_sync(0xffffffffu, copy && half == 0);
-      // bit i: piece i was copied (from the K lanes; the V lanes have the same)
-      unsigned mask = 0;
+      unsigned mask = 0;   // bit i: piece i was copied
 #pragma unroll
       for (int i = 0; i < 8; ++i) mask |= (has >> (i * PARTS) & 1u) << i;
-      const int e = 2 * v + isv, slot = e % S, use = e / S;
-      ok = use == 0 || wait(kBarEmpty + slot, (use - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
+      const int slot = pos.slot;
+      ok = v < S || wait_warp(empties + slot, pos.phase ^ 1);
       if (!ok) break;
-      const uint32_t fb = bar(kBarFull + slot);
-      if ((lane & 15) == 0) {
-        if (isv == 0) {
-          const int n = min(kTile, cs.end_tok - (cs.first_tok + (cs.tile0 + x - cs.begin) * kTile));
-          *reinterpret_cast<int2*>(smem + lay.hdr + (v % kHdrs) * 8) = make_int2(n, (int)mask);
-        }
+      const uint32_t fb = bar(fulls + slot);
+      if (lane == 0) {
+        if (!isv) *reinterpret_cast<int2*>(smem + lay.hdr + (v % kHdrs) * 8) = make_int2(ntok, (int)mask);
         uint32_t bytes = (uint32_t)__popc(mask) * 16u * G::ROW;
-        if constexpr (KV == KV_I8T || KV == KV_U4T) bytes += isv == 0 ? (uint32_t)__popc(mask) * 256u : 0u;
-        if constexpr (KV == KV_I8G) bytes += isv == 0 ? (uint32_t)((mask & 0xF ? 16 : 0) + (mask & 0xF0 ? 16 : 0)) : 0u;
+        if constexpr (KV == KV_I8T || KV == KV_U4T) bytes += !isv ? (uint32_t)__popc(mask) * 256u : 0u;
+        if constexpr (KV == KV_I8G) bytes += !isv ? (uint32_t)((mask & 0xF ? 16 : 0) + (mask & 0xF0 ? 16 : 0)) : 0u;
         if (bytes)
           mbar_arrive_expect_tx(fb, bytes);
         else
           mbar_arrive(fb);
-        if (!QUANT && isv == 0) mbar_arrive(bar(kBarHdr + v % kHdrs));
+        if (!QUANT && !isv) mbar_arrive(bar(kBarHdr + v % kHdrs));
       }
       __syncwarp();
       if (copy) {
-        const size_t row = ((size_t)pg * p.num_kv_heads + cs.head) * p.page_size + tok % p.page_size;
-        uint8_t* dst = smem + lay.ring + (size_t)slot * G::ENTRY;
+        const size_t row = ((size_t)pg * p.num_kv_heads + head) * p.page_size + (tok0 + 16 * piece) % p.page_size;
+        uint8_t* dst = ring + (size_t)slot * G::ENTRY;
         if constexpr (!QUANT) {
-          tma_load_2d(smem_u32(dst + half * 16384 + piece * 2048), isv ? &p.tmap_v : &p.tmap_k, half * 64, (int)row,
-                      fb, pol);
+          tma_load_2d(smem_u32(dst + half * 16384 + piece * 2048), map, half * 64, (int)row, fb, pol);
         } else {
-          bulk_g2s(smem_u32(dst + piece * 16 * G::ROW), (isv ? p.v_pages : p.k_pages) + row * G::ROW, 16 * G::ROW, fb,
-                   pol);
-          if (isv == 0) {
-            uint8_t* raw = smem + lay.raw + (size_t)(v % (S / 2)) * G::RAW_SCALES;
+          bulk_g2s(smem_u32(dst + piece * 16 * G::ROW), pool + row * G::ROW, 16 * G::ROW, fb, pol);
+          if (!isv) {
+            uint8_t* raw = smem + lay.raw + (size_t)slot * G::RAW_SCALES;
             if constexpr (KV != KV_I8G) {
               bulk_g2s(smem_u32(raw + piece * 256), p.kv_sz + row * 4, 256, fb, pol);
             } else if ((mask & ((1u << piece) - 1) & (piece < 4 ? 0xFu : 0xF0u)) == 0) {
@@ -652,81 +789,115 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       __syncwarp();
     }
     // every issued copy lands before the block can end
-    if (lane == 0) {
-      const int n = 2 * v;
-      for (int e = n > S ? n - S : 0; e < n; ++e)
-        if (!mbar_wait_bounded(bar(kBarFull + e % S), (e / S) & 1)) break;
-    }
+    if (lane == 0)
+      for (int e = v > S ? v - S : 0; e < v; ++e)
+        if (!mbar_wait_bounded(bar(fulls + e % S), (e / S) & 1)) break;
+    __syncwarp();
   } else if (warp == 9) {
     // =================================================================== MMA
-    if (lane == 0) {
-      constexpr uint32_t kType = BF ? (1u << 7 | 1u << 10) : 0u;
-      constexpr uint32_t idesc_s = 1u << 4 | kType | (uint32_t)(kTile / 8) << 17 | 8u << 24;
-      constexpr uint32_t idesc_o = 1u << 4 | kType | 1u << 16 | (uint32_t)(D / 8) << 17 | 8u << 24;
-      const uint32_t qb = smem_u32(smem + lay.q), ring = smem_u32(smem + lay.ring);
+    {
+      const uint32_t on = elect_one();
+      auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      constexpr uint32_t kType = 1u << 4 | (BF ? (1u << 7 | 1u << 10) : 0u) | 8u << 24;   // fp32 sums, M = 128
+      constexpr uint32_t idesc_s = kType | (uint32_t)(kTile / 8) << 17;
+      constexpr uint32_t idesc_o = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
+      const uint64_t kmajor = operand_desc(0, 16, 1024), vmajor = operand_desc(0, D == 128 ? 16384 : 0, 1024);
+      const uint64_t pmajor = (uint64_t)(128 >> 4) << 16 | (uint64_t)(2048 >> 4) << 32 | 1ull << 46;   // no swizzle
+      auto at = [](uint64_t d, uint32_t addr) { return d | (uint64_t)(addr >> 4); };
+      const uint32_t qb = smem_u32(smem + lay.q), ring = smem_u32(smem + lay.ring), pt = smem_u32(smem + lay.pt);
       const uint32_t kop = smem_u32(smem + lay.kop), vop = smem_u32(smem + lay.vop);
       int qc = 0, v = 0;
-      uint32_t pn[2] = {0, 0};   // events so far on each stream
+      uint32_t odd = 0;   // bit st: parity of the events so far on stream st
       bool ok = true;
       // the event whose P V product is still to be issued
-      struct { int st, v, steps; bool on, fresh, last_use, seg_end; } pend = {};
+      struct { int st, steps, few; RingPos at; bool on, fresh, last_use, seg_end; } pend = {};
+      RingPos pos;
+      uint32_t vop_phase = 0;   // uses of the converted V tile
       auto issue_pv = [&]() -> bool {
-        const int st = pend.st, e = 2 * pend.v + 1;
-        if (!wait(kBarP + st, (pn[st] - 1) & 1)) return false;
-        uint32_t vb;
-        if constexpr (QUANT) {
-          if (!wait(kBarVop, pend.v & 1)) return false;
-          vb = vop;
-        } else {
-          if (!wait(kBarFull + e % S, (e / S) & 1)) return false;
-          vb = ring + (uint32_t)(e % S) * G::ENTRY;
-        }
+        const int st = pend.st, slot = pend.at.slot;
+        if (!wait_warp(kBarP + st, ~(odd >> st) & 1)) return false;
+        if (!(QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + slot, pend.at.phase))) return false;
+        const uint64_t vd = at(vmajor, QUANT ? vop : ring + (uint32_t)(S + slot) * G::ENTRY);
         tc_after();
-        for (int j = 0; j < pend.steps; ++j) {
-          const uint64_t vd = operand_desc(vb + j * 2048, 16384, 1024);
-          const uint32_t a = tm_s[st] + 32 * (j >> 1) + 8 * (j & 1);
-          mma_ts(tm_o[st], a, vd, idesc_o, !(pend.fresh && j == 0));
-          if (p.two_terms) mma_ts(tm_o[st], a + 16, vd, idesc_o, 1);
+        const uint32_t acc0 = !pend.fresh, o = tm_o(st);
+        if (pend.few) {
+          // O^T (+)= V^T P^T: channels x rows
+          const uint32_t idesc_t = kType | 1u << 15 | 1u << 16 | (uint32_t)(pend.few / 8) << 17;
+          const uint64_t pd = at(pmajor, pt + (uint32_t)st * kPtBytes);
+          const bool terms = pend.few == 16;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (j < pend.steps) {
+              mma_ss(o, vd + j * 128, pd + j * 16, idesc_t, j ? 1u : acc0, on);
+              if (terms) mma_ss(o, vd + j * 128, pd + j * 16 + 256, idesc_t, 1, on);
+            }
+          }
+        } else {
+          const uint32_t a = tm_s(st);
+          if (p.two_terms) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (j < pend.steps) {
+                mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc_o, j ? 1u : acc0, on);
+                mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1) + 16, vd + j * 128, idesc_o, 1, on);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < pend.steps) mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc_o, j ? 1u : acc0, on);
+          }
         }
-        if (pend.last_use) tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarEmpty + e % S));
-        if (pend.seg_end) tc_commit(bar(kBarO + st));
+        if (pend.last_use) {
+          tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarVEmpty + slot), on);
+          vop_phase ^= 1;
+        }
+        if (pend.seg_end) tc_commit(bar(kBarO + st), on);
         pend.on = false;
         return true;
       };
-      for (int x = lo; x < hi && ok;) {
-        const Seg s = locate(plan, x, hi);
-        const bool two = s.rows > kTile;
-        const int n = s.end - s.begin;
-        for (int i = 0; i < n && ok; ++i, ++v) {
-          const int e = 2 * v, slot = e % S;
-          ok = QUANT ? wait(kBarKop, v & 1) : wait(kBarFull + slot, (e / S) & 1);
+      for (int x = uni(lo), end = uni(hi); x < end && ok;) {
+        const Seg s = x == lo ? first : locate(plan, x, hi);
+        const int rows = uni(s.rows), n = uni(s.end - s.begin);
+        const bool two = rows > kTile;
+        const int few = rows <= p.few_rows ? (rows <= 16 ? 16 : 32) : 0;
+        for (int i = 0; i < n && ok; ++i, ++v, pos.next(S)) {
+          const int slot = pos.slot;
+          ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + slot, pos.phase);
           if (!ok) break;
-          const int ntok = *reinterpret_cast<const volatile int*>(smem + lay.hdr + (v % kHdrs) * 8);
-          const uint32_t kb = QUANT ? kop : ring + (uint32_t)slot * G::ENTRY;
+          const int ntok = uni(*reinterpret_cast<const volatile int*>(smem + lay.hdr + (v % kHdrs) * 8));
+          const uint64_t kd = at(kmajor, QUANT ? kop : ring + (uint32_t)slot * G::ENTRY);
           for (int u = 0; u < (two ? 2 : 1) && ok; ++u) {
             const int st = two ? u : v & 1, qs = (qc + (two ? u : 0)) & 1;
             // normally the streams alternate; a score tile is never overwritten
             // before the weights in it are used
             if (pend.on && pend.st == st) ok = issue_pv();
             if (!ok) break;
-            if (i == 0) ok = wait(kBarQFull + qs, ((qc + (two ? u : 0)) >> 1) & 1);
+            if (i == 0) ok = wait_warp(kBarQFull + qs, ((qc + (two ? u : 0)) >> 1) & 1);
             if (!ok) break;
             tc_after();
-            const uint32_t q = qb + (uint32_t)qs * G::OPERAND;
+            const uint64_t qd = at(kmajor, qb + (uint32_t)qs * G::OPERAND);
+            if (few) {
+              // S^T = K Q^T: tokens x rows
+              const uint32_t idesc_t = kType | (uint32_t)(few / 8) << 17;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (uint32_t)(k >> 2) * 16384 + (uint32_t)(k & 3) * 32;
-              mma_ss(tm_s[st], operand_desc(q + off, 16, 1024), operand_desc(kb + off, 16, 1024), idesc_s, k > 0);
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(tm_s(st), kd + (k >> 2) * 1024 + (k & 3) * 2, qd + (k >> 2) * 1024 + (k & 3) * 2, idesc_t, k > 0, on);
+            } else {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(tm_s(st), qd + (k >> 2) * 1024 + (k & 3) * 2, kd + (k >> 2) * 1024 + (k & 3) * 2, idesc_s, k > 0, on);
             }
-            tc_commit(bar(kBarS + st));
+            tc_commit(bar(kBarS + st), on);
             const bool last_s = u == (two ? 1 : 0);
-            if (last_s) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarEmpty + slot));
-            if (i == n - 1) tc_commit(bar(kBarQEmpty + qs));
+            if (last_s) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + slot), on);
+            if (i == n - 1) tc_commit(bar(kBarQEmpty + qs), on);
             if (pend.on) ok = issue_pv();
-            ++pn[st];
+            odd ^= 1u << st;
             pend.st = st;
-            pend.v = v;
+            pend.at = pos;
             pend.steps = (ntok + 15) >> 4;
+            pend.few = few;
             pend.on = true;
             pend.fresh = two ? i == 0 : i < 2;
             pend.last_use = last_s;
@@ -734,55 +905,28 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           }
         }
         qc += two ? 2 : 1;
-        x = s.end;
+        x += n;
       }
       if (ok && pend.on) ok = issue_pv();
       // nothing of the tensor cores is in flight past this point
-      tc_commit(bar(kBarEnd));
-      if (!mbar_wait_bounded(bar(kBarEnd), 0)) flag_status(p.dev_status, PKV_DEV_TIMEOUT);
+      tc_commit(bar(kBarEnd), on);
+      if (!mbar_wait_bounded(bar(kBarEnd), 0) && lane == 0) flag_status(p.dev_status, PKV_DEV_TIMEOUT);
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ============================================================== Q gather
-    constexpr int CH = D / 8;   // 16-byte pieces of a query row
-    int qc = 0;
+    // ============================== Q gather, from the second segment on
+    int qc = first_tiles;
     bool ok = true;
-    for (int x = lo; x < hi && ok;) {
+    for (int x = first.end; x < hi && ok;) {
       const Seg s = locate(plan, x, hi);
       const int tiles = s.rows > kTile ? 2 : 1;
       for (int u = 0; u < tiles && ok; ++u, ++qc) {
         const int qs = qc & 1;
         if (qc >= 2) ok = wait_warp(kBarQEmpty + qs, ((qc >> 1) - 1) & 1);
         if (!ok) break;
-        uint8_t* dst = smem + lay.q + (size_t)qs * G::OPERAND;
-        const int rows = min(kTile, s.rows - u * kTile);
-        for (int i = lane; i < rows * CH; i += 32) {
-          const int r = i / CH, c = i - r * CH;
-          const int R = s.q0 + u * kTile + r;
-          int b = s.row, gq = R;
-          if (s.mem0 >= 0) {
-            const int m = R / Gq;
-            b = members[s.mem0 + m];
-            gq = R - m * Gq;
-          }
-          const uint8_t* src = p.q + (((size_t)b * p.num_q_heads + s.head * Gq + gq) * D + c * 8) * 2;
-          cp_async16(smem_u32(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)), src);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        gather_q(s, u, qs, 0, 1);
         __syncwarp();
-        if constexpr (QUANT) {   // sum of each row's query, for the zero points
-          float* qsum = reinterpret_cast<float*>(smem + lay.qsum) + (qc % kQSums) * kTile;
-          for (int r = lane; r < rows; r += 32) {
-            float t = 0.f;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              const uint4 w = *reinterpret_cast<const uint4*>(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-              t += (low16<BF>(w.x) + high16<BF>(w.x)) + (low16<BF>(w.y) + high16<BF>(w.y)) +
-                   ((low16<BF>(w.z) + high16<BF>(w.z)) + (low16<BF>(w.w) + high16<BF>(w.w)));
-            }
-            qsum[r] = t;
-          }
-        }
+        if constexpr (QUANT) sum_q(s, u, qs, qc % kQSums);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
@@ -793,40 +937,40 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     // ============================================================ converters
     if constexpr (QUANT) {
       const int t = tid - 384;
-      for (int v = 0; v < hi - lo; ++v) {
-        const int ek = 2 * v, ev = ek + 1;
-        if (!wait_warp(kBarFull + ek % S, (ek / S) & 1)) break;
+      RingPos pos;
+      for (int v = 0; v < hi - lo; ++v, pos.next(S)) {
+        const int slot = pos.slot;
+        const uint32_t phase = pos.phase;
+        if (!wait_warp(kBarKFull + slot, phase)) break;
         if (v > 0 && !wait_warp(kBarKop + 1, (v - 1) & 1)) break;   // the previous visit's scores are done
-        convert_tile<D, KV, BF>(smem + lay.ring + (size_t)(ek % S) * G::ENTRY, smem + lay.kop, t);
+        convert_tile<D, KV, BF>(smem + lay.ring + (size_t)slot * G::ENTRY, smem + lay.kop, t);
         // scales of token t, with the middle code's part in the zero points
         const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
         const bool valid = t < hd.x && (hd.y >> (t >> 4) & 1);
-        const float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)(v % (S / 2)) * G::RAW_SCALES +
+        const float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)slot * G::RAW_SCALES +
                                                           (KV == KV_I8G ? t >> 6 : t) * 16);
         float* sc = reinterpret_cast<float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
         sc[t] = valid ? z.x : 0.f;
         sc[kTile + t] = valid ? fmaf(G::CENTRE, z.x, z.y) : 0.f;
         sc[2 * kTile + t] = valid ? z.z : 0.f;
         sc[3 * kTile + t] = valid ? fmaf(G::CENTRE, z.z, z.w) : 0.f;
-        float vm = valid ? z.z : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        const float vm = warp_max(valid ? z.z : 0.f);
         if (lane == 0) reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 16)[warp - 12] = vm;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kBarKop));
           mbar_arrive(bar(kBarHdr + v % kHdrs));
-          mbar_arrive(bar(kBarEmpty + ek % S));
+          mbar_arrive(bar(kBarKEmpty + slot));
         }
-        if (!wait_warp(kBarFull + ev % S, (ev / S) & 1)) break;
+        if (!wait_warp(kBarVFull + slot, phase)) break;
         if (v > 0 && !wait_warp(kBarVop + 1, (v - 1) & 1)) break;
-        convert_tile<D, KV, BF>(smem + lay.ring + (size_t)(ev % S) * G::ENTRY, smem + lay.vop, t);
+        convert_tile<D, KV, BF>(smem + lay.ring + (size_t)(S + slot) * G::ENTRY, smem + lay.vop, t);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kBarVop));
-          mbar_arrive(bar(kBarEmpty + ev % S));
+          mbar_arrive(bar(kBarVEmpty + slot));
         }
       }
     }
@@ -834,13 +978,221 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     // =============================================================== softmax
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t ts = tm_s[st] + lanes, to = tm_o[st] + lanes;
+    const uint32_t ts = tm_s(st) + lanes, to = tm_o(st) + lanes;
     float4* mls = reinterpret_cast<float4*>(smem + lay.ml);
+    const size_t whole = (size_t)2 * B * p.num_q_heads;   // record rows of segments by stream
     int qc = 0, v = 0;
-    uint32_t n_ev = 0, n_seg = 0, n_pair = 0;   // events and segments seen on this stream, meetings
+    uint32_t n_ev = 0, n_seg = 0, n_pair = 0, n_x = 0;   // events, segments and meetings so far
     bool ok = true;
+
+    // the stream's next event: scores of visit v are there; V rows without a token cleared
+    auto begin_event = [&](int& ntok, int& mask) -> bool {
+      if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
+      if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
+      const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
+      ntok = hd.x;
+      mask = hd.y;
+      if constexpr (!QUANT) {
+        if (ntok < kTile || mask != 0xFF) {
+          // rows of V that hold no token of this segment may hold anything, NaN
+          // too, and a weight of 0 would not clear it
+          const int slot = v % S;   // rarely needed: no running position
+          if (!wait_warp(kBarVFull + slot, (v / S) & 1)) return false;
+          if (row < (ntok + 15) / 16 * 16 && (row >= ntok || !(mask >> (row >> 4) & 1))) {
+            uint8_t* vr = smem + lay.ring + (size_t)(S + slot) * G::ENTRY + row * 128;
+#pragma unroll
+            for (int h = 0; h < G::HALVES; ++h)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + h * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      return true;
+    };
+    // a reference for the value scales: the next power of two of the largest, once they outgrow the
+    // last by 2^6 (then every weight x scale stays below 2^15); returns the accumulator's factor
+    auto scale_ref = [&](float& vref) -> float {
+      const float4 vm4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
+      const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
+      if (!(vm > 64.f * vref)) return 1.f;
+      const uint32_t up = (__float_as_uint(vm) + 0x7FFFFFu) & 0x7F800000u;
+      const float nv = __uint_as_float(min(max(up, 27u << 23), 227u << 23));   // 2^-100 .. 2^100
+      const float f = vref / nv;
+      vref = nv;
+      return f;
+    };
+    auto inverse = [](float vref) { return vref > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.f; };
+
+    // ---- few query rows: thread = token for the scores, channel for the values
+    auto few_rows = [&](auto rows_c, const Seg& s) -> bool {
+      constexpr int R = decltype(rows_c)::value;   // 8, 16 or 32
+      const int n = s.end - s.begin;
+      float m[R], l[R];
+      [[maybe_unused]] float zs[R];
+      float vref = 0.f;
+      bool have = false;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        m[j] = -INFINITY;
+        l[j] = 0.f;
+        if constexpr (QUANT) zs[j] = 0.f;
+      }
+      uint8_t* pt = smem + lay.pt + st * kPtBytes;
+      float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 64);
+      auto meet = [&]() -> bool {   // the stream's four warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarX + st));
+        return wait_warp(kBarX + st, n_x++ & 1);
+      };
+      for (int i = 0; i < n; ++i, ++v) {
+        if ((v & 1) != st) continue;
+        int ntok, mask;
+        if (!begin_event(ntok, mask)) return false;
+        tc_after();
+        float a[R];
+        tmem_ld<R>(ts, reinterpret_cast<uint32_t*>(a));
+        tc_wait_ld();
+        const bool valid = row < ntok && (mask >> (row >> 4) & 1);
+        [[maybe_unused]] float vs = 1.f, vz = 0.f;
+        if constexpr (QUANT) {
+          const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
+          const float ks = sc[row] * p.scale, kz = sc[kTile + row] * p.scale;
+          vs = sc[2 * kTile + row];
+          vz = sc[3 * kTile + row];
+          const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + (qc % kQSums) * kTile;
+#pragma unroll
+          for (int j = 0; j < R; j += 4) {
+            const float4 q4 = *reinterpret_cast<const float4*>(qsum + j);
+            a[j] = fmaf(ks, a[j], kz * q4.x);
+            a[j + 1] = fmaf(ks, a[j + 1], kz * q4.y);
+            a[j + 2] = fmaf(ks, a[j + 2], kz * q4.z);
+            a[j + 3] = fmaf(ks, a[j + 3], kz * q4.w);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < R; ++j) a[j] *= p.scale;
+        }
+        // largest score of each row over the tile's tokens
+        float* xb = xch + (n_x & 1) * (4 * 64);
+        float keep = 0.f;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          if (!valid) a[j] = -INFINITY;
+          const float w = warp_max(a[j]);
+          if (lane == j) keep = w;
+        }
+        if (lane < R) xb[quad * 64 + lane] = keep;
+        if (!meet()) return false;
+        const float fv = QUANT ? scale_ref(vref) : 1.f;
+        bool moved = fv != 1.f;
+        float alpha[R];
+#pragma unroll
+        for (int j = 0; j < R; j += 4) {
+          const float4 x0 = *reinterpret_cast<const float4*>(xb + j), x1 = *reinterpret_cast<const float4*>(xb + 64 + j);
+          const float4 x2 = *reinterpret_cast<const float4*>(xb + 128 + j), x3 = *reinterpret_cast<const float4*>(xb + 192 + j);
+          const float mt[4] = {fmaxf(fmaxf(x0.x, x1.x), fmaxf(x2.x, x3.x)), fmaxf(fmaxf(x0.y, x1.y), fmaxf(x2.y, x3.y)),
+                               fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)), fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w))};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            alpha[j + k] = fv;
+            if (mt[k] > m[j + k] + 8.f) {
+              const float f = m[j + k] == -INFINITY ? 0.f : fast_exp2(m[j + k] - mt[k]);
+              m[j + k] = mt[k];
+              l[j + k] *= f;
+              if constexpr (QUANT) zs[j + k] *= f;
+              alpha[j + k] *= f;
+              moved = true;
+            }
+          }
+        }
+        if (have && moved) {   // the same for all threads of the stream
+          uint32_t o[R];
+          tmem_ld<R>(to, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < R; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
+          tmem_st<R>(to, o);
+          tc_wait_st();
+        }
+        if constexpr (QUANT) vs *= inverse(vref);
+        // weights of token `row` for eight rows at a time, as [8-row block][token][8]
+#pragma unroll
+        for (int j = 0; j < R; j += 8) {
+          uint32_t hi16[4], lo16[4];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const float m0 = m[j + k] == -INFINITY ? 0.f : m[j + k], m1 = m[j + k + 1] == -INFINITY ? 0.f : m[j + k + 1];
+            float w0 = fast_exp2(a[j + k] - m0), w1 = fast_exp2(a[j + k + 1] - m1);
+            l[j + k] += w0;
+            l[j + k + 1] += w1;
+            if constexpr (QUANT) {
+              zs[j + k] = fmaf(w0, vz, zs[j + k]);
+              zs[j + k + 1] = fmaf(w1, vz, zs[j + k + 1]);
+              w0 *= vs;
+              w1 *= vs;
+            }
+            hi16[k / 2] = pack16<BF>(w0, w1);
+            if constexpr (R <= 16)
+              lo16[k / 2] = pack16<BF>(w0 - low16<BF>(hi16[k / 2]), w1 - high16<BF>(hi16[k / 2]));
+          }
+          *reinterpret_cast<uint4*>(pt + j * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
+          if constexpr (R <= 16)
+            *reinterpret_cast<uint4*>(pt + 4096 + j * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
+        }
+        have = true;
+        fence_proxy_async_smem();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + st));
+      }
+      if (!have) return true;
+      // ---- the stream's record of each row
+      const size_t rec = s.tile0 > 0 ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + st * kTile : st * whole + s.rec;
+      float* xb = xch + (n_x & 1) * (4 * 64);
+      int j;
+      const float ls = scatter_sum<R>(l, lane, j);
+      xb[quad * 64 + j] = ls;
+      if constexpr (QUANT) xb[quad * 64 + 32 + j] = scatter_sum<R>(zs, lane, j);
+      if (!meet()) return false;
+      if (row < s.rows) {
+        float mr = m[0];
+#pragma unroll
+        for (int k = 1; k < R; ++k) mr = row == k ? m[k] : mr;
+        p.ws_ml[rec + row] = make_float2(mr, (xb[row] + xb[64 + row]) + (xb[128 + row] + xb[192 + row]));
+      }
+      if (!wait_warp(kBarO + st, n_seg++ & 1)) return false;
+      tc_after();
+      if (quad * 32 < D) {
+        uint32_t o[R];
+        tmem_ld<R>(to, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          if (k < s.rows) {
+            float f = __uint_as_float(o[k]);
+            if constexpr (QUANT) f = fmaf(f, vref, (xb[32 + k] + xb[96 + k]) + (xb[160 + k] + xb[224 + k]));
+            p.ws_acc[(rec + k) * D + row] = f;
+          }
+        }
+      }
+      tc_before();
+      return true;
+    };
+
     for (int x = lo; x < hi && ok;) {
-      const Seg s = locate(plan, x, hi);
+      const Seg s = x == lo ? first : locate(plan, x, hi);
+      x = s.end;
+      if (s.rows <= p.few_rows) {
+        if (s.rows <= 8)
+          ok = few_rows(std::integral_constant<int, 8>{}, s);
+        else if (s.rows <= 16)
+          ok = few_rows(std::integral_constant<int, 16>{}, s);
+        else
+          ok = few_rows(std::integral_constant<int, 32>{}, s);
+        ++qc;
+        continue;
+      }
+      // ---- thread = query row
       const bool two = s.rows > kTile;
       const int n = s.end - s.begin;
       const int my_rows = two ? min(kTile, s.rows - st * kTile) : s.rows;
@@ -849,37 +1201,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       bool have = false;
       for (int i = 0; i < n && ok; ++i, ++v) {
         if (!two && (v & 1) != st) continue;
-        ok = wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1);
-        if (ok) ok = wait_warp(kBarS + st, n_ev & 1);
+        int ntok, mask;
+        ok = begin_event(ntok, mask);
         if (!ok) break;
-        ++n_ev;
-        const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
-        const int ntok = hd.x;
-        const bool partial = ntok < kTile || hd.y != 0xFF;
-        if constexpr (!QUANT) {
-          if (partial) {
-            // rows of V that hold no token of this segment may hold anything, NaN
-            // too, and a weight of 0 would not clear it
-            const int e = 2 * v + 1;
-            ok = wait_warp(kBarFull + e % S, (e / S) & 1);
-            if (!ok) break;
-            if (row < (ntok + 15) / 16 * 16 && (row >= ntok || !(hd.y >> (row >> 4) & 1))) {
-              uint8_t* vr = smem + lay.ring + (size_t)(e % S) * G::ENTRY + row * 128;
-#pragma unroll
-              for (int h = 0; h < G::HALVES; ++h)
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(vr + h * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-        }
         if (active) {
           tc_after();
           float a[kTile];
           uint32_t* ar = reinterpret_cast<uint32_t*>(a);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, ar + 32 * c);
+          for (int c = 0; c < 4; ++c) tmem_ld<32>(ts + 32 * c, ar + 32 * c);
           tc_wait_ld();
           const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
           if constexpr (QUANT) {
@@ -895,10 +1225,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               a[j + 3] = fmaf(ks.w, a[j + 3], kz.w * qs);
             }
           }
-          if (partial) {
+          if (ntok < kTile || mask != 0xFF) {
 #pragma unroll
             for (int j = 0; j < kTile; ++j)
-              if (j >= ntok || !(hd.y >> (j >> 4) & 1)) a[j] = -INFINITY;
+              if (j >= ntok || !(mask >> (j >> 4) & 1)) a[j] = -INFINITY;
           }
           float mx[4] = {a[0], a[1], a[2], a[3]};
 #pragma unroll
@@ -913,78 +1243,78 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           }
           float rv = 0.f;
           if constexpr (QUANT) {
-            const float4 vm4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
-            const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
-            if (vm > 64.f * vref) {   // uniform: the next power of two, within 2^-100 .. 2^100
-              const uint32_t up = (__float_as_uint(vm) + 0x7FFFFFu) & 0x7F800000u;
-              const float nv = __uint_as_float(min(max(up, 27u << 23), 227u << 23));
-              alpha *= vref / nv;
-              vref = nv;
-            }
-            rv = vref > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.f;
+            alpha *= scale_ref(vref);
+            rv = inverse(vref);
           }
           if (have && __any_sync(0xffffffffu, alpha != 1.f)) {
             // S of this event is complete, so every earlier product of this stream is
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld<16>(to + 16 * c, o);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32(to + 32 * c, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st<16>(to + 16 * c, o);
             }
           }
           const float mref = m == -INFINITY ? 0.f : m;
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          auto weights = [&](auto terms) {
+            constexpr bool TWO = decltype(terms)::value;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (32 * c < ntok) {
-              uint32_t hi16[16], lo16[16];
+            for (int c = 0; c < 8; ++c) {
+              if (16 * c < ntok) {
+                uint32_t hi16[8], lo16[8];
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                float w0 = fast_exp2(fmaf(a[32 * c + j], p.scale, -mref));
-                float w1 = fast_exp2(fmaf(a[32 * c + j + 1], p.scale, -mref));
-                ls[j & 2] += w0;
-                ls[(j & 2) + 1] += w1;
-                if constexpr (QUANT) {
-                  const float2 vs = *reinterpret_cast<const float2*>(sc + 2 * kTile + 32 * c + j);
-                  const float2 vz = *reinterpret_cast<const float2*>(sc + 3 * kTile + 32 * c + j);
-                  zs = fmaf(w0, vz.x, zs);
-                  zs = fmaf(w1, vz.y, zs);
-                  w0 *= vs.x * rv;
-                  w1 *= vs.y * rv;
+                for (int j = 0; j < 16; j += 2) {
+                  float w0 = fast_exp2(fmaf(a[16 * c + j], p.scale, -mref));
+                  float w1 = fast_exp2(fmaf(a[16 * c + j + 1], p.scale, -mref));
+                  ls[j & 2] += w0;
+                  ls[(j & 2) + 1] += w1;
+                  if constexpr (QUANT) {
+                    const float2 vs = *reinterpret_cast<const float2*>(sc + 2 * kTile + 16 * c + j);
+                    const float2 vz = *reinterpret_cast<const float2*>(sc + 3 * kTile + 16 * c + j);
+                    zs = fmaf(w0, vz.x, zs);
+                    zs = fmaf(w1, vz.y, zs);
+                    w0 *= vs.x * rv;
+                    w1 *= vs.y * rv;
+                  }
+                  // the weights' one rounding to the operand type; a second term
+                  // holds what it left where the output keeps more bits
+                  hi16[j / 2] = pack16<BF>(w0, w1);
+                  if constexpr (TWO)
+                    lo16[j / 2] = pack16<BF>(w0 - low16<BF>(hi16[j / 2]), w1 - high16<BF>(hi16[j / 2]));
                 }
-                // the weights' one rounding to the operand type; a second term
-                // holds what it left where the output keeps more bits
-                hi16[j / 2] = pack16<BF>(w0, w1);
-                if (p.two_terms)
-                  lo16[j / 2] = pack16<BF>(w0 - low16<BF>(hi16[j / 2]), w1 - high16<BF>(hi16[j / 2]));
+                // weights of 32 tokens take the place of their scores: 16
+                // columns of first terms, 16 of second ones
+                tmem_st<8>(ts + 32 * (c >> 1) + 8 * (c & 1), hi16);
+                if constexpr (TWO) tmem_st<8>(ts + 32 * (c >> 1) + 8 * (c & 1) + 16, lo16);
               }
-              tmem_st16(ts + 32 * c, hi16);
-              if (p.two_terms) tmem_st16(ts + 32 * c + 16, lo16);
             }
-          }
+          };
+          if (p.two_terms)
+            weights(std::true_type{});
+          else
+            weights(std::false_type{});
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           tc_wait_st();
           tc_before();
         }
         have = true;
+        if constexpr (!QUANT) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarP + st));
       }
       if (!ok) break;
       // ---- end of the block's part of the segment: one record per query row
-      const bool part = s.tile0 > 0;   // the segment began in an earlier block
       const int tile_row = two ? st * kTile + row : row;
-      const size_t rec = part ? (size_t)2 * p.num_kv_heads * B * Gq + (size_t)blockIdx.x * 2 * kTile + tile_row
-                              : (size_t)s.rec + tile_row;
+      const size_t rec = s.tile0 > 0 ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + tile_row : (size_t)s.rec + tile_row;
       float* acc = p.ws_acc + rec * D;
       const bool both = !two && n > 1;
       if (have) {
-        ok = wait_warp(kBarO + st, n_seg & 1);
+        ok = wait_warp(kBarO + st, n_seg++ & 1);
         if (!ok) break;
-        ++n_seg;
       }
       if (active && !both) {
         if (have) {
@@ -993,7 +1323,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32(to + 32 * c, o);
+            tmem_ld<32>(to + 32 * c, o);
             tc_wait_ld();
             if (row < my_rows) {
 #pragma unroll
@@ -1031,12 +1361,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           f0 *= vref;
           f1 *= other.w;
         }
-        const uint32_t to2 = tm_o[st ^ 1] + lanes;
+        const uint32_t to2 = tm_o(st ^ 1) + lanes;
 #pragma unroll 1
         for (int c = st * (D / 64); c < (st + 1) * (D / 64); ++c) {
           uint32_t o[32], o2[32];
-          tmem_ld32(to + 32 * c, o);
-          tmem_ld32(to2 + 32 * c, o2);
+          tmem_ld<32>(to + 32 * c, o);
+          tmem_ld<32>(to2 + 32 * c, o2);
           tc_wait_ld();
           if (row < my_rows) {
 #pragma unroll
@@ -1062,7 +1392,6 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if (!ok) break;
       }
       qc += two ? 2 : 1;
-      x = s.end;
     }
   }
   tc_before();
@@ -1090,25 +1419,28 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   const int b = item / p.num_q_heads, hq = item - b * p.num_q_heads;
   const int h = hq / p.group, gq = hq - h * p.group;
   const int4 i0 = __ldcg(p.ws_info + 2 * b), i1 = __ldcg(p.ws_info + 2 * b + 1);
-  const long long W = i1.w, N = p.num_ctas;
-  const int base2 = 2 * p.num_kv_heads * p.batch * p.group;
-  // prefix records, then the row's own
-  int c0[2] = {0, 0}, n[2] = {0, 0}, rec[2], sub[2];
+  const int W = i1.w, N = p.num_ctas;
+  const int whole = 2 * p.batch * p.num_q_heads;   // record rows of segments by stream
+  // prefix records, then the row's own; a segment of few rows has one of each stream
+  int c0[2] = {0, 0}, n[2] = {0, 0}, rec[2], sub[2], s0[2] = {0, 0}, s1[2] = {0, 0}, few[2];
   {
     const int R = i0.y * p.group + gq;             // query row within the group
     rec[0] = h * p.batch * p.group + i0.x + R;
     sub[0] = R % (2 * kTile);
-    if (i1.x > 0) {
-      const int s0 = i0.z + (h * i0.w + R / (2 * kTile)) * i1.x;
-      c0[0] = share_of(s0, W, N);
-      n[0] = share_of(s0 + i1.x - 1, W, N) - c0[0] + 1;
-    }
+    const int pair = R / (2 * kTile), pairs = (i0.w + 2 * kTile - 1) / (2 * kTile);
+    few[0] = min(2 * kTile, i0.w - pair * 2 * kTile) <= p.few_rows;
+    s0[0] = i0.z + (h * pairs + pair) * i1.x;
+    s1[0] = s0[0] + i1.x;
     rec[1] = ((p.num_kv_heads + h) * p.batch + b) * p.group + gq;
     sub[1] = gq;
-    if (i1.z > 0) {
-      const int s0 = i1.y + h * i1.z;
-      c0[1] = share_of(s0, W, N);
-      n[1] = share_of(s0 + i1.z - 1, W, N) - c0[1] + 1;
+    few[1] = p.group <= p.few_rows;
+    s0[1] = i1.y + h * i1.z;
+    s1[1] = s0[1] + i1.z;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (s0[k] == s1[k]) continue;
+      c0[k] = share_of(s0[k], W, N);
+      n[k] = (share_of(s1[k] - 1, W, N) - c0[k] + 1) << few[k];
     }
   }
   const int total = n[0] + n[1];
@@ -1124,10 +1456,14 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
       const int k = j >= n[0];
       bool on = j < total;
       if (k) j -= n[0];
-      const int c = c0[k] + j;
-      // a block without visits (fewer visits than blocks) has no record
-      if (on && j > 0) on = share_lo(c, W, N) < share_lo(c + 1, W, N);
-      const size_t r = on ? (j == 0 ? (size_t)rec[k] : (size_t)base2 + (size_t)c * 2 * kTile + sub[k]) : 0;
+      const int c = c0[k] + (j >> few[k]), st = j & few[k];
+      const int lo = share_lo(c, W, N), a0 = max(s0[k], lo), a1 = min(s1[k], share_lo(c + 1, W, N));
+      // a block without visits (fewer visits than blocks) has no record, and one
+      // visit of a segment of few rows is one stream's
+      on = on && a0 < a1 && (!few[k] || a1 - a0 > 1 || ((a0 - lo) & 1) == st);
+      const size_t r = on ? (a0 == s0[k] ? (size_t)st * whole + rec[k] : 2 * (size_t)whole + (size_t)c * 2 * kTile +
+                                                                           st * kTile + sub[k])
+                          : 0;
       ml[i] = on ? __ldcg(p.ws_ml + r) : make_float2(-INFINITY, 0.f);
       a[i] = on ? __ldcg(reinterpret_cast<const float4*>(p.ws_acc + r * D + ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }

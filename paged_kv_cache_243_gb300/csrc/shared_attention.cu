@@ -165,7 +165,6 @@ pkv_status launch_shared(const SharedArgs& a) {
   p.q_dtype = a.q_dtype;
   p.out_dtype = a.out_dtype;
   p.two_terms = a.out_dtype == PKV_F32;
-  p.few_rows = p.two_terms ? 16 : 32;
   p.scale = a.sm_scale * 1.4426950408889634f;
   void* args[] = {&p};
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;

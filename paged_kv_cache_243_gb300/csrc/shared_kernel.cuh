@@ -67,7 +67,9 @@ constexpr int kHdrs = 8;          // visit headers kept (more than the visits th
 constexpr int kScaleSlots = 4;    // visits whose scales are kept for the softmax
 constexpr int kQSums = 8;
 constexpr int kMaxEntries = 6;    // ring entries of K, and of V: at most kHdrs - 2
-constexpr int kPtBytes = 8192;    // transposed weights of a stream: 16 rows in two terms, or 32 in one
+constexpr int kVisits = 128;      // visits described in shared memory, refilled by halves
+constexpr int kFew = 16;          // segments of at most this many query rows run transposed
+constexpr int kPtBytes = 8192;    // transposed weights of a stream: 16 rows, two terms each
 
 struct SharedParams {
   CUtensorMap tmap_k, tmap_v;   // 16-bit pools as [rows][d], boxes of 16 rows x 64 channels
@@ -86,7 +88,7 @@ struct SharedParams {
   float* ws_acc;
   int4* ws_info;
   int num_pages, page_size, num_kv_heads, num_q_heads, group, batch, max_pages, num_groups;
-  int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms, few_rows;
+  int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms;
   float scale;   // sm_scale * log2(e)
 };
 
@@ -105,14 +107,15 @@ struct SharedGeom {
 
 // Shared memory by offset from a 1024-byte boundary.
 struct SharedLayout {
-  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, lens, skip, bpre, gpre, gp, moff, members, rank;
+  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, visits, bpre, gpre, moff, members, lens, skip, gp, rank;
   int total;
 };
 enum SharedBars {   // mbarriers, 8 bytes each
   kBarKFull = 0, kBarVFull = kMaxEntries, kBarKEmpty = 2 * kMaxEntries, kBarVEmpty = 3 * kMaxEntries,
   kBarHdr = 4 * kMaxEntries, kBarQFull = kBarHdr + kHdrs, kBarQEmpty = kBarQFull + 2, kBarS = kBarQEmpty + 2,
   kBarP = kBarS + 2, kBarO = kBarP + 2, kBarX = kBarO + 2, kBarKop = kBarX + 2, kBarVop = kBarKop + 2,
-  kBarPair = kBarVop + 2, kBarEnd = kBarPair + 4, kBarCount = kBarEnd + 1
+  kBarPair = kBarVop + 2, kBarVisits = kBarPair + 4, kBarPassed = kBarVisits + 2, kBarEnd = kBarPassed + 2,
+  kBarCount = kBarEnd + 1
 };
 
 template <class G>
@@ -130,7 +133,7 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.ring = put(2 * entries * G::ENTRY);
   o.raw = put(entries * G::RAW_SCALES);
   o.pt = put(2 * kPtBytes);
-  o.xch = put(2 * 2 * 4 * 64 * 4);
+  o.xch = put(2 * 2 * 4 * 32 * 4);
   o.scales = put(kScaleSlots * G::SCALES);
   o.bars = put(kBarCount * 8);
   o.hdr = put(kHdrs * 8);
@@ -138,15 +141,19 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.qsum = put(G::QUANT ? kQSums * kTile * 4 : 0);
   o.vmax = put(G::QUANT ? kScaleSlots * 16 : 0);
   o.misc = put(40 * 4);
-  o.lens = put(batch * 4);
-  o.skip = put(batch * 4);
+  o.visits = put(kVisits * 32);
   o.bpre = put((batch + 1) * 4);
   o.gpre = put((groups + 1) * 4);
-  o.gp = put(groups * 4);
   o.moff = put((groups + 1) * 4);
   o.members = put(batch * 2);
-  o.rank = put(batch * 2);
   o.total = at;
+  // the plan's other arrays are needed only while the ring is still empty
+  at = o.ring;
+  o.lens = put(batch * 4);
+  o.skip = put(batch * 4);
+  o.gp = put(groups * 4);
+  o.rank = put(batch * 2);
+  if (at > o.total) o.total = at;
   return o;
 }
 
@@ -271,21 +278,28 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 
 // ---------------------------------------------------------------------- plan
 struct SharedPlan {
-  const int *lens, *skip, *bpre, *gpre, *gp, *moff;
+  const int *bpre, *gpre, *moff;   // visits before each row's own tokens and each group's prefix; members
   const uint16_t* members;
-  int batch, groups, heads, group, W, Wp;   // Wp: visits of prefix segments
+  const int *lens, *skip, *gp;     // shared memory (while planning), or NULL: from the inputs again
+  int lo, hi;                      // the block's visits
 };
 
-// The segment that visit x belongs to.
-struct Seg {
-  int begin, end;     // its visits inside the block's range
-  int tile0, tiles;   // tile of visit `begin`, and tiles of the whole segment
-  int first_tok, end_tok;
-  int row, head;      // block-table row to read through, kv head
-  int rows;           // query rows
-  int q0;             // prefix: first query row within the group; suffix: 0
-  int mem0;           // prefix: first member; suffix: -1
-  int rec;            // record row of query row 0 (whole-segment region)
+// One visit: a tile of a segment.
+struct Visit {
+  int tok0;     // its first token
+  int flags;    // its tokens (1 .. 128), and the bits below
+  int row;      // block-table row to read through
+  int head;     // kv head
+  int rows;     // query rows of the segment (up to 256)
+  int q0;       // prefix: the first of them within the group
+  int mem0;     // prefix: the group's first member; a row's own tokens: -1
+  int rec;      // record row of the first query row
+  __device__ __forceinline__ int tokens() const { return flags & 0xFF; }
+  __device__ __forceinline__ bool is(int bit) const { return flags & bit; }
+};
+enum VisitBits {   // place in the block's part of the segment
+  kFirst = 0x100, kLast = 0x200, kEarly = 0x400 /* one of the first two */, kLate = 0x800 /* of the last two */,
+  kMany = 0x1000 /* the part has several */, kContinued = 0x2000 /* the segment began in an earlier block */
 };
 
 __device__ __forceinline__ int upper(const int* pre, int n, int x) {   // largest i with pre[i] <= x
@@ -298,44 +312,77 @@ __device__ __forceinline__ int upper(const int* pre, int n, int x) {   // larges
   return a;
 }
 
-__device__ __forceinline__ Seg locate(const SharedPlan& p, int x, int hi) {
-  Seg s;
-  int rem;
-  if (x < p.Wp) {
-    const int g = upper(p.gpre, p.groups, x);
-    const int T = (p.gp[g] + kTile - 1) / kTile;
-    const int total = (p.moff[g + 1] - p.moff[g]) * p.group;
+// Length of row b within the table, and the tokens it has in common with its
+// group (0: it attends on its own); g: its group, -1 without.
+struct RowPlan {
+  int len, skip, group, bad;
+};
+__device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int b) {
+  RowPlan r;
+  const long long cap = (long long)p.max_pages * p.page_size;
+  int L = p.seq_lens[b], g = p.prefix_group[b];
+  r.bad = 0;
+  if (L < 0 || L > cap) {
+    r.bad |= PKV_DEV_BAD_POSITION;
+    L = L < 0 ? 0 : (int)cap;
+  }
+  if (g < -1 || g >= p.num_groups) {
+    r.bad |= PKV_DEV_BAD_GROUP;
+    g = -1;
+  }
+  const int P = g >= 0 ? p.prefix_lens[g] : 0;
+  if (P < p.round_to || L < P) g = -1;
+  r.len = L;
+  r.group = g;
+  r.skip = g >= 0 ? P / p.round_to * p.round_to : 0;
+  return r;
+}
+
+static __device__ __noinline__ void describe_visit(const SharedParams& p, const SharedPlan& pl, int x, int4* out) {
+  Visit s;
+  int tile, tiles, end_tok, first_tok;
+  if (x < pl.gpre[p.num_groups]) {
+    const int g = upper(pl.gpre, p.num_groups, x);
+    end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] / p.round_to * p.round_to;
+    first_tok = 0;
+    tiles = (end_tok + kTile - 1) / kTile;
+    const int total = (pl.moff[g + 1] - pl.moff[g]) * p.group;
     const int pairs = (total + 2 * kTile - 1) / (2 * kTile);
-    rem = x - p.gpre[g];
-    const int hp = rem / T;
-    rem -= hp * T;
+    const int rem = x - pl.gpre[g], hp = rem / tiles;
+    tile = rem - hp * tiles;
     s.head = hp / pairs;
     s.q0 = (hp - s.head * pairs) * 2 * kTile;
     s.rows = min(2 * kTile, total - s.q0);
-    s.tiles = T;
-    s.first_tok = 0;
-    s.end_tok = p.gp[g];
-    s.mem0 = p.moff[g];
-    s.row = p.members[s.mem0];
+    s.mem0 = pl.moff[g];
+    s.row = pl.members[s.mem0];
     s.rec = s.head * p.batch * p.group + s.mem0 * p.group + s.q0;
   } else {
-    const int b = upper(p.bpre, p.batch, x);
-    s.first_tok = p.skip[b];
-    s.end_tok = p.lens[b];
-    s.tiles = (s.end_tok - s.first_tok + kTile - 1) / kTile;
-    rem = x - p.bpre[b];
-    s.head = rem / s.tiles;
-    rem -= s.head * s.tiles;
+    const int b = upper(pl.bpre, p.batch, x);
+    if (pl.lens) {
+      first_tok = pl.skip[b];
+      end_tok = pl.lens[b];
+    } else {
+      const RowPlan r = row_plan(p, b);
+      first_tok = r.skip;
+      end_tok = r.len;
+    }
+    tiles = (end_tok - first_tok + kTile - 1) / kTile;
+    const int rem = x - pl.bpre[b];
+    s.head = rem / tiles;
+    tile = rem - s.head * tiles;
     s.rows = p.group;
     s.q0 = 0;
     s.mem0 = -1;
     s.row = b;
-    s.rec = ((p.heads + s.head) * p.batch + b) * p.group;
+    s.rec = ((p.num_kv_heads + s.head) * p.batch + b) * p.group;
   }
-  s.tile0 = rem;
-  s.begin = x;
-  s.end = min(hi, x + s.tiles - rem);
-  return s;
+  s.tok0 = first_tok + tile * kTile;
+  const int whole0 = x - tile, x0 = max(pl.lo, whole0), x1 = min(pl.hi, whole0 + tiles);
+  s.flags = min(kTile, end_tok - s.tok0) | (x == x0 ? kFirst : 0) | (x == x1 - 1 ? kLast : 0) |
+            (x < x0 + 2 ? kEarly : 0) | (x >= x1 - 2 ? kLate : 0) | (x1 - x0 > 1 ? kMany : 0) |
+            (x0 > whole0 ? kContinued : 0);
+  out[0] = make_int4(s.tok0, s.flags, s.row, s.head);
+  out[1] = make_int4(s.rows, s.q0, s.mem0, s.rec);
 }
 
 // Exclusive prefix sums over the block's threads of two values, and their totals.
@@ -477,6 +524,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   int* scratch = const_cast<int*>(misc) + 4;
   int* lens = reinterpret_cast<int*>(smem + lay.lens);
   int* skip = reinterpret_cast<int*>(smem + lay.skip);
+  int4* visits = reinterpret_cast<int4*>(smem + lay.visits);
   int* bpre = reinterpret_cast<int*>(smem + lay.bpre);
   int* gpre = reinterpret_cast<int*>(smem + lay.gpre);
   int* gp = reinterpret_cast<int*>(smem + lay.gp);
@@ -506,6 +554,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     mbar_init(bar(kBarVop), 4);
     mbar_init(bar(kBarVop + 1), 1);
     for (int i = 0; i < 4; ++i) mbar_init(bar(kBarPair + i), 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarVisits + i), 1);
+      mbar_init(bar(kBarPassed + i), QUANT ? 15 : 11);   // loaders, MMA, softmax, converters
+    }
     mbar_init(bar(kBarEnd), 1);
     misc[1] = 0;
   }
@@ -520,28 +572,17 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   pdl_launch_dependents();
 
   // ---- plan: lengths, who shares, visits before each segment
-  const long long cap = (long long)p.max_pages * p.page_size;
   for (int g = tid; g < NG; g += NT) {
     const int P = p.prefix_lens[g];
     if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
     gp[g] = max(P, 0) / p.round_to * p.round_to;
   }
   for (int b = tid; b < B; b += NT) {
-    int L = p.seq_lens[b], g = p.prefix_group[b];
-    if (L < 0 || L > cap) {
-      if (blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_POSITION);
-      L = L < 0 ? 0 : (int)cap;
-    }
-    if (g < -1 || g >= NG) {
-      if (blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
-      g = -1;
-    }
-    // a row shares its group's prefix if it has all of it
-    const int P = g >= 0 ? p.prefix_lens[g] : 0;
-    if (P < p.round_to || L < P) g = -1;
-    lens[b] = L;
-    skip[b] = g >= 0 ? P / p.round_to * p.round_to : 0;
-    members[b] = (uint16_t)g;   // the group for now
+    const RowPlan r = row_plan(p, b);
+    if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
+    lens[b] = r.len;
+    skip[b] = r.skip;
+    members[b] = (uint16_t)r.group;   // for now
   }
   __syncthreads();
   if (warp == 0 && NG > 0) {   // each row's place among its group's rows
@@ -611,7 +652,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     mine[i] = b < B ? (int16_t)members[b] : (int16_t)-1;
   }
   __syncthreads();
-  const int Wp = gpre[NG], W = bpre[B];
+  const int W = bpre[B];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int b = tid + i * NT;
@@ -625,14 +666,19 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                                        (lens[b] - skip[b] + kTile - 1) / kTile, W);
     }
   }
-  const SharedPlan plan = {lens, skip, bpre, gpre, gp, moff, members, B, NG, p.num_kv_heads, Gq, W, Wp};
   const int lo = W > 0 ? share_lo(blockIdx.x, W, p.num_ctas) : 0;
   const int hi = W > 0 ? share_lo(blockIdx.x + 1, W, p.num_ctas) : 0;
+  const int nv = hi - lo;
+  SharedPlan plan = {bpre, gpre, moff, members, lens, skip, gp, lo, hi};
+  __syncthreads();
+  if (tid < min(nv, kVisits)) describe_visit(p, plan, lo + tid, visits + 2 * tid);
+  plan.lens = plan.skip = plan.gp = nullptr;
+  fence_proxy_async_smem();   // the ring, so far the plan's, is the copies' from here on
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
-  if (lo >= hi) {   // uniform over the block
+  if (nv <= 0) {   // uniform over the block
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
@@ -656,8 +702,23 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   };
   // for a whole warp: every lane goes on, or none does
   auto wait_warp = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(i, parity)); };
+  // visit v of the block; its description may have to be waited for
+  auto visit = [&](int v, Visit& d) -> bool {
+    if (v >= kVisits && (v & (kVisits / 2 - 1)) == 0 && !wait_warp(kBarVisits + (v / (kVisits / 2) & 1), (v / kVisits - 1) & 1))
+      return false;
+    const int4 a = visits[2 * (v & (kVisits - 1))], b = visits[2 * (v & (kVisits - 1)) + 1];
+    d = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return true;
+  };
+  // this warp needs visit v and those before it no more
+  auto passed = [&](int v) {
+    if ((v & (kVisits / 2 - 1)) == kVisits / 2 - 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarPassed + (v / (kVisits / 2) & 1)));
+    }
+  };
   // queries of tile u of a segment into operand slot qs, by `warps` warps
-  auto gather_q = [&](const Seg& s, int u, int qs, int w, int warps) {
+  auto gather_q = [&](const Visit& s, int u, int qs, int w, int warps) {
     constexpr int CH = D / 8, RPI = 32 / CH;   // 16-byte pieces of a row, rows an instruction
     uint8_t* dst = smem + lay.q + (size_t)qs * G::OPERAND;
     const int rows = min(kTile, s.rows - u * kTile);
@@ -684,7 +745,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   };
   // sums of the queries of a gathered tile, for the zero points
-  auto sum_q = [&](const Seg& s, int u, int qs, int slot) {
+  auto sum_q = [&](const Visit& s, int u, int qs, int slot) {
     const uint8_t* src = smem + lay.q + (size_t)qs * G::OPERAND;
     float* qsum = reinterpret_cast<float*>(smem + lay.qsum) + slot * kTile;
     const int rows = min(kTile, s.rows - u * kTile);
@@ -701,7 +762,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   };
 
   // the first segment's queries, by the warps that have nothing else to do yet
-  const Seg first = locate(plan, lo, hi);
+  Visit first;
+  visit(0, first);
   const int first_tiles = first.rows > kTile ? 2 : 1;
   if (warp < 8) {
     for (int u = 0; u < first_tiles; ++u) gather_q(first, u, u, warp, 8);
@@ -729,21 +791,21 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     const void* map = isv ? &p.tmap_v : &p.tmap_k;
     int v = 0;
     bool ok = true;
-    Seg s = first;
+    Visit d = first;
     // page of this lane's piece, one visit ahead
-    auto lookup = [&](const Seg& sg, int x) -> int {
-      const int tok = sg.first_tok + (sg.tile0 + x - sg.begin) * kTile + 16 * piece;
-      if (piece >= 8 || tok >= sg.end_tok) return -2;   // nothing to copy
-      return p.block_table[(size_t)sg.row * p.max_pages + tok / p.page_size];
+    auto lookup = [&]() -> int {
+      if (16 * piece >= d.tokens()) return -2;   // nothing to copy
+      return p.block_table[(size_t)d.row * p.max_pages + (d.tok0 + 16 * piece) / p.page_size];
     };
-    int page = lookup(s, lo);
+    int page = lookup();
     RingPos pos;
-    for (int x = lo; x < hi && ok; ++x, ++v, pos.next(S)) {
-      const int head = s.head, tok0 = s.first_tok + (s.tile0 + x - s.begin) * kTile;
-      const int ntok = min(kTile, s.end_tok - tok0), pg = page;
-      if (x + 1 < hi) {
-        if (x + 1 == s.end) s = locate(plan, x + 1, hi);
-        page = lookup(s, x + 1);
+    for (; v < nv && ok; ++v, pos.next(S)) {
+      const int head = d.head, tok0 = d.tok0, ntok = d.tokens(), pg = page;
+      passed(v);
+      if (v + 1 < nv) {
+        ok = visit(v + 1, d);
+        if (!ok) break;
+        page = lookup();
       }
       const bool bad = pg != -2 && (pg < 0 || pg >= p.num_pages);
       if (bad && !isv && half == 0) flag_status(p.dev_status, PKV_DEV_BAD_PAGE);
@@ -821,17 +883,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         tc_after();
         const uint32_t acc0 = !pend.fresh, o = tm_o(st);
         if (pend.few) {
-          // O^T (+)= V^T P^T: channels x rows
+          // O^T (+)= V^T [P1^T | P2^T]: channels x rows, first and second terms of
+          // the weights side by side
           const uint32_t idesc_t = kType | 1u << 15 | 1u << 16 | (uint32_t)(pend.few / 8) << 17;
           const uint64_t pd = at(pmajor, pt + (uint32_t)st * kPtBytes);
-          const bool terms = pend.few == 16;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (j < pend.steps) {
-              mma_ss(o, vd + j * 128, pd + j * 16, idesc_t, j ? 1u : acc0, on);
-              if (terms) mma_ss(o, vd + j * 128, pd + j * 16 + 256, idesc_t, 1, on);
-            }
-          }
+          for (int j = 0; j < 8; ++j)
+            if (j < pend.steps) mma_ss(o, vd + j * 128, pd + j * 16, idesc_t, j ? 1u : acc0, on);
         } else {
           const uint32_t a = tm_s(st);
           if (p.two_terms) {
@@ -856,16 +914,18 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         pend.on = false;
         return true;
       };
-      for (int x = uni(lo), end = uni(hi); x < end && ok;) {
-        const Seg s = x == lo ? first : locate(plan, x, hi);
-        const int rows = uni(s.rows), n = uni(s.end - s.begin);
+      for (const int end = uni(nv); v < end && ok; ++v, pos.next(S)) {
+        Visit d;
+        ok = visit(v, d);
+        if (!ok) break;
+        const int rows = uni(d.rows), flags = uni(d.flags);
         const bool two = rows > kTile;
-        const int few = rows <= p.few_rows ? (rows <= 16 ? 16 : 32) : 0;
-        for (int i = 0; i < n && ok; ++i, ++v, pos.next(S)) {
+        const int few = rows > kFew ? 0 : rows > 8 ? 32 : 16;   // two columns a row, for eight rows at a time
+        {
           const int slot = pos.slot;
           ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + slot, pos.phase);
           if (!ok) break;
-          const int ntok = uni(*reinterpret_cast<const volatile int*>(smem + lay.hdr + (v % kHdrs) * 8));
+          const int ntok = flags & 0xFF;
           const uint64_t kd = at(kmajor, QUANT ? kop : ring + (uint32_t)slot * G::ENTRY);
           for (int u = 0; u < (two ? 2 : 1) && ok; ++u) {
             const int st = two ? u : v & 1, qs = (qc + (two ? u : 0)) & 1;
@@ -873,13 +933,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             // before the weights in it are used
             if (pend.on && pend.st == st) ok = issue_pv();
             if (!ok) break;
-            if (i == 0) ok = wait_warp(kBarQFull + qs, ((qc + (two ? u : 0)) >> 1) & 1);
+            if (flags & kFirst) ok = wait_warp(kBarQFull + qs, ((qc + (two ? u : 0)) >> 1) & 1);
             if (!ok) break;
             tc_after();
             const uint64_t qd = at(kmajor, qb + (uint32_t)qs * G::OPERAND);
             if (few) {
               // S^T = K Q^T: tokens x rows
-              const uint32_t idesc_t = kType | (uint32_t)(few / 8) << 17;
+              constexpr uint32_t idesc_t = kType | (uint32_t)(kFew / 8) << 17;
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
                 mma_ss(tm_s(st), kd + (k >> 2) * 1024 + (k & 3) * 2, qd + (k >> 2) * 1024 + (k & 3) * 2, idesc_t, k > 0, on);
@@ -891,7 +951,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             tc_commit(bar(kBarS + st), on);
             const bool last_s = u == (two ? 1 : 0);
             if (last_s) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + slot), on);
-            if (i == n - 1) tc_commit(bar(kBarQEmpty + qs), on);
+            if (flags & kLast) tc_commit(bar(kBarQEmpty + qs), on);
             if (pend.on) ok = issue_pv();
             odd ^= 1u << st;
             pend.st = st;
@@ -899,13 +959,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             pend.steps = (ntok + 15) >> 4;
             pend.few = few;
             pend.on = true;
-            pend.fresh = two ? i == 0 : i < 2;
+            pend.fresh = flags & (two ? kFirst : kEarly);
             pend.last_use = last_s;
-            pend.seg_end = two ? i == n - 1 : i >= n - 2;
+            pend.seg_end = flags & (two ? kLast : kLate);
           }
         }
-        qc += two ? 2 : 1;
-        x += n;
+        if (flags & kLast) qc += two ? 2 : 1;
+        passed(v);
       }
       if (ok && pend.on) ok = issue_pv();
       // nothing of the tensor cores is in flight past this point
@@ -917,8 +977,20 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     // ============================== Q gather, from the second segment on
     int qc = first_tiles;
     bool ok = true;
-    for (int x = first.end; x < hi && ok;) {
-      const Seg s = locate(plan, x, hi);
+    for (int v = 1; v < nv && ok; ++v) {
+      if (v >= kVisits && (v & (kVisits / 2 - 1)) == 0) {
+        // the next half of the visits' descriptions, once the last use of their place is over
+        const int h = v / (kVisits / 2) & 1;
+        ok = wait_warp(kBarPassed + h, (v / kVisits - 1) & 1);
+        if (!ok) break;
+        for (int i = v + lane; i < min(nv, v + kVisits / 2); i += 32)
+          describe_visit(p, plan, lo + i, visits + 2 * (i & (kVisits - 1)));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarVisits + h));
+      }
+      const int4 a = visits[2 * (v & (kVisits - 1))], b = visits[2 * (v & (kVisits - 1)) + 1];
+      const Visit s = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      if (!s.is(kFirst)) continue;
       const int tiles = s.rows > kTile ? 2 : 1;
       for (int u = 0; u < tiles && ok; ++u, ++qc) {
         const int qs = qc & 1;
@@ -931,14 +1003,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
       }
-      x = s.end;
     }
   } else if (warp >= 12) {
     // ============================================================ converters
     if constexpr (QUANT) {
       const int t = tid - 384;
       RingPos pos;
-      for (int v = 0; v < hi - lo; ++v, pos.next(S)) {
+      for (int v = 0; v < nv; ++v, pos.next(S)) {
         const int slot = pos.slot;
         const uint32_t phase = pos.phase;
         if (!wait_warp(kBarKFull + slot, phase)) break;
@@ -972,6 +1043,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           mbar_arrive(bar(kBarVop));
           mbar_arrive(bar(kBarVEmpty + slot));
         }
+        passed(v);
       }
     }
   } else if (warp < 8) {
@@ -1024,9 +1096,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     auto inverse = [](float vref) { return vref > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.f; };
 
     // ---- few query rows: thread = token for the scores, channel for the values
-    auto few_rows = [&](auto rows_c, const Seg& s) -> bool {
-      constexpr int R = decltype(rows_c)::value;   // 8, 16 or 32
-      const int n = s.end - s.begin;
+    auto few_rows = [&](auto rows_c, Visit s) -> bool {
+      constexpr int R = decltype(rows_c)::value;   // 8 or 16
       float m[R], l[R];
       [[maybe_unused]] float zs[R];
       float vref = 0.f;
@@ -1038,14 +1109,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if constexpr (QUANT) zs[j] = 0.f;
       }
       uint8_t* pt = smem + lay.pt + st * kPtBytes;
-      float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 64);
+      float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
       auto meet = [&]() -> bool {   // the stream's four warps
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarX + st));
         return wait_warp(kBarX + st, n_x++ & 1);
       };
-      for (int i = 0; i < n; ++i, ++v) {
-        if ((v & 1) != st) continue;
+      for (;; ++v) {
+        if ((v & 1) == st) {
         int ntok, mask;
         if (!begin_event(ntok, mask)) return false;
         tc_after();
@@ -1073,7 +1144,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           for (int j = 0; j < R; ++j) a[j] *= p.scale;
         }
         // largest score of each row over the tile's tokens
-        float* xb = xch + (n_x & 1) * (4 * 64);
+        float* xb = xch + (n_x & 1) * (4 * 32);
         float keep = 0.f;
 #pragma unroll
         for (int j = 0; j < R; ++j) {
@@ -1081,15 +1152,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           const float w = warp_max(a[j]);
           if (lane == j) keep = w;
         }
-        if (lane < R) xb[quad * 64 + lane] = keep;
+        if (lane < R) xb[quad * 32 + lane] = keep;
         if (!meet()) return false;
         const float fv = QUANT ? scale_ref(vref) : 1.f;
         bool moved = fv != 1.f;
         float alpha[R];
 #pragma unroll
         for (int j = 0; j < R; j += 4) {
-          const float4 x0 = *reinterpret_cast<const float4*>(xb + j), x1 = *reinterpret_cast<const float4*>(xb + 64 + j);
-          const float4 x2 = *reinterpret_cast<const float4*>(xb + 128 + j), x3 = *reinterpret_cast<const float4*>(xb + 192 + j);
+          const float4 x0 = *reinterpret_cast<const float4*>(xb + j), x1 = *reinterpret_cast<const float4*>(xb + 32 + j);
+          const float4 x2 = *reinterpret_cast<const float4*>(xb + 64 + j), x3 = *reinterpret_cast<const float4*>(xb + 96 + j);
           const float mt[4] = {fmaxf(fmaxf(x0.x, x1.x), fmaxf(x2.x, x3.x)), fmaxf(fmaxf(x0.y, x1.y), fmaxf(x2.y, x3.y)),
                                fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)), fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w))};
 #pragma unroll
@@ -1106,12 +1177,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           }
         }
         if (have && moved) {   // the same for all threads of the stream
-          uint32_t o[R];
-          tmem_ld<R>(to, o);
+          uint32_t o[2 * R];
+          tmem_ld<2 * R>(to, o);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < R; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
-          tmem_st<R>(to, o);
+          for (int j = 0; j < 2 * R; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j % R]);
+          tmem_st<2 * R>(to, o);
           tc_wait_st();
         }
         if constexpr (QUANT) vs *= inverse(vref);
@@ -1132,45 +1203,49 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               w1 *= vs;
             }
             hi16[k / 2] = pack16<BF>(w0, w1);
-            if constexpr (R <= 16)
-              lo16[k / 2] = pack16<BF>(w0 - low16<BF>(hi16[k / 2]), w1 - high16<BF>(hi16[k / 2]));
+            lo16[k / 2] = pack16<BF>(w0 - low16<BF>(hi16[k / 2]), w1 - high16<BF>(hi16[k / 2]));
           }
           *reinterpret_cast<uint4*>(pt + j * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
-          if constexpr (R <= 16)
-            *reinterpret_cast<uint4*>(pt + 4096 + j * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
+          *reinterpret_cast<uint4*>(pt + (R + j) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
         }
         have = true;
         fence_proxy_async_smem();
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarP + st));
+        }
+        passed(v);
+        if (s.is(kLast)) break;
+        if (!visit(v + 1, s)) return false;
       }
+      ++v;
       if (!have) return true;
       // ---- the stream's record of each row
-      const size_t rec = s.tile0 > 0 ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + st * kTile : st * whole + s.rec;
-      float* xb = xch + (n_x & 1) * (4 * 64);
+      const size_t rec =
+          s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + st * kTile : st * whole + s.rec;
+      float* xb = xch + (n_x & 1) * (4 * 32);
       int j;
       const float ls = scatter_sum<R>(l, lane, j);
-      xb[quad * 64 + j] = ls;
-      if constexpr (QUANT) xb[quad * 64 + 32 + j] = scatter_sum<R>(zs, lane, j);
+      xb[quad * 32 + j] = ls;
+      if constexpr (QUANT) xb[quad * 32 + 16 + j] = scatter_sum<R>(zs, lane, j);
       if (!meet()) return false;
       if (row < s.rows) {
         float mr = m[0];
 #pragma unroll
         for (int k = 1; k < R; ++k) mr = row == k ? m[k] : mr;
-        p.ws_ml[rec + row] = make_float2(mr, (xb[row] + xb[64 + row]) + (xb[128 + row] + xb[192 + row]));
+        p.ws_ml[rec + row] = make_float2(mr, (xb[row] + xb[32 + row]) + (xb[64 + row] + xb[96 + row]));
       }
       if (!wait_warp(kBarO + st, n_seg++ & 1)) return false;
       tc_after();
       if (quad * 32 < D) {
-        uint32_t o[R];
-        tmem_ld<R>(to, o);
+        uint32_t o[2 * R];
+        tmem_ld<2 * R>(to, o);
         tc_wait_ld();
 #pragma unroll
         for (int k = 0; k < R; ++k) {
           if (k < s.rows) {
-            float f = __uint_as_float(o[k]);
-            if constexpr (QUANT) f = fmaf(f, vref, (xb[32 + k] + xb[96 + k]) + (xb[160 + k] + xb[224 + k]));
+            float f = __uint_as_float(o[k]) + __uint_as_float(o[R + k]);
+            if constexpr (QUANT) f = fmaf(f, vref, (xb[16 + k] + xb[48 + k]) + (xb[80 + k] + xb[112 + k]));
             p.ws_acc[(rec + k) * D + row] = f;
           }
         }
@@ -1179,61 +1254,72 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       return true;
     };
 
-    for (int x = lo; x < hi && ok;) {
-      const Seg s = x == lo ? first : locate(plan, x, hi);
-      x = s.end;
-      if (s.rows <= p.few_rows) {
+    while (v < nv && ok) {
+      Visit s;
+      ok = visit(v, s);
+      if (!ok) break;
+      if (s.rows <= kFew) {
         if (s.rows <= 8)
           ok = few_rows(std::integral_constant<int, 8>{}, s);
-        else if (s.rows <= 16)
-          ok = few_rows(std::integral_constant<int, 16>{}, s);
         else
-          ok = few_rows(std::integral_constant<int, 32>{}, s);
+          ok = few_rows(std::integral_constant<int, 16>{}, s);
         ++qc;
         continue;
       }
       // ---- thread = query row
       const bool two = s.rows > kTile;
-      const int n = s.end - s.begin;
       const int my_rows = two ? min(kTile, s.rows - st * kTile) : s.rows;
       const bool active = quad * 32 < my_rows;   // this warp has query rows
       float m = -INFINITY, l = 0.f, zs = 0.f, vref = 0.f, qs = 0.f;
       bool have = false;
-      for (int i = 0; i < n && ok; ++i, ++v) {
-        if (!two && (v & 1) != st) continue;
+      for (;; ++v) {
+        if (two || (v & 1) == st) {
         int ntok, mask;
         ok = begin_event(ntok, mask);
         if (!ok) break;
         if (active) {
           tc_after();
-          float a[kTile];
-          uint32_t* ar = reinterpret_cast<uint32_t*>(a);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld<32>(ts + 32 * c, ar + 32 * c);
-          tc_wait_ld();
           const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
           if constexpr (QUANT) {
             if (!have)
               qs = reinterpret_cast<const float*>(smem + lay.qsum)[((qc + (two ? st : 0)) % kQSums) * kTile + row];
+          }
+          // Scores are read twice, 32 columns at a time in loops that stay loops: with all
+          // 128 in registers and the code unrolled, the warps waited for instructions
+          // (both SMs of a pair in it: 14000 cycles a visit).
+          const bool whole_tile = ntok == kTile && mask == 0xFF;
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < ntok; c += 32) {
+            float a[32];
+            tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+            tc_wait_ld();
+            if constexpr (QUANT) {
 #pragma unroll
-            for (int j = 0; j < kTile; j += 4) {
-              const float4 ks = *reinterpret_cast<const float4*>(sc + j);
-              const float4 kz = *reinterpret_cast<const float4*>(sc + kTile + j);
-              a[j] = fmaf(ks.x, a[j], kz.x * qs);
-              a[j + 1] = fmaf(ks.y, a[j + 1], kz.y * qs);
-              a[j + 2] = fmaf(ks.z, a[j + 2], kz.z * qs);
-              a[j + 3] = fmaf(ks.w, a[j + 3], kz.w * qs);
+              for (int j = 0; j < 32; j += 4) {
+                const float4 ks = *reinterpret_cast<const float4*>(sc + c + j);
+                const float4 kz = *reinterpret_cast<const float4*>(sc + kTile + c + j);
+                a[j] = fmaf(ks.x, a[j], kz.x * qs);
+                a[j + 1] = fmaf(ks.y, a[j + 1], kz.y * qs);
+                a[j + 2] = fmaf(ks.z, a[j + 2], kz.z * qs);
+                a[j + 3] = fmaf(ks.w, a[j + 3], kz.w * qs);
+              }
             }
-          }
-          if (ntok < kTile || mask != 0xFF) {
+            if (!whole_tile) {
+              const int left = ntok - c;
+              uint32_t keep = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
+              keep &= (mask >> (c >> 4) & 1 ? 0xFFFFu : 0u) | (mask >> (c >> 4) & 2 ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int j = 0; j < kTile; ++j)
-              if (j >= ntok || !(mask >> (j >> 4) & 1)) a[j] = -INFINITY;
-          }
-          float mx[4] = {a[0], a[1], a[2], a[3]};
+              for (int j = 0; j < 32; ++j)
+                if (!(keep >> j & 1)) a[j] = -INFINITY;
+            }
+            if (QUANT || !whole_tile) tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+            float m4[4] = {a[0], a[1], a[2], a[3]};
 #pragma unroll
-          for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], a[j]);
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale;
+            for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], a[j]);
+            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+          }
+          const float mt = mx * p.scale;
           float alpha = 1.f;
           if (mt > m + 8.f) {
             alpha = m == -INFINITY ? 0.f : fast_exp2(m - mt);
@@ -1241,7 +1327,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             l *= alpha;
             zs *= alpha;
           }
-          float rv = 0.f;
+          [[maybe_unused]] float rv = 0.f;
           if constexpr (QUANT) {
             alpha *= scale_ref(vref);
             rv = inverse(vref);
@@ -1249,54 +1335,57 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (have && __any_sync(0xffffffffu, alpha != 1.f)) {
             // S of this event is complete, so every earlier product of this stream is
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld<16>(to + 16 * c, o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld<32>(to + c, o);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st<16>(to + 16 * c, o);
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st<32>(to + c, o);
             }
           }
           const float mref = m == -INFINITY ? 0.f : m;
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          auto weights = [&](auto terms) {
-            constexpr bool TWO = decltype(terms)::value;
+          tc_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < ntok; c += 32) {
+            float a[32];
+            uint32_t hi16[16];
+            tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+            tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              if (16 * c < ntok) {
-                uint32_t hi16[8], lo16[8];
+            for (int j = 0; j < 32; ++j) {
+              a[j] = fast_exp2(fmaf(a[j], p.scale, -mref));
+              ls[j & 3] += a[j];
+            }
+            if constexpr (QUANT) {
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  float w0 = fast_exp2(fmaf(a[16 * c + j], p.scale, -mref));
-                  float w1 = fast_exp2(fmaf(a[16 * c + j + 1], p.scale, -mref));
-                  ls[j & 2] += w0;
-                  ls[(j & 2) + 1] += w1;
-                  if constexpr (QUANT) {
-                    const float2 vs = *reinterpret_cast<const float2*>(sc + 2 * kTile + 16 * c + j);
-                    const float2 vz = *reinterpret_cast<const float2*>(sc + 3 * kTile + 16 * c + j);
-                    zs = fmaf(w0, vz.x, zs);
-                    zs = fmaf(w1, vz.y, zs);
-                    w0 *= vs.x * rv;
-                    w1 *= vs.y * rv;
-                  }
-                  // the weights' one rounding to the operand type; a second term
-                  // holds what it left where the output keeps more bits
-                  hi16[j / 2] = pack16<BF>(w0, w1);
-                  if constexpr (TWO)
-                    lo16[j / 2] = pack16<BF>(w0 - low16<BF>(hi16[j / 2]), w1 - high16<BF>(hi16[j / 2]));
-                }
-                // weights of 32 tokens take the place of their scores: 16
-                // columns of first terms, 16 of second ones
-                tmem_st<8>(ts + 32 * (c >> 1) + 8 * (c & 1), hi16);
-                if constexpr (TWO) tmem_st<8>(ts + 32 * (c >> 1) + 8 * (c & 1) + 16, lo16);
+              for (int j = 0; j < 32; j += 4) {
+                const float4 vs = *reinterpret_cast<const float4*>(sc + 2 * kTile + c + j);
+                const float4 vz = *reinterpret_cast<const float4*>(sc + 3 * kTile + c + j);
+                zs = fmaf(a[j], vz.x, zs);
+                zs = fmaf(a[j + 1], vz.y, zs);
+                zs = fmaf(a[j + 2], vz.z, zs);
+                zs = fmaf(a[j + 3], vz.w, zs);
+                a[j] *= vs.x * rv;
+                a[j + 1] *= vs.y * rv;
+                a[j + 2] *= vs.z * rv;
+                a[j + 3] *= vs.w * rv;
               }
             }
-          };
-          if (p.two_terms)
-            weights(std::true_type{});
-          else
-            weights(std::false_type{});
+            // The weights' one rounding to the operand type. They take the
+            // place of their scores: 16 columns, and 16 more of second terms,
+            // which hold what the rounding left, where the output keeps more bits.
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) hi16[j / 2] = pack16<BF>(a[j], a[j + 1]);
+            tmem_st<16>(ts + c, hi16);
+            if (p.two_terms) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2)
+                hi16[j / 2] = pack16<BF>(a[j] - low16<BF>(hi16[j / 2]), a[j + 1] - high16<BF>(hi16[j / 2]));
+              tmem_st<16>(ts + c + 16, hi16);
+            }
+          }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           tc_wait_st();
           tc_before();
@@ -1305,13 +1394,20 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if constexpr (!QUANT) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarP + st));
+        }
+        passed(v);
+        if (s.is(kLast)) break;
+        ok = visit(v + 1, s);
+        if (!ok) break;
       }
+      ++v;
       if (!ok) break;
       // ---- end of the block's part of the segment: one record per query row
       const int tile_row = two ? st * kTile + row : row;
-      const size_t rec = s.tile0 > 0 ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + tile_row : (size_t)s.rec + tile_row;
+      const size_t rec =
+          s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + tile_row : (size_t)s.rec + tile_row;
       float* acc = p.ws_acc + rec * D;
-      const bool both = !two && n > 1;
+      const bool both = !two && s.is(kMany);
       if (have) {
         ok = wait_warp(kBarO + st, n_seg++ & 1);
         if (!ok) break;
@@ -1428,12 +1524,12 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
     rec[0] = h * p.batch * p.group + i0.x + R;
     sub[0] = R % (2 * kTile);
     const int pair = R / (2 * kTile), pairs = (i0.w + 2 * kTile - 1) / (2 * kTile);
-    few[0] = min(2 * kTile, i0.w - pair * 2 * kTile) <= p.few_rows;
+    few[0] = min(2 * kTile, i0.w - pair * 2 * kTile) <= kFew;
     s0[0] = i0.z + (h * pairs + pair) * i1.x;
     s1[0] = s0[0] + i1.x;
     rec[1] = ((p.num_kv_heads + h) * p.batch + b) * p.group + gq;
     sub[1] = gq;
-    few[1] = p.group <= p.few_rows;
+    few[1] = p.group <= kFew;
     s0[1] = i1.y + h * i1.z;
     s1[1] = s0[1] + i1.z;
 #pragma unroll

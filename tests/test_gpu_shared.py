@@ -59,6 +59,18 @@ def test_split_counts(kind, splits):
     assert int(sb.status.item()) == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "i8t"])
+@pytest.mark.parametrize("rows,g", [(3, 2), (30, 4)])
+def test_many_visits_per_block(kind, rows, g):
+    # one and two blocks for everything: hundreds of tiles each
+    rng = np.random.default_rng(rows)
+    sb = SharedBatch(kind, 1, 64, 32, [(30000, list(rng.integers(0, 300, rows)))], alone=[9000, 50], seed=rows)
+    q, qf = sb.queries(g)
+    for splits in (1, 2):
+        sb.check(sb.run(q, TORCH[sb.src], num_splits=splits), qf, g)
+    assert int(sb.status.item()) == 0
+
+
 def test_long_prefix_many_blocks():
     sb = SharedBatch("bf16", 2, 128, 16, [(20000, [5, 0, 700])], alone=[3000], seed=8)
     q, qf = sb.queries(4)

@@ -508,6 +508,69 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// Rest of a whole warp's bounded wait; the first warp to give up reports it
+// and everyone stops. Out of line: the kernel waits in dozens of places, and its
+// code has to stay small (see the softmax).
+static __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* misc, int32_t* status) {
+  const long long t0 = clock64();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, misc[1] != 0)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > (1ll << 31))) {
+      if ((threadIdx.x & 31) == 0) {
+        misc[1] = 1;
+        flag_status(status, PKV_DEV_TIMEOUT);
+      }
+      return false;
+    }
+  }
+}
+
+// Queries of tile u of a segment into an operand tile (swizzled), by `warps` warps.
+template <int D>
+static __device__ __noinline__ void gather_queries(const SharedParams& p, const Visit& s, const uint16_t* members, int u,
+                                                   uint32_t dst, int w, int warps) {
+  constexpr int CH = D / 8, RPI = 32 / CH;   // 16-byte pieces of a row, rows an instruction
+  const int lane = threadIdx.x & 31;
+  const int rows = min(kTile, s.rows - u * kTile);
+  for (int r0 = 32 * w; r0 < rows; r0 += 32 * warps) {
+    // lane i finds row r0 + i
+    const int R = s.q0 + u * kTile + r0 + lane;
+    int b = s.row, gq = R;
+    if (s.mem0 >= 0) {
+      const int m = R / p.group;
+      b = r0 + lane < rows ? members[s.mem0 + m] : 0;
+      gq = R - m * p.group;
+    }
+    const int qrow = b * p.num_q_heads + s.head * p.group + gq;
+    const int n = min(32, rows - r0), c = lane % CH;
+#pragma unroll 2
+    for (int i = 0; i < n; i += RPI) {
+      const int r = i + lane / CH;
+      const int from = __shfl_sync(0xffffffffu, qrow, r & 31);
+      if (r < n)
+        cp_async16(dst + (c >> 3) * 16384 + (r0 + r) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   p.q + ((size_t)from * D + c * 8) * 2);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Sums of the queries of a gathered tile, for the zero points; a warp.
+template <int D, bool BF>
+static __device__ __noinline__ void sum_queries(const uint8_t* src, float* qsum, int rows) {
+  for (int r = threadIdx.x & 31; r < rows; r += 32) {
+    float t = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 w = *reinterpret_cast<const uint4*>(src + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+      t += (low16<BF>(w.x) + high16<BF>(w.x)) + (low16<BF>(w.y) + high16<BF>(w.y)) +
+           ((low16<BF>(w.z) + high16<BF>(w.z)) + (low16<BF>(w.w) + high16<BF>(w.w)));
+    }
+    qsum[r] = t;
+  }
+}
+
 template <int D, int KV, bool BF>
 __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
@@ -686,22 +749,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   auto tm_s = [&](int st) { return tmem + 128u * (uint32_t)st; };
   auto tm_o = [&](int st) { return tmem + 256u + (uint32_t)(D * st); };
 
-  // Bounded wait; the first warp to give up reports it and everyone stops.
-  auto wait = [&](int i, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar(i), parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar(i), parity)) {
-      if (misc[1]) return false;
-      if (clock64() - t0 > (1ll << 31)) {
-        misc[1] = 1;
-        flag_status(p.dev_status, PKV_DEV_TIMEOUT);
-        return false;
-      }
-    }
-    return true;
-  };
   // for a whole warp: every lane goes on, or none does
-  auto wait_warp = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(i, parity)); };
+  auto wait_warp = [&](int i, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
+    return wait_longer(bar(i), parity, misc, p.dev_status);
+  };
   // visit v of the block; its description may have to be waited for
   auto visit = [&](int v, Visit& d) -> bool {
     if (v >= kVisits && (v & (kVisits / 2 - 1)) == 0 && !wait_warp(kBarVisits + (v / (kVisits / 2) & 1), (v / kVisits - 1) & 1))
@@ -717,48 +769,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       if (lane == 0) mbar_arrive(bar(kBarPassed + (v / (kVisits / 2) & 1)));
     }
   };
-  // queries of tile u of a segment into operand slot qs, by `warps` warps
   auto gather_q = [&](const Visit& s, int u, int qs, int w, int warps) {
-    constexpr int CH = D / 8, RPI = 32 / CH;   // 16-byte pieces of a row, rows an instruction
-    uint8_t* dst = smem + lay.q + (size_t)qs * G::OPERAND;
-    const int rows = min(kTile, s.rows - u * kTile);
-    for (int r0 = 32 * w; r0 < rows; r0 += 32 * warps) {
-      // lane i finds row r0 + i
-      const int R = s.q0 + u * kTile + r0 + lane;
-      int b = s.row, gq = R;
-      if (s.mem0 >= 0) {
-        const int m = R / Gq;
-        b = r0 + lane < rows ? members[s.mem0 + m] : 0;
-        gq = R - m * Gq;
-      }
-      const int qrow = b * p.num_q_heads + s.head * Gq + gq;
-      const int n = min(32, rows - r0), c = lane % CH;
-#pragma unroll 4
-      for (int i = 0; i < n; i += RPI) {
-        const int r = i + lane / CH;
-        const int from = __shfl_sync(0xffffffffu, qrow, r & 31);
-        if (r < n)
-          cp_async16(smem_u32(dst + (c >> 3) * 16384 + (r0 + r) * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                     p.q + ((size_t)from * D + c * 8) * 2);
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    gather_queries<D>(p, s, members, u, smem_u32(smem + lay.q) + (uint32_t)qs * G::OPERAND, w, warps);
   };
-  // sums of the queries of a gathered tile, for the zero points
   auto sum_q = [&](const Visit& s, int u, int qs, int slot) {
-    const uint8_t* src = smem + lay.q + (size_t)qs * G::OPERAND;
-    float* qsum = reinterpret_cast<float*>(smem + lay.qsum) + slot * kTile;
-    const int rows = min(kTile, s.rows - u * kTile);
-    for (int r = lane; r < rows; r += 32) {
-      float t = 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        t += (low16<BF>(w.x) + high16<BF>(w.x)) + (low16<BF>(w.y) + high16<BF>(w.y)) +
-             ((low16<BF>(w.z) + high16<BF>(w.z)) + (low16<BF>(w.w) + high16<BF>(w.w)));
-      }
-      qsum[r] = t;
-    }
+    sum_queries<D, BF>(smem + lay.q + (size_t)qs * G::OPERAND,
+                       reinterpret_cast<float*>(smem + lay.qsum) + slot * kTile, min(kTile, s.rows - u * kTile));
   };
 
   // the first segment's queries, by the warps that have nothing else to do yet
@@ -861,113 +877,117 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       const uint32_t on = elect_one();
       auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       constexpr uint32_t kType = 1u << 4 | (BF ? (1u << 7 | 1u << 10) : 0u) | 8u << 24;   // fp32 sums, M = 128
-      constexpr uint32_t idesc_s = kType | (uint32_t)(kTile / 8) << 17;
-      constexpr uint32_t idesc_o = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
       const uint64_t kmajor = operand_desc(0, 16, 1024), vmajor = operand_desc(0, D == 128 ? 16384 : 0, 1024);
       const uint64_t pmajor = (uint64_t)(128 >> 4) << 16 | (uint64_t)(2048 >> 4) << 32 | 1ull << 46;   // no swizzle
       auto at = [](uint64_t d, uint32_t addr) { return d | (uint64_t)(addr >> 4); };
       const uint32_t qb = smem_u32(smem + lay.q), ring = smem_u32(smem + lay.ring), pt = smem_u32(smem + lay.pt);
       const uint32_t kop = smem_u32(smem + lay.kop), vop = smem_u32(smem + lay.vop);
-      int qc = 0, v = 0;
-      uint32_t odd = 0;   // bit st: parity of the events so far on stream st
-      bool ok = true;
+      uint32_t odd = 0;         // bit st: parity of the events so far on stream st
+      uint32_t vop_phase = 0;   // uses of the converted V tile
+      int qc = 0, v = 0, u = 0;
+      RingPos pos;
       // the event whose P V product is still to be issued
       struct { int st, steps, few; RingPos at; bool on, fresh, last_use, seg_end; } pend = {};
-      RingPos pos;
-      uint32_t vop_phase = 0;   // uses of the converted V tile
-      auto issue_pv = [&]() -> bool {
-        const int st = pend.st, slot = pend.at.slot;
-        if (!wait_warp(kBarP + st, ~(odd >> st) & 1)) return false;
-        if (!(QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + slot, pend.at.phase))) return false;
-        const uint64_t vd = at(vmajor, QUANT ? vop : ring + (uint32_t)(S + slot) * G::ENTRY);
-        tc_after();
-        const uint32_t acc0 = !pend.fresh, o = tm_o(st);
-        if (pend.few) {
-          // O^T (+)= V^T [P1^T | P2^T]: channels x rows, first and second terms of
-          // the weights side by side
-          const uint32_t idesc_t = kType | 1u << 15 | 1u << 16 | (uint32_t)(pend.few / 8) << 17;
-          const uint64_t pd = at(pmajor, pt + (uint32_t)st * kPtBytes);
+      const int end = uni(nv);
+      bool ok = true, begun = false;
+      int rows = 0, flags = 0;
+      // Each pass issues the scores of the next event (visit v, row tile u),
+      // then the P V product of the one before. Normally the streams
+      // alternate; where they do not, the scores wait for a pass of their own,
+      // so that none is overwritten before the weights in it are used.
+      while (ok && (v < end || pend.on)) {
+        if (v < end && !begun) {
+          Visit d;
+          ok = visit(v, d);
+          if (!ok) break;
+          rows = uni(d.rows);
+          flags = uni(d.flags);
+          ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + pos.slot, pos.phase);
+          if (!ok) break;
+          begun = true;
+        }
+        const bool two = rows > kTile;
+        const int st = two ? u : v & 1;
+        const bool scores = v < end && !(pend.on && pend.st == st);
+        const int few = rows > kFew ? 0 : rows > 8 ? 32 : 16;   // two columns a row, for eight rows at a time
+        const bool last_s = !two || u == 1;
+        if (scores) {
+          const int qt = qc + (two ? u : 0), qs = qt & 1;
+          if (flags & kFirst) ok = wait_warp(kBarQFull + qs, (qt >> 1) & 1);
+          if (!ok) break;
+          tc_after();
+          const uint64_t kd = at(kmajor, QUANT ? kop : ring + (uint32_t)pos.slot * G::ENTRY);
+          const uint64_t qd = at(kmajor, qb + (uint32_t)qs * G::OPERAND);
+          // S = Q K^T, rows x tokens; few rows: S^T = K Q^T, tokens x rows
+          const uint64_t ad = few ? kd : qd, bd = few ? qd : kd;
+          const uint32_t idesc = kType | (uint32_t)(few ? kFew / 8 : kTile / 8) << 17;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < pend.steps) mma_ss(o, vd + j * 128, pd + j * 16, idesc_t, j ? 1u : acc0, on);
-        } else {
-          const uint32_t a = tm_s(st);
-          if (p.two_terms) {
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tm_s(st), ad + (k >> 2) * 1024 + (k & 3) * 2, bd + (k >> 2) * 1024 + (k & 3) * 2, idesc, k > 0, on);
+          tc_commit(bar(kBarS + st), on);
+          if (last_s) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + pos.slot), on);
+          if (flags & kLast) tc_commit(bar(kBarQEmpty + qs), on);
+        }
+        if (pend.on) {
+          const int ps = pend.st, slot = pend.at.slot;
+          ok = wait_warp(kBarP + ps, ~(odd >> ps) & 1);
+          if (!ok) break;
+          ok = QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + slot, pend.at.phase);
+          if (!ok) break;
+          tc_after();
+          const uint64_t vd = at(vmajor, QUANT ? vop : ring + (uint32_t)(S + slot) * G::ENTRY);
+          const uint32_t o = tm_o(ps);
+          uint32_t acc = !pend.fresh;
+          if (pend.few) {
+            // O^T (+)= V^T [P1^T | P2^T]: channels x rows, first and second terms of
+            // the weights side by side
+            const uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(pend.few / 8) << 17;
+            const uint64_t pd = at(pmajor, pt + (uint32_t)ps * kPtBytes);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              if (j < pend.steps) {
-                mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc_o, j ? 1u : acc0, on);
-                mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1) + 16, vd + j * 128, idesc_o, 1, on);
-              }
+              if (j < pend.steps) mma_ss(o, vd + j * 128, pd + j * 16, idesc, acc, on);
+              acc = 1;
             }
           } else {
+            constexpr uint32_t idesc = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
+#pragma unroll 1
+            for (uint32_t a = tm_s(ps), last = a + (p.two_terms ? 16 : 0); a <= last; a += 16) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < pend.steps) mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc_o, j ? 1u : acc0, on);
-          }
-        }
-        if (pend.last_use) {
-          tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarVEmpty + slot), on);
-          vop_phase ^= 1;
-        }
-        if (pend.seg_end) tc_commit(bar(kBarO + st), on);
-        pend.on = false;
-        return true;
-      };
-      for (const int end = uni(nv); v < end && ok; ++v, pos.next(S)) {
-        Visit d;
-        ok = visit(v, d);
-        if (!ok) break;
-        const int rows = uni(d.rows), flags = uni(d.flags);
-        const bool two = rows > kTile;
-        const int few = rows > kFew ? 0 : rows > 8 ? 32 : 16;   // two columns a row, for eight rows at a time
-        {
-          const int slot = pos.slot;
-          ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + slot, pos.phase);
-          if (!ok) break;
-          const int ntok = flags & 0xFF;
-          const uint64_t kd = at(kmajor, QUANT ? kop : ring + (uint32_t)slot * G::ENTRY);
-          for (int u = 0; u < (two ? 2 : 1) && ok; ++u) {
-            const int st = two ? u : v & 1, qs = (qc + (two ? u : 0)) & 1;
-            // normally the streams alternate; a score tile is never overwritten
-            // before the weights in it are used
-            if (pend.on && pend.st == st) ok = issue_pv();
-            if (!ok) break;
-            if (flags & kFirst) ok = wait_warp(kBarQFull + qs, ((qc + (two ? u : 0)) >> 1) & 1);
-            if (!ok) break;
-            tc_after();
-            const uint64_t qd = at(kmajor, qb + (uint32_t)qs * G::OPERAND);
-            if (few) {
-              // S^T = K Q^T: tokens x rows
-              constexpr uint32_t idesc_t = kType | (uint32_t)(kFew / 8) << 17;
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_ss(tm_s(st), kd + (k >> 2) * 1024 + (k & 3) * 2, qd + (k >> 2) * 1024 + (k & 3) * 2, idesc_t, k > 0, on);
-            } else {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_ss(tm_s(st), qd + (k >> 2) * 1024 + (k & 3) * 2, kd + (k >> 2) * 1024 + (k & 3) * 2, idesc_s, k > 0, on);
+              for (int j = 0; j < 8; ++j) {
+                if (j < pend.steps) mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc, acc, on);
+                acc = 1;
+              }
             }
-            tc_commit(bar(kBarS + st), on);
-            const bool last_s = u == (two ? 1 : 0);
-            if (last_s) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + slot), on);
-            if (flags & kLast) tc_commit(bar(kBarQEmpty + qs), on);
-            if (pend.on) ok = issue_pv();
-            odd ^= 1u << st;
-            pend.st = st;
-            pend.at = pos;
-            pend.steps = (ntok + 15) >> 4;
-            pend.few = few;
-            pend.on = true;
-            pend.fresh = flags & (two ? kFirst : kEarly);
-            pend.last_use = last_s;
-            pend.seg_end = flags & (two ? kLast : kLate);
+          }
+          if (pend.last_use) {
+            tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarVEmpty + slot), on);
+            vop_phase ^= 1;
+          }
+          if (pend.seg_end) tc_commit(bar(kBarO + ps), on);
+          pend.on = false;
+        }
+        if (scores) {
+          odd ^= 1u << st;
+          pend.st = st;
+          pend.at = pos;
+          pend.steps = ((flags & 0xFF) + 15) >> 4;
+          pend.few = few;
+          pend.on = true;
+          pend.fresh = flags & (two ? kFirst : kEarly);
+          pend.last_use = last_s;
+          pend.seg_end = flags & (two ? kLast : kLate);
+          if (last_s) {
+            if (flags & kLast) qc += two ? 2 : 1;
+            passed(v);
+            ++v;
+            pos.next(S);
+            u = 0;
+            begun = false;
+          } else {
+            u = 1;
           }
         }
-        if (flags & kLast) qc += two ? 2 : 1;
-        passed(v);
       }
-      if (ok && pend.on) ok = issue_pv();
       // nothing of the tensor cores is in flight past this point
       tc_commit(bar(kBarEnd), on);
       if (!mbar_wait_bounded(bar(kBarEnd), 0) && lane == 0) flag_status(p.dev_status, PKV_DEV_TIMEOUT);

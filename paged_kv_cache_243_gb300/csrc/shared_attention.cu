@@ -39,7 +39,7 @@ struct Work {
 Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
   const size_t rows = 4 * (size_t)batch * hq + (size_t)ctas * 2 * kTile;
   Work w;
-  w.ml = align256((size_t)batch * 2 * sizeof(int4));
+  w.ml = align256((size_t)batch * 3 * sizeof(int4));
   w.acc = w.ml + align256(rows * sizeof(float2));
   w.total = w.acc + align256(rows * c->head_dim * sizeof(float)) + 256;
   return w;

@@ -86,7 +86,7 @@ struct SharedParams {
   // workspace: (m, l) and accumulators by record row, and each row's place in the plan
   float2* ws_ml;
   float* ws_acc;
-  int4* ws_info;
+  int4* ws_info;   // three a row
   int num_pages, page_size, num_kv_heads, num_q_heads, group, batch, max_pages, num_groups;
   int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms;
   float scale;   // sm_scale * log2(e)
@@ -107,13 +107,13 @@ struct SharedGeom {
 
 // Shared memory by offset from a 1024-byte boundary.
 struct SharedLayout {
-  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, visits, bpre, gpre, moff, members, lens, skip, gp, rank;
+  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, visits, bpre, gpre, lpre, moff, members, lens, skip, gp, rank, rowg;
   int total;
 };
 enum SharedBars {   // mbarriers, 8 bytes each
   kBarKFull = 0, kBarVFull = kMaxEntries, kBarKEmpty = 2 * kMaxEntries, kBarVEmpty = 3 * kMaxEntries,
   kBarHdr = 4 * kMaxEntries, kBarQFull = kBarHdr + kHdrs, kBarQEmpty = kBarQFull + 2, kBarS = kBarQEmpty + 2,
-  kBarP = kBarS + 2, kBarO = kBarP + 2, kBarX = kBarO + 2, kBarKop = kBarX + 2, kBarVop = kBarKop + 2,
+  kBarP = kBarS + 2, kBarO = kBarP + 2, kBarKop = kBarO + 2, kBarVop = kBarKop + 2,
   kBarPair = kBarVop + 2, kBarVisits = kBarPair + 4, kBarPassed = kBarVisits + 2, kBarEnd = kBarPassed + 2,
   kBarCount = kBarEnd + 1
 };
@@ -140,10 +140,11 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.ml = put(2 * kTile * 16);
   o.qsum = put(G::QUANT ? kQSums * kTile * 4 : 0);
   o.vmax = put(G::QUANT ? kScaleSlots * 16 : 0);
-  o.misc = put(40 * 4);
+  o.misc = put(17 * 16);
   o.visits = put(kVisits * 32);
   o.bpre = put((batch + 1) * 4);
   o.gpre = put((groups + 1) * 4);
+  o.lpre = put((groups + 1) * 4);
   o.moff = put((groups + 1) * 4);
   o.members = put(batch * 2);
   o.total = at;
@@ -153,20 +154,37 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.skip = put(batch * 4);
   o.gp = put(groups * 4);
   o.rank = put(batch * 2);
+  o.rowg = put(batch * 2);
   if (at > o.total) o.total = at;
   return o;
 }
 
-// Blocks' shares of W visits.
-// floor(c W / N) with c <= N < 2^16, in 32 bits
-__device__ __forceinline__ int share_lo(int c, int W, int N) {
-  const uint32_t q = (uint32_t)W / (uint32_t)N, r = (uint32_t)W - q * (uint32_t)N;
-  return (int)((uint32_t)c * q + (uint32_t)c * r / (uint32_t)N);
-}
-// The block that holds visit x: the largest c with floor(c W / N) <= x.
-__device__ __forceinline__ int share_of(long long x, long long W, long long N) {
-  return (int)(((x + 1) * N + W - 1) / W - 1);
-}
+// Shares of the work. Visits are numbered: prefixes of more than one row tile first
+// (`heavy` of them), then the other prefixes, then the rows' own tokens. A heavy visit
+// counts as two units: it has twice the products and exponentials (measured 2.2 us
+// against 1.1-1.3 us). Block c of `blocks` gets the visits that start in its
+// share of the units; every share holds at least one.
+struct Shares {
+  int heavy, blocks, q, r;   // units = blocks q + r
+  __host__ __device__ __forceinline__ Shares() {}
+  __device__ __forceinline__ Shares(int heavy_visits, int visits, int ctas) {
+    heavy = heavy_visits;
+    const int units = visits + heavy;
+    blocks = min(ctas, max(1, units >> 1));
+    q = units / blocks;
+    r = units - q * blocks;
+  }
+  // first visit of block c (c <= blocks)
+  __device__ __forceinline__ int first(int c) const {
+    const int unit = c * q + min(c, r);
+    return unit < 2 * heavy ? (unit + 1) >> 1 : unit - heavy;
+  }
+  // the block of visit x
+  __device__ __forceinline__ int block_of(int x) const {
+    const int unit = x < heavy ? 2 * x : x + heavy, k = r * (q + 1);
+    return unit < k ? unit / (q + 1) : r + (unit - k) / q;
+  }
+};
 
 // ------------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -278,7 +296,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 
 // ---------------------------------------------------------------------- plan
 struct SharedPlan {
-  const int *bpre, *gpre, *moff;   // visits before each row's own tokens and each group's prefix; members
+  const int *gpre, *lpre, *bpre;   // visits before each group's prefix (heavy, other), each row's own tokens
+  const int* moff;                 // members before each group
   const uint16_t* members;
   const int *lens, *skip, *gp;     // shared memory (while planning), or NULL: from the inputs again
   int lo, hi;                      // the block's visits
@@ -299,7 +318,8 @@ struct Visit {
 };
 enum VisitBits {   // place in the block's part of the segment
   kFirst = 0x100, kLast = 0x200, kEarly = 0x400 /* one of the first two */, kLate = 0x800 /* of the last two */,
-  kMany = 0x1000 /* the part has several */, kContinued = 0x2000 /* the segment began in an earlier block */
+  kMany = 0x1000 /* the part has several */, kContinued = 0x2000 /* the segment began in an earlier block */,
+  kTwo = 0x4000 /* two row tiles */
 };
 
 __device__ __forceinline__ int upper(const int* pre, int n, int x) {   // largest i with pre[i] <= x
@@ -334,21 +354,22 @@ __device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int b) {
   if (P < p.round_to || L < P) g = -1;
   r.len = L;
   r.group = g;
-  r.skip = g >= 0 ? P / p.round_to * p.round_to : 0;
+  r.skip = g >= 0 ? P & -p.round_to : 0;
   return r;
 }
 
 static __device__ __noinline__ void describe_visit(const SharedParams& p, const SharedPlan& pl, int x, int4* out) {
   Visit s;
   int tile, tiles, end_tok, first_tok;
-  if (x < pl.gpre[p.num_groups]) {
-    const int g = upper(pl.gpre, p.num_groups, x);
-    end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] / p.round_to * p.round_to;
+  if (x < pl.lpre[p.num_groups]) {
+    const int* pre = x < pl.gpre[p.num_groups] ? pl.gpre : pl.lpre;
+    const int g = upper(pre, p.num_groups, x);
+    end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] & -p.round_to;
     first_tok = 0;
     tiles = (end_tok + kTile - 1) / kTile;
     const int total = (pl.moff[g + 1] - pl.moff[g]) * p.group;
     const int pairs = (total + 2 * kTile - 1) / (2 * kTile);
-    const int rem = x - pl.gpre[g], hp = rem / tiles;
+    const int rem = x - pre[g], hp = rem / tiles;
     tile = rem - hp * tiles;
     s.head = hp / pairs;
     s.q0 = (hp - s.head * pairs) * 2 * kTile;
@@ -380,34 +401,32 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
   const int whole0 = x - tile, x0 = max(pl.lo, whole0), x1 = min(pl.hi, whole0 + tiles);
   s.flags = min(kTile, end_tok - s.tok0) | (x == x0 ? kFirst : 0) | (x == x1 - 1 ? kLast : 0) |
             (x < x0 + 2 ? kEarly : 0) | (x >= x1 - 2 ? kLate : 0) | (x1 - x0 > 1 ? kMany : 0) |
-            (x0 > whole0 ? kContinued : 0);
+            (x0 > whole0 ? kContinued : 0) | (s.rows > kTile ? kTwo : 0);
   out[0] = make_int4(s.tok0, s.flags, s.row, s.head);
   out[1] = make_int4(s.rows, s.q0, s.mem0, s.rec);
 }
 
-// Exclusive prefix sums over the block's threads of two values, and their totals.
-__device__ __forceinline__ void block_scan2(int a, int b, int& pa, int& pb, int& ta, int& tb, int threads,
-                                            int* scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = threads / 32;
-  int ia = a, ib = b;
-#pragma unroll
+// Exclusive prefix sums over the block's threads of four values (in place), and their totals.
+__device__ __forceinline__ int4 block_scan4(int4& x, int threads, int4* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int4 i = x;
+#pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
-    const int ya = __shfl_up_sync(0xffffffffu, ia, off), yb = __shfl_up_sync(0xffffffffu, ib, off);
-    if (lane >= off) {
-      ia += ya;
-      ib += yb;
-    }
+    const int4 y = make_int4(__shfl_up_sync(0xffffffffu, i.x, off), __shfl_up_sync(0xffffffffu, i.y, off),
+                             __shfl_up_sync(0xffffffffu, i.z, off), __shfl_up_sync(0xffffffffu, i.w, off));
+    if (lane >= off) i = make_int4(i.x + y.x, i.y + y.y, i.z + y.z, i.w + y.w);
   }
-  if (lane == 31) {
-    scratch[warp] = ia;
-    scratch[16 + warp] = ib;
-  }
+  if (lane == 31) scratch[warp] = i;
   __syncthreads();
-  int va = lane < warps ? scratch[lane] : 0, vb = lane < warps ? scratch[16 + lane] : 0;
-  pa = ia - a + __reduce_add_sync(0xffffffffu, lane < warp ? va : 0);
-  pb = ib - b + __reduce_add_sync(0xffffffffu, lane < warp ? vb : 0);
-  ta = __reduce_add_sync(0xffffffffu, va);
-  tb = __reduce_add_sync(0xffffffffu, vb);
+  x = make_int4(i.x - x.x, i.y - x.y, i.z - x.z, i.w - x.w);
+  int4 t = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int w = 0; w < threads / 32; ++w) {
+    const int4 y = scratch[w];
+    if (w == warp) x = make_int4(x.x + t.x, x.y + t.y, x.z + t.z, x.w + t.w);
+    t = make_int4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
+  }
+  return t;
 }
 
 // --------------------------------------------------------------- code -> value
@@ -479,27 +498,28 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
 }
 
 // ------------------------------------------------------------------ the kernel
-// Sum of v[j] over the warp, for each j: lane (32 / R) j' + anything ends with the
-// total of one j (returned in `j`), by exchanging halves.
-template <int R>
-__device__ __forceinline__ float scatter_sum(float (&v)[R], int lane, int& j) {
+// Sum over the warp of each of v[0 .. 7], by exchanging halves: a lane ends with the
+// total of one of them, `j`. Overwrites v.
+__device__ __forceinline__ float scatter_sum8(float* v, int lane, int& j) {
   j = 0;
 #pragma unroll
-  for (int n = R, off = 16; off > 0; off >>= 1) {
-    if (n > 1) {
-      n >>= 1;
-      const bool up = lane & off;
+  for (int n = 4, off = 16; n > 0; n >>= 1, off >>= 1) {
+    const bool up = lane & off;
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-      }
-      j += up ? n : 0;
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
     }
+    j += up ? n : 0;
   }
-  return v[0];
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -584,7 +604,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   const uint32_t bars = smem_u32(smem + lay.bars);
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   volatile int* misc = reinterpret_cast<volatile int*>(smem + lay.misc);   // [0] TMEM base, [1] gave up
-  int* scratch = const_cast<int*>(misc) + 4;
+  int4* scratch = reinterpret_cast<int4*>(smem + lay.misc) + 1;
   int* lens = reinterpret_cast<int*>(smem + lay.lens);
   int* skip = reinterpret_cast<int*>(smem + lay.skip);
   int4* visits = reinterpret_cast<int4*>(smem + lay.visits);
@@ -593,7 +613,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   int* gp = reinterpret_cast<int*>(smem + lay.gp);
   int* moff = reinterpret_cast<int*>(smem + lay.moff);
   uint16_t* members = reinterpret_cast<uint16_t*>(smem + lay.members);
+  int* lpre = reinterpret_cast<int*>(smem + lay.lpre);
   uint16_t* rank = reinterpret_cast<uint16_t*>(smem + lay.rank);
+  int16_t* rowg = reinterpret_cast<int16_t*>(smem + lay.rowg);
   const int S = p.entries, B = p.batch, NG = p.num_groups, Gq = p.group;
 
   if (tid == 0) {
@@ -610,7 +632,6 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), 4);
       mbar_init(bar(kBarO + i), 1);
-      mbar_init(bar(kBarX + i), 4);
     }
     mbar_init(bar(kBarKop), 4);        // converted K ready / free again
     mbar_init(bar(kBarKop + 1), 1);
@@ -634,24 +655,27 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- plan: lengths, who shares, visits before each segment
+  // ---- plan: lengths, who shares, visits before each segment. (Its loops stay
+  // loops: this code is fetched anew by every call.)
+#pragma unroll 1
   for (int g = tid; g < NG; g += NT) {
     const int P = p.prefix_lens[g];
     if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
-    gp[g] = max(P, 0) / p.round_to * p.round_to;
+    gp[g] = max(P, 0) & -p.round_to;
   }
+#pragma unroll 1
   for (int b = tid; b < B; b += NT) {
     const RowPlan r = row_plan(p, b);
     if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
     lens[b] = r.len;
     skip[b] = r.skip;
-    members[b] = (uint16_t)r.group;   // for now
+    rowg[b] = (int16_t)r.group;
   }
   __syncthreads();
   if (warp == 0 && NG > 0) {   // each row's place among its group's rows
+#pragma unroll 1
     for (int b0 = 0; b0 < B; b0 += 32) {
-      const int b = b0 + lane;
-      const int g = b < B ? (int)(int16_t)members[b] : -1;
+      const int b = b0 + lane, g = b < B ? rowg[b] : -1;
       const unsigned same = __match_any_sync(0xffffffffu, g);
       const int base = g >= 0 ? moff[g] : 0;
       __syncwarp();
@@ -661,78 +685,67 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
   }
   __syncthreads();
-  // visits of a group's prefix: kv heads x pairs of row tiles x tiles of tokens;
-  // members before each group, in place of their counts
-  {
-    const int per = (NG + NT - 1) / NT;   // <= 3: up to 1024 groups, 384 threads and more
-    const int a = min(NG, tid * per), e = min(NG, a + per);
-    int c[3], w[3], sum = 0, wsum = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      c[i] = a + i < e ? moff[a + i] : 0;
-      w[i] = c[i] == 0 ? 0
-                       : p.num_kv_heads * ((c[i] * Gq + 2 * kTile - 1) / (2 * kTile)) * ((gp[a + i] + kTile - 1) / kTile);
-      sum += c[i];
-      wsum += w[i];
-    }
-    int run, wrun, rt = 0, wt;
-    block_scan2(sum, wsum, run, wrun, rt, wt, NT, scratch);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if (a + i < e) {
-        moff[a + i] = run;
-        gpre[a + i] = wrun;
-      }
-      run += c[i];
-      wrun += w[i];
-    }
-    if (tid == NT - 1) {
-      moff[NG] = rt;
-      gpre[NG] = wt;
-    }
-    // and the rows' own tokens behind them
-    const int per_b = (B + NT - 1) / NT;
-    const int ba = min(B, tid * per_b), be = min(B, ba + per_b);
-    int bsum = 0;
-    for (int b = ba; b < be; ++b) bsum += p.num_kv_heads * ((lens[b] - skip[b] + kTile - 1) / kTile);
-    int brun, dummy, bt, dt;
-    __syncthreads();
-    block_scan2(bsum, 0, brun, dummy, bt, dt, NT, scratch);
-    brun += wt;
-    for (int b = ba; b < be; ++b) {
-      bpre[b] = brun;
-      brun += p.num_kv_heads * ((lens[b] - skip[b] + kTile - 1) / kTile);
-    }
-    if (tid == NT - 1) bpre[B] = wt + bt;
+  auto tiles_of = [](int tokens) { return (uint32_t)(tokens + kTile - 1) / kTile; };
+  // kv heads x pairs of row tiles x tiles of tokens
+  auto prefix_visits = [&](int g) {
+    return moff[g] == 0 ? 0 : (int)(p.num_kv_heads * ((uint32_t)(moff[g] * Gq + 2 * kTile - 1) / (2 * kTile)) * tiles_of(gp[g]));
+  };
+  // each thread's share of the groups and rows: members, heavy visits, other
+  // prefix visits, visits of the rows' own tokens
+  const int per_g = (NG + NT - 1) / NT, per_b = (B + NT - 1) / NT;
+  const int ga = min(NG, tid * per_g), ge = min(NG, ga + per_g), ba = min(B, tid * per_b), be = min(B, ba + per_b);
+  int4 run = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int g = ga; g < ge; ++g) {
+    const int n = prefix_visits(g);
+    run.x += moff[g];
+    (moff[g] * Gq > kTile ? run.y : run.z) += n;
   }
-  // the group of row b is still in members[b]: each thread reads its rows' first
-  int16_t mine[4];
-  constexpr int PER = (1024 + NT - 1) / NT;
-  static_assert(PER <= 4, "rows per thread");
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int b = tid + i * NT;
-    mine[i] = b < B ? (int16_t)members[b] : (int16_t)-1;
+#pragma unroll 1
+  for (int b = ba; b < be; ++b) run.w += p.num_kv_heads * tiles_of(lens[b] - skip[b]);
+  const int4 all = block_scan4(run, NT, scratch);
+#pragma unroll 1
+  for (int g = ga; g < ge; ++g) {
+    const int n = prefix_visits(g), c = moff[g];
+    gpre[g] = run.y;
+    lpre[g] = all.y + run.z;
+    moff[g] = run.x;
+    run.x += c;
+    (c * Gq > kTile ? run.y : run.z) += n;
+  }
+#pragma unroll 1
+  for (int b = ba; b < be; ++b) {
+    bpre[b] = all.y + all.z + run.w;
+    run.w += p.num_kv_heads * tiles_of(lens[b] - skip[b]);
+  }
+  if (tid == 0) {
+    moff[NG] = all.x;
+    gpre[NG] = all.y;
+    lpre[NG] = all.y + all.z;
+    bpre[B] = all.y + all.z + all.w;
   }
   __syncthreads();
-  const int W = bpre[B];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int b = tid + i * NT;
-    if (b >= B) continue;
-    const int g = mine[i];
+  const Shares shares(all.y, all.y + all.z + all.w, p.num_ctas);
+#pragma unroll 1
+  for (int b = tid; b < B; b += NT) {
+    const int g = rowg[b];
     if (g >= 0) members[moff[g] + rank[b]] = (uint16_t)b;
     if (b % (int)gridDim.x == (int)blockIdx.x) {   // for the merge: where row b's segments are
-      const int rows = g >= 0 ? (moff[g + 1] - moff[g]) * Gq : 0;
-      p.ws_info[2 * b] = make_int4(g >= 0 ? moff[g] * Gq : 0, g >= 0 ? rank[b] : 0, g >= 0 ? gpre[g] : 0, rows);
-      p.ws_info[2 * b + 1] = make_int4(g >= 0 ? (gp[g] + kTile - 1) / kTile : 0, bpre[b],
-                                       (lens[b] - skip[b] + kTile - 1) / kTile, W);
+      int4 pre = make_int4(0, 0, 0, 0);
+      int rows = 0;
+      if (g >= 0) {
+        rows = (moff[g + 1] - moff[g]) * Gq;
+        pre = make_int4(moff[g] * Gq, rank[b] * Gq, rows > kTile ? gpre[g] : lpre[g], tiles_of(gp[g]));
+      }
+      p.ws_info[3 * b] = pre;
+      p.ws_info[3 * b + 1] = make_int4(rows, bpre[b], tiles_of(lens[b] - skip[b]), 0);
+      p.ws_info[3 * b + 2] = make_int4(shares.heavy, shares.blocks, shares.q, shares.r);
     }
   }
-  const int lo = W > 0 ? share_lo(blockIdx.x, W, p.num_ctas) : 0;
-  const int hi = W > 0 ? share_lo(blockIdx.x + 1, W, p.num_ctas) : 0;
+  const bool idle = (int)blockIdx.x >= shares.blocks || all.y + all.z + all.w == 0;
+  const int lo = idle ? 0 : shares.first(blockIdx.x), hi = idle ? 0 : shares.first(blockIdx.x + 1);
   const int nv = hi - lo;
-  SharedPlan plan = {bpre, gpre, moff, members, lens, skip, gp, lo, hi};
+  SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, lo, hi};
   __syncthreads();
   if (tid < min(nv, kVisits)) describe_visit(p, plan, lo + tid, visits + 2 * tid);
   plan.lens = plan.skip = plan.gp = nullptr;
@@ -755,13 +768,17 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     return wait_longer(bar(i), parity, misc, p.dev_status);
   };
   // visit v of the block; its description may have to be waited for
+  auto described = [&](int v) -> bool {
+    return v < kVisits || (v & (kVisits / 2 - 1)) != 0 ||
+           wait_warp(kBarVisits + (v / (kVisits / 2) & 1), (v / kVisits - 1) & 1);
+  };
   auto visit = [&](int v, Visit& d) -> bool {
-    if (v >= kVisits && (v & (kVisits / 2 - 1)) == 0 && !wait_warp(kBarVisits + (v / (kVisits / 2) & 1), (v / kVisits - 1) & 1))
-      return false;
+    if (!described(v)) return false;
     const int4 a = visits[2 * (v & (kVisits - 1))], b = visits[2 * (v & (kVisits - 1)) + 1];
     d = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     return true;
   };
+  auto flags_of = [&](int v) { return visits[2 * (v & (kVisits - 1))].y; };
   // this warp needs visit v and those before it no more
   auto passed = [&](int v) {
     if ((v & (kVisits / 2 - 1)) == kVisits / 2 - 1) {
@@ -887,7 +904,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       int qc = 0, v = 0, u = 0;
       RingPos pos;
       // the event whose P V product is still to be issued
-      struct { int st, steps, few; RingPos at; bool on, fresh, last_use, seg_end; } pend = {};
+      struct { int st, steps; RingPos at; bool on, few, fresh, last_use, seg_end; } pend = {};
       const int end = uni(nv);
       bool ok = true, begun = false;
       int rows = 0, flags = 0;
@@ -909,7 +926,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         const bool two = rows > kTile;
         const int st = two ? u : v & 1;
         const bool scores = v < end && !(pend.on && pend.st == st);
-        const int few = rows > kFew ? 0 : rows > 8 ? 32 : 16;   // two columns a row, for eight rows at a time
+        const bool few = rows <= kFew;
         const bool last_s = !two || u == 1;
         if (scores) {
           const int qt = qc + (two ? u : 0), qs = qt & 1;
@@ -941,7 +958,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (pend.few) {
             // O^T (+)= V^T [P1^T | P2^T]: channels x rows, first and second terms of
             // the weights side by side
-            const uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(pend.few / 8) << 17;
+            constexpr uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(2 * kFew / 8) << 17;
             const uint64_t pd = at(pmajor, pt + (uint32_t)ps * kPtBytes);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -1071,250 +1088,193 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm_s(st) + lanes, to = tm_o(st) + lanes;
-    float4* mls = reinterpret_cast<float4*>(smem + lay.ml);
     const size_t whole = (size_t)2 * B * p.num_q_heads;   // record rows of segments by stream
+    float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
     int qc = 0, v = 0;
-    uint32_t n_ev = 0, n_seg = 0, n_pair = 0, n_x = 0;   // events, segments and meetings so far
-    bool ok = true;
-
-    // the stream's next event: scores of visit v are there; V rows without a token cleared
-    auto begin_event = [&](int& ntok, int& mask) -> bool {
-      if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
-      if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
-      const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
-      ntok = hd.x;
-      mask = hd.y;
-      if constexpr (!QUANT) {
-        if (ntok < kTile || mask != 0xFF) {
-          // rows of V that hold no token of this segment may hold anything, NaN
-          // too, and a weight of 0 would not clear it
-          const int slot = v % S;   // rarely needed: no running position
-          if (!wait_warp(kBarVFull + slot, (v / S) & 1)) return false;
-          if (row < (ntok + 15) / 16 * 16 && (row >= ntok || !(mask >> (row >> 4) & 1))) {
-            uint8_t* vr = smem + lay.ring + (size_t)(S + slot) * G::ENTRY + row * 128;
-#pragma unroll
-            for (int h = 0; h < G::HALVES; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + h * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-      }
-      return true;
+    uint32_t n_ev = 0, n_seg = 0, n_pair = 0, n_x = 0;   // events, segments, meetings so far
+    // The state of a segment. Up to 16 rows: lane j of every warp holds row j's
+    // maximum, each thread its token's part of all rows' sums; more rows: the
+    // thread's own row's, in [0].
+    float m = -INFINITY, l[kFew];
+    [[maybe_unused]] float zs[kFew];
+    float vref = 0.f;
+    bool have = false;
+    auto meet = [&](int b, uint32_t& n) -> bool {   // two warps of the same rows
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+      return wait_warp(b, n++ & 1);
     };
-    // a reference for the value scales: the next power of two of the largest, once they outgrow the
-    // last by 2^6 (then every weight x scale stays below 2^15); returns the accumulator's factor
-    auto scale_ref = [&](float& vref) -> float {
-      const float4 vm4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
-      const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
-      if (!(vm > 64.f * vref)) return 1.f;
-      const uint32_t up = (__float_as_uint(vm) + 0x7FFFFFu) & 0x7F800000u;
-      const float nv = __uint_as_float(min(max(up, 27u << 23), 227u << 23));   // 2^-100 .. 2^100
-      const float f = vref / nv;
-      vref = nv;
-      return f;
+    // The stream's four warps. A warp that has given up has arrived here once
+    // more (below), so that this ends, and the others see that it has.
+    auto meet_all = [&]() -> bool {
+      named_bar_sync(2 + st, 128);
+      return misc[1] == 0;
     };
-    auto inverse = [](float vref) { return vref > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.f; };
+    auto inverse = [](float x) { return x > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(x)) : 0.f; };
 
-    // ---- few query rows: thread = token for the scores, channel for the values
-    auto few_rows = [&](auto rows_c, Visit s) -> bool {
-      constexpr int R = decltype(rows_c)::value;   // 8 or 16
-      float m[R], l[R];
-      [[maybe_unused]] float zs[R];
-      float vref = 0.f;
-      bool have = false;
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        m[j] = -INFINITY;
-        l[j] = 0.f;
-        if constexpr (QUANT) zs[j] = 0.f;
-      }
-      uint8_t* pt = smem + lay.pt + st * kPtBytes;
-      float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
-      auto meet = [&]() -> bool {   // the stream's four warps
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarX + st));
-        return wait_warp(kBarX + st, n_x++ & 1);
-      };
-      for (;; ++v) {
-        if ((v & 1) == st) {
-        int ntok, mask;
-        if (!begin_event(ntok, mask)) return false;
-        tc_after();
-        float a[R];
-        tmem_ld<R>(ts, reinterpret_cast<uint32_t*>(a));
-        tc_wait_ld();
-        const bool valid = row < ntok && (mask >> (row >> 4) & 1);
-        [[maybe_unused]] float vs = 1.f, vz = 0.f;
-        if constexpr (QUANT) {
-          const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
-          const float ks = sc[row] * p.scale, kz = sc[kTile + row] * p.scale;
-          vs = sc[2 * kTile + row];
-          vz = sc[3 * kTile + row];
-          const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + (qc % kQSums) * kTile;
-#pragma unroll
-          for (int j = 0; j < R; j += 4) {
-            const float4 q4 = *reinterpret_cast<const float4*>(qsum + j);
-            a[j] = fmaf(ks, a[j], kz * q4.x);
-            a[j + 1] = fmaf(ks, a[j + 1], kz * q4.y);
-            a[j + 2] = fmaf(ks, a[j + 2], kz * q4.z);
-            a[j + 3] = fmaf(ks, a[j + 3], kz * q4.w);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < R; ++j) a[j] *= p.scale;
-        }
-        // largest score of each row over the tile's tokens
-        float* xb = xch + (n_x & 1) * (4 * 32);
-        float keep = 0.f;
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-          if (!valid) a[j] = -INFINITY;
-          const float w = warp_max(a[j]);
-          if (lane == j) keep = w;
-        }
-        if (lane < R) xb[quad * 32 + lane] = keep;
-        if (!meet()) return false;
-        const float fv = QUANT ? scale_ref(vref) : 1.f;
-        bool moved = fv != 1.f;
-        float alpha[R];
-#pragma unroll
-        for (int j = 0; j < R; j += 4) {
-          const float4 x0 = *reinterpret_cast<const float4*>(xb + j), x1 = *reinterpret_cast<const float4*>(xb + 32 + j);
-          const float4 x2 = *reinterpret_cast<const float4*>(xb + 64 + j), x3 = *reinterpret_cast<const float4*>(xb + 96 + j);
-          const float mt[4] = {fmaxf(fmaxf(x0.x, x1.x), fmaxf(x2.x, x3.x)), fmaxf(fmaxf(x0.y, x1.y), fmaxf(x2.y, x3.y)),
-                               fmaxf(fmaxf(x0.z, x1.z), fmaxf(x2.z, x3.z)), fmaxf(fmaxf(x0.w, x1.w), fmaxf(x2.w, x3.w))};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            alpha[j + k] = fv;
-            if (mt[k] > m[j + k] + 8.f) {
-              const float f = m[j + k] == -INFINITY ? 0.f : fast_exp2(m[j + k] - mt[k]);
-              m[j + k] = mt[k];
-              l[j + k] *= f;
-              if constexpr (QUANT) zs[j + k] *= f;
-              alpha[j + k] *= f;
-              moved = true;
-            }
-          }
-        }
-        if (have && moved) {   // the same for all threads of the stream
-          uint32_t o[2 * R];
-          tmem_ld<2 * R>(to, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 2 * R; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j % R]);
-          tmem_st<2 * R>(to, o);
-          tc_wait_st();
-        }
-        if constexpr (QUANT) vs *= inverse(vref);
-        // weights of token `row` for eight rows at a time, as [8-row block][token][8]
-#pragma unroll
-        for (int j = 0; j < R; j += 8) {
-          uint32_t hi16[4], lo16[4];
-#pragma unroll
-          for (int k = 0; k < 8; k += 2) {
-            const float m0 = m[j + k] == -INFINITY ? 0.f : m[j + k], m1 = m[j + k + 1] == -INFINITY ? 0.f : m[j + k + 1];
-            float w0 = fast_exp2(a[j + k] - m0), w1 = fast_exp2(a[j + k + 1] - m1);
-            l[j + k] += w0;
-            l[j + k + 1] += w1;
-            if constexpr (QUANT) {
-              zs[j + k] = fmaf(w0, vz, zs[j + k]);
-              zs[j + k + 1] = fmaf(w1, vz, zs[j + k + 1]);
-              w0 *= vs;
-              w1 *= vs;
-            }
-            hi16[k / 2] = pack16<BF>(w0, w1);
-            lo16[k / 2] = pack16<BF>(w0 - low16<BF>(hi16[k / 2]), w1 - high16<BF>(hi16[k / 2]));
-          }
-          *reinterpret_cast<uint4*>(pt + j * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
-          *reinterpret_cast<uint4*>(pt + (R + j) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
-        }
-        have = true;
-        fence_proxy_async_smem();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + st));
-        }
+    for (; v < nv; ++v) {
+      if (!described(v)) break;
+      const int flags = flags_of(v);
+      const bool two = flags & kTwo, mine = two || (v & 1) == st;
+      if (flags & kFirst) have = false;
+      if (!mine && !(have && flags & kLast)) {   // the other stream's
         passed(v);
-        if (s.is(kLast)) break;
-        if (!visit(v + 1, s)) return false;
-      }
-      ++v;
-      if (!have) return true;
-      // ---- the stream's record of each row
-      const size_t rec =
-          s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + st * kTile : st * whole + s.rec;
-      float* xb = xch + (n_x & 1) * (4 * 32);
-      int j;
-      const float ls = scatter_sum<R>(l, lane, j);
-      xb[quad * 32 + j] = ls;
-      if constexpr (QUANT) xb[quad * 32 + 16 + j] = scatter_sum<R>(zs, lane, j);
-      if (!meet()) return false;
-      if (row < s.rows) {
-        float mr = m[0];
-#pragma unroll
-        for (int k = 1; k < R; ++k) mr = row == k ? m[k] : mr;
-        p.ws_ml[rec + row] = make_float2(mr, (xb[row] + xb[32 + row]) + (xb[64 + row] + xb[96 + row]));
-      }
-      if (!wait_warp(kBarO + st, n_seg++ & 1)) return false;
-      tc_after();
-      if (quad * 32 < D) {
-        uint32_t o[2 * R];
-        tmem_ld<2 * R>(to, o);
-        tc_wait_ld();
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-          if (k < s.rows) {
-            float f = __uint_as_float(o[k]) + __uint_as_float(o[R + k]);
-            if constexpr (QUANT) f = fmaf(f, vref, (xb[16 + k] + xb[48 + k]) + (xb[80 + k] + xb[112 + k]));
-            p.ws_acc[(rec + k) * D + row] = f;
-          }
-        }
-      }
-      tc_before();
-      return true;
-    };
-
-    while (v < nv && ok) {
-      Visit s;
-      ok = visit(v, s);
-      if (!ok) break;
-      if (s.rows <= kFew) {
-        if (s.rows <= 8)
-          ok = few_rows(std::integral_constant<int, 8>{}, s);
-        else
-          ok = few_rows(std::integral_constant<int, 16>{}, s);
-        ++qc;
+        if (flags & kLast) ++qc;
         continue;
       }
-      // ---- thread = query row
-      const bool two = s.rows > kTile;
+      Visit s;
+      visit(v, s);
+      const bool few = s.rows <= kFew;
       const int my_rows = two ? min(kTile, s.rows - st * kTile) : s.rows;
-      const bool active = quad * 32 < my_rows;   // this warp has query rows
-      float m = -INFINITY, l = 0.f, zs = 0.f, vref = 0.f, qs = 0.f;
-      bool have = false;
-      for (;; ++v) {
-        if (two || (v & 1) == st) {
-        int ntok, mask;
-        ok = begin_event(ntok, mask);
-        if (!ok) break;
-        if (active) {
-          tc_after();
-          const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
-          if constexpr (QUANT) {
-            if (!have)
-              qs = reinterpret_cast<const float*>(smem + lay.qsum)[((qc + (two ? st : 0)) % kQSums) * kTile + row];
+      const bool active = few || quad * 32 < my_rows;   // this warp has query rows
+      if (!have) {
+        m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kFew; ++j) {
+          l[j] = 0.f;
+          if constexpr (QUANT) zs[j] = 0.f;
+        }
+        vref = 0.f;
+      }
+      if (mine) {
+        // ---- the stream's next event: the scores of a tile are there
+        if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) break;
+        if (!wait_warp(kBarS + st, n_ev++ & 1)) break;
+        const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
+        const int ntok = hd.x, mask = hd.y;
+        const bool valid = row < ntok && (mask >> (row >> 4) & 1);   // token `row` of the tile
+        if constexpr (!QUANT) {
+          if (ntok < kTile || mask != 0xFF) {
+            // rows of V that hold no token of this segment may hold anything, NaN
+            // too, and a weight of 0 would not clear it
+            const int slot = v % S;
+            if (!wait_warp(kBarVFull + slot, (v / S) & 1)) break;
+            if (row < (ntok + 15) / 16 * 16 && !valid) {
+              uint8_t* vr = smem + lay.ring + (size_t)(S + slot) * G::ENTRY + row * 128;
+#pragma unroll 4
+              for (int i = 0; i < G::HALVES * 8; ++i)
+                *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
           }
-          // Scores are read twice, 32 columns at a time in loops that stay loops: with all
-          // 128 in registers and the code unrolled, the warps waited for instructions
-          // (both SMs of a pair in it: 14000 cycles a visit).
-          const bool whole_tile = ntok == kTile && mask == 0xFF;
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < ntok; c += 32) {
-            float a[32];
-            tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+        }
+        const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
+        const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + ((qc + (two ? st : 0)) % kQSums) * kTile;
+        // A reference for the value scales: the next power of two of the largest, once
+        // they outgrow the last by 2^6 (every weight x scale then stays below 2^15); fv
+        // is the accumulator's factor, the same for the whole stream.
+        float fv = 1.f;
+        if constexpr (QUANT) {
+          const float4 vm4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
+          const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
+          if (vm > 64.f * vref) {
+            const uint32_t up = (__float_as_uint(vm) + 0x7FFFFFu) & 0x7F800000u;
+            const float nv2 = __uint_as_float(min(max(up, 27u << 23), 227u << 23));   // 2^-100 .. 2^100
+            fv = vref / nv2;
+            vref = nv2;
+          }
+        }
+        tc_after();
+        if (few) {
+          // ---- thread = token for the scores, channel for the values; rows in
+          // blocks of eight, of which the second may be empty
+          float a[kFew];
+          float vs = 1.f, vz = 0.f;
+          float ks = p.scale, kz = 0.f;
+          if constexpr (QUANT) {
+            ks *= sc[row];
+            kz = sc[kTile + row] * p.scale;
+            vs = sc[2 * kTile + row] * inverse(vref);
+            vz = sc[3 * kTile + row];
+          }
+          float* xb = xch + (n_x++ & 1) * (4 * 32);
+          float keep = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kFew; e += 8) {
+            if (e > 0 && s.rows <= 8) break;
+            tmem_ld<8>(ts + e, reinterpret_cast<uint32_t*>(a + e));
             tc_wait_ld();
+            float4 q4[2] = {};
             if constexpr (QUANT) {
+              q4[0] = *reinterpret_cast<const float4*>(qsum + e);
+              q4[1] = *reinterpret_cast<const float4*>(qsum + e + 4);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              a[e + j] = QUANT ? fmaf(ks, a[e + j], kz * reinterpret_cast<const float*>(q4)[j]) : a[e + j] * ks;
+              if (!valid) a[e + j] = -INFINITY;
+              const float w = warp_max(a[e + j]);
+              if (lane == e + j) keep = w;
+            }
+          }
+          if (lane < kFew) xb[quad * 32 + lane] = keep;
+          if (!meet_all()) break;
+          // lane j: largest score of row j over the tile's tokens
+          xb += lane & (kFew - 1);
+          const float mt = fmaxf(fmaxf(xb[0], xb[32]), fmaxf(xb[64], xb[96]));
+          float alpha = 1.f;
+          if (mt > m + 8.f) {
+            alpha = fast_exp2(m - mt);   // 0 from -inf
+            m = mt;
+          }
+          if (have && __any_sync(0xffffffffu, alpha * fv != 1.f)) {   // the same for the whole stream
+#pragma unroll
+            for (int e = 0; e < kFew; e += 8) {
+              if (e > 0 && s.rows <= 8) break;
+              uint32_t o[16];
+              tmem_ld<8>(to + e, o);
+              tmem_ld<8>(to + kFew + e, o + 8);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float f = __shfl_sync(0xffffffffu, alpha, e + j);
+                l[e + j] *= f;
+                if constexpr (QUANT) zs[e + j] *= f;
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * (f * fv));
+                o[8 + j] = __float_as_uint(__uint_as_float(o[8 + j]) * (f * fv));
+              }
+              tmem_st<8>(to + e, o);
+              tmem_st<8>(to + kFew + e, o + 8);
+            }
+            tc_wait_st();
+          }
+          const float mref = m == -INFINITY ? 0.f : m;
+          uint8_t* pt = smem + lay.pt + st * kPtBytes;
+#pragma unroll
+          for (int e = 0; e < kFew; e += 8) {
+            if (e > 0 && s.rows <= 8) break;
+            // weights of token `row`, first terms and what their rounding left, as
+            // [8-row block][token][8]
+            uint32_t hi16[4], lo16[4];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              float w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int j = e + k + i;
+                w[i] = fast_exp2(a[j] - __shfl_sync(0xffffffffu, mref, j));
+                l[j] += w[i];
+                if constexpr (QUANT) {
+                  zs[j] = fmaf(w[i], vz, zs[j]);
+                  w[i] *= vs;
+                }
+              }
+              hi16[k / 2] = pack16<BF>(w[0], w[1]);
+              lo16[k / 2] = pack16<BF>(w[0] - low16<BF>(hi16[k / 2]), w[1] - high16<BF>(hi16[k / 2]));
+            }
+            *reinterpret_cast<uint4*>(pt + e * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
+            *reinterpret_cast<uint4*>(pt + (kFew + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
+          }
+        } else if (active) {
+          // ---- thread = query row. Scores are read twice, 64 columns at a time in loops
+          // that stay loops: with all 128 in registers and the code unrolled, the
+          // warps waited for instructions.
+          if constexpr (QUANT) {
+            const float qs = qsum[row];
+#pragma unroll 1
+            for (int c = 0; c < ntok; c += 32) {
+              float a[32];
+              tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+              tc_wait_ld();
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
                 const float4 ks = *reinterpret_cast<const float4*>(sc + c + j);
@@ -1324,33 +1284,47 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 a[j + 2] = fmaf(ks.z, a[j + 2], kz.z * qs);
                 a[j + 3] = fmaf(ks.w, a[j + 3], kz.w * qs);
               }
+              tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
             }
-            if (!whole_tile) {
-              const int left = ntok - c;
-              uint32_t keep = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
-              keep &= (mask >> (c >> 4) & 1 ? 0xFFFFu : 0u) | (mask >> (c >> 4) & 2 ? 0xFFFF0000u : 0u);
+          }
+          if (ntok < kTile || mask != 0xFF) {   // columns without a token
+            if constexpr (QUANT) tc_wait_st();
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 16) {
+              const int left = mask >> (c >> 4) & 1 ? ntok - c : 0;
+              if (left >= 16) continue;
+              float a[16];
+              tmem_ld<16>(ts + c, reinterpret_cast<uint32_t*>(a));
+              tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(keep >> j & 1)) a[j] = -INFINITY;
+              for (int j = 0; j < 16; ++j)
+                if (j >= left) a[j] = -INFINITY;
+              tmem_st<16>(ts + c, reinterpret_cast<uint32_t*>(a));
             }
-            if (QUANT || !whole_tile) tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
-            float m4[4] = {a[0], a[1], a[2], a[3]};
+            tc_wait_st();
+          } else if constexpr (QUANT) {
+            tc_wait_st();
+          }
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < ntok; c += 64) {
+            float a[64];
+            tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+            tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
+            tc_wait_ld();
+            float m4[4] = {mx, a[0], a[1], a[2]};
 #pragma unroll
-            for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], a[j]);
-            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+            for (int j = 3; j < 63; j += 2) m4[j >> 1 & 3] = max3(m4[j >> 1 & 3], a[j], a[j + 1]);
+            mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[63]);
           }
           const float mt = mx * p.scale;
-          float alpha = 1.f;
+          float alpha = fv;
           if (mt > m + 8.f) {
-            alpha = m == -INFINITY ? 0.f : fast_exp2(m - mt);
+            const float f = fast_exp2(m - mt);   // 0 from -inf
             m = mt;
-            l *= alpha;
-            zs *= alpha;
-          }
-          [[maybe_unused]] float rv = 0.f;
-          if constexpr (QUANT) {
-            alpha *= scale_ref(vref);
-            rv = inverse(vref);
+            l[0] *= f;
+            if constexpr (QUANT) zs[0] *= f;
+            alpha *= f;
           }
           if (have && __any_sync(0xffffffffu, alpha != 1.f)) {
             // S of this event is complete, so every earlier product of this stream is
@@ -1364,151 +1338,168 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               tmem_st<32>(to + c, o);
             }
           }
-          const float mref = m == -INFINITY ? 0.f : m;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          tc_wait_st();
+          const float mref = m == -INFINITY ? 0.f : m, rv = QUANT ? inverse(vref) : 0.f;
+          const uint64_t sc2 = pack2f(p.scale, p.scale), mr2 = pack2f(-mref, -mref);
+          uint64_t ls0 = 0, ls1 = 0, z2 = 0;
 #pragma unroll 1
-          for (int c = 0; c < ntok; c += 32) {
-            float a[32];
-            uint32_t hi16[16];
+          for (int c = 0; c < ntok; c += 64) {
+            float a[64];
             tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+            tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              a[j] = fast_exp2(fmaf(a[j], p.scale, -mref));
-              ls[j & 3] += a[j];
+            for (int j = 0; j < 64; j += 2) {
+              float x, y;
+              unpack2f(ffma2(pack2f(a[j], a[j + 1]), sc2, mr2), x, y);
+              a[j] = fast_exp2(x);
+              a[j + 1] = fast_exp2(y);
+              (j & 2 ? ls1 : ls0) = fadd2(j & 2 ? ls1 : ls0, pack2f(a[j], a[j + 1]));
             }
             if constexpr (QUANT) {
+              const uint64_t rv2 = pack2f(rv, rv);
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 vs = *reinterpret_cast<const float4*>(sc + 2 * kTile + c + j);
-                const float4 vz = *reinterpret_cast<const float4*>(sc + 3 * kTile + c + j);
-                zs = fmaf(a[j], vz.x, zs);
-                zs = fmaf(a[j + 1], vz.y, zs);
-                zs = fmaf(a[j + 2], vz.z, zs);
-                zs = fmaf(a[j + 3], vz.w, zs);
-                a[j] *= vs.x * rv;
-                a[j + 1] *= vs.y * rv;
-                a[j + 2] *= vs.z * rv;
-                a[j + 3] *= vs.w * rv;
+              for (int j = 0; j < 64; j += 4) {
+                const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + c + j);
+                const ulonglong2 vz = *reinterpret_cast<const ulonglong2*>(sc + 3 * kTile + c + j);
+                z2 = ffma2(pack2f(a[j], a[j + 1]), vz.x, z2);
+                z2 = ffma2(pack2f(a[j + 2], a[j + 3]), vz.y, z2);
+                unpack2f(fmul2(pack2f(a[j], a[j + 1]), fmul2(vs.x, rv2)), a[j], a[j + 1]);
+                unpack2f(fmul2(pack2f(a[j + 2], a[j + 3]), fmul2(vs.y, rv2)), a[j + 2], a[j + 3]);
               }
             }
             // The weights' one rounding to the operand type. They take the
-            // place of their scores: 16 columns, and 16 more of second terms,
-            // which hold what the rounding left, where the output keeps more bits.
+            // place of their scores: 16 columns for 32 tokens, and 16 more of second
+            // terms, which hold what the rounding left, where the output keeps more bits.
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) hi16[j / 2] = pack16<BF>(a[j], a[j + 1]);
-            tmem_st<16>(ts + c, hi16);
-            if (p.two_terms) {
+            for (int e = 0; e < 64; e += 32) {
+              uint32_t w[16];
 #pragma unroll
-              for (int j = 0; j < 32; j += 2)
-                hi16[j / 2] = pack16<BF>(a[j] - low16<BF>(hi16[j / 2]), a[j + 1] - high16<BF>(hi16[j / 2]));
-              tmem_st<16>(ts + c + 16, hi16);
-            }
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          tc_wait_st();
-          tc_before();
-        }
-        have = true;
-        if constexpr (!QUANT) fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + st));
-        }
-        passed(v);
-        if (s.is(kLast)) break;
-        ok = visit(v + 1, s);
-        if (!ok) break;
-      }
-      ++v;
-      if (!ok) break;
-      // ---- end of the block's part of the segment: one record per query row
-      const int tile_row = two ? st * kTile + row : row;
-      const size_t rec =
-          s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + tile_row : (size_t)s.rec + tile_row;
-      float* acc = p.ws_acc + rec * D;
-      const bool both = !two && s.is(kMany);
-      if (have) {
-        ok = wait_warp(kBarO + st, n_seg++ & 1);
-        if (!ok) break;
-      }
-      if (active && !both) {
-        if (have) {
-          tc_after();
-          if (row < my_rows) p.ws_ml[rec] = make_float2(m, l);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld<32>(to + 32 * c, o);
-            tc_wait_ld();
-            if (row < my_rows) {
+              for (int j = 0; j < 16; ++j) w[j] = pack16<BF>(a[e + 2 * j], a[e + 2 * j + 1]);
+              tmem_st<16>(ts + c + e, w);
+              if (p.two_terms) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                float4 f = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), __uint_as_float(o[j + 2]),
-                                       __uint_as_float(o[j + 3]));
-                if constexpr (QUANT) {
-                  f.x = fmaf(f.x, vref, zs);
-                  f.y = fmaf(f.y, vref, zs);
-                  f.z = fmaf(f.z, vref, zs);
-                  f.w = fmaf(f.w, vref, zs);
-                }
-                *reinterpret_cast<float4*>(acc + 32 * c + j) = f;
+                for (int j = 0; j < 16; ++j)
+                  w[j] = pack16<BF>(a[e + 2 * j] - low16<BF>(w[j]), a[e + 2 * j + 1] - high16<BF>(w[j]));
+                tmem_st<16>(ts + c + e + 16, w);
               }
             }
           }
-          tc_before();
+          l[0] += hsum2(fadd2(ls0, ls1));
+          if constexpr (QUANT) zs[0] += hsum2(z2);
+          tc_wait_st();
         }
-      } else if (active) {
-        // the two streams' states of each row meet: each stream's warp merges
-        // half of the channels of both accumulators
-        mls[st * kTile + row] = make_float4(m, l, zs, vref);
+        have = true;
+        fence_proxy_async_smem();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPair + quad));
-        ok = wait_warp(kBarPair + quad, n_pair++ & 1);
-        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(kBarP + st));
+      }
+      passed(v);
+      if (!s.is(kLast)) continue;
+
+      // ---- end of the block's part of the segment: one record per query row
+      qc += two ? 2 : 1;
+      const bool both = !two && !few && s.is(kMany);   // the streams' states of a row meet
+      const int tile_row = two ? st * kTile + row : row;
+      const size_t rec0 = s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
+                                           : (few ? st * whole : 0) + s.rec;
+      if (!few) {
+        if (!wait_warp(kBarO + st, n_seg++ & 1)) break;
         tc_after();
-        const float4 other = mls[(st ^ 1) * kTile + row];
-        const float M = fmaxf(m, other.x);
-        float f0 = m == -INFINITY ? 0.f : fast_exp2(m - M), f1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - M);
-        if (row < my_rows && st == 0) p.ws_ml[rec] = make_float2(M, fmaf(l, f0, other.y * f1));
-        const float z = fmaf(zs, f0, other.z * f1);
-        if constexpr (QUANT) {
-          f0 *= vref;
-          f1 *= other.w;
+      }
+      if (few) {
+        float* xb = xch + (n_x++ & 1) * (4 * 32);
+#pragma unroll
+        for (int e = 0; e < kFew; e += 8) {
+          if (e > 0 && s.rows <= 8) break;
+          int j;
+          const float ls = scatter_sum8(l + e, lane, j);
+          xb[quad * 32 + e + j] = ls;
+          if constexpr (QUANT) xb[quad * 32 + kFew + e + j] = scatter_sum8(zs + e, lane, j);
         }
+        if (!meet_all()) break;
+        auto total = [&](int i) { return (xb[i] + xb[32 + i]) + (xb[64 + i] + xb[96 + i]); };
+        if (row < s.rows) {
+          p.ws_ml[rec0 + row] = make_float2(m, total(row));
+          if (!s.is(kMany)) {   // a part of one visit: the other stream has nothing
+            const size_t other = s.is(kContinued) ? rec0 + (st ? -kTile : kTile) : st ? s.rec : whole + s.rec;
+            p.ws_ml[other + row] = make_float2(-INFINITY, 0.f);
+          }
+        }
+        if (!wait_warp(kBarO + st, n_seg++ & 1)) break;
+        tc_after();
+        if (quad * 32 < D) {
+#pragma unroll 1
+          for (int e = 0; e < s.rows; e += 8) {
+            uint32_t o[16];
+            tmem_ld<8>(to + e, o);
+            tmem_ld<8>(to + kFew + e, o + 8);
+            tc_wait_ld();
+            float* acc = p.ws_acc + (rec0 + e) * D + row;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (e + k >= s.rows) break;
+              float f = __uint_as_float(o[k]) + __uint_as_float(o[8 + k]);
+              if constexpr (QUANT) f = fmaf(f, vref, total(kFew + e + k));
+              acc[k * D] = f;
+            }
+          }
+        }
+      } else if (active) {
+        const size_t rec = rec0 + tile_row;
+        float* acc = p.ws_acc + rec * D;
+        // this stream's channels and factor; of two streams each writes half
+        // of the channels of both accumulators' sum
+        float M = m, L = l[0], z = 0.f, f0 = QUANT ? vref : 1.f, f1 = 0.f;
+        if constexpr (QUANT) z = zs[0];
+        int from = 0, to_c = D;
+        if (both) {
+          float4* mls = reinterpret_cast<float4*>(smem + lay.ml);
+          mls[st * kTile + row] = make_float4(M, L, z, f0);
+          tc_before();
+          if (!meet(kBarPair + quad, n_pair)) break;
+          tc_after();
+          const float4 other = mls[(st ^ 1) * kTile + row];
+          M = fmaxf(m, other.x);
+          const float Mr = M == -INFINITY ? 0.f : M, g0 = fast_exp2(m - Mr), g1 = fast_exp2(other.x - Mr);
+          L = fmaf(L, g0, other.y * g1);
+          z = fmaf(z, g0, other.z * g1);
+          f0 *= g0;
+          f1 = other.w * g1;
+          from = st * (D / 2);
+          to_c = from + D / 2;
+        }
+        if (row < my_rows && from == 0) p.ws_ml[rec] = make_float2(M, L);
         const uint32_t to2 = tm_o(st ^ 1) + lanes;
 #pragma unroll 1
-        for (int c = st * (D / 64); c < (st + 1) * (D / 64); ++c) {
-          uint32_t o[32], o2[32];
-          tmem_ld<32>(to + 32 * c, o);
-          tmem_ld<32>(to2 + 32 * c, o2);
+        for (int c = from; c < to_c; c += 16) {
+          uint32_t o[16], o2[16];
+          tmem_ld<16>(to + c, o);
+          if (both) tmem_ld<16>(to2 + c, o2);
           tc_wait_ld();
           if (row < my_rows) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float4 f = make_float4(fmaf(__uint_as_float(o[j]), f0, __uint_as_float(o2[j]) * f1),
-                                     fmaf(__uint_as_float(o[j + 1]), f0, __uint_as_float(o2[j + 1]) * f1),
-                                     fmaf(__uint_as_float(o[j + 2]), f0, __uint_as_float(o2[j + 2]) * f1),
-                                     fmaf(__uint_as_float(o[j + 3]), f0, __uint_as_float(o2[j + 3]) * f1));
-              if constexpr (QUANT) {
-                f.x += z;
-                f.y += z;
-                f.z += z;
-                f.w += z;
+            for (int j = 0; j < 16; j += 4) {
+              float f[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                f[k] = __uint_as_float(o[j + k]) * f0;
+                if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k]);
+                if constexpr (QUANT) f[k] += z;
               }
-              *reinterpret_cast<float4*>(acc + 32 * c + j) = f;
+              *reinterpret_cast<float4*>(acc + c + j) = make_float4(f[0], f[1], f[2], f[3]);
             }
           }
         }
-        tc_before();   // neither accumulator is overwritten before both are read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPair + quad));
-        ok = wait_warp(kBarPair + quad, n_pair++ & 1);
-        if (!ok) break;
+        if (both) {   // neither accumulator is overwritten before both are read
+          tc_before();
+          if (!meet(kBarPair + quad, n_pair)) break;
+        }
       }
-      qc += two ? 2 : 1;
+      tc_before();
     }
+    // given up: the stream's other warps may be waiting for this one
+    if (v < nv) asm volatile("bar.arrive %0, 128;" ::"r"(2 + st) : "memory");
   }
   tc_before();
   __syncthreads();
@@ -1517,123 +1508,106 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ the merge
-// Folds a query row's records (from the block where each of its two segments begins
-// and from the blocks that continue them): WPR warps per row, each lane 4 channels of
-// every WPR-th record (two records at a time at 64 channels).
+// Folds a query row's records, from the blocks of its prefix segment and of its own
+// tokens: WPR warps per row, each lane 4 channels of every WPR-th record (two records
+// at a time at 64 channels). Small code: every call fetches it anew.
 constexpr int kMergeThreads = 128;
 
 template <int D, int WPR>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __grid_constant__ SharedParams p) {
   constexpr int LPR = D / 4, SUB = 32 / LPR;       // lanes per record, records side by side in a warp
-  constexpr int STREAMS = WPR * SUB, BATCH = 4;
-  __shared__ float part[4][WPR > 1 ? D + 2 : 1];
-  pdl_launch_dependents();
+  constexpr int STREAMS = WPR * SUB, BATCH = 8;
+  __shared__ float part[WPR][D + 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x * (4 / WPR) + warp / WPR, w = warp % WPR;
   pdl_wait();
   if (item >= p.batch * p.num_q_heads) return;   // uniform over a row's warps
   const int b = item / p.num_q_heads, hq = item - b * p.num_q_heads;
   const int h = hq / p.group, gq = hq - h * p.group;
-  const int4 i0 = __ldcg(p.ws_info + 2 * b), i1 = __ldcg(p.ws_info + 2 * b + 1);
-  const int W = i1.w, N = p.num_ctas;
+  const int4 i0 = __ldcg(p.ws_info + 3 * b), i1 = __ldcg(p.ws_info + 3 * b + 1), i2 = __ldcg(p.ws_info + 3 * b + 2);
+  Shares sh;
+  sh.heavy = i2.x;
+  sh.blocks = i2.y;
+  sh.q = i2.z;
+  sh.r = i2.w;
   const int whole = 2 * p.batch * p.num_q_heads;   // record rows of segments by stream
-  // prefix records, then the row's own; a segment of few rows has one of each stream
-  int c0[2] = {0, 0}, n[2] = {0, 0}, rec[2], sub[2], s0[2] = {0, 0}, s1[2] = {0, 0}, few[2];
-  {
-    const int R = i0.y * p.group + gq;             // query row within the group
-    rec[0] = h * p.batch * p.group + i0.x + R;
-    sub[0] = R % (2 * kTile);
-    const int pair = R / (2 * kTile), pairs = (i0.w + 2 * kTile - 1) / (2 * kTile);
-    few[0] = min(2 * kTile, i0.w - pair * 2 * kTile) <= kFew;
-    s0[0] = i0.z + (h * pairs + pair) * i1.x;
-    s1[0] = s0[0] + i1.x;
-    rec[1] = ((p.num_kv_heads + h) * p.batch + b) * p.group + gq;
-    sub[1] = gq;
-    few[1] = p.group <= kFew;
-    s0[1] = i1.y + h * i1.z;
-    s1[1] = s0[1] + i1.z;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (s0[k] == s1[k]) continue;
-      c0[k] = share_of(s0[k], W, N);
-      n[k] = (share_of(s1[k] - 1, W, N) - c0[k] + 1) << few[k];
-    }
+  // records of the prefix, then of the row's own tokens; a segment of few rows has
+  // one of each stream, and a block's first part, if it continues a
+  // segment, has its place by block
+  int n0 = 0, n1 = 0, c0 = 0, c1 = 0;
+  const int R = i0.y + gq, pair = R / (2 * kTile), pairs = (i1.x + 2 * kTile - 1) / (2 * kTile);
+  const int few0 = i1.x - pair * 2 * kTile <= kFew, few1 = p.group <= kFew;
+  if (i0.w > 0) {
+    const int x = i0.z + (h * pairs + pair) * i0.w;
+    c0 = sh.block_of(x);
+    n0 = (sh.block_of(x + i0.w - 1) - c0 + 1) << few0;
   }
-  const int total = n[0] + n[1];
-  const int my = w * SUB + lane / LPR, ch = (lane % LPR) * 4;
+  if (i1.z > 0) {
+    const int x = i1.y + h * i1.z;
+    c1 = sh.block_of(x);
+    n1 = (sh.block_of(x + i1.z - 1) - c1 + 1) << few1;
+  }
+  const int r0 = h * p.batch * p.group + i0.x + R, r1 = ((p.num_kv_heads + h) * p.batch + b) * p.group + gq;
+  const int ch = (lane % LPR) * 4;
   float M = -INFINITY, L = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = my; j0 < total; j0 += STREAMS * BATCH) {
+#pragma unroll 1
+  for (int j0 = w * SUB + lane / LPR; j0 < n0 + n1; j0 += STREAMS * BATCH) {
     float2 ml[BATCH];
     float4 a[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       int j = j0 + i * STREAMS;
-      const int k = j >= n[0];
-      bool on = j < total;
-      if (k) j -= n[0];
-      const int c = c0[k] + (j >> few[k]), st = j & few[k];
-      const int lo = share_lo(c, W, N), a0 = max(s0[k], lo), a1 = min(s1[k], share_lo(c + 1, W, N));
-      // a block without visits (fewer visits than blocks) has no record, and one
-      // visit of a segment of few rows is one stream's
-      on = on && a0 < a1 && (!few[k] || a1 - a0 > 1 || ((a0 - lo) & 1) == st);
-      const size_t r = on ? (a0 == s0[k] ? (size_t)st * whole + rec[k] : 2 * (size_t)whole + (size_t)c * 2 * kTile +
-                                                                           st * kTile + sub[k])
-                          : 0;
+      const bool on = j < n0 + n1, own = j >= n0;
+      j -= own ? n0 : 0;
+      const int few = own ? few1 : few0, st = j & few, k = j >> few;
+      const size_t r = !on      ? 0
+                       : k == 0 ? (size_t)st * whole + (own ? r1 : r0)
+                                : 2 * (size_t)whole + (size_t)((own ? c1 : c0) + k) * (2 * kTile) + st * kTile +
+                                      (own ? gq : R % (2 * kTile));
       ml[i] = on ? __ldcg(p.ws_ml + r) : make_float2(-INFINITY, 0.f);
-      a[i] = on ? __ldcg(reinterpret_cast<const float4*>(p.ws_acc + r * D + ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      a[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + r * D + ch));
     }
     float Mn = M;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i].x);
-    if (Mn == -INFINITY) continue;
-    const float f0 = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    const float Mr = Mn == -INFINITY ? 0.f : Mn, f0 = exp2f(M - Mr);
+    M = Mn;
     L *= f0;
-    A.x *= f0; A.y *= f0; A.z *= f0; A.w *= f0;
+    A = make_float4(A.x * f0, A.y * f0, A.z * f0, A.w * f0);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       if (ml[i].x == -INFINITY) continue;   // no token: its accumulator means nothing
-      const float f = exp2f(ml[i].x - Mn);
+      const float f = exp2f(ml[i].x - Mr);
       L = fmaf(f, ml[i].y, L);
-      A.x = fmaf(f, a[i].x, A.x);
-      A.y = fmaf(f, a[i].y, A.y);
-      A.z = fmaf(f, a[i].z, A.z);
-      A.w = fmaf(f, a[i].w, A.w);
+      A = make_float4(fmaf(f, a[i].x, A.x), fmaf(f, a[i].y, A.y), fmaf(f, a[i].z, A.z), fmaf(f, a[i].w, A.w));
     }
-    M = Mn;
   }
   auto join = [&](float M2, float L2, float4 A2) {
-    const float Mn = fmaxf(M, M2);
-    if (Mn == -INFINITY) return;
-    const float f = M == -INFINITY ? 0.f : exp2f(M - Mn), f2 = M2 == -INFINITY ? 0.f : exp2f(M2 - Mn);
+    const float Mn = fmaxf(M, M2), Mr = Mn == -INFINITY ? 0.f : Mn;
+    const float f = exp2f(M - Mr), f2 = exp2f(M2 - Mr);
     L = L * f + L2 * f2;
-    A.x = A.x * f + A2.x * f2;
-    A.y = A.y * f + A2.y * f2;
-    A.z = A.z * f + A2.z * f2;
-    A.w = A.w * f + A2.w * f2;
+    A = make_float4(A.x * f + A2.x * f2, A.y * f + A2.y * f2, A.z * f + A2.z * f2, A.w * f + A2.w * f2);
     M = Mn;
   };
   if constexpr (SUB == 2) {
     const float M2 = __shfl_xor_sync(0xffffffffu, M, 16), L2 = __shfl_xor_sync(0xffffffffu, L, 16);
     const float4 A2 = make_float4(__shfl_xor_sync(0xffffffffu, A.x, 16), __shfl_xor_sync(0xffffffffu, A.y, 16),
                                   __shfl_xor_sync(0xffffffffu, A.z, 16), __shfl_xor_sync(0xffffffffu, A.w, 16));
-    if (lane < 16) join(M2, L2, A2);
+    join(M2, L2, A2);   // both halves of the warp hold the same
   }
   if constexpr (WPR > 1) {
     if (lane < LPR) {
-      *reinterpret_cast<float2*>(&part[w][ch]) = make_float2(A.x, A.y);
-      *reinterpret_cast<float2*>(&part[w][ch + 2]) = make_float2(A.z, A.w);
+      *reinterpret_cast<float4*>(&part[w][ch]) = A;
       if (lane == 0) {
         part[w][D] = M;
         part[w][D + 1] = L;
       }
     }
     __syncthreads();
-    if (w != 0 || lane >= LPR) return;
-#pragma unroll
-    for (int o = 1; o < WPR; ++o)
-      join(part[o][D], part[o][D + 1],
-           make_float4(part[o][ch], part[o][ch + 1], part[o][ch + 2], part[o][ch + 3]));
+    if (w != 0) return;
+#pragma unroll 1
+    for (int o = 1; o < WPR; ++o) join(part[o][D], part[o][D + 1], *reinterpret_cast<const float4*>(&part[o][ch]));
   }
   if (lane >= LPR) return;
   // no token at all: zeros (L is 0 only then; a NaN stays one)

@@ -39,7 +39,7 @@ struct Work {
 Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
   const size_t rows = 4 * (size_t)batch * hq + (size_t)ctas * 2 * kTile;
   Work w;
-  w.ml = align256((size_t)batch * 3 * sizeof(int4));
+  w.ml = align256((size_t)batch * c->num_kv_heads * 3 * sizeof(int4));
   w.acc = w.ml + align256(rows * sizeof(float2));
   w.total = w.acc + align256(rows * c->head_dim * sizeof(float)) + 256;
   return w;
@@ -108,7 +108,7 @@ pkv_status launch_shared(const SharedArgs& a) {
   // visits are counted in 32 bits: rows and prefixes at the table's full width
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   if (c->num_kv_heads * tiles * (2ll * a.batch + (long long)a.batch * group / (2 * kTile)) >= (1ll << 31) ||
-      2ll * a.batch * a.num_q_heads >= (1ll << 29))
+      (4ll * a.batch * a.num_q_heads + 512ll * a.num_splits) * D >= (1ll << 31))
     return PKV_ERR_UNSUPPORTED;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
   const Work w = layout(c, a.batch, a.num_q_heads, ctas);
@@ -168,12 +168,12 @@ pkv_status launch_shared(const SharedArgs& a) {
   p.scale = a.sm_scale * 1.4426950408889634f;
   void* args[] = {&p};
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
-  const int rows = a.batch * a.num_q_heads;
+  const long long outs = (long long)a.batch * a.num_q_heads * D, units = (outs + 127) / 128;
   // few rows have many records each
-  const int wpr = rows < 16 * dev.sms ? 4 : 1;
-  const void* merge = D == 64 ? merge_kernel<64>(wpr) : merge_kernel<128>(wpr);
-  const int per = 4 / wpr;
-  return launch_pdl(merge, dim3((rows + per - 1) / per), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
+  const int wpw = units < 16 * dev.sms ? 4 : 1;
+  const void* merge = D == 64 ? merge_kernel<64>(wpw) : merge_kernel<128>(wpw);
+  const int per = 4 / wpw;
+  return launch_pdl(merge, dim3((unsigned)((units + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

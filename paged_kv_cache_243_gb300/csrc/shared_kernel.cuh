@@ -86,7 +86,7 @@ struct SharedParams {
   // workspace: (m, l) and accumulators by record row, and each row's place in the plan
   float2* ws_ml;
   float* ws_acc;
-  int4* ws_info;   // three a row
+  int4* ws_info;   // three for each row and kv head
   int num_pages, page_size, num_kv_heads, num_q_heads, group, batch, max_pages, num_groups;
   int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms;
   float scale;   // sm_scale * log2(e)
@@ -516,6 +516,13 @@ __device__ __forceinline__ float scatter_sum8(float* v, int lane, int& j) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
+// 32 bytes, aligned: a whole sector (each lane of the record stores has a row of its own)
+__device__ __forceinline__ void store32(float* dst, const float (&f)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -727,20 +734,38 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   __syncthreads();
   const Shares shares(all.y, all.y + all.z + all.w, p.num_ctas);
 #pragma unroll 1
-  for (int b = tid; b < B; b += NT) {
-    const int g = rowg[b];
-    if (g >= 0) members[moff[g] + rank[b]] = (uint16_t)b;
-    if (b % (int)gridDim.x == (int)blockIdx.x) {   // for the merge: where row b's segments are
-      int4 pre = make_int4(0, 0, 0, 0);
-      int rows = 0;
-      if (g >= 0) {
-        rows = (moff[g + 1] - moff[g]) * Gq;
-        pre = make_int4(moff[g] * Gq, rank[b] * Gq, rows > kTile ? gpre[g] : lpre[g], tiles_of(gp[g]));
+  for (int b = tid; b < B; b += NT)
+    if (rowg[b] >= 0) members[moff[rowg[b]] + rank[b]] = (uint16_t)b;
+  // for the merge: where the records of row b's heads are (this block's share of them)
+#pragma unroll 1
+  for (int i = blockIdx.x + gridDim.x * tid; i < B * p.num_kv_heads; i += gridDim.x * NT) {
+    const int b = i / p.num_kv_heads, h = i - b * p.num_kv_heads, g = rowg[b];
+    const int whole = 2 * B * p.num_q_heads;
+    // a segment's visits [x, x + n), its rows from query row `row` of its record rows `rec` on
+    auto place = [&](int x, uint32_t n, int rec, int row, bool few) {
+      const int c = shares.block_of(x);
+      return make_int4(rec, 2 * whole + (c + 1) * 2 * kTile + row, shares.block_of(x + n - 1) - c + 1, few);
+    };
+    int4 own = make_int4(0, 0, 0, 0), pre = own, pre2 = own;
+    uint32_t n = tiles_of(lens[b] - skip[b]);
+    if (n > 0)
+      own = place(bpre[b] + h * n, n, ((p.num_kv_heads + h) * B + b) * Gq, 0, Gq <= kFew);
+    if (g >= 0) {
+      const int rows = (moff[g + 1] - moff[g]) * Gq, R = rank[b] * Gq, pairs = (uint32_t)(rows + 2 * kTile - 1) / (2 * kTile);
+      const int rec = h * B * Gq + moff[g] * Gq + R;
+      n = tiles_of(gp[g]);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {   // a row's heads may lie in two pairs of row tiles
+        const int pair = (uint32_t)(R + k * (Gq - 1)) / (2 * kTile);
+        pre2 = place((rows > kTile ? gpre : lpre)[g] + (h * pairs + pair) * n, n, rec, R - pair * 2 * kTile,
+                     rows - pair * 2 * kTile <= kFew);
+        if (k == 0) pre = pre2;
       }
-      p.ws_info[3 * b] = pre;
-      p.ws_info[3 * b + 1] = make_int4(rows, bpre[b], tiles_of(lens[b] - skip[b]), 0);
-      p.ws_info[3 * b + 2] = make_int4(shares.heavy, shares.blocks, shares.q, shares.r);
+      pre.w |= (2 * kTile - R % (2 * kTile)) << 1;   // the head from which on the second holds
     }
+    p.ws_info[3 * i] = own;
+    p.ws_info[3 * i + 1] = pre;
+    p.ws_info[3 * i + 2] = pre2;
   }
   const bool idle = (int)blockIdx.x >= shares.blocks || all.y + all.z + all.w == 0;
   const int lo = idle ? 0 : shares.first(blockIdx.x), hi = idle ? 0 : shares.first(blockIdx.x + 1);
@@ -1479,15 +1504,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           tc_wait_ld();
           if (row < my_rows) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              float f[4];
+            for (int j = 0; j < 16; j += 8) {
+              float f[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int k = 0; k < 8; ++k) {
                 f[k] = __uint_as_float(o[j + k]) * f0;
                 if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k]);
                 if constexpr (QUANT) f[k] += z;
               }
-              *reinterpret_cast<float4*>(acc + c + j) = make_float4(f[0], f[1], f[2], f[3]);
+              store32(acc + c + j, f);
             }
           }
         }
@@ -1508,118 +1533,93 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ the merge
-// Folds a query row's records, from the blocks of its prefix segment and of its own
-// tokens: WPR warps per row, each lane 4 channels of every WPR-th record (two records
-// at a time at 64 channels). Small code: every call fetches it anew.
+// Folds the records of 128 outputs (a query row, or two of 64 channels), from the
+// blocks of its prefix segment and of its own tokens: WPW warps each take every WPW-th
+// record, a lane 4 channels. Where the records are has been worked out by the
+// attention kernel: this kernel is short, as its code is fetched anew by every call.
 constexpr int kMergeThreads = 128;
 
-template <int D, int WPR>
+template <int D, int WPW>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int LPR = D / 4, SUB = 32 / LPR;       // lanes per record, records side by side in a warp
-  constexpr int STREAMS = WPR * SUB, BATCH = 8;
-  __shared__ float part[WPR][D + 4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.x * (4 / WPR) + warp / WPR, w = warp % WPR;
+  constexpr int BATCH = 4;
+  __shared__ float4 part_a[WPW > 1 ? WPW : 1][32];
+  __shared__ float2 part_ml[WPW > 1 ? WPW : 1][32];
+  const int lane = threadIdx.x & 31, w = WPW > 1 ? threadIdx.x >> 5 : 0;
+  const int at = ((int)blockIdx.x * (4 / WPW) + (WPW > 1 ? 0 : (int)threadIdx.x >> 5)) * 128 + lane * 4;   // output
+  const int item = at / D;   // row and query head
   pdl_wait();
-  if (item >= p.batch * p.num_q_heads) return;   // uniform over a row's warps
-  const int b = item / p.num_q_heads, hq = item - b * p.num_q_heads;
-  const int h = hq / p.group, gq = hq - h * p.group;
-  const int4 i0 = __ldcg(p.ws_info + 3 * b), i1 = __ldcg(p.ws_info + 3 * b + 1), i2 = __ldcg(p.ws_info + 3 * b + 2);
-  Shares sh;
-  sh.heavy = i2.x;
-  sh.blocks = i2.y;
-  sh.q = i2.z;
-  sh.r = i2.w;
-  const int whole = 2 * p.batch * p.num_q_heads;   // record rows of segments by stream
-  // records of the prefix, then of the row's own tokens; a segment of few rows has
-  // one of each stream, and a block's first part, if it continues a
-  // segment, has its place by block
-  int n0 = 0, n1 = 0, c0 = 0, c1 = 0;
-  const int R = i0.y + gq, pair = R / (2 * kTile), pairs = (i1.x + 2 * kTile - 1) / (2 * kTile);
-  const int few0 = i1.x - pair * 2 * kTile <= kFew, few1 = p.group <= kFew;
-  if (i0.w > 0) {
-    const int x = i0.z + (h * pairs + pair) * i0.w;
-    c0 = sh.block_of(x);
-    n0 = (sh.block_of(x + i0.w - 1) - c0 + 1) << few0;
-  }
-  if (i1.z > 0) {
-    const int x = i1.y + h * i1.z;
-    c1 = sh.block_of(x);
-    n1 = (sh.block_of(x + i1.z - 1) - c1 + 1) << few1;
-  }
-  const int r0 = h * p.batch * p.group + i0.x + R, r1 = ((p.num_kv_heads + h) * p.batch + b) * p.group + gq;
-  const int ch = (lane % LPR) * 4;
+  if (at >= p.batch * p.num_q_heads * D) return;
+  const int kvi = item / p.group, gq = item - kvi * p.group;   // row and kv head
+  const int4 own = __ldcg(p.ws_info + 3 * kvi);
+  int4 pre = __ldcg(p.ws_info + 3 * kvi + 1);
+  const int4 pre2 = __ldcg(p.ws_info + 3 * kvi + 2);
+  if (gq >= pre.w >> 1) pre = pre2;   // in the next pair of row tiles
+  pre.w &= 1;
+  const int ch = at % D, whole = 2 * p.batch * p.num_q_heads;
+  const int n0 = pre.z << pre.w, n1 = own.z << own.w;
   float M = -INFINITY, L = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int j0 = w * SUB + lane / LPR; j0 < n0 + n1; j0 += STREAMS * BATCH) {
+  for (int j0 = w; j0 < n0 + n1; j0 += WPW * BATCH) {
     float2 ml[BATCH];
     float4 a[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      int j = j0 + i * STREAMS;
-      const bool on = j < n0 + n1, own = j >= n0;
-      j -= own ? n0 : 0;
-      const int few = own ? few1 : few0, st = j & few, k = j >> few;
-      const size_t r = !on      ? 0
-                       : k == 0 ? (size_t)st * whole + (own ? r1 : r0)
-                                : 2 * (size_t)whole + (size_t)((own ? c1 : c0) + k) * (2 * kTile) + st * kTile +
-                                      (own ? gq : R % (2 * kTile));
-      ml[i] = on ? __ldcg(p.ws_ml + r) : make_float2(-INFINITY, 0.f);
-      a[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + r * D + ch));
+      int j = j0 + i * WPW;
+      const bool on = j < n0 + n1;
+      int4 seg = pre;
+      if (j >= n0) {
+        seg = own;
+        j -= n0;
+      }
+      // stream and part; a block's first part, where it continues the segment,
+      // has its place by block
+      const int st = j & seg.w, k = j >> seg.w;
+      int r = k == 0 ? seg.x + st * whole : seg.y + (k - 1) * 2 * kTile + st * kTile;
+      r = on ? r + gq : 0;
+      ml[i] = __ldcg(p.ws_ml + r);
+      if (!on) ml[i].x = -INFINITY;
+      a[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (size_t)r * D + ch));
     }
     float Mn = M;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i].x);
-    const float Mr = Mn == -INFINITY ? 0.f : Mn, f0 = exp2f(M - Mr);
+    const float Mr = Mn == -INFINITY ? 0.f : Mn, f0 = fast_exp2(M - Mr);
     M = Mn;
     L *= f0;
     A = make_float4(A.x * f0, A.y * f0, A.z * f0, A.w * f0);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       if (ml[i].x == -INFINITY) continue;   // no token: its accumulator means nothing
-      const float f = exp2f(ml[i].x - Mr);
+      const float f = fast_exp2(ml[i].x - Mr);
       L = fmaf(f, ml[i].y, L);
       A = make_float4(fmaf(f, a[i].x, A.x), fmaf(f, a[i].y, A.y), fmaf(f, a[i].z, A.z), fmaf(f, a[i].w, A.w));
     }
   }
-  auto join = [&](float M2, float L2, float4 A2) {
-    const float Mn = fmaxf(M, M2), Mr = Mn == -INFINITY ? 0.f : Mn;
-    const float f = exp2f(M - Mr), f2 = exp2f(M2 - Mr);
-    L = L * f + L2 * f2;
-    A = make_float4(A.x * f + A2.x * f2, A.y * f + A2.y * f2, A.z * f + A2.z * f2, A.w * f + A2.w * f2);
-    M = Mn;
-  };
-  if constexpr (SUB == 2) {
-    const float M2 = __shfl_xor_sync(0xffffffffu, M, 16), L2 = __shfl_xor_sync(0xffffffffu, L, 16);
-    const float4 A2 = make_float4(__shfl_xor_sync(0xffffffffu, A.x, 16), __shfl_xor_sync(0xffffffffu, A.y, 16),
-                                  __shfl_xor_sync(0xffffffffu, A.z, 16), __shfl_xor_sync(0xffffffffu, A.w, 16));
-    join(M2, L2, A2);   // both halves of the warp hold the same
-  }
-  if constexpr (WPR > 1) {
-    if (lane < LPR) {
-      *reinterpret_cast<float4*>(&part[w][ch]) = A;
-      if (lane == 0) {
-        part[w][D] = M;
-        part[w][D + 1] = L;
-      }
-    }
+  if constexpr (WPW > 1) {
+    part_a[w][lane] = A;
+    part_ml[w][lane] = make_float2(M, L);
     __syncthreads();
     if (w != 0) return;
 #pragma unroll 1
-    for (int o = 1; o < WPR; ++o) join(part[o][D], part[o][D + 1], *reinterpret_cast<const float4*>(&part[o][ch]));
+    for (int o = 1; o < WPW; ++o) {
+      const float2 ml = part_ml[o][lane];
+      const float4 a = part_a[o][lane];
+      const float Mn = fmaxf(M, ml.x), Mr = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M - Mr), f2 = fast_exp2(ml.x - Mr);
+      L = L * f + ml.y * f2;
+      A = make_float4(A.x * f + a.x * f2, A.y * f + a.y * f2, A.z * f + a.z * f2, A.w * f + a.w * f2);
+      M = Mn;
+    }
   }
-  if (lane >= LPR) return;
   // no token at all: zeros (L is 0 only then; a NaN stays one)
   const float r = L == 0.f ? 0.f : 1.f / L;
-  const size_t o = (size_t)item * D + ch;
   const float4 f = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
   if (p.out_dtype == PKV_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = f;
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = f;
   } else {
     const uint2 v = p.out_dtype == PKV_BF16 ? make_uint2(pack16<true>(f.x, f.y), pack16<true>(f.z, f.w))
                                             : make_uint2(pack16<false>(f.x, f.y), pack16<false>(f.z, f.w));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) = v;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = v;
   }
 }
 

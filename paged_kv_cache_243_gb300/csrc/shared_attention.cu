@@ -71,12 +71,13 @@ bool pool_map(void* base, uint64_t rows, int d, bool bf, CUtensorMap& m) {
 }
 
 template <int D, int KV>
-void sizes(int& threads, int& smem, int& entries, int avail, int batch, int groups) {
+void sizes(int& threads, int& smem, int& entries, SharedLayout& lay, int avail, int batch, int groups) {
   using G = SharedGeom<D, KV, true>;   // operand types have the same sizes
   threads = G::THREADS;
   entries = kMaxEntries;
   while (entries > 1 && 1024 + shared_layout<G>(entries, batch, groups).total > avail) --entries;
-  smem = 1024 + shared_layout<G>(entries, batch, groups).total;
+  lay = shared_layout<G>(entries, batch, groups);
+  smem = 1024 + lay.total;
 }
 
 template <int D>
@@ -124,7 +125,7 @@ pkv_status launch_shared(const SharedArgs& a) {
                                      : shared_kernel_u4t(D, bf);
   int threads = 0, smem = 0, entries = 0;
 #define PKV_SIZES(d, kv) \
-  if (D == d && kind == kv) sizes<d, kv>(threads, smem, entries, dev.smem, a.batch, a.num_groups);
+  if (D == d && kind == kv) sizes<d, kv>(threads, smem, entries, p.lay, dev.smem, a.batch, a.num_groups);
   PKV_SIZES(64, KV_F16) PKV_SIZES(64, KV_BF16) PKV_SIZES(64, KV_I8T) PKV_SIZES(64, KV_I8G) PKV_SIZES(64, KV_U4T)
   PKV_SIZES(128, KV_F16) PKV_SIZES(128, KV_BF16) PKV_SIZES(128, KV_I8T) PKV_SIZES(128, KV_I8G) PKV_SIZES(128, KV_U4T)
 #undef PKV_SIZES

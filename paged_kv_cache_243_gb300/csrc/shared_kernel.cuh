@@ -63,14 +63,24 @@ struct RingPos {
 };
 
 constexpr int kTile = 128;        // tokens of a visit, query rows of a tile
-constexpr int kHdrs = 8;          // visit headers kept (more than the visits the ring holds)
-constexpr int kScaleSlots = 4;    // visits whose scales are kept for the softmax
+// Visit headers kept. The K loader writes header v once entry v - S is free, i.e. its codes are
+// converted; then the scores of v - S - 1 are done, and with them the softmax of
+// v - S - 3 (16-bit caches: one visit later in each step). kMaxEntries + 3 are in use.
+constexpr int kHdrs = 16;
+// Visits whose scales are kept: written for v once the scores of v - 1, and so the
+// softmax of v - 3, are done.
+constexpr int kScaleSlots = 4;
 constexpr int kQSums = 8;
-constexpr int kMaxEntries = 6;    // ring entries of K, and of V: at most kHdrs - 2
+constexpr int kMaxEntries = 6;    // ring entries of K, and of V
 constexpr int kVisits = 128;      // visits described in shared memory, refilled by halves
 constexpr int kFew = 16;          // segments of at most this many query rows run transposed
 constexpr int kPtBytes = 8192;    // transposed weights of a stream: 16 rows, two terms each
 
+// Shared memory by offset from a 1024-byte boundary.
+struct SharedLayout {
+  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, visits, bpre, gpre, lpre, moff, members, lens, skip, gp, rank, rowg;
+  int total;
+};
 struct SharedParams {
   CUtensorMap tmap_k, tmap_v;   // 16-bit pools as [rows][d], boxes of 16 rows x 64 channels
   const uint8_t* k_pages;
@@ -90,6 +100,7 @@ struct SharedParams {
   int num_pages, page_size, num_kv_heads, num_q_heads, group, batch, max_pages, num_groups;
   int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms;
   float scale;   // sm_scale * log2(e)
+  SharedLayout lay;
 };
 
 template <int D, int KV, bool BF>
@@ -101,15 +112,10 @@ struct SharedGeom {
   static constexpr int ENTRY = QUANT ? kTile * ROW : OPERAND;
   static constexpr int RAW_SCALES = QUANT ? (KV == KV_I8G ? 128 : kTile * 16) : 0;
   static constexpr int SCALES = QUANT ? 4 * kTile * 4 : 0;   // ks, kz', vs, vz' of a visit
-  static constexpr int THREADS = QUANT ? 512 : 384;
+  static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr float CENTRE = KV == KV_U4T ? 8.f : 128.f;
 };
 
-// Shared memory by offset from a 1024-byte boundary.
-struct SharedLayout {
-  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, visits, bpre, gpre, lpre, moff, members, lens, skip, gp, rank, rowg;
-  int total;
-};
 enum SharedBars {   // mbarriers, 8 bytes each
   kBarKFull = 0, kBarVFull = kMaxEntries, kBarKEmpty = 2 * kMaxEntries, kBarVEmpty = 3 * kMaxEntries,
   kBarHdr = 4 * kMaxEntries, kBarQFull = kBarHdr + kHdrs, kBarQEmpty = kBarQFull + 2, kBarS = kBarQEmpty + 2,
@@ -603,10 +609,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
   using G = SharedGeom<D, KV, BF>;
   constexpr bool QUANT = G::QUANT;
-  constexpr int NT = G::THREADS;
+  constexpr int NT = G::THREADS, COLS = QUANT ? 32 : 64;   // columns of a pass over the scores
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const SharedLayout lay = shared_layout<G>(p.entries, p.batch, p.num_groups);
+  const SharedLayout& lay = p.lay;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bars = smem_u32(smem + lay.bars);
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     for (int i = 0; i < 4; ++i) mbar_init(bar(kBarPair + i), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarVisits + i), 1);
-      mbar_init(bar(kBarPassed + i), QUANT ? 15 : 11);   // loaders, MMA, softmax, converters
+      mbar_init(bar(kBarPassed + i), QUANT ? 19 : 11);   // loaders, MMA, softmax, converters
     }
     mbar_init(bar(kBarEnd), 1);
     misc[1] = 0;
@@ -1067,43 +1073,41 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       }
     }
   } else if (warp >= 12) {
-    // ============================================================ converters
+    // ============================ converters: K (12-15) and V (16-19)
     if constexpr (QUANT) {
-      const int t = tid - 384;
+      const int t = tid & 127;
+      const bool isv = warp >= 16;
+      const int fulls = isv ? kBarVFull : kBarKFull, empties = isv ? kBarVEmpty : kBarKEmpty;
+      const int ops = isv ? kBarVop : kBarKop;
+      const uint8_t* ring = smem + lay.ring + (isv ? (size_t)S * G::ENTRY : 0);
+      uint8_t* op = smem + (isv ? lay.vop : lay.kop);
       RingPos pos;
       for (int v = 0; v < nv; ++v, pos.next(S)) {
         const int slot = pos.slot;
-        const uint32_t phase = pos.phase;
-        if (!wait_warp(kBarKFull + slot, phase)) break;
-        if (v > 0 && !wait_warp(kBarKop + 1, (v - 1) & 1)) break;   // the previous visit's scores are done
-        convert_tile<D, KV, BF>(smem + lay.ring + (size_t)slot * G::ENTRY, smem + lay.kop, t);
-        // scales of token t, with the middle code's part in the zero points
-        const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
-        const bool valid = t < hd.x && (hd.y >> (t >> 4) & 1);
-        const float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)slot * G::RAW_SCALES +
-                                                          (KV == KV_I8G ? t >> 6 : t) * 16);
-        float* sc = reinterpret_cast<float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
-        sc[t] = valid ? z.x : 0.f;
-        sc[kTile + t] = valid ? fmaf(G::CENTRE, z.x, z.y) : 0.f;
-        sc[2 * kTile + t] = valid ? z.z : 0.f;
-        sc[3 * kTile + t] = valid ? fmaf(G::CENTRE, z.z, z.w) : 0.f;
-        const float vm = warp_max(valid ? z.z : 0.f);
-        if (lane == 0) reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 16)[warp - 12] = vm;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kBarKop));
-          mbar_arrive(bar(kBarHdr + v % kHdrs));
-          mbar_arrive(bar(kBarKEmpty + slot));
+        if (!wait_warp(fulls + slot, pos.phase)) break;
+        // the products with the previous visit's tile are done
+        if (v > 0 && !wait_warp(ops + 1, (v - 1) & 1)) break;
+        convert_tile<D, KV, BF>(ring + (size_t)slot * G::ENTRY, op, t);
+        if (!isv) {
+          // scales of token t, with the middle code's part in the zero points
+          const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
+          const bool valid = t < hd.x && (hd.y >> (t >> 4) & 1);
+          const float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)slot * G::RAW_SCALES +
+                                                            (KV == KV_I8G ? t >> 6 : t) * 16);
+          float* sc = reinterpret_cast<float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
+          sc[t] = valid ? z.x : 0.f;
+          sc[kTile + t] = valid ? fmaf(G::CENTRE, z.x, z.y) : 0.f;
+          sc[2 * kTile + t] = valid ? z.z : 0.f;
+          sc[3 * kTile + t] = valid ? fmaf(G::CENTRE, z.z, z.w) : 0.f;
+          const float vm = warp_max(valid ? z.z : 0.f);
+          if (lane == 0) reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 16)[warp - 12] = vm;
         }
-        if (!wait_warp(kBarVFull + slot, phase)) break;
-        if (v > 0 && !wait_warp(kBarVop + 1, (v - 1) & 1)) break;
-        convert_tile<D, KV, BF>(smem + lay.ring + (size_t)(S + slot) * G::ENTRY, smem + lay.vop, t);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(kBarVop));
-          mbar_arrive(bar(kBarVEmpty + slot));
+          mbar_arrive(bar(ops));
+          if (!isv) mbar_arrive(bar(kBarHdr + v % kHdrs));
+          mbar_arrive(bar(empties + slot));
         }
         passed(v);
       }
@@ -1290,7 +1294,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             *reinterpret_cast<uint4*>(pt + (kFew + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
           }
         } else if (active) {
-          // ---- thread = query row. Scores are read twice, 64 columns at a time in loops
+          // ---- thread = query row. Scores are read twice, COLS columns at a time in loops
           // that stay loops: with all 128 in registers and the code unrolled, the
           // warps waited for instructions.
           if constexpr (QUANT) {
@@ -1332,15 +1336,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           }
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < ntok; c += 64) {
-            float a[64];
+          for (int c = 0; c < ntok; c += COLS) {
+            float a[COLS];
             tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
-            tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
+            if constexpr (COLS == 64) tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
             tc_wait_ld();
             float m4[4] = {mx, a[0], a[1], a[2]};
 #pragma unroll
-            for (int j = 3; j < 63; j += 2) m4[j >> 1 & 3] = max3(m4[j >> 1 & 3], a[j], a[j + 1]);
-            mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[63]);
+            for (int j = 3; j < COLS - 1; j += 2) m4[j >> 1 & 3] = max3(m4[j >> 1 & 3], a[j], a[j + 1]);
+            mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[COLS - 1]);
           }
           const float mt = mx * p.scale;
           float alpha = fv;
@@ -1367,13 +1371,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           const uint64_t sc2 = pack2f(p.scale, p.scale), mr2 = pack2f(-mref, -mref);
           uint64_t ls0 = 0, ls1 = 0, z2 = 0;
 #pragma unroll 1
-          for (int c = 0; c < ntok; c += 64) {
-            float a[64];
+          for (int c = 0; c < ntok; c += COLS) {
+            float a[COLS];
             tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
-            tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
+            if constexpr (COLS == 64) tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
+            for (int j = 0; j < COLS; j += 2) {
               float x, y;
               unpack2f(ffma2(pack2f(a[j], a[j + 1]), sc2, mr2), x, y);
               a[j] = fast_exp2(x);
@@ -1383,7 +1387,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             if constexpr (QUANT) {
               const uint64_t rv2 = pack2f(rv, rv);
 #pragma unroll
-              for (int j = 0; j < 64; j += 4) {
+              for (int j = 0; j < COLS; j += 4) {
                 const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + c + j);
                 const ulonglong2 vz = *reinterpret_cast<const ulonglong2*>(sc + 3 * kTile + c + j);
                 z2 = ffma2(pack2f(a[j], a[j + 1]), vz.x, z2);
@@ -1396,7 +1400,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             // place of their scores: 16 columns for 32 tokens, and 16 more of second
             // terms, which hold what the rounding left, where the output keeps more bits.
 #pragma unroll
-            for (int e = 0; e < 64; e += 32) {
+            for (int e = 0; e < COLS; e += 32) {
               uint32_t w[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) w[j] = pack16<BF>(a[e + 2 * j], a[e + 2 * j + 1]);

@@ -146,7 +146,7 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.ml = put(2 * kTile * 16);
   o.qsum = put(G::QUANT ? kQSums * kTile * 4 : 0);
   o.vmax = put(G::QUANT ? kScaleSlots * 16 : 0);
-  o.misc = put(17 * 16);
+  o.misc = put(21 * 16);
   o.visits = put(kVisits * 32);
   o.bpre = put((batch + 1) * 4);
   o.gpre = put((groups + 1) * 4);
@@ -343,10 +343,10 @@ __device__ __forceinline__ int upper(const int* pre, int n, int x) {   // larges
 struct RowPlan {
   int len, skip, group, bad;
 };
-__device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int b) {
+template <class F>
+__device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int L, int g, F&& prefix_len) {
   RowPlan r;
   const long long cap = (long long)p.max_pages * p.page_size;
-  int L = p.seq_lens[b], g = p.prefix_group[b];
   r.bad = 0;
   if (L < 0 || L > cap) {
     r.bad |= PKV_DEV_BAD_POSITION;
@@ -356,7 +356,7 @@ __device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int b) {
     r.bad |= PKV_DEV_BAD_GROUP;
     g = -1;
   }
-  const int P = g >= 0 ? p.prefix_lens[g] : 0;
+  const int P = prefix_len(g);   // 0 for -1
   if (P < p.round_to || L < P) g = -1;
   r.len = L;
   r.group = g;
@@ -389,7 +389,7 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
       first_tok = pl.skip[b];
       end_tok = pl.lens[b];
     } else {
-      const RowPlan r = row_plan(p, b);
+      const RowPlan r = row_plan(p, p.seq_lens[b], p.prefix_group[b], [&](int g) { return g < 0 ? 0 : p.prefix_lens[g]; });
       first_tok = r.skip;
       end_tok = r.len;
     }
@@ -416,7 +416,7 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
 __device__ __forceinline__ int4 block_scan4(int4& x, int threads, int4* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int4 i = x;
-#pragma unroll 1
+#pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int4 y = make_int4(__shfl_up_sync(0xffffffffu, i.x, off), __shfl_up_sync(0xffffffffu, i.y, off),
                              __shfl_up_sync(0xffffffffu, i.z, off), __shfl_up_sync(0xffffffffu, i.w, off));
@@ -424,15 +424,11 @@ __device__ __forceinline__ int4 block_scan4(int4& x, int threads, int4* scratch)
   }
   if (lane == 31) scratch[warp] = i;
   __syncthreads();
-  x = make_int4(i.x - x.x, i.y - x.y, i.z - x.z, i.w - x.w);
-  int4 t = make_int4(0, 0, 0, 0);
-#pragma unroll 1
-  for (int w = 0; w < threads / 32; ++w) {
-    const int4 y = scratch[w];
-    if (w == warp) x = make_int4(x.x + t.x, x.y + t.y, x.z + t.z, x.w + t.w);
-    t = make_int4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
-  }
-  return t;
+  const int4 t = lane < threads / 32 ? scratch[lane] : make_int4(0, 0, 0, 0);
+  const int4 b = lane < warp ? t : make_int4(0, 0, 0, 0);
+  auto sum = [](int v) { return (int)__reduce_add_sync(0xffffffffu, v); };
+  x = make_int4(i.x - x.x + sum(b.x), i.y - x.y + sum(b.y), i.z - x.z + sum(b.z), i.w - x.w + sum(b.w));
+  return make_int4(sum(t.x), sum(t.y), sum(t.z), sum(t.w));
 }
 
 // --------------------------------------------------------------- code -> value
@@ -522,13 +518,6 @@ __device__ __forceinline__ float scatter_sum8(float* v, int lane, int& j) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// 32 bytes, aligned: a whole sector (each lane of the record stores has a row of its own)
-__device__ __forceinline__ void store32(float* dst, const float (&f)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(f[0]), "f"(f[1]), "f"(f[2]),
-               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-               : "memory");
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -539,6 +528,17 @@ __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Rest of a whole warp's bounded wait; the first warp to give up reports it
@@ -566,6 +566,16 @@ static __device__ __noinline__ void gather_queries(const SharedParams& p, const 
   constexpr int CH = D / 8, RPI = 32 / CH;   // 16-byte pieces of a row, rows an instruction
   const int lane = threadIdx.x & 31;
   const int rows = min(kTile, s.rows - u * kTile);
+  if (s.mem0 < 0) {   // one row's heads: its queries lie together
+    const uint8_t* src = p.q + ((size_t)s.row * p.num_q_heads + s.head * p.group) * D * 2;
+#pragma unroll 2
+    for (int i = 32 * w + lane; i < rows * CH; i += 32 * warps) {
+      const int r = i / CH, c = i % CH;
+      cp_async16(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (size_t)i * 16);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   for (int r0 = 32 * w; r0 < rows; r0 += 32 * warps) {
     // lane i finds row r0 + i
     const int R = s.q0 + u * kTile + r0 + lane;
@@ -577,8 +587,9 @@ static __device__ __noinline__ void gather_queries(const SharedParams& p, const 
     }
     const int qrow = b * p.num_q_heads + s.head * p.group + gq;
     const int n = min(32, rows - r0), c = lane % CH;
-#pragma unroll 2
-    for (int i = 0; i < n; i += RPI) {
+#pragma unroll 8
+    for (int i = 0; i < 32; i += RPI) {
+      if (i >= n) break;
       const int r = i + lane / CH;
       const int from = __shfl_sync(0xffffffffu, qrow, r & 31);
       if (r < n)
@@ -601,6 +612,49 @@ static __device__ __noinline__ void sum_queries(const uint8_t* src, float* qsum,
            ((low16<BF>(w.z) + high16<BF>(w.z)) + (low16<BF>(w.w) + high16<BF>(w.w)));
     }
     qsum[r] = t;
+  }
+}
+
+// For the merge: where the records of the rows' kv heads are (the block's share of
+// them), from the plan and the inputs; one warp.
+static __device__ __noinline__ void place_records(const SharedParams& p, const SharedPlan& pl) {
+  const int lane = threadIdx.x & 31, Gq = p.group, B = p.batch, whole = 2 * B * p.num_q_heads;
+  const Shares shares(pl.gpre[p.num_groups], pl.bpre[B], p.num_ctas);
+#pragma unroll 1
+  for (int i = blockIdx.x + gridDim.x * lane; i < B * p.num_kv_heads; i += gridDim.x * 32) {
+    const int b = i / p.num_kv_heads, h = i - b * p.num_kv_heads;
+    const RowPlan r = row_plan(p, p.seq_lens[b], p.prefix_group[b], [&](int g) { return g < 0 ? 0 : p.prefix_lens[g]; });
+    auto tiles_of = [](int tokens) { return (uint32_t)(tokens + kTile - 1) / kTile; };
+    // a segment's visits [x, x + n), its rows from query row `row` of its record rows `rec` on
+    auto place = [&](int x, uint32_t n, int rec, int row, bool few) {
+      const int c = shares.block_of(x);
+      return make_int4(rec, 2 * whole + (c + 1) * 2 * kTile + row, shares.block_of(x + n - 1) - c + 1, few);
+    };
+    int4 own = make_int4(0, 0, 0, 0), pre = own, pre2 = own;
+    uint32_t n = tiles_of(r.len - r.skip);
+    if (n > 0) own = place(pl.bpre[b] + h * n, n, ((p.num_kv_heads + h) * B + b) * Gq, 0, Gq <= kFew);
+    if (r.group >= 0) {
+      const int g = r.group, m0 = pl.moff[g], m1 = pl.moff[g + 1], rows = (m1 - m0) * Gq;
+      int lo = m0, hi = m1;   // the row among the members, which are in ascending order
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pl.members[mid] <= b) lo = mid;
+        else hi = mid;
+      }
+      const int R = (lo - m0) * Gq, pairs = (uint32_t)(rows + 2 * kTile - 1) / (2 * kTile);
+      n = tiles_of(r.skip);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {   // a row's heads may lie in two pairs of row tiles
+        const int pair = (uint32_t)(R + k * (Gq - 1)) / (2 * kTile);
+        pre2 = place((rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, n, h * B * Gq + m0 * Gq + R,
+                     R - pair * 2 * kTile, rows - pair * 2 * kTile <= kFew);
+        if (k == 0) pre = pre2;
+      }
+      pre.w |= (2 * kTile - R % (2 * kTile)) << 1;   // the head from which on the second holds
+    }
+    p.ws_info[3 * i] = own;
+    p.ws_info[3 * i + 1] = pre;
+    p.ws_info[3 * i + 2] = pre2;
   }
 }
 
@@ -670,19 +724,26 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 
   // ---- plan: lengths, who shares, visits before each segment. (Its loops stay
   // loops: this code is fetched anew by every call.)
+  const int lens32 = lane < NG ? p.prefix_lens[lane] : 0;   // of the first 32 groups
 #pragma unroll 1
-  for (int g = tid; g < NG; g += NT) {
-    const int P = p.prefix_lens[g];
-    if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
-    gp[g] = max(P, 0) & -p.round_to;
-  }
-#pragma unroll 1
-  for (int b = tid; b < B; b += NT) {
-    const RowPlan r = row_plan(p, b);
+  for (int b0 = warp * 32; b0 < B; b0 += NT) {
+    const int b = b0 + lane;
+    const RowPlan r = row_plan(p, b < B ? p.seq_lens[b] : 0, b < B ? p.prefix_group[b] : -1, [&](int g) {
+      if (NG > 32) return g < 0 ? 0 : p.prefix_lens[g];
+      const int P = __shfl_sync(0xffffffffu, lens32, g & 31);
+      return g < 0 ? 0 : P;
+    });
+    if (b >= B) continue;
     if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
     lens[b] = r.len;
     skip[b] = r.skip;
     rowg[b] = (int16_t)r.group;
+  }
+#pragma unroll 1
+  for (int g = tid; g < NG; g += NT) {
+    const int P = g < 32 ? lens32 : p.prefix_lens[g];
+    if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
+    gp[g] = max(P, 0) & -p.round_to;
   }
   __syncthreads();
   if (warp == 0 && NG > 0) {   // each row's place among its group's rows
@@ -742,37 +803,6 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 #pragma unroll 1
   for (int b = tid; b < B; b += NT)
     if (rowg[b] >= 0) members[moff[rowg[b]] + rank[b]] = (uint16_t)b;
-  // for the merge: where the records of row b's heads are (this block's share of them)
-#pragma unroll 1
-  for (int i = blockIdx.x + gridDim.x * tid; i < B * p.num_kv_heads; i += gridDim.x * NT) {
-    const int b = i / p.num_kv_heads, h = i - b * p.num_kv_heads, g = rowg[b];
-    const int whole = 2 * B * p.num_q_heads;
-    // a segment's visits [x, x + n), its rows from query row `row` of its record rows `rec` on
-    auto place = [&](int x, uint32_t n, int rec, int row, bool few) {
-      const int c = shares.block_of(x);
-      return make_int4(rec, 2 * whole + (c + 1) * 2 * kTile + row, shares.block_of(x + n - 1) - c + 1, few);
-    };
-    int4 own = make_int4(0, 0, 0, 0), pre = own, pre2 = own;
-    uint32_t n = tiles_of(lens[b] - skip[b]);
-    if (n > 0)
-      own = place(bpre[b] + h * n, n, ((p.num_kv_heads + h) * B + b) * Gq, 0, Gq <= kFew);
-    if (g >= 0) {
-      const int rows = (moff[g + 1] - moff[g]) * Gq, R = rank[b] * Gq, pairs = (uint32_t)(rows + 2 * kTile - 1) / (2 * kTile);
-      const int rec = h * B * Gq + moff[g] * Gq + R;
-      n = tiles_of(gp[g]);
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {   // a row's heads may lie in two pairs of row tiles
-        const int pair = (uint32_t)(R + k * (Gq - 1)) / (2 * kTile);
-        pre2 = place((rows > kTile ? gpre : lpre)[g] + (h * pairs + pair) * n, n, rec, R - pair * 2 * kTile,
-                     rows - pair * 2 * kTile <= kFew);
-        if (k == 0) pre = pre2;
-      }
-      pre.w |= (2 * kTile - R % (2 * kTile)) << 1;   // the head from which on the second holds
-    }
-    p.ws_info[3 * i] = own;
-    p.ws_info[3 * i + 1] = pre;
-    p.ws_info[3 * i + 2] = pre2;
-  }
   const bool idle = (int)blockIdx.x >= shares.blocks || all.y + all.z + all.w == 0;
   const int lo = idle ? 0 : shares.first(blockIdx.x), hi = idle ? 0 : shares.first(blockIdx.x + 1);
   const int nv = hi - lo;
@@ -786,6 +816,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
   if (nv <= 0) {   // uniform over the block
+    if (warp == 8) place_records(p, plan);
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
@@ -956,11 +987,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         }
         const bool two = rows > kTile;
         const int st = two ? u : v & 1;
-        const bool scores = v < end && !(pend.on && pend.st == st);
+        const int qt = qc + (two ? u : 0), qs = qt & 1;
+        // queries still on their way hold up no product that could go ahead
+        const bool scores =
+            v < end && !(pend.on && (pend.st == st || (flags & kFirst &&
+                                                       !__all_sync(0xffffffffu, mbar_test(bar(kBarQFull + qs), (qt >> 1) & 1)))));
         const bool few = rows <= kFew;
         const bool last_s = !two || u == 1;
         if (scores) {
-          const int qt = qc + (two ? u : 0), qs = qt & 1;
           if (flags & kFirst) ok = wait_warp(kBarQFull + qs, (qt >> 1) & 1);
           if (!ok) break;
           tc_after();
@@ -1044,7 +1078,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   } else if (warp == 10) {
     // ============================== Q gather, from the second segment on
     int qc = first_tiles;
-    bool ok = true;
+    bool ok = true, placed = false;
     for (int v = 1; v < nv && ok; ++v) {
       if (v >= kVisits && (v & (kVisits / 2 - 1)) == 0) {
         // the next half of the visits' descriptions, once the last use of their place is over
@@ -1062,6 +1096,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       const int tiles = s.rows > kTile ? 2 : 1;
       for (int u = 0; u < tiles && ok; ++u, ++qc) {
         const int qs = qc & 1;
+        if (qc >= 2 && !placed) {   // both tiles are in use: time for this
+          place_records(p, plan);
+          placed = true;
+        }
         if (qc >= 2) ok = wait_warp(kBarQEmpty + qs, ((qc >> 1) - 1) & 1);
         if (!ok) break;
         gather_q(s, u, qs, 0, 1);
@@ -1072,6 +1110,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
       }
     }
+    if (!placed) place_records(p, plan);
   } else if (warp >= 12) {
     // ============================ converters: K (12-15) and V (16-19)
     if constexpr (QUANT) {
@@ -1476,7 +1515,6 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         }
       } else if (active) {
         const size_t rec = rec0 + tile_row;
-        float* acc = p.ws_acc + rec * D;
         // this stream's channels and factor; of two streams each writes half
         // of the channels of both accumulators' sum
         float M = m, L = l[0], z = 0.f, f0 = QUANT ? vref : 1.f, f1 = 0.f;
@@ -1499,26 +1537,38 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           to_c = from + D / 2;
         }
         if (row < my_rows && from == 0) p.ws_ml[rec] = make_float2(M, L);
+        // 16 channels at a time through 2 KB of shared memory (the stream's place for
+        // transposed weights), so that a row's 64 bytes are written together
         const uint32_t to2 = tm_o(st ^ 1) + lanes;
+        uint8_t* stage = smem + lay.pt + st * kPtBytes + quad * 2048;
+        const int live = min(32, my_rows - quad * 32);   // the warp's query rows
+        float* out = p.ws_acc + (rec0 + tile_row - lane) * D + (lane & 3) * 4;
 #pragma unroll 1
         for (int c = from; c < to_c; c += 16) {
           uint32_t o[16], o2[16];
           tmem_ld<16>(to + c, o);
           if (both) tmem_ld<16>(to2 + c, o2);
           tc_wait_ld();
-          if (row < my_rows) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              float f[8];
+          for (int j = 0; j < 16; j += 4) {
+            float f[4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                f[k] = __uint_as_float(o[j + k]) * f0;
-                if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k]);
-                if constexpr (QUANT) f[k] += z;
-              }
-              store32(acc + c + j, f);
+            for (int k = 0; k < 4; ++k) {
+              f[k] = __uint_as_float(o[j + k]) * f0;
+              if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k]);
+              if constexpr (QUANT) f[k] += z;
             }
+            *reinterpret_cast<float4*>(stage + lane * 64 + ((j >> 2 ^ lane >> 1 & 3) << 4)) =
+                make_float4(f[0], f[1], f[2], f[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            const int r = i + (lane >> 2);
+            const float4 f = *reinterpret_cast<const float4*>(stage + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
+            if (r < live) *reinterpret_cast<float4*>(out + (size_t)r * D + c) = f;
+          }
+          __syncwarp();
         }
         if (both) {   // neither accumulator is overwritten before both are read
           tc_before();

@@ -31,16 +31,17 @@
 // computed: with more than 128 rows each stream has its own 128 rows and
 // both use every tile; otherwise the tiles alternate between the streams, which
 // merge when the segment ends.
-// The running maximum follows the true one only when that is over 2^8 above it:
-// weights then stay below 2^8, and the accumulator in TMEM is rarely rescaled.
+// Weights are 2^(s - r) with a reference r that follows the running maximum only when
+// that is over 8 above it: weights then stay below 2^8, and the accumulator in TMEM is rarely
+// rescaled.
 //
 // INT8 and 4-bit caches: the codes enter the products as exact small integers, u - c
 // with c the middle code, made by four converter warps from the staged bytes;
 // scales and zero points are applied in fp32:
 //   q . k = ks (q . (u - c)) + (kz + c ks) sum q
 //   sum p v = sum (p vs) (u - c) + sum p (vz + c vs)
-// p vs is divided by a power of two near the largest vs, so that it stays inside
-// fp16's range; the accumulator is rescaled when a later tile's scales outgrow it.
+// There r follows the maximum plus log2 of the values' size, so that p vs stays inside
+// fp16's range.
 #pragma once
 
 #include <type_traits>
@@ -1134,11 +1135,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           const float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)slot * G::RAW_SCALES +
                                                             (KV == KV_I8G ? t >> 6 : t) * 16);
           float* sc = reinterpret_cast<float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
-          sc[t] = valid ? z.x : 0.f;
-          sc[kTile + t] = valid ? fmaf(G::CENTRE, z.x, z.y) : 0.f;
+          // (scores come out in the log2 domain; one without a token is -inf, see the softmax)
+          const float vz = fmaf(G::CENTRE, z.z, z.w);
+          sc[t] = valid ? z.x * p.scale : 1.f;
+          sc[kTile + t] = valid ? fmaf(G::CENTRE, z.x, z.y) * p.scale : 0.f;
           sc[2 * kTile + t] = valid ? z.z : 0.f;
-          sc[3 * kTile + t] = valid ? fmaf(G::CENTRE, z.z, z.w) : 0.f;
-          const float vm = warp_max(valid ? z.z : 0.f);
+          sc[3 * kTile + t] = valid ? vz : 0.f;
+          // the values' size: a scale, or a zero point far above it (where the codes matter less)
+          const float vm = warp_max(valid ? fmaxf(z.z, fabsf(vz) * (1.f / 128.f)) : 0.f);
           if (lane == 0) reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 16)[warp - 12] = vm;
         }
         fence_proxy_async_smem();
@@ -1157,16 +1161,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm_s(st) + lanes, to = tm_o(st) + lanes;
     const size_t whole = (size_t)2 * B * p.num_q_heads;   // record rows of segments by stream
-    float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
     int qc = 0, v = 0;
     uint32_t n_ev = 0, n_seg = 0, n_pair = 0, n_x = 0;   // events, segments, meetings so far
-    // The state of a segment. Up to 16 rows: lane j of every warp holds row j's
-    // maximum, each thread its token's part of all rows' sums; more rows: the
-    // thread's own row's, in [0].
-    float m = -INFINITY, l[kFew];
-    [[maybe_unused]] float zs[kFew];
-    float vref = 0.f;
-    bool have = false;
     auto meet = [&](int b, uint32_t& n) -> bool {   // two warps of the same rows
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(b));
@@ -1178,323 +1174,196 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       named_bar_sync(2 + st, 128);
       return misc[1] == 0;
     };
-    auto inverse = [](float x) { return x > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(x)) : 0.f; };
-
-    for (; v < nv; ++v) {
-      if (!described(v)) break;
-      const int flags = flags_of(v);
-      const bool two = flags & kTwo, mine = two || (v & 1) == st;
-      if (flags & kFirst) have = false;
-      if (!mine && !(have && flags & kLast)) {   // the other stream's
-        passed(v);
-        if (flags & kLast) ++qc;
-        continue;
-      }
-      Visit s;
-      visit(v, s);
-      const bool few = s.rows <= kFew;
-      const int my_rows = two ? min(kTile, s.rows - st * kTile) : s.rows;
-      const bool active = few || quad * 32 < my_rows;   // this warp has query rows
-      if (!have) {
-        m = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kFew; ++j) {
-          l[j] = 0.f;
-          if constexpr (QUANT) zs[j] = 0.f;
-        }
-        vref = 0.f;
-      }
-      if (mine) {
-        // ---- the stream's next event: the scores of a tile are there
-        if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) break;
-        if (!wait_warp(kBarS + st, n_ev++ & 1)) break;
-        const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
-        const int ntok = hd.x, mask = hd.y;
-        const bool valid = row < ntok && (mask >> (row >> 4) & 1);   // token `row` of the tile
-        if constexpr (!QUANT) {
-          if (ntok < kTile || mask != 0xFF) {
-            // rows of V that hold no token of this segment may hold anything, NaN
-            // too, and a weight of 0 would not clear it
-            const int slot = v % S;
-            if (!wait_warp(kBarVFull + slot, (v / S) & 1)) break;
-            if (row < (ntok + 15) / 16 * 16 && !valid) {
-              uint8_t* vr = smem + lay.ring + (size_t)(S + slot) * G::ENTRY + row * 128;
+    // the stream's next event: the scores of visit v are there
+    int ntok = 0, mask = 0;
+    bool valid = false;   // token `row` of the tile
+    const float* sc = nullptr;
+    float lv = 0.f;
+    auto begin = [&]() -> bool {
+      if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
+      if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
+      const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
+      ntok = hd.x;
+      mask = hd.y;
+      valid = row < ntok && (mask >> (row >> 4) & 1);
+      if constexpr (QUANT) {
+        sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
+        // log2 of the values' size, to the next whole number
+        const float4 m4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
+        const uint32_t up = __float_as_uint(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))) + 0x7FFFFFu;
+        lv = (float)(min(max((int)(up >> 23), 27), 227) - 127);
+      } else if (ntok < kTile || mask != 0xFF) {
+        // rows of V that hold no token of this segment may hold anything, NaN
+        // too, and a weight of 0 would not clear it
+        const int slot = v % S;
+        if (!wait_warp(kBarVFull + slot, (v / S) & 1)) return false;
+        if (row < (ntok + 15) / 16 * 16 && !valid) {
+          uint8_t* vr = smem + lay.ring + (size_t)(S + slot) * G::ENTRY + row * 128;
 #pragma unroll 4
-              for (int i = 0; i < G::HALVES * 8; ++i)
-                *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-          }
+          for (int i = 0; i < G::HALVES * 8; ++i)
+            *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
-        const float* sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
-        const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + ((qc + (two ? st : 0)) % kQSums) * kTile;
-        // A reference for the value scales: the next power of two of the largest, once
-        // they outgrow the last by 2^6 (every weight x scale then stays below 2^15); fv
-        // is the accumulator's factor, the same for the whole stream.
-        float fv = 1.f;
-        if constexpr (QUANT) {
-          const float4 vm4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
-          const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
-          if (vm > 64.f * vref) {
-            const uint32_t up = (__float_as_uint(vm) + 0x7FFFFFu) & 0x7F800000u;
-            const float nv2 = __uint_as_float(min(max(up, 27u << 23), 227u << 23));   // 2^-100 .. 2^100
-            fv = vref / nv2;
-            vref = nv2;
-          }
-        }
-        tc_after();
-        if (few) {
-          // ---- thread = token for the scores, channel for the values; rows in
-          // blocks of eight, of which the second may be empty
-          float a[kFew];
-          float vs = 1.f, vz = 0.f;
-          float ks = p.scale, kz = 0.f;
-          if constexpr (QUANT) {
-            ks *= sc[row];
-            kz = sc[kTile + row] * p.scale;
-            vs = sc[2 * kTile + row] * inverse(vref);
-            vz = sc[3 * kTile + row];
-          }
-          float* xb = xch + (n_x++ & 1) * (4 * 32);
-          float keep = -INFINITY;
+      }
+      tc_after();
+      return true;
+    };
+    auto end_event = [&]() {   // the weights are written
+      fence_proxy_async_smem();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarP + st));
+    };
+    // Weights are 2^(score - r), for each query row with a reference r that follows
+    // (largest score) + lv, lv the log2 of the values' size (quantised caches; else 0),
+    // only once that is more than 8 above it: a weight times a value's scale stays
+    // within fp16's range, and the accumulator is rarely rescaled.
+
+    bool ok = true;
+    while (v < nv && ok) {
+      Visit s;
+      ok = visit(v, s);
+      if (!ok) break;
+      const bool two = s.is(kTwo), few = s.rows <= kFew;
+      const size_t rec0 = s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
+                                           : (few ? st * whole : 0) + s.rec;
+      const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + ((qc + (two ? st : 0)) % kQSums) * kTile;
+      qc += two ? 2 : 1;
+      bool have = false;
+      if (few) {
+        // ---- up to 16 query rows: thread = token for the scores, channel for the values;
+        // rows in blocks of eight, of which the second may be empty. Lane j of every
+        // warp holds row j's reference, each thread its token's part of the rows' sums.
+        float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
+        uint8_t* pt = smem + lay.pt + st * kPtBytes;
+        const bool wide = s.rows > 8;
+        float r = -INFINITY, l[kFew];
+        [[maybe_unused]] float zs[kFew];
+        int flags = s.flags;
+        for (;;) {
+          if ((v & 1) == st) {
+            ok = begin();
+            if (!ok) break;
+            if (!have) {
 #pragma unroll
-          for (int e = 0; e < kFew; e += 8) {
-            if (e > 0 && s.rows <= 8) break;
-            tmem_ld<8>(ts + e, reinterpret_cast<uint32_t*>(a + e));
-            tc_wait_ld();
-            float4 q4[2] = {};
-            if constexpr (QUANT) {
-              q4[0] = *reinterpret_cast<const float4*>(qsum + e);
-              q4[1] = *reinterpret_cast<const float4*>(qsum + e + 4);
+              for (int j = 0; j < kFew; ++j) {
+                l[j] = 0.f;
+                if constexpr (QUANT) zs[j] = 0.f;
+              }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              a[e + j] = QUANT ? fmaf(ks, a[e + j], kz * reinterpret_cast<const float*>(q4)[j]) : a[e + j] * ks;
-              if (!valid) a[e + j] = -INFINITY;
-              const float w = warp_max(a[e + j]);
-              if (lane == e + j) keep = w;
-            }
-          }
-          if (lane < kFew) xb[quad * 32 + lane] = keep;
-          if (!meet_all()) break;
-          // lane j: largest score of row j over the tile's tokens
-          xb += lane & (kFew - 1);
-          const float mt = fmaxf(fmaxf(xb[0], xb[32]), fmaxf(xb[64], xb[96]));
-          float alpha = 1.f;
-          if (mt > m + 8.f) {
-            alpha = fast_exp2(m - mt);   // 0 from -inf
-            m = mt;
-          }
-          if (have && __any_sync(0xffffffffu, alpha * fv != 1.f)) {   // the same for the whole stream
+            float a[kFew];
+            const float ks = QUANT ? sc[row] : p.scale;
+            const float kz = QUANT ? sc[kTile + row] : 0.f, vs = QUANT ? sc[2 * kTile + row] : 1.f;
+            [[maybe_unused]] const float vz = QUANT ? sc[3 * kTile + row] : 0.f;
+            float* xb = xch + (n_x++ & 1) * (4 * 32);
+            float keep = -INFINITY;
 #pragma unroll
             for (int e = 0; e < kFew; e += 8) {
-              if (e > 0 && s.rows <= 8) break;
-              uint32_t o[16];
-              tmem_ld<8>(to + e, o);
-              tmem_ld<8>(to + kFew + e, o + 8);
+              if (e > 0 && !wide) break;
+              tmem_ld<8>(ts + e, reinterpret_cast<uint32_t*>(a + e));
+              float4 q4[2] = {};
+              if constexpr (QUANT) {
+                q4[0] = *reinterpret_cast<const float4*>(qsum + e);
+                q4[1] = *reinterpret_cast<const float4*>(qsum + e + 4);
+              }
               tc_wait_ld();
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float f = __shfl_sync(0xffffffffu, alpha, e + j);
-                l[e + j] *= f;
-                if constexpr (QUANT) zs[e + j] *= f;
-                o[j] = __float_as_uint(__uint_as_float(o[j]) * (f * fv));
-                o[8 + j] = __float_as_uint(__uint_as_float(o[8 + j]) * (f * fv));
+                a[e + j] = QUANT ? fmaf(ks, a[e + j], kz * reinterpret_cast<const float*>(q4)[j]) : a[e + j] * ks;
+                if (!valid) a[e + j] = -INFINITY;
+                const float w = warp_max(a[e + j]);
+                if (lane == e + j) keep = w;
               }
-              tmem_st<8>(to + e, o);
-              tmem_st<8>(to + kFew + e, o + 8);
             }
-            tc_wait_st();
-          }
-          const float mref = m == -INFINITY ? 0.f : m;
-          uint8_t* pt = smem + lay.pt + st * kPtBytes;
+            if (lane < kFew) xb[quad * 32 + lane] = keep;
+            ok = meet_all();
+            if (!ok) break;
+            // lane j: the largest score of row j over the tile's tokens
+            xb += lane & (kFew - 1);
+            const float t = fmaxf(fmaxf(xb[0], xb[32]), fmaxf(xb[64], xb[96])) + lv;
+            float alpha = 1.f;
+            if (t > r + 8.f) {
+              alpha = fast_exp2(r - t);   // 0 from -inf
+              r = t;
+            }
+            if (have && __any_sync(0xffffffffu, alpha != 1.f)) {   // the same for the whole stream
 #pragma unroll
-          for (int e = 0; e < kFew; e += 8) {
-            if (e > 0 && s.rows <= 8) break;
-            // weights of token `row`, first terms and what their rounding left, as
-            // [8-row block][token][8]
-            uint32_t hi16[4], lo16[4];
+              for (int e = 0; e < kFew; e += 8) {
+                if (e > 0 && !wide) break;
+                uint32_t o[16];
+                tmem_ld<8>(to + e, o);
+                tmem_ld<8>(to + kFew + e, o + 8);
+                tc_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-              float w[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int j = e + k + i;
-                w[i] = fast_exp2(a[j] - __shfl_sync(0xffffffffu, mref, j));
-                l[j] += w[i];
-                if constexpr (QUANT) {
-                  zs[j] = fmaf(w[i], vz, zs[j]);
-                  w[i] *= vs;
+                for (int j = 0; j < 8; ++j) {
+                  const float f = __shfl_sync(0xffffffffu, alpha, e + j);
+                  l[e + j] *= f;
+                  if constexpr (QUANT) zs[e + j] *= f;
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                  o[8 + j] = __float_as_uint(__uint_as_float(o[8 + j]) * f);
                 }
+                tmem_st<8>(to + e, o);
+                tmem_st<8>(to + kFew + e, o + 8);
               }
-              hi16[k / 2] = pack16<BF>(w[0], w[1]);
-              lo16[k / 2] = pack16<BF>(w[0] - low16<BF>(hi16[k / 2]), w[1] - high16<BF>(hi16[k / 2]));
+              tc_wait_st();
             }
-            *reinterpret_cast<uint4*>(pt + e * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
-            *reinterpret_cast<uint4*>(pt + (kFew + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
-          }
-        } else if (active) {
-          // ---- thread = query row. Scores are read twice, COLS columns at a time in loops
-          // that stay loops: with all 128 in registers and the code unrolled, the
-          // warps waited for instructions.
-          if constexpr (QUANT) {
-            const float qs = qsum[row];
-#pragma unroll 1
-            for (int c = 0; c < ntok; c += 32) {
-              float a[32];
-              tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
-              tc_wait_ld();
+            const float ref = r == -INFINITY ? 0.f : r;
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 ks = *reinterpret_cast<const float4*>(sc + c + j);
-                const float4 kz = *reinterpret_cast<const float4*>(sc + kTile + c + j);
-                a[j] = fmaf(ks.x, a[j], kz.x * qs);
-                a[j + 1] = fmaf(ks.y, a[j + 1], kz.y * qs);
-                a[j + 2] = fmaf(ks.z, a[j + 2], kz.z * qs);
-                a[j + 3] = fmaf(ks.w, a[j + 3], kz.w * qs);
+            for (int e = 0; e < kFew; e += 8) {
+              if (e > 0 && !wide) break;
+              // weights of token `row`, first terms and what their rounding left, as
+              // [8-row block][token][8]
+              uint32_t hi16[4], lo16[4];
+#pragma unroll
+              for (int k = 0; k < 8; k += 2) {
+                float w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int j = e + k + i;
+                  w[i] = fast_exp2(a[j] - __shfl_sync(0xffffffffu, ref, j));
+                  l[j] += w[i];
+                  if constexpr (QUANT) {
+                    zs[j] = fmaf(w[i], vz, zs[j]);
+                    w[i] *= vs;
+                  }
+                }
+                hi16[k / 2] = pack16<BF>(w[0], w[1]);
+                lo16[k / 2] = pack16<BF>(w[0] - low16<BF>(hi16[k / 2]), w[1] - high16<BF>(hi16[k / 2]));
               }
-              tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+              *reinterpret_cast<uint4*>(pt + e * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
+              *reinterpret_cast<uint4*>(pt + (kFew + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
             }
+            have = true;
+            end_event();
           }
-          if (ntok < kTile || mask != 0xFF) {   // columns without a token
-            if constexpr (QUANT) tc_wait_st();
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 16) {
-              const int left = mask >> (c >> 4) & 1 ? ntok - c : 0;
-              if (left >= 16) continue;
-              float a[16];
-              tmem_ld<16>(ts + c, reinterpret_cast<uint32_t*>(a));
-              tc_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j >= left) a[j] = -INFINITY;
-              tmem_st<16>(ts + c, reinterpret_cast<uint32_t*>(a));
-            }
-            tc_wait_st();
-          } else if constexpr (QUANT) {
-            tc_wait_st();
-          }
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < ntok; c += COLS) {
-            float a[COLS];
-            tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
-            if constexpr (COLS == 64) tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
-            tc_wait_ld();
-            float m4[4] = {mx, a[0], a[1], a[2]};
-#pragma unroll
-            for (int j = 3; j < COLS - 1; j += 2) m4[j >> 1 & 3] = max3(m4[j >> 1 & 3], a[j], a[j + 1]);
-            mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[COLS - 1]);
-          }
-          const float mt = mx * p.scale;
-          float alpha = fv;
-          if (mt > m + 8.f) {
-            const float f = fast_exp2(m - mt);   // 0 from -inf
-            m = mt;
-            l[0] *= f;
-            if constexpr (QUANT) zs[0] *= f;
-            alpha *= f;
-          }
-          if (have && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // S of this event is complete, so every earlier product of this stream is
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld<32>(to + c, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st<32>(to + c, o);
-            }
-          }
-          const float mref = m == -INFINITY ? 0.f : m, rv = QUANT ? inverse(vref) : 0.f;
-          const uint64_t sc2 = pack2f(p.scale, p.scale), mr2 = pack2f(-mref, -mref);
-          uint64_t ls0 = 0, ls1 = 0, z2 = 0;
-#pragma unroll 1
-          for (int c = 0; c < ntok; c += COLS) {
-            float a[COLS];
-            tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
-            if constexpr (COLS == 64) tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
-            tc_wait_ld();
-#pragma unroll
-            for (int j = 0; j < COLS; j += 2) {
-              float x, y;
-              unpack2f(ffma2(pack2f(a[j], a[j + 1]), sc2, mr2), x, y);
-              a[j] = fast_exp2(x);
-              a[j + 1] = fast_exp2(y);
-              (j & 2 ? ls1 : ls0) = fadd2(j & 2 ? ls1 : ls0, pack2f(a[j], a[j + 1]));
-            }
-            if constexpr (QUANT) {
-              const uint64_t rv2 = pack2f(rv, rv);
-#pragma unroll
-              for (int j = 0; j < COLS; j += 4) {
-                const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + c + j);
-                const ulonglong2 vz = *reinterpret_cast<const ulonglong2*>(sc + 3 * kTile + c + j);
-                z2 = ffma2(pack2f(a[j], a[j + 1]), vz.x, z2);
-                z2 = ffma2(pack2f(a[j + 2], a[j + 3]), vz.y, z2);
-                unpack2f(fmul2(pack2f(a[j], a[j + 1]), fmul2(vs.x, rv2)), a[j], a[j + 1]);
-                unpack2f(fmul2(pack2f(a[j + 2], a[j + 3]), fmul2(vs.y, rv2)), a[j + 2], a[j + 3]);
-              }
-            }
-            // The weights' one rounding to the operand type. They take the
-            // place of their scores: 16 columns for 32 tokens, and 16 more of second
-            // terms, which hold what the rounding left, where the output keeps more bits.
-#pragma unroll
-            for (int e = 0; e < COLS; e += 32) {
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = pack16<BF>(a[e + 2 * j], a[e + 2 * j + 1]);
-              tmem_st<16>(ts + c + e, w);
-              if (p.two_terms) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  w[j] = pack16<BF>(a[e + 2 * j] - low16<BF>(w[j]), a[e + 2 * j + 1] - high16<BF>(w[j]));
-                tmem_st<16>(ts + c + e + 16, w);
-              }
-            }
-          }
-          l[0] += hsum2(fadd2(ls0, ls1));
-          if constexpr (QUANT) zs[0] += hsum2(z2);
-          tc_wait_st();
+          passed(v++);
+          if (flags & kLast) break;
+          ok = described(v);
+          if (!ok) break;
+          flags = flags_of(v);
         }
-        have = true;
-        fence_proxy_async_smem();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + st));
-      }
-      passed(v);
-      if (!s.is(kLast)) continue;
-
-      // ---- end of the block's part of the segment: one record per query row
-      qc += two ? 2 : 1;
-      const bool both = !two && !few && s.is(kMany);   // the streams' states of a row meet
-      const int tile_row = two ? st * kTile + row : row;
-      const size_t rec0 = s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
-                                           : (few ? st * whole : 0) + s.rec;
-      if (!few) {
-        if (!wait_warp(kBarO + st, n_seg++ & 1)) break;
-        tc_after();
-      }
-      if (few) {
+        if (!ok || !have) continue;   // !have: a part of one visit, the other stream's
+        // ---- the stream's record of each row
         float* xb = xch + (n_x++ & 1) * (4 * 32);
 #pragma unroll
         for (int e = 0; e < kFew; e += 8) {
-          if (e > 0 && s.rows <= 8) break;
+          if (e > 0 && !wide) break;
           int j;
           const float ls = scatter_sum8(l + e, lane, j);
           xb[quad * 32 + e + j] = ls;
           if constexpr (QUANT) xb[quad * 32 + kFew + e + j] = scatter_sum8(zs + e, lane, j);
         }
-        if (!meet_all()) break;
+        ok = meet_all();
+        if (!ok) break;
         auto total = [&](int i) { return (xb[i] + xb[32 + i]) + (xb[64 + i] + xb[96 + i]); };
         if (row < s.rows) {
-          p.ws_ml[rec0 + row] = make_float2(m, total(row));
+          p.ws_ml[rec0 + row] = make_float2(r, total(row));
           if (!s.is(kMany)) {   // a part of one visit: the other stream has nothing
             const size_t other = s.is(kContinued) ? rec0 + (st ? -kTile : kTile) : st ? s.rec : whole + s.rec;
             p.ws_ml[other + row] = make_float2(-INFINITY, 0.f);
           }
         }
-        if (!wait_warp(kBarO + st, n_seg++ & 1)) break;
+        ok = wait_warp(kBarO + st, n_seg++ & 1);
+        if (!ok) break;
         tc_after();
         if (quad * 32 < D) {
 #pragma unroll 1
@@ -1508,35 +1377,175 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             for (int k = 0; k < 8; ++k) {
               if (e + k >= s.rows) break;
               float f = __uint_as_float(o[k]) + __uint_as_float(o[8 + k]);
-              if constexpr (QUANT) f = fmaf(f, vref, total(kFew + e + k));
+              if constexpr (QUANT) f += total(kFew + e + k);
               acc[k * D] = f;
             }
           }
         }
-      } else if (active) {
-        const size_t rec = rec0 + tile_row;
-        // this stream's channels and factor; of two streams each writes half
-        // of the channels of both accumulators' sum
-        float M = m, L = l[0], z = 0.f, f0 = QUANT ? vref : 1.f, f1 = 0.f;
-        if constexpr (QUANT) z = zs[0];
+        tc_before();
+        continue;
+      }
+
+      // ---- more rows: thread = query row. Scores are read twice, COLS columns at a time in
+      // loops that stay loops: with all 128 in registers and the code unrolled, the warps
+      // waited for instructions.
+      const int my_rows = two ? min(kTile, s.rows - st * kTile) : s.rows;
+      const bool active = quad * 32 < my_rows;   // this warp has query rows
+      float r = -INFINITY, l = 0.f;
+      [[maybe_unused]] float zs = 0.f, qs = 0.f;
+      for (;;) {
+        if (two || (v & 1) == st) {
+          ok = begin();
+          if (!ok) break;
+          if (active) {
+            if (QUANT && !have) qs = qsum[row];
+            const uint64_t qs2 = pack2f(qs, qs), scale2 = pack2f(p.scale, p.scale);
+            if (ntok < kTile || mask != 0xFF) {   // columns without a token
+#pragma unroll 1
+              for (int c = 0; c < kTile; c += 16) {
+                const int left = mask >> (c >> 4) & 1 ? ntok - c : 0;
+                if (left >= 16) continue;
+                float a[16];
+                tmem_ld<16>(ts + c, reinterpret_cast<uint32_t*>(a));
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (j >= left) a[j] = -INFINITY;
+                tmem_st<16>(ts + c, reinterpret_cast<uint32_t*>(a));
+              }
+              tc_wait_st();
+            }
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < ntok; c += COLS) {
+              float a[COLS];
+              tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+              if constexpr (COLS == 64) tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
+              tc_wait_ld();
+              if constexpr (QUANT) {
+#pragma unroll
+                for (int j = 0; j < COLS; j += 4) {
+                  const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + c + j);
+                  const ulonglong2 kz = *reinterpret_cast<const ulonglong2*>(sc + kTile + c + j);
+                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), ks.x, fmul2(kz.x, qs2)), a[j], a[j + 1]);
+                  unpack2f(ffma2(pack2f(a[j + 2], a[j + 3]), ks.y, fmul2(kz.y, qs2)), a[j + 2], a[j + 3]);
+                }
+              }
+              float m4[4] = {mx, a[0], a[1], a[2]};
+#pragma unroll
+              for (int j = 3; j < COLS - 1; j += 2) m4[j >> 1 & 3] = max3(m4[j >> 1 & 3], a[j], a[j + 1]);
+              mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[COLS - 1]);
+            }
+            const float t = QUANT ? mx + lv : mx * p.scale;
+            float alpha = 1.f;
+            if (t > r + 8.f) {
+              alpha = fast_exp2(r - t);   // 0 from -inf
+              r = t;
+              l *= alpha;
+              if constexpr (QUANT) zs *= alpha;
+            }
+            if (have && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // S of this event is complete, so every earlier product of this stream is
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld<32>(to + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st<32>(to + c, o);
+              }
+            }
+            const float ref = r == -INFINITY ? 0.f : r;
+            const uint64_t ref2 = pack2f(-ref, -ref);
+            uint64_t ls0 = 0, ls1 = 0, z2 = 0;
+#pragma unroll 1
+            for (int c = 0; c < ntok; c += COLS) {
+              float a[COLS];
+              tmem_ld<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+              if constexpr (COLS == 64) tmem_ld<32>(ts + c + 32, reinterpret_cast<uint32_t*>(a + 32));
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < COLS; j += 2) {
+                float x, y;
+                if constexpr (QUANT) {
+                  const uint64_t ks = *reinterpret_cast<const uint64_t*>(sc + c + j);
+                  const uint64_t kz = *reinterpret_cast<const uint64_t*>(sc + kTile + c + j);
+                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), ks, ffma2(kz, qs2, ref2)), x, y);
+                } else {
+                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), scale2, ref2), x, y);
+                }
+                a[j] = fast_exp2(x);
+                a[j + 1] = fast_exp2(y);
+                const uint64_t w2 = pack2f(a[j], a[j + 1]);
+                (j & 2 ? ls1 : ls0) = fadd2(j & 2 ? ls1 : ls0, w2);
+                if constexpr (QUANT) {
+                  const uint64_t vs = *reinterpret_cast<const uint64_t*>(sc + 2 * kTile + c + j);
+                  const uint64_t vz = *reinterpret_cast<const uint64_t*>(sc + 3 * kTile + c + j);
+                  z2 = ffma2(w2, vz, z2);
+                  unpack2f(fmul2(w2, vs), a[j], a[j + 1]);
+                }
+              }
+              // The weights' one rounding to the operand type. They take the
+              // place of their scores: 16 columns for 32 tokens, and 16 more of
+              // second terms, which hold what the rounding left, where the output
+              // keeps more bits.
+#pragma unroll
+              for (int e = 0; e < COLS; e += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack16<BF>(a[e + 2 * j], a[e + 2 * j + 1]);
+                tmem_st<16>(ts + c + e, w);
+                if (p.two_terms) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    w[j] = pack16<BF>(a[e + 2 * j] - low16<BF>(w[j]), a[e + 2 * j + 1] - high16<BF>(w[j]));
+                  tmem_st<16>(ts + c + e + 16, w);
+                }
+              }
+            }
+            l += hsum2(fadd2(ls0, ls1));
+            if constexpr (QUANT) zs += hsum2(z2);
+            tc_wait_st();
+          }
+          have = true;
+          end_event();
+        }
+        passed(v++);
+        if (s.is(kLast)) break;
+        ok = described(v);
+        if (!ok) break;
+        s.flags = flags_of(v);
+      }
+      if (!ok || !have) continue;
+      // ---- one record per query row; where both streams have tiles of the same
+      // rows, their states meet and each writes half of the channels of their sum
+      const bool both = !two && s.is(kMany);
+      const int tile_row = two ? st * kTile + row : row;
+      ok = wait_warp(kBarO + st, n_seg++ & 1);
+      if (!ok) break;
+      tc_after();
+      if (active) {
+        float R = r, L = l, z = QUANT ? zs : 0.f, f0 = 1.f, f1 = 0.f;
         int from = 0, to_c = D;
         if (both) {
           float4* mls = reinterpret_cast<float4*>(smem + lay.ml);
-          mls[st * kTile + row] = make_float4(M, L, z, f0);
+          mls[st * kTile + row] = make_float4(r, l, z, 0.f);
           tc_before();
-          if (!meet(kBarPair + quad, n_pair)) break;
+          ok = meet(kBarPair + quad, n_pair);
+          if (!ok) break;
           tc_after();
           const float4 other = mls[(st ^ 1) * kTile + row];
-          M = fmaxf(m, other.x);
-          const float Mr = M == -INFINITY ? 0.f : M, g0 = fast_exp2(m - Mr), g1 = fast_exp2(other.x - Mr);
-          L = fmaf(L, g0, other.y * g1);
-          z = fmaf(z, g0, other.z * g1);
-          f0 *= g0;
-          f1 = other.w * g1;
+          R = fmaxf(r, other.x);
+          const float Rr = R == -INFINITY ? 0.f : R;
+          f0 = fast_exp2(r - Rr);
+          f1 = fast_exp2(other.x - Rr);
+          L = fmaf(l, f0, other.y * f1);
+          z = fmaf(z, f0, other.z * f1);
           from = st * (D / 2);
           to_c = from + D / 2;
         }
-        if (row < my_rows && from == 0) p.ws_ml[rec] = make_float2(M, L);
+        if (row < my_rows && from == 0) p.ws_ml[rec0 + tile_row] = make_float2(R, L);
         // 16 channels at a time through 2 KB of shared memory (the stream's place for
         // transposed weights), so that a row's 64 bytes are written together
         const uint32_t to2 = tm_o(st ^ 1) + lanes;
@@ -1554,8 +1563,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             float f[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              f[k] = __uint_as_float(o[j + k]) * f0;
-              if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k]);
+              f[k] = __uint_as_float(o[j + k]);
+              if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k] * f0);
               if constexpr (QUANT) f[k] += z;
             }
             *reinterpret_cast<float4*>(stage + lane * 64 + ((j >> 2 ^ lane >> 1 & 3) << 4)) =
@@ -1564,21 +1573,22 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
-            const int r = i + (lane >> 2);
-            const float4 f = *reinterpret_cast<const float4*>(stage + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
-            if (r < live) *reinterpret_cast<float4*>(out + (size_t)r * D + c) = f;
+            const int q = i + (lane >> 2);
+            const float4 f = *reinterpret_cast<const float4*>(stage + q * 64 + (((lane & 3) ^ (q >> 1 & 3)) << 4));
+            if (q < live) *reinterpret_cast<float4*>(out + (size_t)q * D + c) = f;
           }
           __syncwarp();
         }
         if (both) {   // neither accumulator is overwritten before both are read
           tc_before();
-          if (!meet(kBarPair + quad, n_pair)) break;
+          ok = meet(kBarPair + quad, n_pair);
+          if (!ok) break;
         }
       }
       tc_before();
     }
     // given up: the stream's other warps may be waiting for this one
-    if (v < nv) asm volatile("bar.arrive %0, 128;" ::"r"(2 + st) : "memory");
+    if (!ok) asm volatile("bar.arrive %0, 128;" ::"r"(2 + st) : "memory");
   }
   tc_before();
   __syncthreads();

@@ -112,7 +112,7 @@ struct SharedGeom {
   static constexpr int ROW = KV == KV_U4T ? D / 2 : (QUANT ? D : 2 * D);
   static constexpr int ENTRY = QUANT ? kTile * ROW : OPERAND;
   static constexpr int RAW_SCALES = QUANT ? (KV == KV_I8G ? 128 : kTile * 16) : 0;
-  static constexpr int SCALES = QUANT ? 4 * kTile * 4 : 0;   // ks, kz', vs, vz' of a visit
+  static constexpr int SCALES = QUANT ? 4 * kTile * 4 : 0;   // of a visit: by pairs of tokens (ks, ks, kz', kz'), then (vs, vs, vz', vz')
   static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr float CENTRE = KV == KV_U4T ? 8.f : 128.f;
 };
@@ -885,66 +885,80 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     uint8_t* ring = smem + lay.ring + (isv ? (size_t)S * G::ENTRY : 0);
     const uint8_t* pool = isv ? p.v_pages : p.k_pages;
     const void* map = isv ? &p.tmap_v : &p.tmap_k;
-    int v = 0;
-    bool ok = true;
-    Visit d = first;
-    // page of this lane's piece, one visit ahead
-    auto lookup = [&]() -> int {
-      if (16 * piece >= d.tokens()) return -2;   // nothing to copy
-      return p.block_table[(size_t)d.row * p.max_pages + (d.tok0 + 16 * piece) / p.page_size];
+    // Block-table entries of four visits at a time, a batch ahead: lane 8 j + i has piece
+    // i (16 tokens) of visit j of the batch. Its pool row, or -1 for none.
+    int page = 0, base = 0, tok = 0;   // of the next batch, the load on its way
+    auto fetch = [&](int v0) -> bool {
+      if (v0 < nv && !described(v0)) return false;
+      const int v = v0 + (lane >> 3), i = lane & 7;
+      page = -2;
+      if (v < nv) {
+        const int4 d = visits[2 * (v & (kVisits - 1))];
+        if (16 * i < (d.y & 0xFF)) {
+          tok = d.x + 16 * i;
+          base = d.w;
+          page = p.block_table[(size_t)d.z * p.max_pages + tok / p.page_size];
+        }
+      }
+      return true;
     };
-    int page = lookup();
+    int v = 0;
+    bool ok = fetch(0);
     RingPos pos;
-    for (; v < nv && ok; ++v, pos.next(S)) {
-      const int head = d.head, tok0 = d.tok0, ntok = d.tokens(), pg = page;
-      passed(v);
-      if (v + 1 < nv) {
-        ok = visit(v + 1, d);
+    for (int v0 = 0; v0 < nv && ok; v0 += 4) {
+      const bool good = page >= 0 && page < p.num_pages;
+      if (page != -2 && !good && !isv) flag_status(p.dev_status, PKV_DEV_BAD_PAGE);
+      // (the host keeps pool rows below 2^31)
+      const int rows4 = good ? (page * p.num_kv_heads + base) * p.page_size + tok % p.page_size : -1;
+      const unsigned have = __ballot_sync(0xffffffffu, good);
+      const int n = min(4, nv - v0);
+      // descriptions of the next four visits may themselves still be on their
+      // way behind these
+      const bool wait_later = ((v0 + 4) & (kVisits / 2 - 1)) == 0;
+      int lens4 = 0;
+      if (!isv && lane < n) lens4 = visits[2 * ((v0 + lane) & (kVisits - 1))].y & 0xFF;
+      if (wait_later) passed(v0 + 3);
+      if (!wait_later) fetch(v0 + 4);
+      for (int j = 0; j < n; ++j, ++v, pos.next(S)) {
+        const uint32_t mask = have >> (8 * j) & 0xFFu;   // bit i: piece i is copied
+        const int row = __shfl_sync(0xffffffffu, rows4, 8 * j + (piece & 7));
+        const int ntok = __shfl_sync(0xffffffffu, lens4, j);
+        const int slot = pos.slot;
+        ok = v < S || wait_warp(empties + slot, pos.phase ^ 1);
         if (!ok) break;
-        page = lookup();
-      }
-      const bool bad = pg != -2 && (pg < 0 || pg >= p.num_pages);
-      if (bad && !isv && half == 0) flag_status(p.dev_status, PKV_DEV_BAD_PAGE);
-      const bool copy = pg != -2 && !bad;
-      const unsigned has = __ballot_sync(0xffffffffu, copy && half == 0);
-      unsigned mask = 0;   // bit i: piece i was copied
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mask |= (has >> (i * PARTS) & 1u) << i;
-      const int slot = pos.slot;
-      ok = v < S || wait_warp(empties + slot, pos.phase ^ 1);
-      if (!ok) break;
-      const uint32_t fb = bar(fulls + slot);
-      if (lane == 0) {
-        if (!isv) *reinterpret_cast<int2*>(smem + lay.hdr + (v % kHdrs) * 8) = make_int2(ntok, (int)mask);
-        uint32_t bytes = (uint32_t)__popc(mask) * 16u * G::ROW;
-        if constexpr (KV == KV_I8T || KV == KV_U4T) bytes += !isv ? (uint32_t)__popc(mask) * 256u : 0u;
-        if constexpr (KV == KV_I8G) bytes += !isv ? (uint32_t)((mask & 0xF ? 16 : 0) + (mask & 0xF0 ? 16 : 0)) : 0u;
-        if (bytes)
-          mbar_arrive_expect_tx(fb, bytes);
-        else
-          mbar_arrive(fb);
-        if (!QUANT && !isv) mbar_arrive(bar(kBarHdr + v % kHdrs));
-      }
-      __syncwarp();
-      if (copy) {
-        const size_t row = ((size_t)pg * p.num_kv_heads + head) * p.page_size + (tok0 + 16 * piece) % p.page_size;
-        uint8_t* dst = ring + (size_t)slot * G::ENTRY;
-        if constexpr (!QUANT) {
-          tma_load_2d(smem_u32(dst + half * 16384 + piece * 2048), map, half * 64, (int)row, fb, pol);
-        } else {
-          bulk_g2s(smem_u32(dst + piece * 16 * G::ROW), pool + row * G::ROW, 16 * G::ROW, fb, pol);
-          if (!isv) {
-            uint8_t* raw = smem + lay.raw + (size_t)slot * G::RAW_SCALES;
-            if constexpr (KV != KV_I8G) {
-              bulk_g2s(smem_u32(raw + piece * 256), p.kv_sz + row * 4, 256, fb, pol);
-            } else if ((mask & ((1u << piece) - 1) & (piece < 4 ? 0xFu : 0xF0u)) == 0) {
-              // the first copied piece of a 64-token group brings its scales
-              bulk_g2s(smem_u32(raw + (piece >> 2) * 16), p.kv_sz + row / 64 * 4, 16, fb, pol);
+        const uint32_t fb = bar(fulls + slot);
+        if (lane == 0) {
+          if (!isv) *reinterpret_cast<int2*>(smem + lay.hdr + (v % kHdrs) * 8) = make_int2(ntok, (int)mask);
+          uint32_t bytes = (uint32_t)__popc(mask) * 16u * G::ROW;
+          if constexpr (KV == KV_I8T || KV == KV_U4T) bytes += !isv ? (uint32_t)__popc(mask) * 256u : 0u;
+          if constexpr (KV == KV_I8G) bytes += !isv ? (uint32_t)((mask & 0xF ? 16 : 0) + (mask & 0xF0 ? 16 : 0)) : 0u;
+          if (bytes)
+            mbar_arrive_expect_tx(fb, bytes);
+          else
+            mbar_arrive(fb);
+          if (!QUANT && !isv) mbar_arrive(bar(kBarHdr + v % kHdrs));
+        }
+        __syncwarp();
+        if (piece < 8 && row >= 0) {
+          uint8_t* dst = ring + (size_t)slot * G::ENTRY;
+          if constexpr (!QUANT) {
+            tma_load_2d(smem_u32(dst + half * 16384 + piece * 2048), map, half * 64, row, fb, pol);
+          } else {
+            bulk_g2s(smem_u32(dst + piece * 16 * G::ROW), pool + (size_t)row * G::ROW, 16 * G::ROW, fb, pol);
+            if (!isv) {
+              uint8_t* raw = smem + lay.raw + (size_t)slot * G::RAW_SCALES;
+              if constexpr (KV != KV_I8G) {
+                bulk_g2s(smem_u32(raw + piece * 256), p.kv_sz + (size_t)row * 4, 256, fb, pol);
+              } else if ((mask & ((1u << piece) - 1) & (piece < 4 ? 0xFu : 0xF0u)) == 0) {
+                // the first copied piece of a 64-token group brings its scales
+                bulk_g2s(smem_u32(raw + (piece >> 2) * 16), p.kv_sz + (size_t)(row / 64) * 4, 16, fb, pol);
+              }
             }
           }
         }
+        __syncwarp();
       }
-      __syncwarp();
+      if (ok && wait_later) ok = fetch(v0 + 4);
     }
     // every issued copy lands before the block can end
     if (lane == 0)
@@ -1137,10 +1151,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           float* sc = reinterpret_cast<float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
           // (scores come out in the log2 domain; one without a token is -inf, see the softmax)
           const float vz = fmaf(G::CENTRE, z.z, z.w);
-          sc[t] = valid ? z.x * p.scale : 1.f;
-          sc[kTile + t] = valid ? fmaf(G::CENTRE, z.x, z.y) * p.scale : 0.f;
-          sc[2 * kTile + t] = valid ? z.z : 0.f;
-          sc[3 * kTile + t] = valid ? vz : 0.f;
+          sc += (t >> 1) * 4 + (t & 1);
+          sc[0] = valid ? z.x * p.scale : 1.f;
+          sc[2] = valid ? fmaf(G::CENTRE, z.x, z.y) * p.scale : 0.f;
+          sc[2 * kTile] = valid ? z.z : 0.f;
+          sc[2 * kTile + 2] = valid ? vz : 0.f;
           // the values' size: a scale, or a zero point far above it (where the codes matter less)
           const float vm = warp_max(valid ? fmaxf(z.z, fabsf(vz) * (1.f / 128.f)) : 0.f);
           if (lane == 0) reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 16)[warp - 12] = vm;
@@ -1251,9 +1266,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               }
             }
             float a[kFew];
-            const float ks = QUANT ? sc[row] : p.scale;
-            const float kz = QUANT ? sc[kTile + row] : 0.f, vs = QUANT ? sc[2 * kTile + row] : 1.f;
-            [[maybe_unused]] const float vz = QUANT ? sc[3 * kTile + row] : 0.f;
+            const int at = (row >> 1) * 4 + (row & 1);
+            const float ks = QUANT ? sc[at] : p.scale;
+            const float kz = QUANT ? sc[at + 2] : 0.f, vs = QUANT ? sc[2 * kTile + at] : 1.f;
+            [[maybe_unused]] const float vz = QUANT ? sc[2 * kTile + at + 2] : 0.f;
             float* xb = xch + (n_x++ & 1) * (4 * 32);
             float keep = -INFINITY;
 #pragma unroll
@@ -1424,11 +1440,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               tc_wait_ld();
               if constexpr (QUANT) {
 #pragma unroll
-                for (int j = 0; j < COLS; j += 4) {
-                  const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + c + j);
-                  const ulonglong2 kz = *reinterpret_cast<const ulonglong2*>(sc + kTile + c + j);
-                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), ks.x, fmul2(kz.x, qs2)), a[j], a[j + 1]);
-                  unpack2f(ffma2(pack2f(a[j + 2], a[j + 3]), ks.y, fmul2(kz.y, qs2)), a[j + 2], a[j + 3]);
+                for (int j = 0; j < COLS; j += 2) {
+                  const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * (c + j));
+                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), k2.x, fmul2(k2.y, qs2)), a[j], a[j + 1]);
                 }
               }
               float m4[4] = {mx, a[0], a[1], a[2]};
@@ -1469,9 +1483,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               for (int j = 0; j < COLS; j += 2) {
                 float x, y;
                 if constexpr (QUANT) {
-                  const uint64_t ks = *reinterpret_cast<const uint64_t*>(sc + c + j);
-                  const uint64_t kz = *reinterpret_cast<const uint64_t*>(sc + kTile + c + j);
-                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), ks, ffma2(kz, qs2, ref2)), x, y);
+                  const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * (c + j));
+                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), k2.x, ffma2(k2.y, qs2, ref2)), x, y);
                 } else {
                   unpack2f(ffma2(pack2f(a[j], a[j + 1]), scale2, ref2), x, y);
                 }
@@ -1480,10 +1493,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 const uint64_t w2 = pack2f(a[j], a[j + 1]);
                 (j & 2 ? ls1 : ls0) = fadd2(j & 2 ? ls1 : ls0, w2);
                 if constexpr (QUANT) {
-                  const uint64_t vs = *reinterpret_cast<const uint64_t*>(sc + 2 * kTile + c + j);
-                  const uint64_t vz = *reinterpret_cast<const uint64_t*>(sc + 3 * kTile + c + j);
-                  z2 = ffma2(w2, vz, z2);
-                  unpack2f(fmul2(w2, vs), a[j], a[j + 1]);
+                  const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + 2 * (c + j));
+                  z2 = ffma2(w2, v2.y, z2);
+                  unpack2f(fmul2(w2, v2.x), a[j], a[j + 1]);
                 }
               }
               // The weights' one rounding to the operand type. They take the

@@ -70,12 +70,12 @@ constexpr int kTile = 128;        // tokens of a visit, query rows of a tile
 constexpr int kHdrs = 16;
 // Visits whose scales are kept: written for v once the scores of v - 1, and so the
 // softmax of v - 3, are done.
-constexpr int kScaleSlots = 4;
-constexpr int kQSums = 8;
+constexpr int kScaleSlots = 3;
+// Query tiles whose sums are kept: tile t is gathered once the last scores of tile t - 2
+// are done, when at most the last two events are still to be read, of tiles from t - 4 on.
+constexpr int kQSums = 6;
 constexpr int kMaxEntries = 6;    // ring entries of K, and of V
-constexpr int kVisits = 128;      // visits described in shared memory, refilled by halves
-constexpr int kFew = 16;          // segments of at most this many query rows run transposed
-constexpr int kPtBytes = 8192;    // transposed weights of a stream: 16 rows, two terms each
+constexpr int kVisits = 64;      // visits described in shared memory, refilled by halves
 
 // Shared memory by offset from a 1024-byte boundary.
 struct SharedLayout {
@@ -113,6 +113,9 @@ struct SharedGeom {
   static constexpr int ENTRY = QUANT ? kTile * ROW : OPERAND;
   static constexpr int RAW_SCALES = QUANT ? (KV == KV_I8G ? 128 : kTile * 16) : 0;
   static constexpr int SCALES = QUANT ? 4 * kTile * 4 : 0;   // of a visit: by pairs of tokens (ks, ks, kz', kz'), then (vs, vs, vz', vz')
+  // segments of at most FEW query rows run transposed; PT: a stream's weights of them, two
+  // terms each (quantised caches have no room for 16 rows beside their converted tiles)
+  static constexpr int FEW = QUANT ? 8 : 16, PT = FEW * 2 * kTile * 2;
   static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr float CENTRE = KV == KV_U4T ? 8.f : 128.f;
 };
@@ -139,7 +142,7 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.vop = put(G::QUANT ? G::OPERAND : 0);
   o.ring = put(2 * entries * G::ENTRY);
   o.raw = put(entries * G::RAW_SCALES);
-  o.pt = put(2 * kPtBytes);
+  o.pt = put(2 * G::PT);
   o.xch = put(2 * 2 * 4 * 32 * 4);
   o.scales = put(kScaleSlots * G::SCALES);
   o.bars = put(kBarCount * 8);
@@ -618,7 +621,7 @@ static __device__ __noinline__ void sum_queries(const uint8_t* src, float* qsum,
 
 // For the merge: where the records of the rows' kv heads are (the block's share of
 // them), from the plan and the inputs; one warp.
-static __device__ __noinline__ void place_records(const SharedParams& p, const SharedPlan& pl) {
+static __device__ __noinline__ void place_records(const SharedParams& p, const SharedPlan& pl, int few_max) {
   const int lane = threadIdx.x & 31, Gq = p.group, B = p.batch, whole = 2 * B * p.num_q_heads;
   const Shares shares(pl.gpre[p.num_groups], pl.bpre[B], p.num_ctas);
 #pragma unroll 1
@@ -633,7 +636,7 @@ static __device__ __noinline__ void place_records(const SharedParams& p, const S
     };
     int4 own = make_int4(0, 0, 0, 0), pre = own, pre2 = own;
     uint32_t n = tiles_of(r.len - r.skip);
-    if (n > 0) own = place(pl.bpre[b] + h * n, n, ((p.num_kv_heads + h) * B + b) * Gq, 0, Gq <= kFew);
+    if (n > 0) own = place(pl.bpre[b] + h * n, n, ((p.num_kv_heads + h) * B + b) * Gq, 0, Gq <= few_max);
     if (r.group >= 0) {
       const int g = r.group, m0 = pl.moff[g], m1 = pl.moff[g + 1], rows = (m1 - m0) * Gq;
       int lo = m0, hi = m1;   // the row among the members, which are in ascending order
@@ -648,7 +651,7 @@ static __device__ __noinline__ void place_records(const SharedParams& p, const S
       for (int k = 0; k < 2; ++k) {   // a row's heads may lie in two pairs of row tiles
         const int pair = (uint32_t)(R + k * (Gq - 1)) / (2 * kTile);
         pre2 = place((rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, n, h * B * Gq + m0 * Gq + R,
-                     R - pair * 2 * kTile, rows - pair * 2 * kTile <= kFew);
+                     R - pair * 2 * kTile, rows - pair * 2 * kTile <= few_max);
         if (k == 0) pre = pre2;
       }
       pre.w |= (2 * kTile - R % (2 * kTile)) << 1;   // the head from which on the second holds
@@ -665,6 +668,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   using G = SharedGeom<D, KV, BF>;
   constexpr bool QUANT = G::QUANT;
   constexpr int NT = G::THREADS, COLS = QUANT ? 32 : 64;   // columns of a pass over the scores
+  constexpr int FEW = G::FEW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const SharedLayout& lay = p.lay;
@@ -817,7 +821,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
   if (nv <= 0) {   // uniform over the block
-    if (warp == 8) place_records(p, plan);
+    if (warp == 8) place_records(p, plan, FEW);
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
@@ -1007,7 +1011,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         const bool scores =
             v < end && !(pend.on && (pend.st == st || (flags & kFirst &&
                                                        !__all_sync(0xffffffffu, mbar_test(bar(kBarQFull + qs), (qt >> 1) & 1)))));
-        const bool few = rows <= kFew;
+        const bool few = rows <= FEW;
         const bool last_s = !two || u == 1;
         if (scores) {
           if (flags & kFirst) ok = wait_warp(kBarQFull + qs, (qt >> 1) & 1);
@@ -1017,7 +1021,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           const uint64_t qd = at(kmajor, qb + (uint32_t)qs * G::OPERAND);
           // S = Q K^T, rows x tokens; few rows: S^T = K Q^T, tokens x rows
           const uint64_t ad = few ? kd : qd, bd = few ? qd : kd;
-          const uint32_t idesc = kType | (uint32_t)(few ? kFew / 8 : kTile / 8) << 17;
+          const uint32_t idesc = kType | (uint32_t)(few ? 16 / 8 : kTile / 8) << 17;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ss(tm_s(st), ad + (k >> 2) * 1024 + (k & 3) * 2, bd + (k >> 2) * 1024 + (k & 3) * 2, idesc, k > 0, on);
@@ -1038,8 +1042,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (pend.few) {
             // O^T (+)= V^T [P1^T | P2^T]: channels x rows, first and second terms of
             // the weights side by side
-            constexpr uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(2 * kFew / 8) << 17;
-            const uint64_t pd = at(pmajor, pt + (uint32_t)ps * kPtBytes);
+            constexpr uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(2 * FEW / 8) << 17;
+            const uint64_t pd = at(pmajor, pt + (uint32_t)ps * G::PT);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               if (j < pend.steps) mma_ss(o, vd + j * 128, pd + j * 16, idesc, acc, on);
@@ -1112,7 +1116,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       for (int u = 0; u < tiles && ok; ++u, ++qc) {
         const int qs = qc & 1;
         if (qc >= 2 && !placed) {   // both tiles are in use: time for this
-          place_records(p, plan);
+          place_records(p, plan, FEW);
           placed = true;
         }
         if (qc >= 2) ok = wait_warp(kBarQEmpty + qs, ((qc >> 1) - 1) & 1);
@@ -1125,7 +1129,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
       }
     }
-    if (!placed) place_records(p, plan);
+    if (!placed) place_records(p, plan, FEW);
   } else if (warp >= 12) {
     // ============================ converters: K (12-15) and V (16-19)
     if constexpr (QUANT) {
@@ -1238,7 +1242,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       Visit s;
       ok = visit(v, s);
       if (!ok) break;
-      const bool two = s.is(kTwo), few = s.rows <= kFew;
+      const bool two = s.is(kTwo), few = s.rows <= FEW;
       const size_t rec0 = s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
                                            : (few ? st * whole : 0) + s.rec;
       const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + ((qc + (two ? st : 0)) % kQSums) * kTile;
@@ -1249,10 +1253,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         // rows in blocks of eight, of which the second may be empty. Lane j of every
         // warp holds row j's reference, each thread its token's part of the rows' sums.
         float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
-        uint8_t* pt = smem + lay.pt + st * kPtBytes;
+        uint8_t* pt = smem + lay.pt + st * G::PT;
         const bool wide = s.rows > 8;
-        float r = -INFINITY, l[kFew];
-        [[maybe_unused]] float zs[kFew];
+        float r = -INFINITY, l[FEW];
+        [[maybe_unused]] float zs[FEW];
         int flags = s.flags;
         for (;;) {
           if ((v & 1) == st) {
@@ -1260,12 +1264,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             if (!ok) break;
             if (!have) {
 #pragma unroll
-              for (int j = 0; j < kFew; ++j) {
+              for (int j = 0; j < FEW; ++j) {
                 l[j] = 0.f;
                 if constexpr (QUANT) zs[j] = 0.f;
               }
             }
-            float a[kFew];
+            float a[FEW];
             const int at = (row >> 1) * 4 + (row & 1);
             const float ks = QUANT ? sc[at] : p.scale;
             const float kz = QUANT ? sc[at + 2] : 0.f, vs = QUANT ? sc[2 * kTile + at] : 1.f;
@@ -1273,7 +1277,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             float* xb = xch + (n_x++ & 1) * (4 * 32);
             float keep = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < kFew; e += 8) {
+            for (int e = 0; e < FEW; e += 8) {
               if (e > 0 && !wide) break;
               tmem_ld<8>(ts + e, reinterpret_cast<uint32_t*>(a + e));
               float4 q4[2] = {};
@@ -1290,11 +1294,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 if (lane == e + j) keep = w;
               }
             }
-            if (lane < kFew) xb[quad * 32 + lane] = keep;
+            if (lane < FEW) xb[quad * 32 + lane] = keep;
             ok = meet_all();
             if (!ok) break;
             // lane j: the largest score of row j over the tile's tokens
-            xb += lane & (kFew - 1);
+            xb += lane & (FEW - 1);
             const float t = fmaxf(fmaxf(xb[0], xb[32]), fmaxf(xb[64], xb[96])) + lv;
             float alpha = 1.f;
             if (t > r + 8.f) {
@@ -1303,11 +1307,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             }
             if (have && __any_sync(0xffffffffu, alpha != 1.f)) {   // the same for the whole stream
 #pragma unroll
-              for (int e = 0; e < kFew; e += 8) {
+              for (int e = 0; e < FEW; e += 8) {
                 if (e > 0 && !wide) break;
                 uint32_t o[16];
                 tmem_ld<8>(to + e, o);
-                tmem_ld<8>(to + kFew + e, o + 8);
+                tmem_ld<8>(to + FEW + e, o + 8);
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -1318,13 +1322,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                   o[8 + j] = __float_as_uint(__uint_as_float(o[8 + j]) * f);
                 }
                 tmem_st<8>(to + e, o);
-                tmem_st<8>(to + kFew + e, o + 8);
+                tmem_st<8>(to + FEW + e, o + 8);
               }
               tc_wait_st();
             }
             const float ref = r == -INFINITY ? 0.f : r;
 #pragma unroll
-            for (int e = 0; e < kFew; e += 8) {
+            for (int e = 0; e < FEW; e += 8) {
               if (e > 0 && !wide) break;
               // weights of token `row`, first terms and what their rounding left, as
               // [8-row block][token][8]
@@ -1346,7 +1350,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 lo16[k / 2] = pack16<BF>(w[0] - low16<BF>(hi16[k / 2]), w[1] - high16<BF>(hi16[k / 2]));
               }
               *reinterpret_cast<uint4*>(pt + e * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
-              *reinterpret_cast<uint4*>(pt + (kFew + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
+              *reinterpret_cast<uint4*>(pt + (FEW + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
             }
             have = true;
             end_event();
@@ -1361,12 +1365,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         // ---- the stream's record of each row
         float* xb = xch + (n_x++ & 1) * (4 * 32);
 #pragma unroll
-        for (int e = 0; e < kFew; e += 8) {
+        for (int e = 0; e < FEW; e += 8) {
           if (e > 0 && !wide) break;
           int j;
           const float ls = scatter_sum8(l + e, lane, j);
           xb[quad * 32 + e + j] = ls;
-          if constexpr (QUANT) xb[quad * 32 + kFew + e + j] = scatter_sum8(zs + e, lane, j);
+          if constexpr (QUANT) xb[quad * 32 + FEW + e + j] = scatter_sum8(zs + e, lane, j);
         }
         ok = meet_all();
         if (!ok) break;
@@ -1386,14 +1390,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           for (int e = 0; e < s.rows; e += 8) {
             uint32_t o[16];
             tmem_ld<8>(to + e, o);
-            tmem_ld<8>(to + kFew + e, o + 8);
+            tmem_ld<8>(to + FEW + e, o + 8);
             tc_wait_ld();
             float* acc = p.ws_acc + (rec0 + e) * D + row;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               if (e + k >= s.rows) break;
               float f = __uint_as_float(o[k]) + __uint_as_float(o[8 + k]);
-              if constexpr (QUANT) f += total(kFew + e + k);
+              if constexpr (QUANT) f += total(FEW + e + k);
               acc[k * D] = f;
             }
           }
@@ -1558,20 +1562,21 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           to_c = from + D / 2;
         }
         if (row < my_rows && from == 0) p.ws_ml[rec0 + tile_row] = make_float2(R, L);
-        // 16 channels at a time through 2 KB of shared memory (the stream's place for
-        // transposed weights), so that a row's 64 bytes are written together
+        // CHUNK channels at a time through shared memory (the stream's place for transposed
+        // weights), so that a row's 64 (32) bytes are written together
         const uint32_t to2 = tm_o(st ^ 1) + lanes;
-        uint8_t* stage = smem + lay.pt + st * kPtBytes + quad * 2048;
+        constexpr int CHUNK = G::PT / 512, PARTS4 = CHUNK / 4;   // 16 or 8
+        uint8_t* stage = smem + lay.pt + st * G::PT + quad * (32 * CHUNK * 4);
         const int live = min(32, my_rows - quad * 32);   // the warp's query rows
-        float* out = p.ws_acc + (rec0 + tile_row - lane) * D + (lane & 3) * 4;
+        float* out = p.ws_acc + (rec0 + tile_row - lane) * D + (lane & (PARTS4 - 1)) * 4;
 #pragma unroll 1
-        for (int c = from; c < to_c; c += 16) {
-          uint32_t o[16], o2[16];
-          tmem_ld<16>(to + c, o);
-          if (both) tmem_ld<16>(to2 + c, o2);
+        for (int c = from; c < to_c; c += CHUNK) {
+          uint32_t o[CHUNK], o2[CHUNK];
+          tmem_ld<CHUNK>(to + c, o);
+          if (both) tmem_ld<CHUNK>(to2 + c, o2);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < CHUNK; j += 4) {
             float f[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -1579,14 +1584,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               if (both) f[k] = fmaf(__uint_as_float(o2[j + k]), f1, f[k] * f0);
               if constexpr (QUANT) f[k] += z;
             }
-            *reinterpret_cast<float4*>(stage + lane * 64 + ((j >> 2 ^ lane >> 1 & 3) << 4)) =
+            *reinterpret_cast<float4*>(stage + (lane * PARTS4 + (j >> 2 ^ lane / (8 / PARTS4) & (PARTS4 - 1))) * 16) =
                 make_float4(f[0], f[1], f[2], f[3]);
           }
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const int q = i + (lane >> 2);
-            const float4 f = *reinterpret_cast<const float4*>(stage + q * 64 + (((lane & 3) ^ (q >> 1 & 3)) << 4));
+          for (int i = 0; i < 32; i += 32 / PARTS4) {
+            const int q = i + lane / PARTS4, j = lane & (PARTS4 - 1);
+            const float4 f =
+                *reinterpret_cast<const float4*>(stage + (q * PARTS4 + (j ^ q / (8 / PARTS4) & (PARTS4 - 1))) * 16);
             if (q < live) *reinterpret_cast<float4*>(out + (size_t)q * D + c) = f;
           }
           __syncwarp();

@@ -6,6 +6,7 @@ append, scoring, selection and attention runs in libpkv's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Dict, Optional, Tuple
@@ -49,6 +50,8 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None) -> None:
 
 def _host_ids(ids, name: str) -> np.ndarray:
     """Page or row ids on the host as contiguous int32 (a list, an array or a CPU tensor)."""
+    if type(ids) is np.ndarray and ids.dtype == np.int32 and ids.ndim == 1 and ids.flags.c_contiguous:
+        return ids
     if isinstance(ids, torch.Tensor):
         if ids.is_cuda:
             raise ValueError(f"{name} must be on the host")
@@ -70,6 +73,16 @@ def _pair_ids(src, dst, what: str) -> Tuple[np.ndarray, np.ndarray]:
     if s.size != d.size:
         raise ValueError(f"{s.size} source and {d.size} destination {what}")
     return s, d
+
+
+def _addr(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]
+
+
+# torch's own way to the current stream's handle; the public one makes a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_same_device = contextlib.nullcontext()
 
 
 class PagedKVCache:
@@ -277,8 +290,16 @@ class PagedKVCache:
 
 
     # --------------------------------------------------- sequences that share pages
+    # (these calls may take less time on the device than their checks here: they are written
+    # for few Python operations)
+    def _on_device(self):
+        """Context in which the cache's device is the current one."""
+        if torch.cuda.current_device() == self.device.index:
+            return _same_device
+        return torch.cuda.device(self.device)
+
     def _launch_stream(self, stream: Optional[torch.cuda.Stream]) -> int:
-        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        return _raw_stream(self.device.index) if stream is None else stream.cuda_stream
 
     def copy_pages(self, src_pages, dst_pages, src_rows=None, dst_rows=None,
                    stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -286,10 +307,13 @@ class PagedKVCache:
         tail row dst_rows[i] of row src_rows[i] (per-group caches). The ids are on the host:
         lists, int32 arrays or CPU tensors, as PageAllocator.unshare and .compact give them."""
         sp, dp = _pair_ids(src_pages, dst_pages, "pages")
-        sr, dr = _pair_ids(() if src_rows is None else src_rows, () if dst_rows is None else dst_rows, "rows")
-        with torch.cuda.device(self.device):
-            B.copy_pages(self._desc, sp.size, sp.ctypes.data, dp.ctypes.data, sr.size, sr.ctypes.data,
-                         dr.ctypes.data, self._launch_stream(stream))
+        if src_rows is None and dst_rows is None:
+            n_rows = sr = dr = 0
+        else:
+            rows = _pair_ids(() if src_rows is None else src_rows, () if dst_rows is None else dst_rows, "rows")
+            n_rows, sr, dr = rows[0].size, _addr(rows[0]), _addr(rows[1])
+        with self._on_device():
+            B.copy_pages(self._desc, sp.size, _addr(sp), _addr(dp), n_rows, sr, dr, self._launch_stream(stream))
 
     def remap_table(self, block_table: torch.Tensor, src_pages, dst_pages,
                     stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -300,19 +324,21 @@ class PagedKVCache:
         sp, dp = _pair_ids(src_pages, dst_pages, "pages")
         if block_table.numel() == 0:
             return
-        with torch.cuda.device(self.device):
+        with self._on_device():
             B.remap_block_table(block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
-                                self.num_pages, sp.size, sp.ctypes.data, dp.ctypes.data,
-                                self._launch_stream(stream))
+                                self.num_pages, sp.size, _addr(sp), _addr(dp), self._launch_stream(stream))
 
     def shared_workspace(self, batch: int, num_q_heads: int, num_splits: int = 0,
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Workspace of shared_attention for these shapes, kept and reused by stream."""
-        key = ("shared", batch, num_q_heads, num_splits, self._launch_stream(stream))
+        with self._on_device():
+            return self._shared_workspace(batch, num_q_heads, num_splits, self._launch_stream(stream))
+
+    def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
+        key = (stream, batch, num_q_heads, num_splits, "shared")
         ws = self._ws.get(key)
         if ws is None:
-            with torch.cuda.device(self.device):
-                n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
+            n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
             ws = self._ws[key] = torch.empty(n, dtype=torch.uint8, device=self.device)
         return ws
 
@@ -330,33 +356,36 @@ class PagedKVCache:
         workspace: memory of shared_workspace()'s size for this call alone. By default one
         workspace per shape and stream is kept; graphs captured on one stream and replayed
         at the same time on others need one each."""
-        for t, n, dt, shape in ((q, "q", None, None), (block_table, "block_table", torch.int32, None),
-                                (seq_lens, "seq_lens", torch.int32, (q.shape[0],)),
-                                (prefix_group, "prefix_group", torch.int32, (q.shape[0],)),
-                                (prefix_lens, "prefix_lens", torch.int32, None)):
-            _need(t, n, dt, self.device)
-            if shape is not None and t.shape != shape:
-                raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
-        if q.dim() != 3 or q.shape[2] != self.head_dim:
-            raise ValueError(f"q must be [batch][heads][{self.head_dim}], got {list(q.shape)}")
-        if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or prefix_lens.dim() != 1:
-            raise ValueError("block_table must be [batch][pages] and prefix_lens [groups]")
+        index = -1 if self.device.index is None else self.device.index
+        for t, n in ((q, "q"), (block_table, "block_table"), (seq_lens, "seq_lens"), (prefix_group, "prefix_group"),
+                     (prefix_lens, "prefix_lens")):
+            if t.get_device() != index or not t.is_contiguous() or (t is not q and t.dtype is not torch.int32):
+                _need(t, n, None if t is q else torch.int32, self.device)
+        if q.dim() != 3 or block_table.dim() != 2 or prefix_lens.dim() != 1:
+            raise ValueError("q must be [batch][heads][channels], block_table [batch][pages], prefix_lens [groups]")
         Bsz, Hq, d = q.shape
+        rows, width = block_table.shape
+        if d != self.head_dim or rows != Bsz or seq_lens.shape != (Bsz,) or prefix_group.shape != (Bsz,):
+            raise ValueError(f"for q {list(q.shape)} and head_dim {self.head_dim}: block_table {list(block_table.shape)}, "
+                             f"seq_lens {list(seq_lens.shape)}, prefix_group {list(prefix_group.shape)}")
         if out is None:
             out = torch.empty((Bsz, Hq, d), dtype=out_dtype, device=self.device)
         else:
             _need(out, "out", None, self.device)
             if out.shape != q.shape:
                 raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-        with torch.cuda.device(self.device):
-            ws = workspace if workspace is not None else self.shared_workspace(Bsz, Hq, num_splits, stream)
-            _need(ws, "workspace", None, self.device)
+        with self._on_device():
+            st = self._launch_stream(stream)
+            if workspace is None:
+                ws = self._shared_workspace(Bsz, Hq, num_splits, st)
+            else:
+                ws = workspace
+                _need(ws, "workspace", None, self.device)
             B.shared_prefix_attention(
                 self._desc, Bsz, Hq, q.data_ptr(), pkv_dtype(q),
-                1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(),
-                block_table.shape[1], seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(),
-                prefix_lens.shape[0], out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(),
-                ws.numel() * ws.element_size(), _ptr(dev_status), self._launch_stream(stream))
+                1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(), width,
+                seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(), prefix_lens.shape[0],
+                out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(), ws.nbytes, _ptr(dev_status), st)
         return out
 
 

@@ -7,6 +7,7 @@
 // and handed to the kernels by value as launch parameters: no device list, no
 // host-to-device copy whose buffer would have to outlive the call, and nothing
 // the kernels could find wrong.
+#include <type_traits>
 #include <vector>
 
 #include "pkv_internal.h"
@@ -15,11 +16,14 @@ namespace pkv {
 namespace {
 
 // A launch's (source, destination) pairs. Launch parameters hold at most
-// 32764 bytes; short lists take the small form (their launch carries less).
-constexpr int kSmallPairs = 64, kLargePairs = 4000;
-template <int N>
+// 32764 bytes; short lists take the small form (their launch carries less), and ids
+// below 65536 are passed in 16 bits.
+constexpr int kSmallPairs = 64;
+template <class T>
+constexpr int kLargePairs = 16000 / (int)sizeof(T);
+template <class T, int N>
 struct PairList {
-  int32_t src[N], dst[N];
+  T src[N], dst[N];
 };
 
 struct CopyParams {
@@ -34,9 +38,9 @@ struct CopyParams {
 constexpr uint32_t kPiece = 16384;
 constexpr int kCopyThreads = 256;
 
-template <int N>
+template <class T, int N>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p,
-                                                                  const __grid_constant__ PairList<N> list) {
+                                                                  const __grid_constant__ PairList<T, N> list) {
   pdl_wait();
   pdl_launch_dependents();
   uint32_t e, part = 0, piece;
@@ -70,26 +74,34 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
   }
 }
 
-// Table entries that equal a source become its destination. Each block puts
-// the pairs into a hash table in shared memory (open addressing, at most half
-// full), then looks up a share of the entries. Sources are distinct and no
-// destination is a source (checked on the host), so neither the order of the
-// insertions nor that of several launches matters.
-constexpr int kRemapThreads = 256;
+// Table entries that equal a source become its destination. Block (x, y) puts
+// the y-th kRemapChunk pairs into a hash table in shared memory (open
+// addressing, at most half full, source and destination in one word), then looks up a
+// share of the entries. Sources are distinct and no destination is a source (checked on
+// the host), so an entry is changed by one block at most, whatever the order of the
+// blocks, insertions or launches. Pairs are split because the threads of a warp read
+// launch parameters at different places one after the other: 3635 pairs in each
+// block took 15 us, most of it there.
+constexpr int kRemapThreads = 256, kRemapChunk = 512, kRemapSlots = 2 * kRemapChunk;
+template <class T>
+using RemapSlot = std::conditional_t<sizeof(T) == 2, unsigned int, unsigned long long>;
 
-template <int N>
+template <class T, int N>
 __global__ void __launch_bounds__(kRemapThreads) remap_kernel(int32_t* __restrict__ table, long long entries, int n,
-                                                              const __grid_constant__ PairList<N> list) {
-  constexpr int SLOTS = N <= kSmallPairs ? 128 : 8192;   // a power of two, >= 2 N
-  extern __shared__ int32_t slots[];   // keys, then values
-  int32_t* val = slots + SLOTS;
-  for (int i = threadIdx.x; i < SLOTS; i += kRemapThreads) slots[i] = -1;
+                                                              const __grid_constant__ PairList<T, N> list) {
+  using Slot = RemapSlot<T>;
+  constexpr int BITS = 8 * (int)sizeof(T);
+  constexpr Slot kNone = ~(Slot)0;   // no pair: a page is not moved onto itself
+  __shared__ Slot slots[kRemapSlots];
+  for (int i = threadIdx.x; i < kRemapSlots; i += kRemapThreads) slots[i] = kNone;
   __syncthreads();
-  auto hash = [](int32_t x) { return (int)(((uint32_t)x * 2654435761u) >> 16) & (SLOTS - 1); };
-  for (int i = threadIdx.x; i < n; i += kRemapThreads) {
-    int h = hash(list.src[i]);
-    while (atomicCAS(&slots[h], -1, list.src[i]) != -1) h = (h + 1) & (SLOTS - 1);
-    val[h] = list.dst[i];
+  auto hash = [](uint32_t x) { return (int)((x * 2654435761u) >> 16) & (kRemapSlots - 1); };
+  const int first = blockIdx.y * kRemapChunk, end = min(n, first + kRemapChunk);
+  for (int i = first + threadIdx.x; i < end; i += kRemapThreads) {
+    const uint32_t key = (uint32_t)list.src[i];
+    const Slot pair = (Slot)key << BITS | (Slot)(uint32_t)list.dst[i];
+    int h = hash(key);
+    while (atomicCAS(&slots[h], kNone, pair) != kNone) h = (h + 1) & (kRemapSlots - 1);
   }
   __syncthreads();
   pdl_wait();
@@ -97,96 +109,72 @@ __global__ void __launch_bounds__(kRemapThreads) remap_kernel(int32_t* __restric
   const long long step = (long long)gridDim.x * kRemapThreads;
   for (long long i = (long long)blockIdx.x * kRemapThreads + threadIdx.x; i < entries; i += step) {
     const int32_t t = table[i];
-    if (t < 0) continue;
-    for (int h = hash(t); slots[h] != -1; h = (h + 1) & (SLOTS - 1)) {
-      if (slots[h] == t) {
-        table[i] = val[h];
+    if (t < 0 || (BITS == 16 && t > 0xFFFF)) continue;
+    for (int h = hash((uint32_t)t); slots[h] != kNone; h = (h + 1) & (kRemapSlots - 1)) {
+      if ((uint32_t)(slots[h] >> BITS) == (uint32_t)t) {
+        table[i] = (int32_t)(slots[h] & (((Slot)1 << BITS) - 1));
         break;
       }
     }
   }
 }
 
-// A set of small whole numbers with an O(1) clear of what was added; kept per
-// thread, so a call allocates only when a larger pool is seen.
-class Marks {
- public:
-  bool reserve(size_t n) {
-    try {
-      if (bits_.size() < (n + 63) / 64) bits_.resize((n + 63) / 64, 0);
-    } catch (...) {
-      return false;
-    }
-    return true;
-  }
-  bool add(uint32_t x) {   // false: was there
-    const uint64_t m = 1ull << (x & 63);
-    const bool had = bits_[x >> 6] & m;
-    bits_[x >> 6] |= m;
-    return !had;
-  }
-  bool has(uint32_t x) const { return bits_[x >> 6] >> (x & 63) & 1; }
-  void remove(uint32_t x) { bits_[x >> 6] &= ~(1ull << (x & 63)); }
-
- private:
-  std::vector<uint64_t> bits_;
-};
-
 // All entries of both lists in [0, limit), `once` without repeats, and none of
-// it in `other`.
+// it in `other`. The marks are kept per thread and left clear, so a call
+// allocates only when a larger pool is seen.
 pkv_status check_lists(int32_t n, const int32_t* once, const int32_t* other, int32_t limit) {
   if (n < 0 || (n > 0 && (!once || !other))) return PKV_ERR_INVALID_ARG;
-  for (int32_t i = 0; i < n; ++i)
-    if (once[i] < 0 || once[i] >= limit || other[i] < 0 || other[i] >= limit) return PKV_ERR_INVALID_ARG;
   if (n == 0) return PKV_OK;
-  static thread_local Marks marks;
-  if (!marks.reserve((size_t)limit)) return PKV_ERR_HOST_MEMORY;
-  pkv_status st = PKV_OK;
-  int32_t added = 0;
-  while (added < n && marks.add((uint32_t)once[added])) ++added;
-  if (added < n) st = PKV_ERR_INVALID_ARG;
-  for (int32_t i = 0; st == PKV_OK && i < n; ++i)
-    if (marks.has((uint32_t)other[i])) st = PKV_ERR_INVALID_ARG;
-  for (int32_t i = 0; i < added; ++i) marks.remove((uint32_t)once[i]);
-  return st;
+  uint32_t over = 0;
+  for (int32_t i = 0; i < n; ++i)
+    over |= (uint32_t)((uint32_t)once[i] >= (uint32_t)limit) | (uint32_t)((uint32_t)other[i] >= (uint32_t)limit);
+  if (over) return PKV_ERR_INVALID_ARG;
+  static thread_local std::vector<uint8_t> marks;
+  try {
+    if (marks.size() < (size_t)limit) marks.resize((size_t)limit, 0);
+  } catch (...) {
+    return PKV_ERR_HOST_MEMORY;
+  }
+  uint8_t* const seen = marks.data();
+  uint32_t bad = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t x = once[i];
+    bad |= seen[x];
+    seen[x] = 1;
+  }
+  for (int32_t i = 0; i < n; ++i) bad |= seen[other[i]];
+  for (int32_t i = 0; i < n; ++i) seen[once[i]] = 0;
+  return bad ? PKV_ERR_INVALID_ARG : PKV_OK;
 }
 
-template <int N>
+template <class T, int N>
 pkv_status launch_copy(CopyParams p, const int32_t* src, const int32_t* dst, const int32_t* src_rows,
                        const int32_t* dst_rows, cudaStream_t st) {
-  PairList<N> list;
+  PairList<T, N> list;
   const int np = (int)p.num_pairs, nr = (int)p.num_rows;
-  for (int i = 0; i < np; ++i) {
-    list.src[i] = src[i];
-    list.dst[i] = dst[i];
-  }
+  for (int i = 0; i < np; ++i) list.src[i] = (T)src[i];
+  for (int i = 0; i < np; ++i) list.dst[i] = (T)dst[i];
   for (int i = 0; i < nr; ++i) {
-    list.src[np + i] = src_rows[i];
-    list.dst[np + i] = dst_rows[i];
+    list.src[np + i] = (T)src_rows[i];
+    list.dst[np + i] = (T)dst_rows[i];
   }
   const unsigned grid = p.num_pairs * p.page_pieces + p.num_rows * p.pieces[4];
   void* args[] = {&p, &list};
-  const void* fn = reinterpret_cast<const void*>(&copy_pages_kernel<N>);
+  const void* fn = reinterpret_cast<const void*>(&copy_pages_kernel<T, N>);
   return launch_pdl(fn, dim3(grid), dim3(kCopyThreads), 0, st, args) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int N>
+template <class T, int N>
 pkv_status launch_remap(int32_t* table, long long entries, int n, const int32_t* src, const int32_t* dst,
                         cudaStream_t st) {
-  PairList<N> list;
-  for (int i = 0; i < n; ++i) {
-    list.src[i] = src[i];
-    list.dst[i] = dst[i];
-  }
-  constexpr size_t smem = (N <= kSmallPairs ? 128 : 8192) * 2 * sizeof(int32_t);
-  const void* fn = reinterpret_cast<const void*>(&remap_kernel<N>);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return PKV_ERR_CUDA;
+  PairList<T, N> list;
+  for (int i = 0; i < n; ++i) list.src[i] = (T)src[i];
+  for (int i = 0; i < n; ++i) list.dst[i] = (T)dst[i];
+  const void* fn = reinterpret_cast<const void*>(&remap_kernel<T, N>);
   const long long blocks = (entries + kRemapThreads - 1) / kRemapThreads;
   void* args[] = {&table, &entries, &n, &list};
-  return launch_pdl(fn, dim3((unsigned)(blocks < 304 ? blocks : 304)), dim3(kRemapThreads), smem, st, args) ==
-                 cudaSuccess
+  const dim3 grid((unsigned)(blocks < 304 ? blocks : 304), (unsigned)((n + kRemapChunk - 1) / kRemapChunk));
+  return launch_pdl(fn, grid, dim3(kRemapThreads), 0, st, args) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }
@@ -195,6 +183,8 @@ pkv_status launch_remap(int32_t* table, long long entries, int n, const int32_t*
 
 pkv_status copy_pages(const pkv_cache* c, int32_t n, const int32_t* src, const int32_t* dst, int32_t n_rows,
                       const int32_t* src_rows, const int32_t* dst_rows, cudaStream_t stream) {
+  // (no pool of this many pages fits a device: 1280 bytes is the smallest page's)
+  if (c->num_pages > (1 << 28) || c->tail_rows > (1 << 28)) return PKV_ERR_UNSUPPORTED;
   pkv_status st = check_lists(n, dst, src, c->num_pages);
   if (st != PKV_OK) return st;
   if (n_rows != 0 && (c->quant != PKV_QUANT_PER_GROUP64 || !c->tail)) return PKV_ERR_INVALID_ARG;
@@ -219,7 +209,11 @@ pkv_status copy_pages(const pkv_cache* c, int32_t n, const int32_t* src, const i
   const int64_t total = (int64_t)n + n_rows;
   if (total == 0) return PKV_OK;
   // as many pairs a launch as its parameters and its grid (below 2^31 blocks) hold
-  int64_t cap = total <= kSmallPairs ? kSmallPairs : kLargePairs;
+  const bool narrow = c->num_pages <= 65536 && (n_rows == 0 || c->tail_rows <= 65536);
+  const auto go = total <= kSmallPairs ? &launch_copy<int32_t, kSmallPairs>
+                  : narrow             ? &launch_copy<uint16_t, kLargePairs<uint16_t>>
+                                       : &launch_copy<int32_t, kLargePairs<int32_t>>;
+  int64_t cap = total <= kSmallPairs ? kSmallPairs : narrow ? kLargePairs<uint16_t> : kLargePairs<int32_t>;
   const int64_t widest = p.page_pieces > p.pieces[4] ? p.page_pieces : p.pieces[4];
   if (cap * widest >= (1ll << 31)) cap = ((1ll << 31) - 1) / widest;
   for (int64_t at = 0; at < total; at += cap) {
@@ -228,7 +222,6 @@ pkv_status copy_pages(const pkv_cache* c, int32_t n, const int32_t* src, const i
     const int64_t r0 = at > n ? at - n : 0, r1 = end > n ? end - n : 0;   // rows [r0, r1)
     p.num_pairs = (uint32_t)(p1 - p0);
     p.num_rows = (uint32_t)(r1 - r0);
-    auto go = cap <= kSmallPairs ? &launch_copy<kSmallPairs> : &launch_copy<kLargePairs>;
     st = go(p, src + p0, dst + p0, src_rows + r0, dst_rows + r0, stream);
     if (st != PKV_OK) return st;
   }
@@ -237,11 +230,16 @@ pkv_status copy_pages(const pkv_cache* c, int32_t n, const int32_t* src, const i
 
 pkv_status remap_block_table(int32_t* table, long long entries, int32_t num_pages, int32_t n, const int32_t* src,
                              const int32_t* dst, cudaStream_t stream) {
+  if (num_pages > (1 << 28)) return PKV_ERR_UNSUPPORTED;
   pkv_status st = check_lists(n, src, dst, num_pages);
   if (st != PKV_OK || n == 0 || entries == 0) return st;
-  for (int32_t at = 0; at < n; at += kLargePairs) {
-    const int m = n - at < kLargePairs ? n - at : kLargePairs;
-    auto go = m <= kSmallPairs ? &launch_remap<kSmallPairs> : &launch_remap<kLargePairs>;
+  const bool narrow = num_pages <= 65536;
+  const int cap = narrow ? kLargePairs<uint16_t> : kLargePairs<int32_t>;
+  for (int64_t at = 0; at < n; at += cap) {
+    const int m = n - at < cap ? (int)(n - at) : cap;
+    const auto go = m <= kSmallPairs ? &launch_remap<int32_t, kSmallPairs>
+                    : narrow         ? &launch_remap<uint16_t, kLargePairs<uint16_t>>
+                                     : &launch_remap<int32_t, kLargePairs<int32_t>>;
     st = go(table, entries, m, src + at, dst + at, stream);
     if (st != PKV_OK) return st;
   }

@@ -2,6 +2,8 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <set>
+#include <utility>
 
 #include "shared_kernel.cuh"
 
@@ -18,16 +20,45 @@ namespace {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Device {
-  int sms, smem;
+  int index = 0, sms = 0, smem = 0;
 };
 
+// The current device; its numbers are asked for once.
 pkv_status device(Device& d) {
+  constexpr int kMost = 64;
+  static std::mutex mu;
+  static Device known[kMost];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&d.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-    return PKV_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (dev < 0 || dev >= kMost) return PKV_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lk(mu);
+  if (known[dev].sms == 0) {
+    Device n;
+    n.index = dev;
+    if (cudaDeviceGetAttribute(&n.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return PKV_ERR_CUDA;
+    known[dev] = n;
+  }
+  d = known[dev];
   return PKV_OK;
+}
+
+// Let a kernel have the device's shared memory; once per device and kernel.
+pkv_status allow_smem(const void* fn, const Device& d) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  try {
+    std::lock_guard<std::mutex> lk(mu);
+    const auto key = std::make_pair(d.index, fn);
+    if (done.count(key)) return PKV_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem) != cudaSuccess)
+      return PKV_ERR_CUDA;
+    done.insert(key);
+    return PKV_OK;
+  } catch (...) {
+    return PKV_ERR_HOST_MEMORY;
+  }
 }
 
 // Workspace: each row's place in the plan, (m, l) by record row, accumulators.
@@ -89,7 +120,7 @@ const void* merge_kernel(int warps) {
 }  // namespace
 
 pkv_status shared_workspace_bytes(const pkv_cache* c, int batch, int num_q_heads, int num_splits, size_t& bytes) {
-  Device dev = {0, 0};
+  Device dev;
   if (num_splits == 0) {
     const pkv_status st = device(dev);
     if (st != PKV_OK) return st;
@@ -130,9 +161,8 @@ pkv_status launch_shared(const SharedArgs& a) {
   PKV_SIZES(128, KV_F16) PKV_SIZES(128, KV_BF16) PKV_SIZES(128, KV_I8T) PKV_SIZES(128, KV_I8G) PKV_SIZES(128, KV_U4T)
 #undef PKV_SIZES
   if (smem > dev.smem) return PKV_ERR_UNSUPPORTED;
-  // the limit is set to the device's, once and for all sizes
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem) != cudaSuccess)
-    return PKV_ERR_CUDA;
+  st = allow_smem(fn, dev);
+  if (st != PKV_OK) return st;
   if (kind == KV_F16 || kind == KV_BF16) {
     const uint64_t rows = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
     if (!pool_map(c->k_pages, rows, D, bf, p.tmap_k) || !pool_map(c->v_pages, rows, D, bf, p.tmap_v))

@@ -51,10 +51,11 @@ def test_copies_are_exact_and_touch_nothing_else(kind, hkv, d, ps, meta, n):
         assert np.array_equal(a, b)
 
 
-def test_long_lists_and_the_empty_one():
-    c = make_cache("u4t", 20001, 1, 64, 16, False)
+@pytest.mark.parametrize("pages", [20001, 70001])      # ids of 16 and of 32 bits
+def test_long_lists_and_the_empty_one(pages):
+    c = make_cache("u4t", pages, 1, 64, 16, False)
     before = bits(c)
-    order = np.random.default_rng(0).permutation(20001)
+    order = np.random.default_rng(0).permutation(pages)
     n = 9003                                    # more pairs than one launch holds
     c.copy_pages(order[:n], order[n:2 * n])
     c.copy_pages([], [])
@@ -62,28 +63,29 @@ def test_long_lists_and_the_empty_one():
     for a, b in zip(before, bits(c)):
         a[order[n:2 * n]] = a[order[:n]]
         assert np.array_equal(a, b)
-    table = np.random.default_rng(1).integers(-1, 20001, (37, 1001)).astype(np.int32)
+    table = np.random.default_rng(1).integers(-1, pages, (37, 1001)).astype(np.int32)
     table[3, 5], table[4, 6] = 10 ** 9, -(10 ** 9)     # ids outside the pool stay
     dev = int_dev(table)
     c.remap_table(dev, order[:n], order[n:2 * n])
-    to = np.arange(20001)
+    to = np.arange(pages)
     to[order[:n]] = order[n:2 * n]
-    ok = (table >= 0) & (table < 20001)
+    ok = (table >= 0) & (table < pages)
     assert np.array_equal(dev.cpu().numpy(), np.where(ok, to[np.where(ok, table, 0)], table))
 
 
-@pytest.mark.parametrize("n", [1, 63, 64, 65, 3999, 4000, 4001])
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 4000, 4001, 8000, 8001])
+@pytest.mark.parametrize("pages", [16100, 66000])
 @pytest.mark.parametrize("shape", [(1, 1), (3, 7), (64, 513)])
-def test_remap(n, shape):
-    c = make_cache("f16", 9000, 1, 64, 16, False)
+def test_remap(n, pages, shape):
+    c = make_cache("u4t", pages, 1, 64, 16, False)
     rng = np.random.default_rng(n)
-    order = rng.permutation(9000)
+    order = rng.permutation(pages)
     src, dst = order[:n], rng.choice(order[n:], n)     # several pages may become one
-    table = rng.integers(0, 9000, shape).astype(np.int32)
+    table = rng.integers(0, pages, shape).astype(np.int32)
     table.reshape(-1)[0] = src[0]
     dev = int_dev(table)
     c.remap_table(dev, src, dst)
-    to = np.arange(9000)
+    to = np.arange(pages)
     to[src] = dst
     assert np.array_equal(dev.cpu().numpy(), to[table])
 

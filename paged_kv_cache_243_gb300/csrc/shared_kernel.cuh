@@ -476,13 +476,14 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
       const int i = it * 128 + t, r = i / PER, c = i % PER;
       const uint4 v = *reinterpret_cast<const uint4*>(src + (size_t)i * 16);
       uint8_t* row = dst + (c >> 1) * 16384 + r * 128;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const bool h = c >> 1;   // (see below)
+      const uint32_t w[4] = {h ? v.z : v.x, h ? v.w : v.y, h ? v.x : v.z, h ? v.y : v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t w4 = w[k] >> 4;
         const uint4 o = make_uint4(pair_of_nibbles<BF>(w[k], w4, 0), pair_of_nibbles<BF>(w[k], w4, 1),
                                    pair_of_nibbles<BF>(w[k], w4, 2), pair_of_nibbles<BF>(w[k], w4, 3));
-        *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + k) ^ (r & 7)) << 4)) = o;
+        *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + (k ^ h * 2)) ^ (r & 7)) << 4)) = o;
       }
     }
   } else {
@@ -492,12 +493,15 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
       const int i = it * 128 + t, r = i / PER, c = i % PER;
       const uint4 v = *reinterpret_cast<const uint4*>(src + (size_t)i * 16);
       uint8_t* row = dst + (c >> 2) * 16384 + r * 128;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // Lanes of the second half write their pieces in another order, so that eight
+      // lanes reach all banks at once.
+      const bool h = c >> 2;
+      const uint32_t w[4] = {h ? v.z : v.x, h ? v.w : v.y, h ? v.x : v.z, h ? v.y : v.w};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint4 o = make_uint4(pair_of_bytes<BF>(w[2 * k], 0), pair_of_bytes<BF>(w[2 * k], 2),
                                    pair_of_bytes<BF>(w[2 * k + 1], 0), pair_of_bytes<BF>(w[2 * k + 1], 2));
-        *reinterpret_cast<uint4*>(row + ((((c & 3) * 2 + k) ^ (r & 7)) << 4)) = o;
+        *reinterpret_cast<uint4*>(row + ((((c & 3) * 2 + (k ^ h)) ^ (r & 7)) << 4)) = o;
       }
     }
   }
@@ -1044,19 +1048,38 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             // the weights side by side
             constexpr uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(2 * FEW / 8) << 17;
             const uint64_t pd = at(pmajor, pt + (uint32_t)ps * G::PT);
+            // (without a condition in between: with one, the products went out 100 cycles apart)
+            auto step = [&](int j) { mma_ss(o, vd + j * 128, pd + j * 16, idesc, acc, on); };
+            if (pend.steps == 8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (j < pend.steps) mma_ss(o, vd + j * 128, pd + j * 16, idesc, acc, on);
-              acc = 1;
+              for (int j = 0; j < 8; ++j) {
+                step(j);
+                acc = 1;
+              }
+            } else {
+#pragma unroll 1
+              for (int j = 0; j < pend.steps; ++j) {
+                step(j);
+                acc = 1;
+              }
             }
           } else {
             constexpr uint32_t idesc = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
+            auto step = [&](uint32_t a, int j) { mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc, acc, on); };
 #pragma unroll 1
             for (uint32_t a = tm_s(ps), last = a + (p.two_terms ? 16 : 0); a <= last; a += 16) {
+              if (pend.steps == 8) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (j < pend.steps) mma_ts(o, a + 32 * (j >> 1) + 8 * (j & 1), vd + j * 128, idesc, acc, on);
-                acc = 1;
+                for (int j = 0; j < 8; ++j) {
+                  step(a, j);
+                  acc = 1;
+                }
+              } else {
+#pragma unroll 1
+                for (int j = 0; j < pend.steps; ++j) {
+                  step(a, j);
+                  acc = 1;
+                }
               }
             }
           }

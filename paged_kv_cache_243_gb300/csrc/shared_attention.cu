@@ -139,10 +139,10 @@ pkv_status launch_shared(const SharedArgs& a) {
                    : c->quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G;
   // visits are counted in 32 bits: rows and prefixes at the table's full width
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
-  if (c->num_kv_heads * tiles * (2ll * a.batch + (long long)a.batch * group / (2 * kTile)) >= (1ll << 31) ||
-      (4ll * a.batch * a.num_q_heads + 512ll * a.num_splits) * D >= (1ll << 31))
-    return PKV_ERR_UNSUPPORTED;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
+  if (c->num_kv_heads * tiles * (2ll * a.batch + (long long)a.batch * group / (2 * kTile)) >= (1ll << 31) ||
+      (4ll * a.batch * a.num_q_heads + 512ll * ctas) * D >= (1ll << 31))
+    return PKV_ERR_UNSUPPORTED;
   const Work w = layout(c, a.batch, a.num_q_heads, ctas);
   if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < w.total)
     return PKV_ERR_WORKSPACE;

@@ -1238,6 +1238,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         // rows of V that hold no token of this segment may hold anything, NaN
         // too, and a weight of 0 would not clear it
         const int slot = v % S;
+        // (a slot's parity tells its last two uses apart, and V of v - 2 is done with: with a
+        // single slot, v - 1 has to be done with, too)
+        if (S == 1 && v > 0 && !wait_warp(kBarVEmpty, (v - 1) & 1)) return false;
         if (!wait_warp(kBarVFull + slot, (v / S) & 1)) return false;
         if (row < (ntok + 15) / 16 * 16 && !valid) {
           uint8_t* vr = smem + lay.ring + (size_t)(S + slot) * G::ENTRY + row * 128;

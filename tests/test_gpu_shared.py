@@ -115,6 +115,21 @@ def test_bf16_queries_on_quantised_caches(kind):
     sb.check(sb.run(q, torch.bfloat16), qf, 4, "bf16")
 
 
+@pytest.mark.parametrize("kind", ALL)
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_most_groups(kind, d):
+    # 1024 groups take so much shared memory that fp16/bf16 caches of 128 channels have one
+    # tile of K and V at a time: partial tiles right behind whole ones
+    rng = np.random.default_rng(d)
+    sb = SharedBatch(kind, 2, d, 64, [(256, [300, 44, 172, 1]), (130, [260, 2])],
+                     alone=[int(n) for n in rng.integers(129, 600, 12)], seed=21)
+    sb.prefix_dev = int_dev(np.concatenate([sb.prefix, np.full(1024 - len(sb.prefix), 64, dtype=np.int32)]))
+    q, qf = sb.queries(4)
+    for splits in (0, 1, 5):
+        sb.check(sb.run(q, num_splits=splits), qf, 4)
+    assert int(sb.status.item()) == 0
+
+
 def test_empty_rows_and_padding():
     # rows of length 0 (finished or padded), rows shorter than their group's prefix, a group with
     # no such rows at all, and no groups

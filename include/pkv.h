@@ -381,7 +381,7 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
  *   q            : [batch][num_q_heads][head_dim], F16 or BF16: for fp16/bf16
  *                  caches the cache's type, for INT8 and 4-bit caches either.
  *   out          : [batch][num_q_heads][head_dim] of out_dtype (F32/F16/BF16).
- *                  With a 16-bit out_dtype the softmax weights enter the
+ *                  With a 16-bit out_dtype the softmax weights may enter the
  *                  second product rounded to q's type (one rounding of the
  *                  size of the output's own); with F32 they enter as a sum of
  *                  two such values.
@@ -389,7 +389,9 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
  *   workspace    : >= pkv_shared_prefix_workspace_bytes(...) bytes, 256-byte
  *                  aligned, any contents. Two calls (two replays of captured
  *                  calls as well) that share one must not run concurrently.
- * num_q_heads / num_kv_heads is at most 128, batch and num_groups at most 1024.
+ * num_q_heads / num_kv_heads is at most 128, batch and num_groups at most 1024,
+ * num_splits at most 65535 (PKV_ERR_UNSUPPORTED beyond). Within one call nothing
+ * depends on the order in which blocks run: the same call gives the same bits.
  * Two launches, in stream order with everything before and after them.
  * A row with no tokens yields zeros.
  * Device errors: PKV_DEV_BAD_PAGE (16 tokens skipped at a time),
@@ -418,9 +420,12 @@ size_t pkv_shared_prefix_workspace_bytes(const pkv_cache* cache, int32_t batch, 
  *       returns. Within each pair of lists no destination may occur twice or
  *       be a source too; a source may be copied to several places. A captured
  *       call copies the same pages at every replay.
+ * An attention call right behind this one may not promise fresh_rows (this call
+ * writes old rows); the same holds behind pkv_remap_block_table.
  * Errors: PKV_ERR_INVALID_ARG for an id outside [0, num_pages) or
- * [0, tail_rows), a list as above, or rows for a cache without `tail`; nothing
- * is launched then.
+ * [0, tail_rows), a list as above, or rows for a cache without `tail`;
+ * PKV_ERR_UNSUPPORTED for more than 2^28 pages or rows, or a page of more than
+ * 2^30 bytes in one pool; nothing is launched then.
  */
 pkv_status pkv_copy_pages(const pkv_cache* cache, int32_t num_copies, const int32_t* src_pages,
                           const int32_t* dst_pages, int32_t num_rows, const int32_t* src_rows,

@@ -35,6 +35,13 @@ struct CopyParams {
   uint32_t num_pairs, num_rows;   // list entries [0, num_pairs) are pages, the next num_rows rows
 };
 
+// dst page := src page in every part, byte for byte. Bound by memory: each byte is read and
+// written once, past the caches' retention (streaming loads and stores: it comes back no
+// sooner than a step later). A block moves one 16 KB piece, four 16-byte loads in flight
+// per thread before the first store; pieces of all pages and parts are one grid, so that one
+// page of K and V (64 KB) is four blocks and 1024 pages are 16384. 1024 pages of 32 kv heads
+// x 16 x 128 bf16: 78.9 us, 6.8 TB/s, the rate of a plain copy; one page of 8 kv heads: 2 us,
+// the launch.
 constexpr uint32_t kPiece = 16384;
 constexpr int kCopyThreads = 256;
 
@@ -80,8 +87,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 // share of the entries. Sources are distinct and no destination is a source (checked on
 // the host), so an entry is changed by one block at most, whatever the order of the
 // blocks, insertions or launches. Pairs are split because the threads of a warp read
-// launch parameters at different places one after the other: 3635 pairs in each
-// block took 15 us, most of it there.
+// launch parameters at different places one after the other: 3635 pairs over a table
+// of 48 rows took 22 us with all of them in each block, and take 8 us so, the copy of
+// those pages 39 us.
 constexpr int kRemapThreads = 256, kRemapChunk = 512, kRemapSlots = 2 * kRemapChunk;
 template <class T>
 using RemapSlot = std::conditional_t<sizeof(T) == 2, unsigned int, unsigned long long>;

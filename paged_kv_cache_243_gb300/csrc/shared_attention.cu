@@ -200,8 +200,11 @@ pkv_status launch_shared(const SharedArgs& a) {
   void* args[] = {&p};
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
   const long long outs = (long long)a.batch * a.num_q_heads * D, units = (outs + 127) / 128;
-  // few rows have many records each
-  const int wpw = units < 16 * dev.sms ? 4 : 1;
+  // Few outputs have many records each, and four warps apiece do not fill the device; more of them
+  // are better off with a warp each. One warp against four: 64 units (2 rows x 64K) 58 and
+  // 50 us a call, 768 (24 rows x 16K, 4-bit) 44.8 and 41.9, 1024 (32 rows x 2K) 23.4 and 25.7,
+  // 2048 (64 rows x 8K, INT8) 58 and 60, 8192 (256 rows x 8K) 83 and 104.
+  const int wpw = units < 6 * dev.sms ? 4 : 1;
   const void* merge = D == 64 ? merge_kernel<64>(wpw) : merge_kernel<128>(wpw);
   const int per = 4 / wpw;
   return launch_pdl(merge, dim3((unsigned)((units + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess

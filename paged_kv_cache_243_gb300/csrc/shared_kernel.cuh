@@ -11,29 +11,40 @@
 // P is the group's prefix rounded down to 16 tokens (64 for per-group scales,
 // whose open group depends on what follows); the rest is read with the row.
 //
+// What bounds it. Bytes of K and V where a prefix serves few query rows, 4 d operations per
+// query row and token where it serves many; in between and for short calls the latency of
+// what follows one another: scores, softmax, P V.
+//
 // Work decomposition. A segment is one of the products above for one kv head:
 // up to 256 query rows over a token range. It is cut into tiles of 128 tokens; one
-// visit is one tile for all of the segment's rows. Visits of all segments are
-// laid end to end (prefixes first) and block c of N takes visits [c W / N,
-// (c + 1) W / N): every SM streams the same number of K/V tiles whatever the
+// visit is one tile for all of the segment's rows. The visits of all segments are
+// laid end to end and each block takes an equal share of them (see Shares), whatever the
 // lengths are. A block that covers part of a segment leaves a partial state; the
-// second launch merges them.
+// second launch merges them. Every block makes the plan for itself from the lengths: with a
+// launch of its own it would cost more than the 1.3 us that it takes.
 //
 // Inside a block (one per SM, TMEM fully used: two score tiles of 128 columns and two
 // accumulators of d columns):
-//   loader warp   TMA copies of K and V tiles, 16 tokens a box (a page may end every
-//                 16), into a ring; block-table entries one visit ahead
-//   MMA thread    S = Q K^T (both operands in shared memory, 128-byte swizzle), O += P V
-//                 (P in TMEM, over the scores it was made from; V as stored, MN-major)
-//   Q warp        gathers the rows' queries into the swizzled operand tile, a segment ahead
-//   2 x 4 softmax warps, one per stream; thread = query row
-// Two streams keep the tensor cores busy while the exponentials of the other are
-// computed: with more than 128 rows each stream has its own 128 rows and
-// both use every tile; otherwise the tiles alternate between the streams, which
-// merge when the segment ends.
+//   warps 0-7    softmax, four for each of two streams
+//   warps 8, 11  K and V tiles into a ring each, 16 tokens a copy (a page may end every 16);
+//                block-table entries of four visits a load, a batch ahead
+//   warp 9       the products: S of the next event, then P V of the one before
+//   warp 10      the next segment's queries into the swizzled operand tile; descriptions of
+//                the visits to come; for the merge, where the records will be
+//   12-15, 16-19 quantised caches: codes of K and of V into operand tiles
+// An event is a visit's scores for one row tile. Two streams keep the tensor cores busy
+// while the exponentials of the other are computed: with more than 128 rows each has its own
+// 128 rows and both use every tile; otherwise the tiles alternate between the streams,
+// whose states meet when the segment ends.
+//   Few rows (16, quantised caches 8): transposed, S^T = K Q^T and O^T = V^T P^T, a thread has
+//     a token, so that a tile costs 8 or 16 exponentials a thread and not 128. The weights'
+//     two terms are two halves of one operand.
+//   More: a thread has a query row. P lies in TMEM over the scores it was made from.
+// V enters as stored (MN-major); Q and K with 128-byte swizzle.
+//
 // Weights are 2^(s - r) with a reference r that follows the running maximum only when
 // that is over 8 above it: weights then stay below 2^8, and the accumulator in TMEM is rarely
-// rescaled.
+// rescaled. Maxima, sums and accumulators are fp32.
 //
 // INT8 and 4-bit caches: the codes enter the products as exact small integers, u - c
 // with c the middle code, made by four converter warps from the staged bytes;
@@ -41,7 +52,21 @@
 //   q . k = ks (q . (u - c)) + (kz + c ks) sum q
 //   sum p v = sum (p vs) (u - c) + sum p (vz + c vs)
 // There r follows the maximum plus log2 of the values' size, so that p vs stays inside
-// fp16's range.
+// fp16's range. (Scales folded into the codes would round every key to 11 bits, or 8.)
+//
+// Measured, both launches, back to back (peaks 6.78 TB/s, 1.91 PFLOP/s; d = 128):
+//   2 rows x 64K, 32 heads over 8, bf16      50 us, 5.3 TB/s; INT8 55 us, 4-bit 58 us
+//   64 rows alone x ~2K, bf16                87 us, 6.2 TB/s
+//   16 rows x 32K, 32 kv heads, bf16         90 us, 6.1 TB/s
+//   64 rows x 16K, 32 heads over 8, bf16     49 us, 0.35 PFLOP/s; INT8 74 us
+// Counters of the last kind: tensor pipe active 23 % of the cycles, issue slots 25 %, DRAM
+// 32 %: bound by the chain of an event (softmax 1600 cycles, then P V and S of 520 each
+// with 200-700 cycles of hand-over each), twice which is a visit's period of 4600.
+// INT8: softmax 6000 cycles (three reads of the scales, 96 registers).
+//
+// Code size is a cost of its own: the two SMs of a pair share an instruction cache, and
+// 155 KB of code took 16 rows x 32K from 97 to 117 us. So loops stay loops, waits and plans
+// are out of line, and each product is written once.
 #pragma once
 
 #include <type_traits>
@@ -112,9 +137,12 @@ struct SharedGeom {
   static constexpr int ROW = KV == KV_U4T ? D / 2 : (QUANT ? D : 2 * D);
   static constexpr int ENTRY = QUANT ? kTile * ROW : OPERAND;
   static constexpr int RAW_SCALES = QUANT ? (KV == KV_I8G ? 128 : kTile * 16) : 0;
-  static constexpr int SCALES = QUANT ? 4 * kTile * 4 : 0;   // of a visit: by pairs of tokens (ks, ks, kz', kz'), then (vs, vs, vz', vz')
-  // segments of at most FEW query rows run transposed; PT: a stream's weights of them, two
-  // terms each (quantised caches have no room for 16 rows beside their converted tiles)
+  // scales of a visit: by pairs of tokens (ks, ks, kz', kz'), then (vs, vs, vz', vz')
+  static constexpr int SCALES = QUANT ? 4 * kTile * 4 : 0;
+  // Segments of at most FEW query rows run transposed; PT: a stream's weights of them, two
+  // terms each. 16 against 8 on 16-bit caches: 16 rows x 32K 90.5 and 93.0 us, 32 rows x 2K
+  // 25.7 and 26.6, 256 rows x 8K 82.8 and 84.5, but 256 rows x ~128 alone, four query rows
+  // each, 44 and 41. Quantised caches have no room for 16 beside their converted tiles.
   static constexpr int FEW = QUANT ? 8 : 16, PT = FEW * 2 * kTile * 2;
   static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr float CENTRE = KV == KV_U4T ? 8.f : 128.f;
@@ -171,8 +199,9 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
 
 // Shares of the work. Visits are numbered: prefixes of more than one row tile first
 // (`heavy` of them), then the other prefixes, then the rows' own tokens. A heavy visit
-// counts as two units: it has twice the products and exponentials (measured 2.2 us
-// against 1.1-1.3 us). Block c of `blocks` gets the visits that start in its
+// counts as two units: it has twice the products and exponentials. (256 rows x 8K bf16,
+// 256 tokens of their own, with a ratio of 1, 1.5, 2, 3: 103, 92, 83, 95 us; INT8 with 1, 2,
+// 2.5, 3: 77, 60, 65, 67 us.) Block c of `blocks` gets the visits that start in its
 // share of the units; every share holds at least one.
 struct Shares {
   int heavy, blocks, q, r;   // units = blocks q + r
@@ -1641,10 +1670,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ the merge
-// Folds the records of 128 outputs (a query row, or two of 64 channels), from the
-// blocks of its prefix segment and of its own tokens: WPW warps each take every WPW-th
-// record, a lane 4 channels. Where the records are has been worked out by the
-// attention kernel: this kernel is short, as its code is fetched anew by every call.
+// out = sum 2^(m_i - M) a_i / sum 2^(m_i - M) l_i over the records of 128 outputs (a query
+// row, or two of 64 channels), from the blocks of its prefix segment and of its own
+// tokens: WPW warps each take every WPW-th record, a lane 4 channels. Bound by latency
+// (records come from L2, four at a time in flight per warp): 3 to 6 us a call, of which about 2
+// are the launch. Where the records are has been worked out by the attention kernel: this
+// kernel is short, as its code is fetched anew by every call.
 constexpr int kMergeThreads = 128;
 
 template <int D, int WPW>

@@ -86,11 +86,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 // addressing, at most half full, source and destination in one word), then looks up a
 // share of the entries. Sources are distinct and no destination is a source (checked on
 // the host), so an entry is changed by one block at most, whatever the order of the
-// blocks, insertions or launches. Pairs are split because the threads of a warp read
-// launch parameters at different places one after the other: 3635 pairs over a table
-// of 48 rows took 22 us with all of them in each block, and take 8 us so, the copy of
-// those pages 39 us.
-constexpr int kRemapThreads = 256, kRemapChunk = 512, kRemapSlots = 2 * kRemapChunk;
+// blocks, insertions or launches. Bound by building the tables, not by the entries
+// (4 bytes read each): pairs are split over blocks, 1024 to a table. 3635 pairs over
+// 48 x 512 and over 48 x 4096 entries: 10 and 26 us with 512 pairs to a table read through the
+// constant cache, 4.3 and 12 read as below, 5.0 and 8.6 with 1024, 7.9 and 9.6 with 2048;
+// one table of all of them took 22 us and more.
+constexpr int kRemapThreads = 256, kRemapChunk = 1024, kRemapSlots = 2 * kRemapChunk;
 template <class T>
 using RemapSlot = std::conditional_t<sizeof(T) == 2, unsigned int, unsigned long long>;
 
@@ -105,9 +106,13 @@ __global__ void __launch_bounds__(kRemapThreads) remap_kernel(int32_t* __restric
   __syncthreads();
   auto hash = [](uint32_t x) { return (int)((x * 2654435761u) >> 16) & (kRemapSlots - 1); };
   const int first = blockIdx.y * kRemapChunk, end = min(n, first + kRemapChunk);
+  // (as ordinary memory: by way of the constant cache the lanes of a warp, which read at different
+  // places, would be served one after the other)
+  const T *src = list.src, *dst = list.dst;
+  asm("" : "+l"(src), "+l"(dst));
   for (int i = first + threadIdx.x; i < end; i += kRemapThreads) {
-    const uint32_t key = (uint32_t)list.src[i];
-    const Slot pair = (Slot)key << BITS | (Slot)(uint32_t)list.dst[i];
+    const uint32_t key = (uint32_t)src[i];
+    const Slot pair = (Slot)key << BITS | (Slot)(uint32_t)dst[i];
     int h = hash(key);
     while (atomicCAS(&slots[h], kNone, pair) != kNone) h = (h + 1) & (kRemapSlots - 1);
   }

@@ -331,8 +331,8 @@ class PagedKVCache:
     def shared_workspace(self, batch: int, num_q_heads: int, num_splits: int = 0,
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Workspace of shared_attention for these shapes, kept and reused by stream."""
-        with self._on_device():
-            return self._shared_workspace(batch, num_q_heads, num_splits, self._launch_stream(stream))
+        with self._on_device() if stream is None else torch.cuda.stream(stream):
+            return self._shared_workspace(batch, num_q_heads, num_splits, _raw_stream(self.device.index))
 
     def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
         key = (stream, batch, num_q_heads, num_splits, "shared")
@@ -355,7 +355,13 @@ class PagedKVCache:
 
         workspace: memory of shared_workspace()'s size for this call alone. By default one
         workspace per shape and stream is kept; graphs captured on one stream and replayed
-        at the same time on others need one each."""
+        at the same time on others need one each.
+        stream: the call's, and that of the memory it allocates; the current one by default."""
+        if stream is not None:
+            # (memory allocated on another stream may still be in use there)
+            with torch.cuda.stream(stream):
+                return self.shared_attention(q, block_table, seq_lens, prefix_group, prefix_lens, sm_scale, out,
+                                             out_dtype, num_splits, dev_status, None, workspace)
         index = -1 if self.device.index is None else self.device.index
         for t, n in ((q, "q"), (block_table, "block_table"), (seq_lens, "seq_lens"), (prefix_group, "prefix_group"),
                      (prefix_lens, "prefix_lens")):
@@ -375,7 +381,7 @@ class PagedKVCache:
             if out.shape != q.shape:
                 raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
         with self._on_device():
-            st = self._launch_stream(stream)
+            st = _raw_stream(self.device.index)
             if workspace is None:
                 ws = self._shared_workspace(Bsz, Hq, num_splits, st)
             else:

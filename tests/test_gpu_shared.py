@@ -253,6 +253,23 @@ def test_streams_capture_and_devices():
         sb.check(o, qf2, 4)
 
 
+def test_an_explicit_stream_owns_the_call_and_its_memory():
+    sb = SharedBatch("f16", 2, 128, 16, [(300, [20, 5, 61])], alone=[33], seed=23)
+    q, qf = sb.queries(4)
+    ref = sb.run(q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        # the current stream is busy with memory that it gives back at once
+        torch.empty(1 << 20, device="cuda").fill_(float("nan"))
+        outs.append(sb.cache.shared_attention(q, sb.table_dev, sb.lens_dev, sb.group_dev, sb.prefix_dev, stream=s))
+    assert sb.cache.shared_workspace(sb.B, 8, stream=s) is not sb.cache.shared_workspace(sb.B, 8)
+    s.synchronize()
+    for o in outs:
+        assert torch.equal(o, ref)
+
+
 def test_same_call_twice_gives_the_same_bits():
     sb = SharedBatch("i8t", 4, 128, 16, [(3000, [400, 10, 70, 8])], alone=[900], seed=18)
     q, _ = sb.queries(4)

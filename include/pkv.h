@@ -393,7 +393,9 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
  * num_splits at most 65535 (PKV_ERR_UNSUPPORTED beyond). Within one call nothing
  * depends on the order in which blocks run: the same call gives the same bits.
  * Two launches, in stream order with everything before and after them.
- * A row with no tokens yields zeros.
+ * A row with no tokens yields zeros. A NaN score (from a query, or from a key or a scale that
+ * the row attends to) makes the row's output NaN, however the work is split; what lies
+ * behind a row's length, or in a page it skips, is never seen.
  * Device errors: PKV_DEV_BAD_PAGE (16 tokens skipped at a time),
  * PKV_DEV_BAD_POSITION (length beyond the table or negative: clamped),
  * PKV_DEV_BAD_GROUP (the row attends on its own), PKV_DEV_TIMEOUT.

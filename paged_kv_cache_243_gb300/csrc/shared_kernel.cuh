@@ -1718,7 +1718,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
       int r = k == 0 ? seg.x + st * whole : seg.y + (k - 1) * 2 * kTile + st * kTile;
       r = on ? r + gq : 0;
       ml[i] = __ldcg(p.ws_ml + r);
-      if (!on) ml[i].x = -INFINITY;
+      if (!on) ml[i] = make_float2(-INFINITY, 0.f);
       a[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (size_t)r * D + ch));
     }
     float Mn = M;
@@ -1730,7 +1730,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
     A = make_float4(A.x * f0, A.y * f0, A.z * f0, A.w * f0);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (ml[i].x == -INFINITY) continue;   // no token: its accumulator means nothing
+      // no token: its accumulator means nothing. (Maxima pass over NaN scores, so a record of
+      // nothing else has m = -inf too; its l is NaN, and so is what becomes of it.)
+      if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;
       const float f = fast_exp2(ml[i].x - Mr);
       L = fmaf(f, ml[i].y, L);
       A = make_float4(fmaf(f, a[i].x, A.x), fmaf(f, a[i].y, A.y), fmaf(f, a[i].z, A.z), fmaf(f, a[i].w, A.w));
@@ -1751,7 +1753,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
       M = Mn;
     }
   }
-  // no token at all: zeros (L is 0 only then; a NaN stays one)
+  // no token at all: zeros (L is 0 only then, or where every score is -inf; a NaN stays one)
   const float r = L == 0.f ? 0.f : 1.f / L;
   const float4 f = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
   if (p.out_dtype == PKV_F32) {

@@ -385,6 +385,10 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
  *                  second product rounded to q's type (one rounding of the
  *                  size of the output's own); with F32 they enter as a sum of
  *                  two such values.
+ *                  With F16 queries fp16's smallest step counts as well: a weight
+ *                  is at most 2^-32 of the row's largest one off (quantised
+ *                  caches: a weight times the token's value scale, 2^-28 of
+ *                  the largest such product).
  *   num_splits   : thread blocks that share the work; 0 = automatic.
  *   workspace    : >= pkv_shared_prefix_workspace_bytes(...) bytes, 256-byte
  *                  aligned, any contents. Two calls (two replays of captured

@@ -42,17 +42,21 @@
 //   More: a thread has a query row. P lies in TMEM over the scores it was made from.
 // V enters as stored (MN-major); Q and K with 128-byte swizzle.
 //
-// Weights are 2^(s - r) with a reference r that follows the running maximum only when
-// that is over 8 above it: weights then stay below 2^8, and the accumulator in TMEM is rarely
-// rescaled. Maxima, sums and accumulators are fp32.
+// Weights are 2^(s - r) with a reference r that follows the running maximum, less kWeightBits,
+// only when that is over 8 above it: the largest weight then lies in [2^7, 2^15], in the upper part
+// of fp16's range (2^-24 to 65504), so that the smallest still count, and the accumulator in TMEM
+// is rarely rescaled. Maxima, sums and accumulators are fp32.
 //
 // INT8 and 4-bit caches: the codes enter the products as exact small integers, u - c
 // with c the middle code, made by four converter warps from the staged bytes;
 // scales and zero points are applied in fp32:
 //   q . k = ks (q . (u - c)) + (kz + c ks) sum q
 //   sum p v = sum (p vs) (u - c) + sum p (vz + c vs)
-// There r follows the maximum plus log2 of the values' size, so that p vs stays inside
-// fp16's range. (Scales folded into the codes would round every key to 11 bits, or 8.)
+// There r follows the largest of score + log2(that token's value size), so that p vs stays inside
+// fp16's range and a large value of no weight costs the others no bits: few rows token by
+// token, more rows by the tile's largest score and largest size as long as the sizes in
+// the tile are within 2^kEvenBits of one another. (Scales folded into the codes would round every key
+// to 11 bits, or 8.)
 //
 // Measured, both launches, back to back (peaks 6.78 TB/s, 1.91 PFLOP/s; d = 128):
 //   2 rows x 64K, 32 heads over 8, bf16      50 us, 5.3 TB/s; INT8 55 us, 4-bit 58 us
@@ -100,6 +104,12 @@ constexpr int kScaleSlots = 3;
 // are done, when at most the last two events are still to be read, of tiles from t - 4 on.
 constexpr int kQSums = 6;
 constexpr int kMaxEntries = 6;    // ring entries of K, and of V
+// The largest weight (times its value's size) is stored as at least 2^kWeightBits, and 2^8 times as
+// much at most: 2^15 with sizes of at most 1.
+constexpr float kWeightBits = 7.f;
+// Value sizes of a tile that differ by more are looked at token by token: what the tile's largest
+// one costs the others stays below this many bits.
+constexpr int kEvenBits = 4;
 constexpr int kVisits = 64;      // visits described in shared memory, refilled by halves
 
 // Shared memory by offset from a 1024-byte boundary.
@@ -177,7 +187,7 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.hdr = put(kHdrs * 8);
   o.ml = put(2 * kTile * 16);
   o.qsum = put(G::QUANT ? kQSums * kTile * 4 : 0);
-  o.vmax = put(G::QUANT ? kScaleSlots * 16 : 0);
+  o.vmax = put(G::QUANT ? kScaleSlots * 32 : 0);
   o.misc = put(21 * 16);
   o.visits = put(kVisits * 32);
   o.bpre = put((batch + 1) * 4);
@@ -565,6 +575,14 @@ __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Log2 of the size of a quantised token's values, to the next whole number. Their size is that of a
+// step of the codes, or of the codes' middle, where that is far above it (the codes matter less
+// then). Within [-80, 122], so that weights, up to 2^15 / size, and their sums stay in fp32's range.
+__device__ __forceinline__ float value_size(float step, float middle) { return fmaxf(fabsf(step), fabsf(middle) * (1.f / 128.f)); }
+__device__ __forceinline__ int size_exponent(float size) {
+  return min(max((int)((__float_as_uint(size) + 0x7FFFFFu) >> 23), 47), 249) - 127;
 }
 
 // Whether a phase is over, without waiting.
@@ -1212,9 +1230,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           sc[2] = valid ? fmaf(G::CENTRE, z.x, z.y) * p.scale : 0.f;
           sc[2 * kTile] = valid ? z.z : 0.f;
           sc[2 * kTile + 2] = valid ? vz : 0.f;
-          // the values' size: a scale, or a zero point far above it (where the codes matter less)
-          const float vm = warp_max(valid ? fmaxf(z.z, fabsf(vz) * (1.f / 128.f)) : 0.f);
-          if (lane == 0) reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 16)[warp - 12] = vm;
+          // the largest of the values' sizes, and the smallest
+          const float size = value_size(z.z, vz);
+          const float most = warp_max(valid ? size : 0.f), least = -warp_max(valid ? -size : -INFINITY);
+          if (lane == 0) {
+            float* vm = reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 32) + (warp - 12);
+            vm[0] = most;
+            vm[4] = least;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1250,6 +1273,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     bool valid = false;   // token `row` of the tile
     const float* sc = nullptr;
     float lv = 0.f;
+    bool even = true;
     auto begin = [&]() -> bool {
       if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
       if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
@@ -1259,10 +1283,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       valid = row < ntok && (mask >> (row >> 4) & 1);
       if constexpr (QUANT) {
         sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
-        // log2 of the values' size, to the next whole number
-        const float4 m4 = *reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 16);
-        const uint32_t up = __float_as_uint(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))) + 0x7FFFFFu;
-        lv = (float)(min(max((int)(up >> 23), 27), 227) - 127);
+        const float4* vm = reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 32);
+        const int most = size_exponent(fmaxf(fmaxf(vm[0].x, vm[0].y), fmaxf(vm[0].z, vm[0].w)));
+        even = most - size_exponent(fminf(fminf(vm[1].x, vm[1].y), fminf(vm[1].z, vm[1].w))) <= kEvenBits;
+        lv = (float)most;
       } else if (ntok < kTile || mask != 0xFF) {
         // rows of V that hold no token of this segment may hold anything, NaN
         // too, and a weight of 0 would not clear it
@@ -1287,10 +1311,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarP + st));
     };
-    // Weights are 2^(score - r), for each query row with a reference r that follows
-    // (largest score) + lv, lv the log2 of the values' size (quantised caches; else 0),
-    // only once that is more than 8 above it: a weight times a value's scale stays
-    // within fp16's range, and the accumulator is rarely rescaled.
+    // Weights are 2^(score - r), for each query row with a reference r that follows the largest
+    // score (quantised caches: score + log2 of the token's value size) less kWeightBits, only
+    // once that is more than 8 above it: a weight (times a value's scale) stays within fp16's
+    // range, and the accumulator is rarely rescaled.
 
     bool ok = true;
     while (v < nv && ok) {
@@ -1329,6 +1353,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             const float ks = QUANT ? sc[at] : p.scale;
             const float kz = QUANT ? sc[at + 2] : 0.f, vs = QUANT ? sc[2 * kTile + at] : 1.f;
             [[maybe_unused]] const float vz = QUANT ? sc[2 * kTile + at + 2] : 0.f;
+            [[maybe_unused]] const float lt = QUANT ? (float)size_exponent(value_size(vs, vz)) : 0.f;
             float* xb = xch + (n_x++ & 1) * (4 * 32);
             float keep = -INFINITY;
 #pragma unroll
@@ -1345,16 +1370,16 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               for (int j = 0; j < 8; ++j) {
                 a[e + j] = QUANT ? fmaf(ks, a[e + j], kz * reinterpret_cast<const float*>(q4)[j]) : a[e + j] * ks;
                 if (!valid) a[e + j] = -INFINITY;
-                const float w = warp_max(a[e + j]);
+                const float w = warp_max(QUANT ? a[e + j] + lt : a[e + j]);
                 if (lane == e + j) keep = w;
               }
             }
             if (lane < FEW) xb[quad * 32 + lane] = keep;
             ok = meet_all();
             if (!ok) break;
-            // lane j: the largest score of row j over the tile's tokens
+            // lane j: the largest of row j over the tile's tokens
             xb += lane & (FEW - 1);
-            const float t = fmaxf(fmaxf(xb[0], xb[32]), fmaxf(xb[64], xb[96])) + lv;
+            const float t = fmaxf(fmaxf(xb[0], xb[32]), fmaxf(xb[64], xb[96])) - kWeightBits;
             float alpha = 1.f;
             if (t > r + 8.f) {
               alpha = fast_exp2(r - t);   // 0 from -inf
@@ -1512,7 +1537,27 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[COLS - 1]);
             }
             if constexpr (QUANT) tc_wait_st();
-            const float t = QUANT ? mx + lv : mx * p.scale;
+            if constexpr (QUANT) {
+              if (!even) {   // uniform over the block
+                mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < ntok; c += 8) {
+                  float a[8];
+                  tmem_ld<8>(ts + c, reinterpret_cast<uint32_t*>(a));
+                  tc_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    const float* v2 = sc + 2 * kTile + 2 * (c + (j & -2)) + (j & 1);
+                    mx = fmaxf(mx, a[j] + (float)size_exponent(value_size(v2[0], v2[2])));
+                  }
+                }
+              } else {
+                mx += lv;
+              }
+            } else {
+              mx *= p.scale;
+            }
+            const float t = mx - kWeightBits;
             float alpha = 1.f;
             if (t > r + 8.f) {
               alpha = fast_exp2(r - t);   // 0 from -inf

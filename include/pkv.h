@@ -102,7 +102,11 @@ typedef enum {
  *                      original values of each sequence's open (partially filled)
  *                      64-token group, kept so that every append re-quantises
  *                      the open group from its members. Row b belongs to batch
- *                      row b of kv_append. Contents are managed by kv_append.
+ *                      row b of kv_append. Contents are managed by kv_append; a
+ *                      new row is zero-filled, or begins with a sequence's token 0.
+ *                      Place 63 never holds originals (a full group is closed):
+ *                      its first 4 bytes are the int32 position at which the
+ *                      originals kept in that parity end (0: none).
  *   page_meta        : optional (NULL = no sparse metadata), fp32
  *                      [num_pages][num_kv_heads][2][head_dim]: per channel, the
  *                      minimum (row 0) and maximum (row 1) of the page's valid
@@ -155,7 +159,10 @@ void pkv_tuning_reload(void);
  * F16/BF16 caches store the values (converted to kv_dtype). INT8 caches
  * quantise: per token over head_dim values; per group over the group's
  * members, re-quantising the open group from the originals kept in `tail`
- * (closed groups never change). If page_meta is set, the bounding box of every
+ * (closed groups never change). Where a sequence goes on inside a group whose
+ * originals its row does not hold (forked inside a closed group, cut back by more
+ * than a group), the earlier members are what their stored codes say, at the
+ * cost of one more rounding. If page_meta is set, the bounding box of every
  * page the append touched is recomputed from the stored keys.
  * Quantiser (bit-exact definition, fp32 ops, ties to even):
  *   I8: s = (max - min) / 255; z = min; code = clamp(rint((x - z) / s), 0, 255) - 128,
@@ -420,8 +427,10 @@ size_t pkv_shared_prefix_workspace_bytes(const pkv_cache* cache, int32_t batch, 
 /*
  * copy_pages — page dst_pages[i] becomes a copy of page src_pages[i], in every
  * part the cache keeps (K, V, scales, boxes), and row dst_rows[i] of `tail` a
- * copy of row src_rows[i] (PER_GROUP64: the open group's originals, which a
- * forked sequence needs in its own batch row before it appends).
+ * copy of row src_rows[i]. PER_GROUP64: a forked sequence is given its parent's
+ * row in this way before it first appends, wherever it was forked, so that its
+ * row tells which originals it has. Without it what an earlier sequence left in
+ * the batch row could be taken for the child's.
  *   src_pages, dst_pages, src_rows, dst_rows : HOST arrays, read before the call
  *       returns. Within each pair of lists no destination may occur twice or
  *       be a source too; a source may be copied to several places. A captured
@@ -465,8 +474,11 @@ pkv_status pkv_alloc_reserve(pkv_allocator* a, int64_t seq_id, int32_t total_tok
                              int32_t page_size, int32_t* block_table_row, int32_t max_pages);
 /* Sequence `child`, which must not exist, gets the first ceil(tokens / page_size)
  * pages of `parent` as its own too; writes them into block_table_row as above.
- * The pages are shared: before either sequence writes into one of them, it
- * calls pkv_alloc_unshare. */
+ * The pages are shared: before either sequence, the parent too, writes into one
+ * of them, it calls pkv_alloc_unshare and copies what that replaces. With a
+ * PER_GROUP64 cache the child is also given the parent's row of originals
+ * (pkv_copy_pages); forked inside a closed 64-token group it goes on from that
+ * group's codes. */
 pkv_status pkv_alloc_fork(pkv_allocator* a, int64_t parent, int64_t child, int32_t tokens, int32_t page_size,
                           int32_t* block_table_row, int32_t max_pages);
 /* Give seq_id pages of its own in place of the shared ones from the page of

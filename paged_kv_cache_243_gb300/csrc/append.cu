@@ -210,10 +210,20 @@ __device__ __forceinline__ float* tail_row(const AppendParams& p, int b, int g, 
   return p.tail + ((((size_t)b * p.num_kv_heads + g) * 2 + kv) * 2 + parity) * 64 * p.head_dim;
 }
 
+// Which tokens' originals a row holds: the last of a group's 64 places is never needed (a group of
+// 64 is closed), so its first word holds the position at which they end; they begin where that
+// position's group does. 0: none. It shows when a sequence goes on inside a group whose originals
+// the row does not have, as after a fork inside a closed group.
+__device__ __forceinline__ int32_t* tail_end(const AppendParams& p, int b, int g, int kv, int parity) {
+  return reinterpret_cast<int32_t*>(tail_row(p, b, g, kv, parity) + 63 * p.head_dim);
+}
+
 // Per-64-token-group INT8. grid (group slot, kv head * 2 + kv, row); one block
 // re-quantises one group that received tokens: its members are the kept
 // originals of earlier tokens of the open group (tail) plus the new tokens.
 // write_tail: also keep the new members of a group that stays open.
+// Where the tail does not hold the earlier members, they are what their codes say (one more
+// rounding), and are kept in the tail from then on.
 // Each thread holds up to kGroupVec4 float4s of the group in registers; all
 // of its loads (tail and new tokens) are issued before the first use, and
 // before the block-table lookup, so the block pays about one memory latency.
@@ -236,6 +246,7 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_per_group_kernel(cons
   const int nf = (t_end - t0) * D / 4;      // float4s of the group
   const void* sp = kv ? p.v_new : p.k_new;
   const float* tl = tail_row(p, b, g, kv, gi & 1);
+  const int had = pos > t0 ? *tail_end(p, b, g, kv, gi & 1) : pos;
   float4 x[kGroupVec4];
 #pragma unroll
   for (int k = 0; k < kGroupVec4; ++k) {
@@ -247,6 +258,26 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_per_group_kernel(cons
     }
   }
   if (threadIdx.x == 0) ok_s = page_of(p, b, page_div(p, t0));
+  const int off0 = page_mod(p, t0);
+  const bool lost = had < pos || had > t0 + 63;   // uniform over the block
+  if (lost) {
+    const int phys = p.block_table[(size_t)b * p.max_pages + page_div(p, t0)];
+    if (phys >= 0 && phys < p.num_pages) {
+      const size_t row = ((size_t)phys * H + g) * p.page_size + off0;
+      const uint8_t* codes = reinterpret_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages) + row * D;
+      const float2 sz = *reinterpret_cast<const float2*>(p.kv_sz + row / 64 * 4 + kv * 2);
+      auto value = [&](uint32_t w, int i) { return __fadd_rn(__fmul_rn((float)(w >> (8 * i) & 0xFF), sz.x), sz.y); };
+#pragma unroll
+      for (int k = 0; k < kGroupVec4; ++k) {
+        const int f = threadIdx.x + k * kGroupThreads;
+        if (f < (pos - t0) * D / 4) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + 4 * f);
+          x[k] = make_float4(value(w, 0), value(w, 1), value(w, 2), value(w, 3));
+          *reinterpret_cast<float4*>(tail_row(p, b, g, kv, gi & 1) + 4 * f) = x[k];
+        }
+      }
+    }
+  }
   float mn = INFINITY, mx = -INFINITY;
 #pragma unroll
   for (int k = 0; k < kGroupVec4; ++k) {
@@ -277,7 +308,6 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_per_group_kernel(cons
   const float s = __fdiv_rn(__fsub_rn(mx, mn), 255.f);
   const float z = mn;
   const float rs = quant_recip(s);
-  const int off0 = page_mod(p, t0);
   uint8_t* dst = reinterpret_cast<uint8_t*>(kv ? p.v_pages : p.k_pages) +
                 (((size_t)phys * H + g) * p.page_size + off0) * D;
   float* tw = tail_row(p, b, g, kv, gi & 1);
@@ -298,6 +328,13 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_per_group_kernel(cons
     float* szp = p.kv_sz + (((size_t)phys * H + g) * (p.page_size / 64) + off0 / 64) * 4;
     szp[kv * 2 + 0] = s;
     szp[kv * 2 + 1] = z;
+    // (without write_tail the tail kernel has the last word on a group that stays open; originals
+    // of another group that this one did not overwrite stay)
+    int32_t* const ends = tail_end(p, b, g, kv, gi & 1);
+    if (keep || pos > t0)
+      *ends = keep ? t_end : pos;
+    else if (*ends > t0 && *ends < t0 + 64)
+      *ends = 0;
   }
 }
 
@@ -326,6 +363,8 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_group_bulk_kernel(con
   const uint16_t* ks = reinterpret_cast<const uint16_t*>(p.k_new);
   const uint16_t* vs = reinterpret_cast<const uint16_t*>(p.v_new);
   uint2 kr[NV], vr[NV];
+  int32_t* const ends = threadIdx.x < 2 ? tail_end(p, b, g, threadIdx.x, gi & 1) : nullptr;
+  const int had = ends ? *ends : 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int f = threadIdx.x + k * kGroupThreads;
@@ -396,6 +435,8 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_group_bulk_kernel(con
     float* szp = p.kv_sz + (((size_t)phys * H + g) * (p.page_size / 64) + off0 / 64) * 4;
     *reinterpret_cast<float4*>(szp) = make_float4(sk, kmn, sv, vmn);
   }
+  // originals of this group's earlier contents (the open group's are kept by the tail kernel, after this one)
+  if (had > t0 && had < t0 + 64) *ends = 0;
 }
 
 // Keeps the new members of each row's open group (appends longer than one
@@ -414,6 +455,7 @@ __global__ void append_tail_kernel(const AppendParams p) {
   const int first = max(t0, pos);
   const void* sp = kv ? p.v_new : p.k_new;
   float* tw = tail_row(p, b, g, kv, gi & 1);
+  if (threadIdx.x == 0) *tail_end(p, b, g, kv, gi & 1) = end;
   for (int i = threadIdx.x; i < (end - first) * D; i += blockDim.x) {
     const int tt = i / D, e = i - tt * D;
     const int tok = first + tt;

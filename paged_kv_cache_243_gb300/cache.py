@@ -132,6 +132,9 @@ class PagedKVCache:
             self.k_pages.data_ptr(), self.v_pages.data_ptr(), _ptr(self.kv_sz), _ptr(self.tail),
             0 if self.tail is None else self.tail.shape[0], _ptr(self.page_meta))
         self._ws: Dict[Tuple, torch.Tensor] = {}
+        self._shared_sizes: Dict[Tuple[int, int, int], int] = {}
+        self._shared_ws: Dict[int, torch.Tensor] = {}     # by stream
+        self._shared_lent: Dict[int, torch.Tensor] = {}   # by address
 
     @classmethod
     def from_pools(cls, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_dtype: str = "bf16",
@@ -330,16 +333,30 @@ class PagedKVCache:
 
     def shared_workspace(self, batch: int, num_q_heads: int, num_splits: int = 0,
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-        """Workspace of shared_attention for these shapes, kept and reused by stream."""
+        """A workspace large enough for shared_attention with these shapes: the stream's own, which
+        the cache also uses by default, until a larger call needs a larger one. It is kept alive
+        as long as the cache (a captured graph may refer to it)."""
         with self._on_device() if stream is None else torch.cuda.stream(stream):
-            return self._shared_workspace(batch, num_q_heads, num_splits, _raw_stream(self.device.index))
+            ws = self._shared_workspace(batch, num_q_heads, num_splits, _raw_stream(self.device.index))
+        self._shared_lent[ws.data_ptr()] = ws
+        return ws
 
     def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
-        key = (stream, batch, num_q_heads, num_splits, "shared")
-        ws = self._ws.get(key)
-        if ws is None:
-            n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
-            ws = self._ws[key] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        shape = (batch, num_q_heads, num_splits)
+        n = self._shared_sizes.get(shape)
+        if n is None:
+            n = self._shared_sizes[shape] = B.shared_prefix_workspace_bytes(self._desc, *shape)
+        if torch.cuda.is_current_stream_capturing():
+            # from the graph's memory pool and this call's alone: graphs share it with nothing that
+            # could run beside them, and it goes when they go
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        # One per stream, of any contents. A quarter more at a time, so that those lent out and
+        # outgrown add up to a few times the largest at most.
+        ws = self._shared_ws.get(stream)
+        if ws is None or ws.numel() < n:
+            if ws is not None:
+                n = max(n, ws.numel() + ws.numel() // 4)
+            ws = self._shared_ws[stream] = torch.empty(n, dtype=torch.uint8, device=self.device)
         return ws
 
     def shared_attention(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -353,9 +370,10 @@ class PagedKVCache:
         none) have their first prefix_lens[g] tokens in common, which are then read once.
         Results are those of attention(); see pkv_shared_prefix_attention in include/pkv.h.
 
-        workspace: memory of shared_workspace()'s size for this call alone. By default one
-        workspace per shape and stream is kept; graphs captured on one stream and replayed
-        at the same time on others need one each.
+        workspace: memory of shared_workspace()'s size for this call alone. By default the calls
+        of a stream share one that grows with them, and a call that torch.cuda.graph captures
+        has its own in the graph's memory pool. (A capture that does not go through
+        torch.cuda.graph needs the argument: nothing would keep the call's own memory.)
         stream: the call's, and that of the memory it allocates; the current one by default."""
         if stream is not None:
             # (memory allocated on another stream may still be in use there)

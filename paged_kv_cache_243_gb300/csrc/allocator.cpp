@@ -193,19 +193,16 @@ pkv_status pkv_alloc_free(pkv_allocator* a, int64_t seq_id) {
   auto it = a->owned.find(seq_id);
   if (it == a->owned.end()) return PKV_ERR_INVALID_ARG;
   return guarded([&] {
-    // from the first page on: the order in which they return to the list. A
-    // page that could not be added to the list stays owned.
-    std::vector<int32_t>& pages = it->second;
-    size_t i = 0;
+    // from the first page on: the order in which they return to the list
+    const size_t before = a->free_list.size();
     try {
-      for (; i < pages.size(); ++i) {
-        if (a->refs[pages[i]] == 1) a->free_list.push_back(pages[i]);
-        --a->refs[pages[i]];
-      }
+      for (int32_t pg : it->second)
+        if (a->refs[pg] == 1) a->free_list.push_back(pg);
     } catch (...) {
-      pages.erase(pages.begin(), pages.begin() + i);
+      while (a->free_list.size() > before) a->free_list.pop_back();
       throw;
     }
+    for (int32_t pg : it->second) --a->refs[pg];
     a->owned.erase(it);
     return PKV_OK;
   });

@@ -633,13 +633,8 @@ static __device__ __noinline__ void gather_queries(const SharedParams& p, const 
   }
   for (int r0 = 32 * w; r0 < rows; r0 += 32 * warps) {
     // lane i finds row r0 + i
-    const int R = s.q0 + u * kTile + r0 + lane;
-    int b = s.row, gq = R;
-    if (s.mem0 >= 0) {
-      const int m = R / p.group;
-      b = r0 + lane < rows ? members[s.mem0 + m] : 0;
-      gq = R - m * p.group;
-    }
+    const int R = s.q0 + u * kTile + r0 + lane, m = R / p.group, gq = R - m * p.group;
+    const int b = r0 + lane < rows ? members[s.mem0 + m] : 0;
     const int qrow = b * p.num_q_heads + s.head * p.group + gq;
     const int n = min(32, rows - r0), c = lane % CH;
 #pragma unroll 8

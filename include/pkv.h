@@ -401,7 +401,8 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
  *                  aligned, any contents. Two calls (two replays of captured
  *                  calls as well) that share one must not run concurrently.
  * num_q_heads / num_kv_heads is at most 128, batch and num_groups at most 1024,
- * num_splits at most 65535 (PKV_ERR_UNSUPPORTED beyond). Within one call nothing
+ * num_splits at most 65535, max_pages * page_size at most 2^31 - 257
+ * (PKV_ERR_UNSUPPORTED beyond); sm_scale is positive and below 1e30. Within one call nothing
  * depends on the order in which blocks run: the same call gives the same bits.
  * Two launches, in stream order with everything before and after them.
  * A row with no tokens yields zeros. A NaN score (from a query, or from a key or a scale that
@@ -435,8 +436,9 @@ size_t pkv_shared_prefix_workspace_bytes(const pkv_cache* cache, int32_t batch, 
  *       returns. Within each pair of lists no destination may occur twice or
  *       be a source too; a source may be copied to several places. A captured
  *       call copies the same pages at every replay.
- * An attention call right behind this one may not promise fresh_rows (this call
- * writes old rows); the same holds behind pkv_remap_block_table.
+ * An attention call right behind this one may not promise fresh_rows, nor a scoring
+ * call early_start (this call writes old rows and boxes); the same holds behind
+ * pkv_remap_block_table.
  * Errors: PKV_ERR_INVALID_ARG for an id outside [0, num_pages) or
  * [0, tail_rows), a list as above, or rows for a cache without `tail`;
  * PKV_ERR_UNSUPPORTED for more than 2^28 pages or rows, or a page of more than

@@ -795,8 +795,8 @@ pkv_status pkv_shared_prefix_attention(const pkv_cache* cache, int32_t batch, in
     return PKV_ERR_UNSUPPORTED;
   if (max_pages <= 0 || num_groups < 0) return PKV_ERR_INVALID_ARG;
   if (num_groups > 1024) return PKV_ERR_UNSUPPORTED;
-  // token positions are 32-bit, and so are tensor-copy row coordinates
-  if ((long long)max_pages * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  // token positions are 32-bit, rounded up to whole tiles, and so are tensor-copy row coordinates
+  if ((long long)max_pages * cache->page_size > INT32_MAX - 256) return PKV_ERR_UNSUPPORTED;
   if ((long long)cache->num_pages * cache->num_kv_heads * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (!(sm_scale > 0.f) || !(sm_scale < 1e30f)) return PKV_ERR_INVALID_ARG;
   if (batch == 0) return PKV_OK;

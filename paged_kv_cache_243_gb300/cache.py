@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import threading
 from typing import Dict, Optional, Tuple
 
 import numpy as np
@@ -135,6 +136,7 @@ class PagedKVCache:
         self._shared_sizes: Dict[Tuple[int, int, int], int] = {}
         self._shared_ws: Dict[int, torch.Tensor] = {}     # by stream
         self._shared_lent: Dict[int, torch.Tensor] = {}   # by address
+        self._shared_lock = threading.Lock()
 
     @classmethod
     def from_pools(cls, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_dtype: str = "bf16",
@@ -335,10 +337,12 @@ class PagedKVCache:
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """A workspace large enough for shared_attention with these shapes: the stream's own, which
         the cache also uses by default, until a larger call needs a larger one. It is kept alive
-        as long as the cache (a captured graph may refer to it)."""
+        as long as the cache (a captured graph may refer to it). During a capture: memory of the
+        graph's pool."""
         with self._on_device() if stream is None else torch.cuda.stream(stream):
             ws = self._shared_workspace(batch, num_q_heads, num_splits, _raw_stream(self.device.index))
-        self._shared_lent[ws.data_ptr()] = ws
+            if not torch.cuda.is_current_stream_capturing():
+                self._shared_lent[ws.data_ptr()] = ws
         return ws
 
     def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
@@ -368,12 +372,16 @@ class PagedKVCache:
                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Decode attention for q [B][Hq][d] where the rows of group g (prefix_group [B], -1:
         none) have their first prefix_lens[g] tokens in common, which are then read once.
-        Results are those of attention(); see pkv_shared_prefix_attention in include/pkv.h.
+        Results are those of attention() up to rounding: with a 16-bit out_dtype softmax weights
+        may be rounded once to q's type, where attention() keeps more; see
+        pkv_shared_prefix_attention in include/pkv.h. q is f16 or bf16, for 16-bit caches of the
+        cache's type.
 
         workspace: memory of shared_workspace()'s size for this call alone. By default the calls
         of a stream share one that grows with them, and a call that torch.cuda.graph captures
         has its own in the graph's memory pool. (A capture that does not go through
-        torch.cuda.graph needs the argument: nothing would keep the call's own memory.)
+        torch.cuda.graph needs the argument: nothing would keep the call's own memory.) Threads
+        that call on the same stream with an argument of their own each need separate ones.
         stream: the call's, and that of the memory it allocates; the current one by default."""
         if stream is not None:
             # (memory allocated on another stream may still be in use there)
@@ -405,11 +413,12 @@ class PagedKVCache:
             else:
                 ws = workspace
                 _need(ws, "workspace", None, self.device)
-            B.shared_prefix_attention(
-                self._desc, Bsz, Hq, q.data_ptr(), pkv_dtype(q),
-                1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(), width,
-                seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(), prefix_lens.shape[0],
-                out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(), ws.nbytes, _ptr(dev_status), st)
+            args = (self._desc, Bsz, Hq, q.data_ptr(), pkv_dtype(q),
+                    1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(), width,
+                    seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(), prefix_lens.shape[0],
+                    out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(), ws.nbytes, _ptr(dev_status), st)
+            with self._shared_lock:   # a call's two launches follow one another on the stream
+                B.shared_prefix_attention(*args)
         return out
 
 

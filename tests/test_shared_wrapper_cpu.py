@@ -1,6 +1,8 @@
 """What the wrappers for shared pages hand to the library, without a GPU: the device they make
 current, the stream they launch on, and the memory they keep."""
 import contextlib
+import threading
+import time
 import types
 
 import pytest
@@ -122,3 +124,30 @@ def test_a_captured_call_has_a_workspace_of_its_own(fake):
     state.capturing = False
     ws = [c["args"][15] for c in calls.named("shared_prefix_attention")]
     assert own.data_ptr() == ws[0] not in ws[1:] and cache._shared_ws[111] is own and kept(cache) == 3000
+    state.capturing = True
+    cache.shared_workspace(9, 4)
+    assert kept(cache) == 3000      # a graph's memory goes with the graph
+
+
+def test_threads_take_turns_on_the_workspace(fake, monkeypatch):
+    # a call is two launches with records in between: another thread's may not come between them
+    from paged_kv_cache_243_gb300 import cache as C
+    cache, calls, state = fake
+    inside, most = [], []
+
+    def call(*args):
+        inside.append(args[1])
+        most.append(len(inside))
+        time.sleep(0.002)
+        inside.remove(args[1])
+
+    monkeypatch.setattr(C.B, "shared_prefix_attention", call)
+    state.current = 1
+    monkeypatch.setattr(C.PagedKVCache, "_on_device", lambda self: contextlib.nullcontext())
+    threads = [threading.Thread(target=lambda b=b: [cache.shared_attention(*arguments(b)) for _ in range(10)])
+               for b in (2, 3, 5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(most) == 30 and max(most) == 1

@@ -133,8 +133,8 @@ class PagedKVCache:
             self.k_pages.data_ptr(), self.v_pages.data_ptr(), _ptr(self.kv_sz), _ptr(self.tail),
             0 if self.tail is None else self.tail.shape[0], _ptr(self.page_meta))
         self._ws: Dict[Tuple, torch.Tensor] = {}
-        self._shared_sizes: Dict[Tuple[int, int, int], int] = {}
         self._shared_ws: Dict[int, torch.Tensor] = {}     # by stream
+        self._shared_fit: Dict[Tuple[int, int, int, int], torch.Tensor] = {}   # the same, by stream and shape
         self._shared_lent: Dict[int, torch.Tensor] = {}   # by address
         self._shared_lock = threading.Lock()
 
@@ -346,11 +346,13 @@ class PagedKVCache:
         return ws
 
     def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
-        shape = (batch, num_q_heads, num_splits)
-        n = self._shared_sizes.get(shape)
-        if n is None:
-            n = self._shared_sizes[shape] = B.shared_prefix_workspace_bytes(self._desc, *shape)
-        if torch.cuda.is_current_stream_capturing():
+        capturing = torch.cuda.is_current_stream_capturing()
+        key = (stream, batch, num_q_heads, num_splits)
+        ws = self._shared_fit.get(key)
+        if ws is not None and not capturing:
+            return ws
+        n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
+        if capturing:
             # from the graph's memory pool and this call's alone: graphs share it with nothing that
             # could run beside them, and it goes when they go
             return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -361,6 +363,8 @@ class PagedKVCache:
             if ws is not None:
                 n = max(n, ws.numel() + ws.numel() // 4)
             ws = self._shared_ws[stream] = torch.empty(n, dtype=torch.uint8, device=self.device)
+            self._shared_fit.clear()
+        self._shared_fit[key] = ws
         return ws
 
     def shared_attention(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -413,12 +417,12 @@ class PagedKVCache:
             else:
                 ws = workspace
                 _need(ws, "workspace", None, self.device)
-            args = (self._desc, Bsz, Hq, q.data_ptr(), pkv_dtype(q),
+            with self._shared_lock:   # a call's two launches follow one another on the stream
+                B.shared_prefix_attention(
+                    self._desc, Bsz, Hq, q.data_ptr(), pkv_dtype(q),
                     1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(), width,
                     seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(), prefix_lens.shape[0],
                     out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(), ws.nbytes, _ptr(dev_status), st)
-            with self._shared_lock:   # a call's two launches follow one another on the stream
-                B.shared_prefix_attention(*args)
         return out
 
 

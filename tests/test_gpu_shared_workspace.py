@@ -17,13 +17,17 @@ def first(sb, q, n, **kw):
     return sb.cache.shared_attention(q[:n], sb.table_dev[:n], sb.lens_dev[:n], sb.group_dev[:n], sb.prefix_dev, **kw)
 
 
+def forget(cache):
+    for kept in (cache._shared_ws, cache._shared_fit, cache._shared_lent):
+        kept.clear()
+
+
 def test_every_batch_size_leaves_one_workspace():
     sb, q = batch(47, 1)
     ws = torch.empty_like(sb.cache.shared_workspace(48, 8))
     refs = {n: first(sb, q, n, workspace=ws) for n in range(1, 49)}
     most = ws.numel()
-    sb.cache._shared_ws.clear()
-    sb.cache._shared_lent.clear()
+    forget(sb.cache)
     before = torch.cuda.memory_allocated()
     for n in list(range(1, 49)) + list(range(48, 0, -1)):
         assert torch.equal(first(sb, q, n), refs[n])
@@ -33,7 +37,7 @@ def test_every_batch_size_leaves_one_workspace():
 def test_graphs_keep_their_workspace_when_larger_batches_come():
     sb, q = batch(47, 2)
     large = first(sb, q, 48)
-    sb.cache._shared_ws.clear()
+    forget(sb.cache)
     ref = first(sb, q, 4)
     out = torch.empty_like(ref)
     graph = torch.cuda.CUDAGraph()

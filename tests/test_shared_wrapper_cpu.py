@@ -61,7 +61,7 @@ def arguments(batch):
 
 
 def kept(cache):
-    return sum({t.data_ptr(): t.nbytes for d in (cache._ws, cache._shared_ws, cache._shared_lent)
+    return sum({t.data_ptr(): t.nbytes for d in (cache._ws, cache._shared_ws, cache._shared_fit, cache._shared_lent)
                 for t in d.values()}.values())
 
 

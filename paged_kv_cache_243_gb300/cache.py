@@ -83,6 +83,7 @@ def _addr(a: np.ndarray) -> int:
 # torch's own way to the current stream's handle; the public one makes a Stream object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 _same_device = contextlib.nullcontext()
 
 
@@ -341,12 +342,12 @@ class PagedKVCache:
         graph's pool."""
         with self._on_device() if stream is None else torch.cuda.stream(stream):
             ws = self._shared_workspace(batch, num_q_heads, num_splits, _raw_stream(self.device.index))
-            if not torch.cuda.is_current_stream_capturing():
+            if not _capturing():
                 self._shared_lent[ws.data_ptr()] = ws
         return ws
 
     def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
-        capturing = torch.cuda.is_current_stream_capturing()
+        capturing = _capturing()
         key = (stream, batch, num_q_heads, num_splits)
         ws = self._shared_fit.get(key)
         if ws is not None and not capturing:

@@ -42,7 +42,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: state.current)
     monkeypatch.setattr(torch.cuda, "device", on_device)
     monkeypatch.setattr(torch.cuda, "stream", on_stream)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
+    monkeypatch.setattr(C, "_capturing", lambda: state.capturing)
     monkeypatch.setattr(C, "_raw_stream", lambda index: state.streams[1])
     for name in ("copy_pages", "remap_block_table", "shared_prefix_attention"):
         monkeypatch.setattr(C.B, name, record(name))

@@ -372,7 +372,9 @@ pkv_status pkv_paged_decode_attention_noalloc(const pkv_cache* cache, int32_t ba
  * dense mode, where each prefix is read once for all rows of its group and
  * multiplied with all their query heads together. The pages have no
  * counterpart; it serves what pkv_alloc_fork makes (parallel samples, beams,
- * one system prompt in front of many requests).
+ * one system prompt in front of many requests). Below 2 rows a prefix with 16-bit
+ * caches, and below 2 to 16 with quantised ones (fewer the longer the prefix),
+ * pkv_paged_decode_attention on the same tables is the faster call.
  *   prefix_group : int32 [batch], the group of each row, in any order; -1: none.
  *   prefix_lens  : int32 [num_groups], the tokens that the rows of a group have
  *                  in common: tokens [0, prefix_lens[g]) hold the same values

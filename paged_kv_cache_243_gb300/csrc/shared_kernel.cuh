@@ -59,11 +59,11 @@
 // to 11 bits, or 8.)
 //
 // Measured, both launches, back to back (peaks 6.78 TB/s, 1.91 PFLOP/s; d = 128):
-//   2 rows x 64K, 32 heads over 8, bf16      50 us, 5.3 TB/s; INT8 55 us, 4-bit 58 us
+//   2 rows x 64K, 32 heads over 8, bf16      50 us, 5.3 TB/s; INT8 56 us, 4-bit 59 us
 //   64 rows alone x ~2K, bf16                87 us, 6.2 TB/s
 //   16 rows x 32K, 32 kv heads, bf16         90 us, 6.1 TB/s
-//   64 rows x 16K, 32 heads over 8, bf16     49 us, 0.35 PFLOP/s; INT8 74 us
-// Counters of the last kind: tensor pipe active 23 % of the cycles, issue slots 25 %, DRAM
+//   64 rows x 16K, 32 heads over 8, bf16     50 us, 0.34 PFLOP/s; INT8 74 us
+// Counters of 256 rows x 8K: tensor pipe active 23 % of the cycles, issue slots 25 %, DRAM
 // 32 %: bound by the chain of an event (softmax 1600 cycles, then P V and S of 520 each
 // with 200-700 cycles of hand-over each), twice which is a visit's period of 4600.
 // INT8: softmax 6000 cycles (two reads of the scales, 96 registers).

@@ -79,7 +79,9 @@ def outcome(sb, kf, vf, q, g, out_dtype):
                 values = np.abs(vv) if sb.kind == "f16" else np.full_like(vv, 8 if sb.kind == "u4t" else 128)
                 e += np.minimum(w, step * most) @ values
             if out_dtype != torch.float32:
-                e += (np.abs(out[b, h]) + e) * torch.finfo(out_dtype).eps / 2
+                # the output's own rounding: half a step of its type, whose smallest is 2^-24 in fp16
+                least = 2.0 ** -25 if out_dtype == torch.float16 else 0.0
+                e += np.maximum((np.abs(out[b, h]) + e) * torch.finfo(out_dtype).eps / 2, least)
             bound[b, h] = e + 1e-30
     return out, bound
 

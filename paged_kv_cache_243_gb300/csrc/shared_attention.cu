@@ -201,9 +201,10 @@ pkv_status launch_shared(const SharedArgs& a) {
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
   const long long outs = (long long)a.batch * a.num_q_heads * D, units = (outs + 127) / 128;
   // Few outputs have many records each, and four warps apiece do not fill the device; more of them
-  // are better off with a warp each. One warp against four: 64 units (2 rows x 64K) 58 and
-  // 50 us a call, 768 (24 rows x 16K, 4-bit) 44.8 and 41.9, 1024 (32 rows x 2K) 23.4 and 25.7,
-  // 2048 (64 rows x 8K, INT8) 58 and 60, 8192 (256 rows x 8K) 83 and 104.
+  // are better off with a warp each. One warp against four, us a call: 8 units (2 short rows) 10.8 and
+  // 11.2, 64 (2 rows x 64K) 59 and 51, INT8 65 and 56, 512 (16 rows x 32K) 94 and 91, 768 (24 rows x
+  // 16K, 4-bit) 45.6 and 42.5, 1024 (32 rows x 2K) 23.3 and 25.1, 2048 (64 rows x 16K) 49.4 and 48.1,
+  // (64 rows x 8K, INT8) 58.1 and 59.9, 3904 (5 groups x 5K) 46.6 and 57.6, 8192 (256 rows x 8K) 83 and 104.
   const int wpw = units < 6 * dev.sms ? 4 : 1;
   const void* merge = D == 64 ? merge_kernel<64>(wpw) : merge_kernel<128>(wpw);
   const int per = 4 / wpw;

@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define PKV_ABI_VERSION 7
+#define PKV_ABI_VERSION 8
 
 typedef enum {
   PKV_OK = 0,
@@ -460,6 +460,138 @@ pkv_status pkv_copy_pages(const pkv_cache* cache, int32_t num_copies, const int3
 pkv_status pkv_remap_block_table(int32_t* block_table, int32_t batch, int32_t max_pages, int32_t num_pages,
                                  int32_t num_moves, const int32_t* src_pages, const int32_t* dst_pages,
                                  void* stream);
+
+/*
+ * rotary_frequencies — the frequencies w_i = base^(-2 i / rot_dim) by which a token at position m
+ * turns its channels' pairs i (by the angle m w_i), and what they become in contexts longer than
+ * the model's own. The pages have no counterpart. Host code only.
+ *   rot_dim     : channels that turn, a multiple of 16 and at most 128.
+ *   scaling     : PKV_ROTARY_PLAIN   w_i
+ *                 PKV_ROTARY_LINEAR  w_i / factor
+ *                 PKV_ROTARY_BASE    with base factor^(rot_dim / (rot_dim - 2)) in place of base
+ *                 PKV_ROTARY_BANDS   w_i where the pair turns more than `high` times within `original`
+ *                                    tokens, w_i / factor below `low` times, in between in proportion
+ *                 PKV_ROTARY_RAMP    the same by the pair's index between those of the pairs that turn
+ *                                    `high` times (rounded down) and `low` times (up), and a
+ *                                    *table_scale of 0.1 ln(factor) + 1
+ *   factor      : at least 1; low, high, original: positive, low < high (BANDS and RAMP only).
+ *   inv_freq    : HOST, rot_dim / 2 values; table_scale: HOST, one value (1 but for RAMP).
+ */
+typedef enum {
+  PKV_ROTARY_PLAIN = 0,
+  PKV_ROTARY_LINEAR = 1,
+  PKV_ROTARY_BASE = 2,
+  PKV_ROTARY_BANDS = 3,
+  PKV_ROTARY_RAMP = 4
+} pkv_rotary_scaling;
+
+pkv_status pkv_rotary_frequencies(int32_t rot_dim, double base, pkv_rotary_scaling scaling, double factor, double low,
+                                  double high, double original, double* inv_freq, double* table_scale);
+
+/*
+ * rotary_table — cosines and sines for positions 0 .. positions - 1, worked out in 64 bits and
+ * rounded once: row m holds rot_dim / 2 cosines of m w_i, then the sines, all times table_scale. A
+ * program makes it once; any other fp32 table of this layout serves pkv_rotary_append as well.
+ *   cos_sin  : fp32 [positions][rot_dim], DEVICE memory, 16-byte aligned.
+ *   inv_freq : HOST, rot_dim / 2 values w_i, read before the call returns.
+ */
+pkv_status pkv_rotary_table(float* cos_sin, int32_t positions, int32_t rot_dim, const double* inv_freq,
+                            double table_scale, void* stream);
+
+/*
+ * rotary_append — pkv_kv_append of rotated keys, and the rotated queries of the same tokens. Of each
+ * head's channels the first rot_dim turn, those behind them pass. With c and s the table's row of
+ * the token's position, and a pair (x1, x2) of channels (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved = 1 (bit-exact definition, fp32 operations):
+ *   y1 = fl(fl(x1 c_i) - fl(x2 s_i)),  y2 = fl(fl(x2 c_i) + fl(x1 s_i)).
+ * Rotated queries are rounded once to src_dtype. Rotated keys are rounded once to a 16-bit cache's
+ * type, or quantised as pkv_kv_append quantises, from the fp32 values (which are also the originals
+ * that PER_GROUP64 keeps). Values are appended as by pkv_kv_append, and boxes refreshed.
+ *   q                : [batch][t_new][num_q_heads][head_dim] of src_dtype, with q_stride elements from a
+ *                      token to the next (of the next batch row as well): at least the heads' own, a
+ *                      multiple of 8. k_new, v_new: the same with num_kv_heads, k_stride and v_stride;
+ *                      so all three may be slices of one projection's output. num_q_heads = 0: no queries.
+ *   cos_sin          : fp32 [table_positions][rot_dim] as pkv_rotary_table lays it out.
+ *   rotary_positions : int32 [batch][t_new], the tokens' rows of the table (drafts of a tree turn by
+ *                      their depth); NULL: their positions in the sequence, positions[b] + t.
+ *   positions, new_lens, block_table: as for pkv_kv_append.
+ *   q_out            : [batch][t_new][num_q_heads][head_dim] of src_dtype. May be q itself where q_stride
+ *                      is num_q_heads * head_dim. Rows of tokens beyond new_lens[b], or of a batch row
+ *                      with a bad position, are left as they were.
+ * One launch; PER_GROUP64 two or three, and one more with boxes. An attention call right behind this
+ * one may not promise fresh_rows, nor a scoring call early_start: this call writes queries.
+ * Device errors: those of pkv_kv_append, and PKV_DEV_BAD_POSITION for a row beyond the table (the
+ * nearest one is taken).
+ */
+pkv_status pkv_rotary_append(const pkv_cache* cache, int32_t batch, int32_t t_new, int32_t num_q_heads, const void* q,
+                             const void* k_new, const void* v_new, pkv_dtype src_dtype, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float* cos_sin, int32_t table_positions,
+                             int32_t rot_dim, int32_t interleaved, const int32_t* rotary_positions,
+                             const int32_t* block_table, int32_t max_pages, const int32_t* positions,
+                             const int32_t* new_lens, void* q_out, int32_t* dev_status, void* stream);
+
+/*
+ * tree_attention — decode attention for several drafted tokens of each sequence at once. The last
+ * n_b = draft_lens[b] of the seq_lens[b] tokens in the cache are drafts (appended before the call),
+ * the others its context, of base_b = seq_lens[b] - n_b tokens:
+ *   out[b][t][h] = softmax(sm_scale * q[b][t][h] . K^T) V  over the context and the drafts j < n_b that
+ *                  draft t attends to, K and V of kv head h / G (G = num_q_heads / num_kv_heads).
+ * The pages have no counterpart; it verifies a tree (or a chain) of guesses in one pass over the
+ * context, which is read once for all drafts and all heads of a group.
+ *   t_draft    : drafts of a sequence at most, 0 to 256.
+ *   q          : [batch][t_draft][num_q_heads][head_dim], F16 or BF16: for fp16/bf16 caches the
+ *                cache's type, for INT8 and 4-bit caches either.
+ *   draft_lens : int32 [batch], or NULL for t_draft each.
+ *   tree_mask  : int64 [batch][t_draft][ceil(t_draft / 64)], or the same without [batch] and mask_shared =
+ *                1: bit j % 64 of word j / 64 says that draft t attends to draft j. Any set of drafts
+ *                will do; in a tree it is the path to t with t itself (nothing adds that).
+ *                NULL: draft t attends to drafts 0 .. t. Bits from n_b on mean nothing.
+ *   out        : [batch][t_draft][num_q_heads][head_dim] of out_dtype. Rows t >= n_b, and rows that
+ *                attend to nothing, are zeros. Roundings are those of pkv_shared_prefix_attention.
+ *   num_splits : thread blocks that share the work; 0 = automatic.
+ *   workspace  : >= pkv_tree_workspace_bytes(...) bytes, 256-byte aligned, any contents. Two calls (two
+ *                replays of captured calls as well) that share one must not run concurrently.
+ * What a row does not attend to never reaches it, infinities and NaNs included. Among what it attends to,
+ * a NaN score makes the row NaN, and a value that is an infinity or NaN makes its channel infinite or NaN.
+ * G is at most 128, batch at most 1024, num_splits at most 65535, max_pages * page_size at most
+ * 2^31 - 257, and the counts of query rows and tiles are 32-bit (PKV_ERR_UNSUPPORTED beyond);
+ * sm_scale is positive and below 1e30. The same call gives the same bits. Two launches, in stream
+ * order with everything before and after them.
+ * Device errors: PKV_DEV_BAD_PAGE (16 tokens skipped at a time), PKV_DEV_BAD_POSITION (a length
+ * beyond the table, or more drafts than t_draft or tokens: clamped), PKV_DEV_TIMEOUT.
+ */
+pkv_status pkv_tree_attention(const pkv_cache* cache, int32_t batch, int32_t t_draft, int32_t num_q_heads,
+                              const void* q, pkv_dtype q_dtype, float sm_scale, const int32_t* block_table,
+                              int32_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                              const int64_t* tree_mask, int32_t mask_shared, void* out, pkv_dtype out_dtype,
+                              int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                              void* stream);
+
+/* Workspace bytes of pkv_tree_attention for these shapes on the current device
+ * (num_splits as in the call); 0 on bad input. */
+size_t pkv_tree_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t t_draft, int32_t num_q_heads,
+                                int32_t num_splits);
+
+/*
+ * keep_tokens — keep the drafts that were accepted: token first[b] + keep[b][j] of row b becomes token
+ * first[b] + j, for j < keep_lens[b], in every part the cache keeps (K, V, scales). The sequence is
+ * then first[b] + keep_lens[b] tokens long. Boxes of the pages from token first[b] - 1 on are made
+ * anew for that length.
+ *   keep      : int32 [batch][max_keep], strictly ascending from 0 on (drafts are numbered from
+ *               first[b] on, each behind its parent); max_keep is at most 256.
+ *   keep_lens : int32 [batch], or NULL for max_keep each; 0 keeps nothing (boxes only).
+ *   first     : int32 [batch], the tokens before the drafts.
+ * Pages that it writes are the sequence's own (pkv_alloc_unshare). PER_GROUP64 is
+ * PKV_ERR_UNSUPPORTED: codes of another group's scale cannot be moved; append the accepted tokens
+ * anew with pkv_kv_append at first[b], which goes on from the originals of the open group.
+ * One launch. An attention call right behind this one may not promise fresh_rows, nor a
+ * scoring call early_start.
+ * Device errors: PKV_DEV_BAD_POSITION (a list or a length as above, or beyond the table: the row stays
+ * as it is), PKV_DEV_BAD_PAGE (the token stays).
+ */
+pkv_status pkv_keep_tokens(const pkv_cache* cache, int32_t batch, int32_t max_keep, const int32_t* keep,
+                           const int32_t* keep_lens, const int32_t* block_table, int32_t max_pages,
+                           const int32_t* first, int32_t* dev_status, void* stream);
 
 /*
  * Host page allocator [HBM-layout page, section 三 allocate_blocks /

@@ -6,7 +6,7 @@ arguments to the C ABI; `cache` wraps device tensors for PyTorch users.
 """
 from . import binding  # noqa: F401
 
-__all__ = ["binding", "build", "PagedKVCache", "PageAllocator"]
+__all__ = ["binding", "build", "PagedKVCache", "PageAllocator", "rotary_frequencies", "rotary_table", "tree_mask"]
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -15,7 +15,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
 
 
 def __getattr__(name):
-    if name in ("PagedKVCache", "PageAllocator"):
+    if name in __all__:
         from . import cache
         return getattr(cache, name)
     raise AttributeError(name)

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import Optional
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libpkv.so")
@@ -22,6 +22,7 @@ SELECT_PER_HEAD, SELECT_GROUP_SUM, SELECT_GROUP_MAX = 0, 1, 2
  ERR_HOST_MEMORY) = range(7)
 DEV_BAD_PAGE, DEV_BAD_SELECTED, DEV_BAD_POSITION, DEV_TIMEOUT, DEV_BAD_CONFIG = 1, 2, 4, 8, 16
 DEV_BAD_GROUP = 32
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_BANDS, ROTARY_RAMP = range(5)
 
 EXPORTED = [
     "pkv_status_string", "pkv_abi_version", "pkv_tuning_reload", "pkv_kv_append", "pkv_page_score_topk",
@@ -29,6 +30,8 @@ EXPORTED = [
     "pkv_paged_decode_attention_noalloc",
     "pkv_shared_prefix_attention", "pkv_shared_prefix_workspace_bytes", "pkv_copy_pages",
     "pkv_remap_block_table",
+    "pkv_rotary_frequencies", "pkv_rotary_table", "pkv_rotary_append", "pkv_tree_attention",
+    "pkv_tree_workspace_bytes", "pkv_keep_tokens",
     "pkv_alloc_create", "pkv_alloc_destroy", "pkv_alloc_reserve", "pkv_alloc_free",
     "pkv_alloc_fork", "pkv_alloc_unshare", "pkv_alloc_compact", "pkv_alloc_table", "pkv_alloc_page_refs",
     "pkv_alloc_num_free", "pkv_alloc_seq_pages", "pkv_alloc_check",
@@ -87,6 +90,14 @@ def lib() -> ctypes.CDLL:
         "pkv_shared_prefix_workspace_bytes": (c_size_t, [P, i32, i32, i32]),
         "pkv_copy_pages": (c_int, [P, i32, vp, vp, i32, vp, vp, vp]),
         "pkv_remap_block_table": (c_int, [vp, i32, i32, i32, i32, vp, vp, vp]),
+        "pkv_rotary_frequencies": (c_int, [i32, c_double, c_int, c_double, c_double, c_double, c_double, vp, vp]),
+        "pkv_rotary_table": (c_int, [vp, i32, i32, vp, c_double, vp]),
+        "pkv_rotary_append": (c_int, [P, i32, i32, i32, vp, vp, vp, c_int, i64, i64, i64, vp, i32, i32, i32, vp,
+                                      vp, i32, vp, vp, vp, vp, vp]),
+        "pkv_tree_attention": (c_int, [P, i32, i32, i32, vp, c_int, c_float, vp, i32, vp, vp, vp, i32, vp, c_int, i32,
+                                       vp, c_size_t, vp, vp]),
+        "pkv_tree_workspace_bytes": (c_size_t, [P, i32, i32, i32, i32]),
+        "pkv_keep_tokens": (c_int, [P, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
         "pkv_alloc_create": (c_int, [i32, POINTER(c_void_p)]),
         "pkv_alloc_destroy": (None, [vp]),
         "pkv_alloc_reserve": (c_int, [vp, i64, i32, i32, vp, i32]),
@@ -230,6 +241,55 @@ def remap_block_table(block_table: int, batch: int, max_pages: int, num_pages: i
     _check(lib().pkv_remap_block_table(block_table or None, batch, max_pages, num_pages, num_moves,
                                        src_pages or None, dst_pages or None, stream or None),
            "remap_block_table")
+
+
+def rotary_frequencies(rot_dim: int, base: float, scaling: int, factor: float, low: float, high: float,
+                       original: float, inv_freq: int, table_scale: int) -> None:
+    """inv_freq and table_scale are host addresses of doubles."""
+    _check(lib().pkv_rotary_frequencies(rot_dim, base, scaling, factor, low, high, original, inv_freq or None,
+                                        table_scale or None), "rotary_frequencies")
+
+
+def rotary_table(cos_sin: int, positions: int, rot_dim: int, inv_freq: int, table_scale: float, stream: int) -> None:
+    """inv_freq is a host address of doubles."""
+    _check(lib().pkv_rotary_table(cos_sin or None, positions, rot_dim, inv_freq or None, table_scale, stream or None),
+           "rotary_table")
+
+
+def rotary_append(cache: PkvCache, batch: int, t_new: int, num_q_heads: int, q: int, k_new: int, v_new: int,
+                  src_dtype: int, q_stride: int, k_stride: int, v_stride: int, cos_sin: int, table_positions: int,
+                  rot_dim: int, interleaved: int, rotary_positions: int, block_table: int, max_pages: int,
+                  positions: int, new_lens: int, q_out: int, dev_status: int, stream: int) -> None:
+    _check(lib().pkv_rotary_append(ctypes.byref(cache), batch, t_new, num_q_heads, q or None, k_new or None,
+                                   v_new or None, src_dtype, q_stride, k_stride, v_stride, cos_sin or None,
+                                   table_positions, rot_dim, interleaved, rotary_positions or None, block_table or None,
+                                   max_pages, positions or None, new_lens or None, q_out or None, dev_status or None,
+                                   stream or None), "rotary_append")
+
+
+def tree_workspace_bytes(cache: PkvCache, batch: int, t_draft: int, num_q_heads: int, num_splits: int) -> int:
+    n = lib().pkv_tree_workspace_bytes(ctypes.byref(cache), batch, t_draft, num_q_heads, num_splits)
+    if n == 0:
+        raise PkvError(ERR_INVALID_ARG, "tree_workspace_bytes")
+    return n
+
+
+def tree_attention(cache: PkvCache, batch: int, t_draft: int, num_q_heads: int, q: int, q_dtype: int, sm_scale: float,
+                   block_table: int, max_pages: int, seq_lens: int, draft_lens: int, tree_mask: int, mask_shared: int,
+                   out: int, out_dtype: int, num_splits: int, workspace: int, workspace_bytes: int, dev_status: int,
+                   stream: int) -> None:
+    _check(lib().pkv_tree_attention(ctypes.byref(cache), batch, t_draft, num_q_heads, q or None, q_dtype, sm_scale,
+                                    block_table or None, max_pages, seq_lens or None, draft_lens or None,
+                                    tree_mask or None, mask_shared, out or None, out_dtype, num_splits,
+                                    workspace or None, workspace_bytes, dev_status or None, stream or None),
+           "tree_attention")
+
+
+def keep_tokens(cache: PkvCache, batch: int, max_keep: int, keep: int, keep_lens: int, block_table: int, max_pages: int,
+                first: int, dev_status: int, stream: int) -> None:
+    _check(lib().pkv_keep_tokens(ctypes.byref(cache), batch, max_keep, keep or None, keep_lens or None,
+                                 block_table or None, max_pages, first or None, dev_status or None, stream or None),
+           "keep_tokens")
 
 
 def alloc_create(num_pages: int) -> int:

@@ -87,6 +87,67 @@ _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.
 _same_device = contextlib.nullcontext()
 
 
+_SCALING = {"plain": B.ROTARY_PLAIN, "linear": B.ROTARY_LINEAR, "base": B.ROTARY_BASE, "bands": B.ROTARY_BANDS,
+            "ramp": B.ROTARY_RAMP}
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                       low: float = 1.0, high: float = 4.0, original: float = 8192) -> Tuple[np.ndarray, float]:
+    """(frequencies of the rot_dim / 2 pairs, what a table is multiplied with), both in 64 bits.
+    scaling: "plain", or what pkv_rotary_frequencies in include/pkv.h calls "linear", "base", "bands" or
+    "ramp", with its factor, low, high and original."""
+    if scaling not in _SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+    w, scale = np.empty(max(1, rot_dim // 2), dtype=np.float64), np.empty(1, dtype=np.float64)
+    B.rotary_frequencies(rot_dim, base, _SCALING[scaling], factor, low, high, original, _addr(w), _addr(scale))
+    return w, float(scale[0])
+
+
+def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, device: str = "cuda",
+                 stream: Optional[torch.cuda.Stream] = None, **scaling) -> torch.Tensor:
+    """The table [positions][rot_dim] of cosines and sines for PagedKVCache.rotary_append (one serves all
+    layers). Further arguments: rotary_frequencies'."""
+    w, scale = rotary_frequencies(rot_dim, base, **scaling)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        out = torch.empty((positions, rot_dim), dtype=torch.float32, device=device)
+        with torch.cuda.device(out.device):
+            B.rotary_table(out.data_ptr(), positions, rot_dim, _addr(w), scale, _raw_stream(out.device.index))
+    return out
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """Masks for PagedKVCache.tree_attention of trees given by every draft's parent (an earlier
+    draft, or -1): int64 [..., T, ceil(T / 64)] on the host, for parents [T] or [batch][T]."""
+    p = np.asarray(parents.cpu().numpy() if isinstance(parents, torch.Tensor) else parents)
+    if p.ndim not in (1, 2) or p.dtype.kind not in "iu":
+        raise TypeError("parents must be whole numbers, [drafts] or [batch][drafts]")
+    T = p.shape[-1]
+    if p.size and (p.min() < -1 or (p >= np.arange(T)).any()):
+        raise ValueError("the parent of a draft is an earlier one, or -1")
+    rows = p.reshape(-1, T)
+    mask = np.zeros((rows.shape[0], T, -(-T // 64)), dtype=np.uint64)
+    every = np.arange(rows.shape[0])
+    for t in range(T):
+        mask[:, t] = np.where((rows[:, t] >= 0)[:, None], mask[every, rows[:, t]], np.uint64(0))
+        mask[:, t, t // 64] |= np.uint64(1 << t % 64)
+    return torch.from_numpy(mask.view(np.int64).reshape(*p.shape, -1))
+
+
+def _token_stride(t: torch.Tensor, name: str, shape: Tuple[int, ...], device: int) -> int:
+    """Elements from a token of t [batch][tokens][heads][channels] to the next, of which the tokens may
+    have any number but the heads lie together."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the cache's device")
+    rows, tokens, heads, d = shape
+    s0, s1, s2, s3 = t.stride()
+    step = s1 if tokens > 1 else s0 if rows > 1 else heads * d
+    if s3 != 1 or (heads > 1 and s2 != d) or (rows > 1 and tokens > 1 and s0 != tokens * s1):
+        raise ValueError(f"{name}: a token's heads must lie together, and tokens at one distance")
+    return step
+
+
 class PagedKVCache:
     """One layer's paged K/V pools (see pkv_cache in include/pkv.h for layouts)."""
 
@@ -135,7 +196,7 @@ class PagedKVCache:
             0 if self.tail is None else self.tail.shape[0], _ptr(self.page_meta))
         self._ws: Dict[Tuple, torch.Tensor] = {}
         self._shared_ws: Dict[int, torch.Tensor] = {}     # by stream
-        self._shared_fit: Dict[Tuple[int, int, int, int], torch.Tensor] = {}   # the same, by stream and shape
+        self._shared_fit: Dict[Tuple[int, int, int, int, int], torch.Tensor] = {}   # the same, by stream and shape
         self._shared_lent: Dict[int, torch.Tensor] = {}   # by address
         self._shared_lock = threading.Lock()
 
@@ -346,13 +407,18 @@ class PagedKVCache:
                 self._shared_lent[ws.data_ptr()] = ws
         return ws
 
-    def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int) -> torch.Tensor:
+    def _shared_workspace(self, batch: int, num_q_heads: int, num_splits: int, stream: int,
+                          t_draft: int = 0) -> torch.Tensor:
+        """For shared_attention, or with t_draft for tree_attention."""
         capturing = _capturing()
-        key = (stream, batch, num_q_heads, num_splits)
+        key = (stream, batch, num_q_heads, num_splits, t_draft)
         ws = self._shared_fit.get(key)
         if ws is not None and not capturing:
             return ws
-        n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
+        if t_draft:
+            n = B.tree_workspace_bytes(self._desc, batch, t_draft, num_q_heads, num_splits)
+        else:
+            n = B.shared_prefix_workspace_bytes(self._desc, batch, num_q_heads, num_splits)
         if capturing:
             # from the graph's memory pool and this call's alone: graphs share it with nothing that
             # could run beside them, and it goes when they go
@@ -425,6 +491,146 @@ class PagedKVCache:
                     seq_lens.data_ptr(), prefix_group.data_ptr(), prefix_lens.data_ptr(), prefix_lens.shape[0],
                     out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(), ws.nbytes, _ptr(dev_status), st)
         return out
+
+    # ------------------------------------------------------- steps with drafted tokens
+    def _ints(self, *named) -> None:
+        """Each (tensor, name, shape): int32 of that shape on the cache's device; None passes."""
+        index = -1 if self.device.index is None else self.device.index
+        for t, name, shape in named:
+            if t is None:
+                continue
+            if t.get_device() != index or t.dtype is not torch.int32 or not t.is_contiguous():
+                _need(t, name, torch.int32, self.device)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+    def rotary_append(self, q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                      cos_sin: torch.Tensor, block_table: torch.Tensor, positions: torch.Tensor,
+                      rotary_positions: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                      interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                      dev_status: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+        """append() of the keys k_new [B][T][Hkv][d], rotated, and the values v_new; returns the queries
+        q [B][T][Hq][d] of the same tokens, rotated (q may be None). All three may be slices of one
+        projection's output. cos_sin: a rotary_table. rotary_positions [B][T]: where the tokens
+        stand in it, by default at their positions in the sequence. interleaved: pairs of
+        neighbouring channels instead of the rotated part's two halves. q_out may be q itself.
+        Behind this call an attention call has no fresh_rows to promise: the queries are new."""
+        if stream is not None:
+            with torch.cuda.stream(stream):   # q_out is allocated on it
+                return self.rotary_append(q, k_new, v_new, cos_sin, block_table, positions, rotary_positions, new_lens,
+                                          interleaved, q_out, dev_status)
+        if k_new.dim() != 4 or block_table.dim() != 2 or cos_sin.dim() != 2 or (q is not None and q.dim() != 4):
+            raise ValueError("q, k_new, v_new must be [batch][tokens][heads][channels], block_table [batch][pages], "
+                             "cos_sin [positions][channels]")
+        index = -1 if self.device.index is None else self.device.index
+        Bsz, T = k_new.shape[:2]
+        d, dtype = self.head_dim, k_new.dtype
+        shape = (Bsz, T, self.num_kv_heads, d)
+        ks = _token_stride(k_new, "k_new", shape, index)
+        vs = _token_stride(v_new, "v_new", shape, index)
+        if v_new.dtype is not dtype or (q is not None and q.dtype is not dtype):
+            raise TypeError("q, k_new and v_new must have one type")
+        if cos_sin.get_device() != index or cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
+            _need(cos_sin, "cos_sin", torch.float32, self.device)
+        width = block_table.shape[1]
+        self._ints((block_table, "block_table", (Bsz, width)), (positions, "positions", (Bsz,)),
+                   (rotary_positions, "rotary_positions", (Bsz, T)), (new_lens, "new_lens", (Bsz,)))
+        Hq = qs = qp = op = 0
+        if q is not None:
+            Hq = q.shape[2]
+            qs = _token_stride(q, "q", (Bsz, T, Hq, d), index)
+            if q_out is None:
+                q_out = torch.empty((Bsz, T, Hq, d), dtype=dtype, device=self.device)
+            elif q_out.shape != q.shape or q_out.dtype is not dtype or q_out.get_device() != index or \
+                    not q_out.is_contiguous():
+                raise ValueError(f"q_out must be {list(q.shape)}, contiguous and of q's type and device")
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        with self._on_device():
+            B.rotary_append(self._desc, Bsz, T, Hq, qp, k_new.data_ptr(), v_new.data_ptr(), pkv_dtype(k_new), qs, ks, vs,
+                            cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
+                            _ptr(rotary_positions), block_table.data_ptr(), width, positions.data_ptr(), _ptr(new_lens),
+                            op, _ptr(dev_status), _raw_stream(self.device.index))
+        return q_out if q is not None else None
+
+    def tree_workspace(self, batch: int, t_draft: int, num_q_heads: int, num_splits: int = 0,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """shared_workspace's counterpart for tree_attention (one memory for both)."""
+        with self._on_device() if stream is None else torch.cuda.stream(stream):
+            ws = self._shared_workspace(batch, num_q_heads, num_splits, _raw_stream(self.device.index), t_draft)
+            if not _capturing():
+                self._shared_lent[ws.data_ptr()] = ws
+        return ws
+
+    def tree_attention(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                       mask: Optional[torch.Tensor] = None, draft_lens: Optional[torch.Tensor] = None,
+                       sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       out_dtype: torch.dtype = torch.float32, num_splits: int = 0,
+                       dev_status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Decode attention for the T drafts q [B][T][Hq][d] of each sequence, which are the last of its
+        seq_lens tokens in the cache (draft_lens [B] of them, by default T): each attends to the tokens
+        before the drafts and to those drafts that mask, int64 [B][T][ceil(T / 64)] or [T][ceil(T / 64)],
+        has a bit for (tree_mask makes one; None: all up to itself). Rows beyond draft_lens are zeros.
+        workspace, stream: as for shared_attention."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.tree_attention(q, block_table, seq_lens, mask, draft_lens, sm_scale, out, out_dtype,
+                                           num_splits, dev_status, None, workspace)
+        if q.dim() != 4 or block_table.dim() != 2:
+            raise ValueError("q must be [batch][drafts][heads][channels], block_table [batch][pages]")
+        index = -1 if self.device.index is None else self.device.index
+        Bsz, T, Hq, d = q.shape
+        if d != self.head_dim:
+            raise ValueError(f"q has {d} channels, the cache {self.head_dim}")
+        if q.get_device() != index or not q.is_contiguous():
+            _need(q, "q", None, self.device)
+        width = block_table.shape[1]
+        self._ints((block_table, "block_table", (Bsz, width)), (seq_lens, "seq_lens", (Bsz,)),
+                   (draft_lens, "draft_lens", (Bsz,)))
+        if mask is not None:
+            if mask.get_device() != index or mask.dtype is not torch.int64 or not mask.is_contiguous():
+                _need(mask, "mask", torch.int64, self.device)
+            if mask.shape[-2:] != (T, (T + 63) // 64) or (mask.dim() != 2 and mask.shape[:-2] != (Bsz,)):
+                raise ValueError(f"mask must be {[Bsz, T, (T + 63) // 64]}, with or without the first, got {list(mask.shape)}")
+        if out is None:
+            out = torch.empty((Bsz, T, Hq, d), dtype=out_dtype, device=self.device)
+        else:
+            _need(out, "out", None, self.device)
+            if out.shape != q.shape:
+                raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+        if T == 0 or Bsz == 0:
+            return out
+        with self._on_device():
+            st = _raw_stream(self.device.index)
+            if workspace is None:
+                ws = self._shared_workspace(Bsz, Hq, num_splits, st, T)
+            else:
+                ws = workspace
+                _need(ws, "workspace", None, self.device)
+            with self._shared_lock:   # a call's two launches follow one another on the stream
+                B.tree_attention(
+                    self._desc, Bsz, T, Hq, q.data_ptr(), pkv_dtype(q),
+                    1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale), block_table.data_ptr(), width,
+                    seq_lens.data_ptr(), _ptr(draft_lens), _ptr(mask), 1 if mask is not None and mask.dim() == 2 else 0,
+                    out.data_ptr(), pkv_dtype(out), num_splits, ws.data_ptr(), ws.nbytes, _ptr(dev_status), st)
+        return out
+
+    def keep_tokens(self, keep: torch.Tensor, keep_lens: Optional[torch.Tensor], block_table: torch.Tensor,
+                    first: torch.Tensor, dev_status: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Token first[b] + keep[b][j] of row b becomes token first[b] + j, for j < keep_lens[b] (by default
+        all of keep [B][K], strictly ascending): of the drafts from first[b] on the accepted
+        path stays. Not for per-group caches: append the accepted tokens anew at first[b]."""
+        if keep.dim() != 2 or block_table.dim() != 2:
+            raise ValueError("keep must be [batch][tokens], block_table [batch][pages]")
+        Bsz, K = keep.shape
+        width = block_table.shape[1]
+        self._ints((keep, "keep", (Bsz, K)), (keep_lens, "keep_lens", (Bsz,)), (block_table, "block_table", (Bsz, width)),
+                   (first, "first", (Bsz,)))
+        with self._on_device():
+            B.keep_tokens(self._desc, Bsz, K, keep.data_ptr(), _ptr(keep_lens), block_table.data_ptr(), width,
+                          first.data_ptr(), _ptr(dev_status), self._launch_stream(stream))
 
 
 class PageAllocator:

@@ -175,6 +175,36 @@ pkv_status check_cache(const pkv_cache* c, bool need_pools) {
   return PKV_OK;
 }
 
+AppendParams append_params(const pkv_cache* cache, int batch, int t_new, const void* k_new, const void* v_new,
+                           int src_dtype, const int32_t* block_table, int max_pages, const int32_t* positions,
+                           const int32_t* new_lens, int32_t* dev_status) {
+  AppendParams p = {};
+  p.k_pages = cache->k_pages;
+  p.v_pages = cache->v_pages;
+  p.kv_sz = cache->kv_sz;
+  p.tail = cache->tail;
+  p.page_meta = cache->page_meta;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.block_table = block_table;
+  p.positions = positions;
+  p.new_lens = new_lens;
+  p.dev_status = dev_status;
+  p.num_pages = cache->num_pages;
+  p.page_size = cache->page_size;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.head_dim = cache->head_dim;
+  p.kv_dtype = cache->kv_dtype;
+  p.quant = cache->quant;
+  p.src_dtype = src_dtype;
+  p.batch = batch;
+  p.t_new = t_new;
+  p.max_pages = max_pages;
+  p.pos_bias = 0;
+  p.ps_shift = page_shift(cache->page_size);
+  return p;
+}
+
 int kv_kind(const pkv_cache* c) {
   if (c->kv_dtype == PKV_F16) return KV_F16;
   if (c->kv_dtype == PKV_BF16) return KV_BF16;
@@ -640,30 +670,9 @@ pkv_status pkv_append_decode_attention(const pkv_cache* cache, int32_t batch, in
     if (q_dtype != PKV_F16 && q_dtype != PKV_BF16 && q_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
     if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
     if (!(sm_scale > 0.f) || !(sm_scale < 1e30f) || fresh_rows < -1) return PKV_ERR_INVALID_ARG;
-    AppendParams ap = {};
-    ap.k_pages = cache->k_pages;
-    ap.v_pages = cache->v_pages;
-    ap.kv_sz = cache->kv_sz;
-    ap.tail = cache->tail;
-    ap.page_meta = cache->page_meta;
-    ap.k_new = k_new;
-    ap.v_new = v_new;
-    ap.block_table = block_table;
-    ap.positions = seq_lens;
+    AppendParams ap = append_params(cache, batch, 1, k_new, v_new, src_dtype, block_table, max_pages, seq_lens, nullptr,
+                                    dev_status);
     ap.pos_bias = -1;
-    ap.new_lens = nullptr;
-    ap.dev_status = dev_status;
-    ap.num_pages = cache->num_pages;
-    ap.page_size = cache->page_size;
-    ap.num_kv_heads = cache->num_kv_heads;
-    ap.head_dim = cache->head_dim;
-    ap.kv_dtype = cache->kv_dtype;
-    ap.quant = cache->quant;
-    ap.src_dtype = src_dtype;
-    ap.batch = batch;
-    ap.t_new = 1;
-    ap.max_pages = max_pages;
-    ap.ps_shift = page_shift(cache->page_size);
     st = launch_append(ap, static_cast<cudaStream_t>(stream));
     if (st != PKV_OK) return st;
     return attention_impl(cache, batch, num_q_heads, q, q_dtype, sm_scale, block_table, max_pages, seq_lens,
@@ -693,30 +702,8 @@ pkv_status pkv_kv_append(const pkv_cache* cache, int32_t batch, int32_t t_new, c
     return PKV_ERR_INVALID_ARG;
   if ((long long)t_new > (long long)max_pages * cache->page_size) return PKV_ERR_INVALID_ARG;
   if (batch > 65535 || cache->num_kv_heads > 32767) return PKV_ERR_UNSUPPORTED;   // grid y / z limits
-  AppendParams p = {};
-  p.k_pages = cache->k_pages;
-  p.v_pages = cache->v_pages;
-  p.kv_sz = cache->kv_sz;
-  p.tail = cache->tail;
-  p.page_meta = cache->page_meta;
-  p.k_new = k_new;
-  p.v_new = v_new;
-  p.block_table = block_table;
-  p.positions = positions;
-  p.new_lens = new_lens;
-  p.dev_status = dev_status;
-  p.num_pages = cache->num_pages;
-  p.page_size = cache->page_size;
-  p.num_kv_heads = cache->num_kv_heads;
-  p.head_dim = cache->head_dim;
-  p.kv_dtype = cache->kv_dtype;
-  p.quant = cache->quant;
-  p.src_dtype = src_dtype;
-  p.batch = batch;
-  p.t_new = t_new;
-  p.max_pages = max_pages;
-  p.pos_bias = 0;
-  p.ps_shift = page_shift(cache->page_size);
+  const AppendParams p = append_params(cache, batch, t_new, k_new, v_new, src_dtype, block_table, max_pages, positions,
+                                       new_lens, dev_status);
   return launch_append(p, static_cast<cudaStream_t>(stream));
 }
 
@@ -770,6 +757,22 @@ pkv_status check_shared(const pkv_cache* cache, int32_t batch, int32_t num_q_hea
   return PKV_OK;
 }
 
+// What the tensor-core calls ask of types, the table and the scale.
+pkv_status check_products(const pkv_cache* cache, int32_t max_pages, pkv_dtype q_dtype, pkv_dtype out_dtype,
+                          float sm_scale) {
+  if (q_dtype != PKV_F16 && q_dtype != PKV_BF16 && q_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
+  if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
+  if (q_dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+  if ((cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) && q_dtype != cache->kv_dtype)
+    return PKV_ERR_UNSUPPORTED;
+  if (max_pages <= 0) return PKV_ERR_INVALID_ARG;
+  // token positions are 32-bit, rounded up to whole tiles, and so are tensor-copy row coordinates
+  if ((long long)max_pages * cache->page_size > INT32_MAX - 256) return PKV_ERR_UNSUPPORTED;
+  if ((long long)cache->num_pages * cache->num_kv_heads * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (!(sm_scale > 0.f) || !(sm_scale < 1e30f)) return PKV_ERR_INVALID_ARG;
+  return PKV_OK;
+}
+
 }  // namespace
 
 size_t pkv_shared_prefix_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t num_q_heads,
@@ -787,18 +790,10 @@ pkv_status pkv_shared_prefix_attention(const pkv_cache* cache, int32_t batch, in
                                        size_t workspace_bytes, int32_t* dev_status, void* stream) {
   pkv_status st = check_cache(cache, true);
   if (st == PKV_OK) st = check_shared(cache, batch, num_q_heads, num_splits);
+  if (st == PKV_OK) st = check_products(cache, max_pages, q_dtype, out_dtype, sm_scale);
   if (st != PKV_OK) return st;
-  if (q_dtype != PKV_F16 && q_dtype != PKV_BF16 && q_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
-  if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32) return PKV_ERR_INVALID_ARG;
-  if (q_dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
-  if ((cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) && q_dtype != cache->kv_dtype)
-    return PKV_ERR_UNSUPPORTED;
-  if (max_pages <= 0 || num_groups < 0) return PKV_ERR_INVALID_ARG;
+  if (num_groups < 0) return PKV_ERR_INVALID_ARG;
   if (num_groups > 1024) return PKV_ERR_UNSUPPORTED;
-  // token positions are 32-bit, rounded up to whole tiles, and so are tensor-copy row coordinates
-  if ((long long)max_pages * cache->page_size > INT32_MAX - 256) return PKV_ERR_UNSUPPORTED;
-  if ((long long)cache->num_pages * cache->num_kv_heads * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  if (!(sm_scale > 0.f) || !(sm_scale < 1e30f)) return PKV_ERR_INVALID_ARG;
   if (batch == 0) return PKV_OK;
   if (!q || !out || !block_table || !seq_lens || !prefix_group || (num_groups > 0 && !prefix_lens) ||
       !aligned16(q) || !aligned16(out))
@@ -824,6 +819,145 @@ pkv_status pkv_shared_prefix_attention(const pkv_cache* cache, int32_t batch, in
   a.dev_status = dev_status;
   a.stream = static_cast<cudaStream_t>(stream);
   return launch_shared(a);
+}
+
+namespace {
+
+pkv_status check_tree(const pkv_cache* cache, int32_t batch, int32_t t_draft, int32_t num_q_heads, int32_t num_splits) {
+  const pkv_status st = check_shared(cache, batch, num_q_heads, num_splits);
+  if (st != PKV_OK) return st;
+  if (t_draft < 0) return PKV_ERR_INVALID_ARG;
+  return t_draft > 256 ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+}  // namespace
+
+size_t pkv_tree_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t t_draft, int32_t num_q_heads,
+                                int32_t num_splits) {
+  size_t n = 0;
+  if (check_cache(cache, false) != PKV_OK || check_tree(cache, batch, t_draft, num_q_heads, num_splits) != PKV_OK)
+    return 0;
+  return tree_workspace_bytes(cache, batch, t_draft, num_q_heads, num_splits, n) == PKV_OK ? n : 0;
+}
+
+pkv_status pkv_tree_attention(const pkv_cache* cache, int32_t batch, int32_t t_draft, int32_t num_q_heads,
+                              const void* q, pkv_dtype q_dtype, float sm_scale, const int32_t* block_table,
+                              int32_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                              const int64_t* tree_mask, int32_t mask_shared, void* out, pkv_dtype out_dtype,
+                              int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                              void* stream) {
+  pkv_status st = check_cache(cache, true);
+  if (st == PKV_OK) st = check_tree(cache, batch, t_draft, num_q_heads, num_splits);
+  if (st == PKV_OK) st = check_products(cache, max_pages, q_dtype, out_dtype, sm_scale);
+  if (st != PKV_OK) return st;
+  if (mask_shared != 0 && mask_shared != 1) return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || t_draft == 0) return PKV_OK;
+  if (!q || !out || !block_table || !seq_lens || !aligned16(q) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return PKV_ERR_INVALID_ARG;
+  TreeArgs a = {};
+  a.cache = cache;
+  a.batch = batch;
+  a.drafts = t_draft;
+  a.num_q_heads = num_q_heads;
+  a.max_pages = max_pages;
+  a.num_splits = num_splits;
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.out_dtype = out_dtype;
+  a.sm_scale = sm_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.draft_lens = draft_lens;
+  a.tree_mask = tree_mask;
+  a.mask_shared = mask_shared;
+  a.out = out;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.dev_status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_tree(a);
+}
+
+pkv_status pkv_rotary_frequencies(int32_t rot_dim, double base, pkv_rotary_scaling scaling, double factor, double low,
+                                  double high, double original, double* inv_freq, double* table_scale) {
+  return rotary_frequencies(rot_dim, base, scaling, factor, low, high, original, inv_freq, table_scale);
+}
+
+pkv_status pkv_rotary_table(float* cos_sin, int32_t positions, int32_t rot_dim, const double* inv_freq,
+                            double table_scale, void* stream) {
+  if (positions < 0 || rot_dim <= 0) return PKV_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0 || rot_dim > 128) return PKV_ERR_UNSUPPORTED;
+  if (positions == 0) return PKV_OK;
+  if (!cos_sin || !aligned16(cos_sin) || !inv_freq) return PKV_ERR_INVALID_ARG;
+  return launch_rotary_table(cos_sin, positions, rot_dim, inv_freq, table_scale, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_rotary_append(const pkv_cache* cache, int32_t batch, int32_t t_new, int32_t num_q_heads, const void* q,
+                             const void* k_new, const void* v_new, pkv_dtype src_dtype, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float* cos_sin, int32_t table_positions,
+                             int32_t rot_dim, int32_t interleaved, const int32_t* rotary_positions,
+                             const int32_t* block_table, int32_t max_pages, const int32_t* positions,
+                             const int32_t* new_lens, void* q_out, int32_t* dev_status, void* stream) {
+  pkv_status st = check_cache(cache, true);
+  if (st != PKV_OK) return st;
+  if (src_dtype != PKV_F16 && src_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  const int D = cache->head_dim;
+  if (batch < 0 || t_new < 0 || max_pages <= 0 || num_q_heads < 0 || table_positions <= 0 || rot_dim <= 0 ||
+      rot_dim > D || (interleaved != 0 && interleaved != 1))
+    return PKV_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  // (rows of one token's heads; the 16-byte pieces of every row must lie on 16-byte boundaries)
+  const int64_t kv_row = (int64_t)cache->num_kv_heads * D, q_row = (int64_t)num_q_heads * D;
+  if (k_stride < kv_row || v_stride < kv_row || q_stride < q_row || (k_stride | v_stride | q_stride) % 8 != 0)
+    return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || t_new == 0) return PKV_OK;
+  if (!k_new || !v_new || !cos_sin || !block_table || !positions || !aligned16(k_new) || !aligned16(v_new) ||
+      !aligned16(cos_sin) || (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))))
+    return PKV_ERR_INVALID_ARG;
+  if (cache->quant == PKV_QUANT_PER_GROUP64 && (!cache->tail || !aligned16(cache->tail) || cache->tail_rows < batch))
+    return PKV_ERR_INVALID_ARG;
+  if ((long long)t_new > (long long)max_pages * cache->page_size) return PKV_ERR_INVALID_ARG;
+  if (batch > 65535 || cache->num_kv_heads > 32767) return PKV_ERR_UNSUPPORTED;   // grid y / z limits
+  if ((long long)batch * t_new > INT32_MAX / 2 || (long long)num_q_heads + 2 * cache->num_kv_heads > 65535)
+    return PKV_ERR_UNSUPPORTED;
+  RotaryParams p = {};
+  p.a = append_params(cache, batch, t_new, k_new, v_new, src_dtype, block_table, max_pages, positions, new_lens, dev_status);
+  p.a.k_stride = k_stride;
+  p.a.v_stride = v_stride;
+  p.a.cos_sin = cos_sin;
+  p.a.rotary_positions = rotary_positions;
+  p.a.table_positions = table_positions;
+  p.a.rot_dim = rot_dim;
+  p.a.interleaved = interleaved;
+  p.q = q;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.num_q_heads = num_q_heads;
+  return launch_rotary_append(p, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_keep_tokens(const pkv_cache* cache, int32_t batch, int32_t max_keep, const int32_t* keep,
+                           const int32_t* keep_lens, const int32_t* block_table, int32_t max_pages,
+                           const int32_t* first, int32_t* dev_status, void* stream) {
+  const pkv_status st = check_cache(cache, true);
+  if (st != PKV_OK) return st;
+  if (cache->quant == PKV_QUANT_PER_GROUP64) return PKV_ERR_UNSUPPORTED;
+  if (batch < 0 || max_keep < 0 || max_pages <= 0) return PKV_ERR_INVALID_ARG;
+  if (max_keep > 256 || (long long)batch * cache->num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if ((max_keep > 0 && !keep) || !block_table || !first) return PKV_ERR_INVALID_ARG;
+  KeepParams p = {};
+  p.cache = *cache;
+  p.keep = keep;
+  p.keep_lens = keep_lens;
+  p.block_table = block_table;
+  p.first = first;
+  p.dev_status = dev_status;
+  p.batch = batch;
+  p.max_keep = max_keep;
+  p.max_pages = max_pages;
+  return launch_keep(p, static_cast<cudaStream_t>(stream));
 }
 
 pkv_status pkv_copy_pages(const pkv_cache* cache, int32_t num_copies, const int32_t* src_pages,

@@ -52,6 +52,34 @@ __device__ __forceinline__ int page_of(const AppendParams& p, int b, int lp) {
   return phys;
 }
 
+// Four consecutive values of new token n (batch row * t_new + token), kv head g, as loaded, for rotary
+// appends: its source rows have a stride of their own, and keys are turned (see rotary.cu for the formula).
+__device__ __forceinline__ float4 load_rotated4(const AppendParams& p, bool isv, int n, int pos, int g, int e) {
+  const uint16_t* row = static_cast<const uint16_t*>(isv ? p.v_new : p.k_new) + n * (isv ? p.v_stride : p.k_stride) +
+                        (size_t)g * p.head_dim;
+  const float4 x = load_src4(row, p.src_dtype, e);
+  if (isv || e >= p.rot_dim) return x;
+  int m = p.rotary_positions ? p.rotary_positions[n] : pos;
+  if (m < 0 || m >= p.table_positions) {
+    flag_status(p.dev_status, PKV_DEV_BAD_POSITION);
+    m = m < 0 ? 0 : p.table_positions - 1;
+  }
+  const float* table = p.cos_sin + (size_t)m * p.rot_dim;
+  const int half = p.rot_dim / 2;
+  auto less = [](float u, float c, float v, float s) { return __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s)); };
+  auto more = [](float u, float c, float v, float s) { return __fadd_rn(__fmul_rn(u, c), __fmul_rn(v, s)); };
+  if (p.interleaved) {
+    const float2 c = *reinterpret_cast<const float2*>(table + e / 2), s = *reinterpret_cast<const float2*>(table + half + e / 2);
+    return make_float4(less(x.x, c.x, x.y, s.x), more(x.y, c.x, x.x, s.x), less(x.z, c.y, x.w, s.y), more(x.w, c.y, x.z, s.y));
+  }
+  const bool first = e < half;
+  const int i = first ? e : e - half;
+  const float4 y = load_src4(row, p.src_dtype, first ? e + half : i);
+  const float4 c = *reinterpret_cast<const float4*>(table + i), s = *reinterpret_cast<const float4*>(table + half + i);
+  return first ? make_float4(less(x.x, c.x, y.x, s.x), less(x.y, c.y, y.y, s.y), less(x.z, c.z, y.z, s.z), less(x.w, c.w, y.w, s.w))
+               : make_float4(more(x.x, c.x, y.x, s.x), more(x.y, c.y, y.y, s.y), more(x.z, c.z, y.z, s.z), more(x.w, c.w, y.w, s.w));
+}
+
 // fp16/bf16 cache: copy (with conversion when the source dtype differs).
 // grid (t_new, batch); each thread moves 8 elements per pass. The source rows
 // are loaded before the block-table lookup so the two latencies overlap.
@@ -228,8 +256,8 @@ __device__ __forceinline__ int32_t* tail_end(const AppendParams& p, int b, int g
 // of its loads (tail and new tokens) are issued before the first use, and
 // before the block-table lookup, so the block pays about one memory latency.
 constexpr int kGroupThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kGroupThreads, 4) append_per_group_kernel(const AppendParams p, int write_tail) {
+template <int D, bool ROTATED>
+__global__ void __launch_bounds__(kGroupThreads, ROTATED ? 2 : 4) append_per_group_kernel(const AppendParams p, int write_tail) {
   constexpr int kGroupVec4 = 64 * D / 4 / kGroupThreads;   // float4s of a full group per thread
   pdl_wait();
   pdl_launch_dependents();
@@ -254,6 +282,7 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_per_group_kernel(cons
     if (f < nf) {
       const int i = 4 * f, tt = i / D, e = i - tt * D, tok = t0 + tt;
       x[k] = tok < pos ? *reinterpret_cast<const float4*>(tl + i)
+             : ROTATED ? load_rotated4(p, kv, b * p.t_new + (tok - pos), tok, g, e)
                        : load_src4(sp, p.src_dtype, (((size_t)b * p.t_new + (tok - pos)) * H + g) * D + e);
     }
   }
@@ -442,6 +471,7 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_group_bulk_kernel(con
 // Keeps the new members of each row's open group (appends longer than one
 // group, run after the quantise kernel so no block reads a tail row another
 // block rewrites). grid (kv head * 2 + kv, row).
+template <bool ROTATED>
 __global__ void append_tail_kernel(const AppendParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -456,6 +486,14 @@ __global__ void append_tail_kernel(const AppendParams p) {
   const void* sp = kv ? p.v_new : p.k_new;
   float* tw = tail_row(p, b, g, kv, gi & 1);
   if (threadIdx.x == 0) *tail_end(p, b, g, kv, gi & 1) = end;
+  if constexpr (ROTATED) {
+    for (int i = 4 * threadIdx.x; i < (end - first) * D; i += 4 * blockDim.x) {
+      const int tt = i / D, e = i - tt * D, tok = first + tt;
+      *reinterpret_cast<float4*>(tw + (size_t)(tok - t0) * D + e) =
+          load_rotated4(p, kv, b * p.t_new + (tok - pos), tok, g, e);
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < (end - first) * D; i += blockDim.x) {
     const int tt = i / D, e = i - tt * D;
     const int tok = first + tt;
@@ -602,6 +640,44 @@ __global__ void __launch_bounds__(128) append_meta_kernel(const AppendParams p) 
 
 }  // namespace
 
+// Rotary appends to per-group caches. Every group slot goes through the kernel that holds a group in
+// 32 bits: rotated keys have no 16-bit form. (A group that the append leaves open is kept by the
+// tail kernel where two slots of one parity may be open, as above.)
+pkv_status launch_append_rotated_groups(const AppendParams& p, cudaStream_t st) {
+  const int groups = (p.t_new + 63) / 64 + 1;
+  AppendParams pc = p;
+  int inline_tail = p.t_new <= 64;
+  void* args[] = {&pc, &inline_tail};
+  const void* fn = p.head_dim == 128 ? reinterpret_cast<const void*>(&append_per_group_kernel<128, true>)
+                                     : reinterpret_cast<const void*>(&append_per_group_kernel<64, true>);
+  cudaError_t e = launch_pdl(fn, dim3(groups, p.num_kv_heads * 2, p.batch), dim3(kGroupThreads), 0, st, args);
+  if (e == cudaSuccess && !inline_tail) {
+    e = launch_pdl(reinterpret_cast<const void*>(&append_tail_kernel<true>), dim3(p.num_kv_heads * 2, p.batch), dim3(256),
+                   0, st, args);
+  }
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status launch_append_boxes(const AppendParams& p, cudaStream_t st) {
+  AppendParams pc = p;
+  void* args[] = {&pc};
+  const int pages = (p.t_new + p.page_size - 1) / p.page_size + 1;
+  const int kind = p.kv_dtype == PKV_U4 ? KV_U4T
+                 : p.kv_dtype == PKV_I8 ? (p.quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G)
+                 : p.kv_dtype == PKV_BF16 ? KV_BF16 : KV_F16;
+  const void* fn = nullptr;
+#define PKV_META(d, k) \
+  if (p.head_dim == d && kind == k) fn = reinterpret_cast<const void*>(&append_meta_kernel<d, k>);
+  PKV_META(64, KV_F16) PKV_META(64, KV_BF16) PKV_META(64, KV_I8T) PKV_META(64, KV_I8G) PKV_META(64, KV_U4T)
+  PKV_META(128, KV_F16) PKV_META(128, KV_BF16) PKV_META(128, KV_I8T) PKV_META(128, KV_I8G)
+  PKV_META(128, KV_U4T)
+#undef PKV_META
+  if (!fn) return PKV_ERR_UNSUPPORTED;
+  return launch_pdl(fn, dim3(pages, (p.num_kv_heads + 3) / 4, p.batch), dim3(128), 0, st, args) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
 pkv_status launch_append(const AppendParams& p, cudaStream_t st) {
   const int H = p.num_kv_heads;
   AppendParams pc = p;
@@ -626,8 +702,8 @@ pkv_status launch_append(const AppendParams& p, cudaStream_t st) {
     const int groups = (p.t_new + 63) / 64 + 1;
     int inline_tail = p.t_new <= 64;
     void* args2[] = {&pc, &inline_tail};
-    const void* fn = p.head_dim == 128 ? reinterpret_cast<const void*>(&append_per_group_kernel<128>)
-                                       : reinterpret_cast<const void*>(&append_per_group_kernel<64>);
+    const void* fn = p.head_dim == 128 ? reinterpret_cast<const void*>(&append_per_group_kernel<128, false>)
+                                       : reinterpret_cast<const void*>(&append_per_group_kernel<64, false>);
     // appends longer than a group: the first group slot (which may hold
     // earlier members of the open group) here, the others, all new tokens,
     // in the bulk kernel; the tail kernel then keeps the open group's members
@@ -639,23 +715,12 @@ pkv_status launch_append(const AppendParams& p, cudaStream_t st) {
       e = launch_pdl(fb, dim3(groups - 1, H, p.batch), dim3(kGroupThreads), 0, st, args1);
     }
     if (e == cudaSuccess && !inline_tail)
-      e = launch_pdl(reinterpret_cast<const void*>(&append_tail_kernel), dim3(H * 2, p.batch), dim3(256), 0,
+      e = launch_pdl(reinterpret_cast<const void*>(&append_tail_kernel<false>), dim3(H * 2, p.batch), dim3(256), 0,
                      st, args1);
   }
   if (e == cudaSuccess && p.page_meta) {
-    const int pages = (p.t_new + p.page_size - 1) / p.page_size + 1;
-    const int kind = p.kv_dtype == PKV_U4 ? KV_U4T
-                   : p.kv_dtype == PKV_I8 ? (p.quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G)
-                   : p.kv_dtype == PKV_BF16 ? KV_BF16 : KV_F16;
-    const void* fn = nullptr;
-#define PKV_META(d, k) \
-    if (p.head_dim == d && kind == k) fn = reinterpret_cast<const void*>(&append_meta_kernel<d, k>);
-    PKV_META(64, KV_F16) PKV_META(64, KV_BF16) PKV_META(64, KV_I8T) PKV_META(64, KV_I8G) PKV_META(64, KV_U4T)
-    PKV_META(128, KV_F16) PKV_META(128, KV_BF16) PKV_META(128, KV_I8T) PKV_META(128, KV_I8G)
-    PKV_META(128, KV_U4T)
-#undef PKV_META
-    if (!fn) return PKV_ERR_UNSUPPORTED;
-    e = launch_pdl(fn, dim3(pages, (H + 3) / 4, p.batch), dim3(128), 0, st, args1);
+    const pkv_status boxes = launch_append_boxes(p, st);
+    if (boxes != PKV_OK) return boxes;
   }
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

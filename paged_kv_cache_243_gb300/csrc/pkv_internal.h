@@ -22,6 +22,29 @@ struct AppendParams {
   int batch, t_new, max_pages;
   int pos_bias;   // added to positions[b] (-1: positions are the lengths after the append)
   int ps_shift;   // log2(page_size) when it is a power of two, else -1
+  // rotary appends: elements from one new token to the next, and the table of cosines and sines
+  int64_t k_stride, v_stride;
+  const float* cos_sin;               // [table_positions][rot_dim]: rot_dim / 2 cosines, then the sines
+  const int32_t* rotary_positions;    // [batch][t_new], or NULL: the positions in the sequence
+  int table_positions, rot_dim, interleaved;
+};
+
+struct RotaryParams {
+  AppendParams a;
+  const void* q;
+  void* q_out;
+  int64_t q_stride;
+  int num_q_heads, heads_per_task, token_tasks, tasks;
+};
+
+struct KeepParams {
+  pkv_cache cache;
+  const int32_t* keep;
+  const int32_t* keep_lens;
+  const int32_t* block_table;
+  const int32_t* first;
+  int32_t* dev_status;
+  int batch, max_keep, max_pages;
 };
 
 struct TopkParams {
@@ -41,6 +64,17 @@ struct TopkParams {
 
 pkv_status launch_append(const AppendParams& p, cudaStream_t st);
 pkv_status launch_topk(const TopkParams& p, cudaStream_t st);
+
+// New keys and values into the cache as launch_append, the keys rotated, and rotated queries.
+pkv_status launch_rotary_append(RotaryParams p, cudaStream_t st);
+// launch_append's parts for it: per-group caches, and the boxes.
+pkv_status launch_append_rotated_groups(const AppendParams& p, cudaStream_t st);
+pkv_status launch_append_boxes(const AppendParams& p, cudaStream_t st);
+pkv_status launch_rotary_table(float* cos_sin, int positions, int rot_dim, const double* inv_freq, double scale,
+                               cudaStream_t st);
+pkv_status rotary_frequencies(int rot_dim, double base, int scaling, double factor, double low, double high,
+                              double original, double* inv_freq, double* scale);
+pkv_status launch_keep(const KeepParams& p, cudaStream_t st);
 
 // Page copies and block-table renaming; the lists are host memory.
 pkv_status copy_pages(const pkv_cache* c, int32_t n, const int32_t* src, const int32_t* dst, int32_t n_rows,
@@ -67,6 +101,28 @@ struct SharedArgs {
 };
 pkv_status launch_shared(const SharedArgs& a);
 pkv_status shared_workspace_bytes(const pkv_cache* c, int batch, int num_q_heads, int num_splits, size_t& bytes);
+
+// Attention for trees of drafts: what the entry point has checked.
+struct TreeArgs {
+  const pkv_cache* cache;
+  int batch, drafts, num_q_heads, max_pages, num_splits;
+  const void* q;
+  int q_dtype, out_dtype;
+  float sm_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* draft_lens;
+  const int64_t* tree_mask;
+  bool mask_shared;
+  void* out;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* dev_status;
+  cudaStream_t stream;
+};
+pkv_status launch_tree(const TreeArgs& a);
+pkv_status tree_workspace_bytes(const pkv_cache* c, int batch, int drafts, int num_q_heads, int num_splits,
+                                size_t& bytes);
 
 // Attention kernels, one getter per KV kind (each in its own translation unit).
 // mma: the tensor-core variant (query-head groups of 2, 4 or 8); self_fed:

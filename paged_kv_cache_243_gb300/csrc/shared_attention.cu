@@ -1,4 +1,5 @@
-// Shared-prefix attention: launch plan of the kernels in shared_kernel.cuh.
+// Shared-prefix attention, and attention for trees of drafts: launch plans of the kernels in
+// shared_kernel.cuh.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -14,6 +15,11 @@ const void* shared_kernel_bf16(int D);
 const void* shared_kernel_i8t(int D, bool bf);
 const void* shared_kernel_i8g(int D, bool bf);
 const void* shared_kernel_u4t(int D, bool bf);
+const void* tree_kernel_f16(int D);
+const void* tree_kernel_bf16(int D);
+const void* tree_kernel_i8t(int D, bool bf);
+const void* tree_kernel_i8g(int D, bool bf);
+const void* tree_kernel_u4t(int D, bool bf);
 
 namespace {
 
@@ -76,6 +82,18 @@ Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
   return w;
 }
 
+// For trees: each pair of row tiles' place, and one record row per query row and stream besides the
+// blocks' 256.
+Work tree_layout(const pkv_cache* c, int rows, int sequences, int pairs, int hq, int ctas) {
+  const size_t recs = 2 * (size_t)rows * hq + (size_t)ctas * 2 * kTile;
+  Work w;
+  w.ml = align256((size_t)sequences * c->num_kv_heads * pairs * sizeof(int4));
+  w.acc = w.ml + align256(recs * sizeof(float2));
+  w.total = w.acc + align256(recs * c->head_dim * sizeof(float)) + 256;
+  return w;
+}
+int tree_pairs(int drafts, int group) { return (drafts * group + 2 * kTile - 1) / (2 * kTile); }
+
 using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
 EncodeTiledFn encode_fn() {
   static std::once_flag once;
@@ -101,20 +119,52 @@ bool pool_map(void* base, uint64_t rows, int d, bool bf, CUtensorMap& m) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int kind_of(const pkv_cache* c) {
+  return c->kv_dtype == PKV_F16 ? KV_F16 : c->kv_dtype == PKV_BF16 ? KV_BF16 : c->kv_dtype == PKV_U4 ? KV_U4T
+         : c->quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G;
+}
+
 template <int D, int KV>
-void sizes(int& threads, int& smem, int& entries, SharedLayout& lay, int avail, int batch, int groups) {
+void sizes(int& threads, int& smem, int& entries, SharedLayout& lay, int avail, int batch, int groups, bool tree) {
   using G = SharedGeom<D, KV, true>;   // operand types have the same sizes
   threads = G::THREADS;
   entries = kMaxEntries;
-  while (entries > 1 && 1024 + shared_layout<G>(entries, batch, groups).total > avail) --entries;
-  lay = shared_layout<G>(entries, batch, groups);
+  while (entries > 1 && 1024 + shared_layout<G>(entries, batch, groups, tree).total > avail) --entries;
+  lay = shared_layout<G>(entries, batch, groups, tree);
   smem = 1024 + lay.total;
 }
 
-template <int D>
+// Block and shared memory of the attention kernel, and its parameters from the cache.
+pkv_status cache_params(const pkv_cache* c, const Device& dev, const void* fn, int rows, int groups, bool tree,
+                        SharedParams& p, int& threads, int& smem) {
+  const int D = c->head_dim, kind = kind_of(c);
+#define PKV_SIZES(d, kv) \
+  if (D == d && kind == kv) sizes<d, kv>(threads, smem, p.entries, p.lay, dev.smem, rows, groups, tree);
+  PKV_SIZES(64, KV_F16) PKV_SIZES(64, KV_BF16) PKV_SIZES(64, KV_I8T) PKV_SIZES(64, KV_I8G) PKV_SIZES(64, KV_U4T)
+  PKV_SIZES(128, KV_F16) PKV_SIZES(128, KV_BF16) PKV_SIZES(128, KV_I8T) PKV_SIZES(128, KV_I8G) PKV_SIZES(128, KV_U4T)
+#undef PKV_SIZES
+  if (smem > dev.smem) return PKV_ERR_UNSUPPORTED;
+  const pkv_status st = allow_smem(fn, dev);
+  if (st != PKV_OK) return st;
+  if (kind == KV_F16 || kind == KV_BF16) {
+    const uint64_t n = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
+    if (!pool_map(c->k_pages, n, D, kind == KV_BF16, p.tmap_k) || !pool_map(c->v_pages, n, D, kind == KV_BF16, p.tmap_v))
+      return PKV_ERR_CUDA;
+  }
+  p.k_pages = static_cast<const uint8_t*>(c->k_pages);
+  p.v_pages = static_cast<const uint8_t*>(c->v_pages);
+  p.kv_sz = c->kv_sz;
+  p.num_pages = c->num_pages;
+  p.page_size = c->page_size;
+  p.num_kv_heads = c->num_kv_heads;
+  p.kv_kind = kind;
+  return PKV_OK;
+}
+
+template <int D, bool TREE>
 const void* merge_kernel(int warps) {
-  return warps == 4 ? reinterpret_cast<const void*>(&shared_merge_kernel<D, 4>)
-                    : reinterpret_cast<const void*>(&shared_merge_kernel<D, 1>);
+  return warps == 4 ? reinterpret_cast<const void*>(&shared_merge_kernel<D, 4, TREE>)
+                    : reinterpret_cast<const void*>(&shared_merge_kernel<D, 1, TREE>);
 }
 
 }  // namespace
@@ -134,9 +184,7 @@ pkv_status launch_shared(const SharedArgs& a) {
   Device dev;
   pkv_status st = device(dev);
   if (st != PKV_OK) return st;
-  const int D = c->head_dim, group = a.num_q_heads / c->num_kv_heads;
-  const int kind = c->kv_dtype == PKV_F16 ? KV_F16 : c->kv_dtype == PKV_BF16 ? KV_BF16 : c->kv_dtype == PKV_U4 ? KV_U4T
-                   : c->quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G;
+  const int D = c->head_dim, group = a.num_q_heads / c->num_kv_heads, kind = kind_of(c);
   // visits are counted in 32 bits: rows and prefixes at the table's full width
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
@@ -154,23 +202,9 @@ pkv_status launch_shared(const SharedArgs& a) {
                    : kind == KV_I8T  ? shared_kernel_i8t(D, bf)
                    : kind == KV_I8G  ? shared_kernel_i8g(D, bf)
                                      : shared_kernel_u4t(D, bf);
-  int threads = 0, smem = 0, entries = 0;
-#define PKV_SIZES(d, kv) \
-  if (D == d && kind == kv) sizes<d, kv>(threads, smem, entries, p.lay, dev.smem, a.batch, a.num_groups);
-  PKV_SIZES(64, KV_F16) PKV_SIZES(64, KV_BF16) PKV_SIZES(64, KV_I8T) PKV_SIZES(64, KV_I8G) PKV_SIZES(64, KV_U4T)
-  PKV_SIZES(128, KV_F16) PKV_SIZES(128, KV_BF16) PKV_SIZES(128, KV_I8T) PKV_SIZES(128, KV_I8G) PKV_SIZES(128, KV_U4T)
-#undef PKV_SIZES
-  if (smem > dev.smem) return PKV_ERR_UNSUPPORTED;
-  st = allow_smem(fn, dev);
+  int threads = 0, smem = 0;
+  st = cache_params(c, dev, fn, a.batch, a.num_groups, false, p, threads, smem);
   if (st != PKV_OK) return st;
-  if (kind == KV_F16 || kind == KV_BF16) {
-    const uint64_t rows = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
-    if (!pool_map(c->k_pages, rows, D, bf, p.tmap_k) || !pool_map(c->v_pages, rows, D, bf, p.tmap_v))
-      return PKV_ERR_CUDA;
-  }
-  p.k_pages = static_cast<const uint8_t*>(c->k_pages);
-  p.v_pages = static_cast<const uint8_t*>(c->v_pages);
-  p.kv_sz = c->kv_sz;
   p.q = static_cast<const uint8_t*>(a.q);
   p.out = a.out;
   p.block_table = a.block_table;
@@ -182,16 +216,12 @@ pkv_status launch_shared(const SharedArgs& a) {
   p.ws_info = reinterpret_cast<int4*>(ws);
   p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
   p.ws_acc = reinterpret_cast<float*>(ws + w.acc);
-  p.num_pages = c->num_pages;
-  p.page_size = c->page_size;
-  p.num_kv_heads = c->num_kv_heads;
   p.num_q_heads = a.num_q_heads;
   p.group = group;
   p.batch = a.batch;
   p.max_pages = a.max_pages;
   p.num_groups = a.num_groups;
   p.num_ctas = ctas;
-  p.entries = entries;
   p.round_to = kind == KV_I8G ? 64 : 16;
   p.q_dtype = a.q_dtype;
   p.out_dtype = a.out_dtype;
@@ -206,7 +236,82 @@ pkv_status launch_shared(const SharedArgs& a) {
   // 16K, 4-bit) 45.6 and 42.5, 1024 (32 rows x 2K) 23.3 and 25.1, 2048 (64 rows x 16K) 49.4 and 48.1,
   // (64 rows x 8K, INT8) 58.1 and 59.9, 3904 (5 groups x 5K) 46.6 and 57.6, 8192 (256 rows x 8K) 83 and 104.
   const int wpw = units < 6 * dev.sms ? 4 : 1;
-  const void* merge = D == 64 ? merge_kernel<64>(wpw) : merge_kernel<128>(wpw);
+  const void* merge = D == 64 ? merge_kernel<64, false>(wpw) : merge_kernel<128, false>(wpw);
+  const int per = 4 / wpw;
+  return launch_pdl(merge, dim3((unsigned)((units + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+pkv_status tree_workspace_bytes(const pkv_cache* c, int batch, int drafts, int num_q_heads, int num_splits,
+                                size_t& bytes) {
+  Device dev;
+  if (num_splits == 0) {
+    const pkv_status st = device(dev);
+    if (st != PKV_OK) return st;
+  }
+  bytes = tree_layout(c, batch * drafts, batch, tree_pairs(drafts, num_q_heads / c->num_kv_heads), num_q_heads,
+                      num_splits ? num_splits : dev.sms)
+              .total;
+  return PKV_OK;
+}
+
+pkv_status launch_tree(const TreeArgs& a) {
+  const pkv_cache* c = a.cache;
+  Device dev;
+  pkv_status st = device(dev);
+  if (st != PKV_OK) return st;
+  const int D = c->head_dim, group = a.num_q_heads / c->num_kv_heads, kind = kind_of(c);
+  const int rows = a.batch * a.drafts, pairs = tree_pairs(a.drafts, group);
+  // visits, two units each at most, and values of records are counted in 32 bits
+  const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
+  const int ctas = a.num_splits ? a.num_splits : dev.sms;
+  if (2 * tiles >= (1ll << 31) / ((long long)c->num_kv_heads * a.batch * pairs) ||
+      (2ll * rows * a.num_q_heads + 512ll * ctas) * D >= (1ll << 31))
+    return PKV_ERR_UNSUPPORTED;
+  const Work w = tree_layout(c, rows, a.batch, pairs, a.num_q_heads, ctas);
+  if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < w.total)
+    return PKV_ERR_WORKSPACE;
+  SharedParams p = {};
+  const bool bf = a.q_dtype == PKV_BF16;
+  const void* fn = kind == KV_F16    ? tree_kernel_f16(D)
+                   : kind == KV_BF16 ? tree_kernel_bf16(D)
+                   : kind == KV_I8T  ? tree_kernel_i8t(D, bf)
+                   : kind == KV_I8G  ? tree_kernel_i8g(D, bf)
+                                     : tree_kernel_u4t(D, bf);
+  int threads = 0, smem = 0;
+  st = cache_params(c, dev, fn, 0, a.batch, true, p, threads, smem);
+  if (st != PKV_OK) return st;
+  p.q = static_cast<const uint8_t*>(a.q);
+  p.out = a.out;
+  p.block_table = a.block_table;
+  p.seq_lens = a.seq_lens;
+  p.dev_status = a.dev_status;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.ws_info = reinterpret_cast<int4*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.ws_acc = reinterpret_cast<float*>(ws + w.acc);
+  p.num_q_heads = a.num_q_heads;
+  p.group = group;
+  p.batch = rows;
+  p.max_pages = a.max_pages;
+  p.num_groups = a.batch;
+  p.num_ctas = ctas;
+  p.q_dtype = a.q_dtype;
+  p.out_dtype = a.out_dtype;
+  p.two_terms = a.out_dtype == PKV_F32;
+  p.scale = a.sm_scale * 1.4426950408889634f;
+  p.draft_lens = a.draft_lens;
+  p.tree_mask = reinterpret_cast<const uint64_t*>(a.tree_mask);
+  p.drafts = a.drafts;
+  p.mask_words = (a.drafts + 63) / 64;
+  p.mask_stride = a.mask_shared ? 0 : (long long)a.drafts * p.mask_words;
+  p.pairs = pairs;
+  void* args[] = {&p};
+  if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
+  const long long outs = (long long)rows * a.num_q_heads * D, units = (outs + 127) / 128;
+  const int wpw = units < 6 * dev.sms ? 4 : 1;   // (see above)
+  const void* merge = D == 64 ? merge_kernel<64, true>(wpw) : merge_kernel<128, true>(wpw);
   const int per = 4 / wpw;
   return launch_pdl(merge, dim3((unsigned)((units + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
              ? PKV_OK

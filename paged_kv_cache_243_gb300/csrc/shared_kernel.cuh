@@ -111,10 +111,12 @@ constexpr float kWeightBits = 7.f;
 // one costs the others stays below this many bits.
 constexpr int kEvenBits = 4;
 constexpr int kVisits = 64;      // visits described in shared memory, refilled by halves
+// Visits whose values that are no numbers are marked: the two streams are less than three visits apart.
+constexpr int kBadSlots = 4;
 
 // Shared memory by offset from a 1024-byte boundary.
 struct SharedLayout {
-  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, misc, visits, bpre, gpre, lpre, moff, members, lens, skip, gp, rank, rowg;
+  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, bad, misc, visits, bpre, gpre, lpre, moff, members, lens, skip, gp, rank, rowg;
   int total;
 };
 struct SharedParams {
@@ -136,6 +138,11 @@ struct SharedParams {
   int num_pages, page_size, num_kv_heads, num_q_heads, group, batch, max_pages, num_groups;
   int num_ctas, entries /* of K, and of V */, round_to, q_dtype, out_dtype, two_terms;
   float scale;   // sm_scale * log2(e)
+  // trees of drafts: the groups are the sequences, each row of the batch a draft
+  const int32_t* draft_lens;   // drafts of each sequence, or NULL: `drafts` of each
+  const uint64_t* tree_mask;   // [sequences][drafts][mask_words], or NULL: each after the one before
+  int drafts, mask_words, pairs, kv_kind;
+  long long mask_stride;       // words from one sequence's masks to the next's (0: the same)
   SharedLayout lay;
 };
 
@@ -167,7 +174,7 @@ enum SharedBars {   // mbarriers, 8 bytes each
 };
 
 template <class G>
-__host__ __device__ inline SharedLayout shared_layout(int entries, int batch, int groups) {
+__host__ __device__ inline SharedLayout shared_layout(int entries, int batch, int groups, bool tree = false) {
   SharedLayout o;
   int at = 0;
   auto put = [&](int bytes) {
@@ -188,6 +195,7 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.ml = put(2 * kTile * 16);
   o.qsum = put(G::QUANT ? kQSums * kTile * 4 : 0);
   o.vmax = put(G::QUANT ? kScaleSlots * 32 : 0);
+  o.bad = put(tree ? (G::QUANT ? kHdrs * 16 : kBadSlots * kTile * 4) : 0);
   o.misc = put(21 * 16);
   o.visits = put(kVisits * 32);
   o.bpre = put((batch + 1) * 4);
@@ -368,7 +376,8 @@ struct Visit {
 enum VisitBits {   // place in the block's part of the segment
   kFirst = 0x100, kLast = 0x200, kEarly = 0x400 /* one of the first two */, kLate = 0x800 /* of the last two */,
   kMany = 0x1000 /* the part has several */, kContinued = 0x2000 /* the segment began in an earlier block */,
-  kTwo = 0x4000 /* two row tiles */
+  kTwo = 0x4000 /* two row tiles */,
+  kDrafts = 0x8000 /* some of its tokens are drafts, which some rows do not attend to */
 };
 
 __device__ __forceinline__ int upper(const int* pre, int n, int x) {   // largest i with pre[i] <= x
@@ -407,13 +416,76 @@ __device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int L, int g,
   return r;
 }
 
+// Trees of drafts: the tokens of sequence g within the table, the last `drafts` of which are drafts.
+struct TreePlan {
+  int len, drafts, bad;
+};
+__device__ __forceinline__ TreePlan tree_plan(const SharedParams& p, int g) {
+  TreePlan r;
+  const long long cap = (long long)p.max_pages * p.page_size;
+  int L = p.seq_lens[g], n = p.draft_lens ? p.draft_lens[g] : p.drafts;
+  r.bad = L < 0 || L > cap || n < 0 || n > p.drafts || n > L ? PKV_DEV_BAD_POSITION : 0;
+  L = L < 0 ? 0 : (int)(L > cap ? cap : L);
+  r.drafts = max(0, min(n, min(p.drafts, L)));
+  r.len = r.drafts ? L : 0;   // without a draft there is nothing to do
+  return r;
+}
+
+// Which of 32 tokens draft t attends to, the first of them draft j0 of its sequence (below 0: tokens
+// before the drafts, to which all attend). Bits of drafts that do not exist mean nothing.
+__device__ __forceinline__ uint32_t tree_bits(const SharedParams& p, const uint64_t* words, int t, int j0) {
+  if (j0 <= -32) return 0xffffffffu;
+  if (!words) {   // drafts up to t
+    const int n = t + 1 - j0;
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  }
+  const int at = max(j0, 0), w = at >> 6, s = at & 63;
+  uint64_t x = w < p.mask_words ? __ldg(words + w) >> s : 0;
+  if (s > 32 && w + 1 < p.mask_words) x |= __ldg(words + w + 1) << (64 - s);
+  return j0 >= 0 ? (uint32_t)x : (uint32_t)x << -j0 | ((1u << -j0) - 1u);
+}
+__device__ __forceinline__ const uint64_t* tree_words(const SharedParams& p, int g, int t) {
+  return p.tree_mask ? p.tree_mask + g * p.mask_stride + (size_t)t * p.mask_words : nullptr;
+}
+
+// The four words of a tile's 128 tokens for draft t of sequence g.
+static __device__ __noinline__ uint4 tree_window(const SharedParams& p, int g, int t, int tok0) {
+  const TreePlan r = tree_plan(p, g);
+  const int j0 = tok0 - (r.len - r.drafts);
+  const uint64_t* w = tree_words(p, g, t);
+  return make_uint4(tree_bits(p, w, t, j0), tree_bits(p, w, t, j0 + 32), tree_bits(p, w, t, j0 + 64),
+                    tree_bits(p, w, t, j0 + 96));
+}
+
+// Which of a segment's few query rows attend to token `tok` of the sequence.
+static __device__ __noinline__ uint32_t tree_rows(const SharedParams& p, const Visit& s, int tok) {
+  const TreePlan r = tree_plan(p, s.row);
+  const int j = tok - (r.len - r.drafts);
+  if (j < 0) return 0xffffffffu;
+  uint32_t rows = 0;
+#pragma unroll 4
+  for (int i = 0; i < s.rows; ++i) {
+    const int t = (s.q0 + i) / p.group;
+    rows |= (tree_bits(p, tree_words(p, s.row, t), t, j) & 1u) << i;
+  }
+  return rows;
+}
+
+template <bool TREE>
 static __device__ __noinline__ void describe_visit(const SharedParams& p, const SharedPlan& pl, int x, int4* out) {
   Visit s;
   int tile, tiles, end_tok, first_tok;
-  if (x < pl.lpre[p.num_groups]) {
+  [[maybe_unused]] int drafts = 0;
+  if (TREE || x < pl.lpre[p.num_groups]) {
     const int* pre = x < pl.gpre[p.num_groups] ? pl.gpre : pl.lpre;
     const int g = upper(pre, p.num_groups, x);
-    end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] & -p.round_to;
+    if constexpr (TREE) {
+      const TreePlan r = tree_plan(p, g);
+      end_tok = r.len;
+      drafts = r.drafts;
+    } else {
+      end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] & -p.round_to;
+    }
     first_tok = 0;
     tiles = (end_tok + kTile - 1) / kTile;
     const int total = (pl.moff[g + 1] - pl.moff[g]) * p.group;
@@ -424,7 +496,7 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
     s.q0 = (hp - s.head * pairs) * 2 * kTile;
     s.rows = min(2 * kTile, total - s.q0);
     s.mem0 = pl.moff[g];
-    s.row = pl.members[s.mem0];
+    s.row = TREE ? g : pl.members[s.mem0];
     s.rec = s.head * p.batch * p.group + s.mem0 * p.group + s.q0;
   } else {
     const int b = upper(pl.bpre, p.batch, x);
@@ -451,6 +523,7 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
   s.flags = min(kTile, end_tok - s.tok0) | (x == x0 ? kFirst : 0) | (x == x1 - 1 ? kLast : 0) |
             (x < x0 + 2 ? kEarly : 0) | (x >= x1 - 2 ? kLate : 0) | (x1 - x0 > 1 ? kMany : 0) |
             (x0 > whole0 ? kContinued : 0) | (s.rows > kTile ? kTwo : 0);
+  if (TREE && s.tok0 + kTile > end_tok - drafts) s.flags |= kDrafts;
   out[0] = make_int4(s.tok0, s.flags, s.row, s.head);
   out[1] = make_int4(s.rows, s.q0, s.mem0, s.rec);
 }
@@ -615,13 +688,13 @@ static __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, v
 }
 
 // Queries of tile u of a segment into an operand tile (swizzled), by `warps` warps.
-template <int D>
+template <int D, bool TREE>
 static __device__ __noinline__ void gather_queries(const SharedParams& p, const Visit& s, const uint16_t* members, int u,
                                                    uint32_t dst, int w, int warps) {
   constexpr int CH = D / 8, RPI = 32 / CH;   // 16-byte pieces of a row, rows an instruction
   const int lane = threadIdx.x & 31;
   const int rows = min(kTile, s.rows - u * kTile);
-  if (s.mem0 < 0) {   // one row's heads: its queries lie together
+  if (!TREE && s.mem0 < 0) {   // one row's heads: its queries lie together
     const uint8_t* src = p.q + ((size_t)s.row * p.num_q_heads + s.head * p.group) * D * 2;
 #pragma unroll 2
     for (int i = 32 * w + lane; i < rows * CH; i += 32 * warps) {
@@ -634,7 +707,8 @@ static __device__ __noinline__ void gather_queries(const SharedParams& p, const 
   for (int r0 = 32 * w; r0 < rows; r0 += 32 * warps) {
     // lane i finds row r0 + i
     const int R = s.q0 + u * kTile + r0 + lane, m = R / p.group, gq = R - m * p.group;
-    const int b = r0 + lane < rows ? members[s.mem0 + m] : 0;
+    int b = 0;
+    if (r0 + lane < rows) b = TREE ? s.row * p.drafts + m : members[s.mem0 + m];
     const int qrow = b * p.num_q_heads + s.head * p.group + gq;
     const int n = min(32, rows - r0), c = lane % CH;
 #pragma unroll 8
@@ -663,6 +737,26 @@ static __device__ __noinline__ void sum_queries(const uint8_t* src, float* qsum,
     }
     qsum[r] = t;
   }
+}
+
+// Infinities and NaNs of a tile's row of 16-bit values become 0, the row marked (before that: another
+// warp that finds the 0 finds the mark, too).
+template <int HALVES, bool BF>
+static __device__ __noinline__ void clear_no_numbers(uint8_t* tile, int row, volatile int* mark, int v) {
+  constexpr uint32_t E = BF ? 0x7F80u : 0x7C00u;
+#pragma unroll 1
+  for (int i = 0; i < HALVES * 8; ++i) {
+    uint4* at = reinterpret_cast<uint4*>(tile + (i >> 3) * 16384 + row * 128 + ((i & 7) ^ (row & 7)) * 16);
+    uint4 x = *at;
+    auto none = [](uint32_t w) { return ((w & E) == E ? 0xFFFFu : 0u) | ((w >> 16 & E) == E ? 0xFFFF0000u : 0u); };
+    const uint4 m = make_uint4(none(x.x), none(x.y), none(x.z), none(x.w));
+    if (m.x | m.y | m.z | m.w) {
+      *mark = v;
+      __threadfence_block();
+      *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+    }
+  }
+  __threadfence_block();
 }
 
 // For the merge: where the records of the rows' kv heads are (the block's share of
@@ -708,7 +802,28 @@ static __device__ __noinline__ void place_records(const SharedParams& p, const S
   }
 }
 
-template <int D, int KV, bool BF>
+// The same for trees of drafts: for each sequence, kv head and pair of row tiles its record rows (of the
+// first block, of those that continue it), parts and query rows, and whether both streams have a record.
+static __device__ __noinline__ void place_tree_records(const SharedParams& p, const SharedPlan& pl, int few_max) {
+  const int lane = threadIdx.x & 31, whole = p.batch * p.num_q_heads;
+  const Shares shares(pl.gpre[p.num_groups], pl.lpre[p.num_groups], p.num_ctas);
+#pragma unroll 1
+  for (int i = blockIdx.x + gridDim.x * lane; i < p.num_groups * p.num_kv_heads * p.pairs; i += gridDim.x * 32) {
+    const int gh = i / p.pairs, pair = i - gh * p.pairs, g = gh / p.num_kv_heads, h = gh - g * p.num_kv_heads;
+    const TreePlan r = tree_plan(p, g);
+    const int rows = r.drafts * p.group, pairs = (rows + 2 * kTile - 1) / (2 * kTile);
+    const int n = (int)((uint32_t)(r.len + kTile - 1) / kTile), mine = min(2 * kTile, rows - pair * 2 * kTile);
+    int4 info = make_int4(0, 0, 0, 0);
+    if (mine > 0) {
+      const int x = (rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, c = shares.block_of(x);
+      info = make_int4(h * p.batch * p.group + pl.moff[g] * p.group + pair * 2 * kTile, 2 * whole + (c + 1) * 2 * kTile,
+                       (shares.block_of(x + n - 1) - c + 1) | mine << 16, mine <= few_max);
+    }
+    p.ws_info[i] = info;
+  }
+}
+
+template <int D, int KV, bool BF, bool TREE>
 __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
   using G = SharedGeom<D, KV, BF>;
@@ -734,7 +849,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   int* lpre = reinterpret_cast<int*>(smem + lay.lpre);
   uint16_t* rank = reinterpret_cast<uint16_t*>(smem + lay.rank);
   int16_t* rowg = reinterpret_cast<int16_t*>(smem + lay.rowg);
-  const int S = p.entries, B = p.batch, NG = p.num_groups, Gq = p.group;
+  // (trees of drafts: the groups are all there is)
+  const int S = p.entries, B = TREE ? 0 : p.batch, NG = p.num_groups, Gq = p.group;
 
   if (tid == 0) {
     for (int i = 0; i < kMaxEntries; ++i) {
@@ -775,41 +891,55 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 
   // ---- plan: lengths, who shares, visits before each segment. (Its loops stay
   // loops: this code is fetched anew by every call.)
-  const int lens32 = lane < NG ? p.prefix_lens[lane] : 0;   // of the first 32 groups
+  if constexpr (TREE) {
 #pragma unroll 1
-  for (int b0 = warp * 32; b0 < B; b0 += NT) {
-    const int b = b0 + lane;
-    const RowPlan r = row_plan(p, b < B ? p.seq_lens[b] : 0, b < B ? p.prefix_group[b] : -1, [&](int g) {
-      if (NG > 32) return g < 0 ? 0 : p.prefix_lens[g];
-      const int P = __shfl_sync(0xffffffffu, lens32, g & 31);
-      return g < 0 ? 0 : P;
-    });
-    if (b >= B) continue;
-    if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
-    lens[b] = r.len;
-    skip[b] = r.skip;
-    rowg[b] = (int16_t)r.group;
-  }
-#pragma unroll 1
-  for (int g = tid; g < NG; g += NT) {
-    const int P = g < 32 ? lens32 : p.prefix_lens[g];
-    if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
-    gp[g] = max(P, 0) & -p.round_to;
-  }
-  __syncthreads();
-  if (warp == 0 && NG > 0) {   // each row's place among its group's rows
-#pragma unroll 1
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      const int b = b0 + lane, g = b < B ? rowg[b] : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, g);
-      const int base = g >= 0 ? moff[g] : 0;
-      __syncwarp();
-      if (g >= 0 && lane == __ffs(same) - 1) moff[g] = base + __popc(same);
-      __syncwarp();
-      if (b < B) rank[b] = (uint16_t)(base + __popc(same & ((1u << lane) - 1)));
+    for (int g = tid; g < NG; g += NT) {
+      const TreePlan r = tree_plan(p, g);
+      if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
+      moff[g] = r.drafts;
+      gp[g] = r.len;
     }
+    if constexpr (!QUANT) {   // no visit's marks
+      for (int i = tid; i < kBadSlots * kTile; i += NT) reinterpret_cast<int*>(smem + lay.bad)[i] = -1;
+    }
+    __syncthreads();
+  } else {
+    const int lens32 = lane < NG ? p.prefix_lens[lane] : 0;   // of the first 32 groups
+  #pragma unroll 1
+    for (int b0 = warp * 32; b0 < B; b0 += NT) {
+      const int b = b0 + lane;
+      const RowPlan r = row_plan(p, b < B ? p.seq_lens[b] : 0, b < B ? p.prefix_group[b] : -1, [&](int g) {
+        if (NG > 32) return g < 0 ? 0 : p.prefix_lens[g];
+        const int P = __shfl_sync(0xffffffffu, lens32, g & 31);
+        return g < 0 ? 0 : P;
+      });
+      if (b >= B) continue;
+      if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
+      lens[b] = r.len;
+      skip[b] = r.skip;
+      rowg[b] = (int16_t)r.group;
+    }
+  #pragma unroll 1
+    for (int g = tid; g < NG; g += NT) {
+      const int P = g < 32 ? lens32 : p.prefix_lens[g];
+      if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
+      gp[g] = max(P, 0) & -p.round_to;
+    }
+    __syncthreads();
+    if (warp == 0 && NG > 0) {   // each row's place among its group's rows
+  #pragma unroll 1
+      for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane, g = b < B ? rowg[b] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, g);
+        const int base = g >= 0 ? moff[g] : 0;
+        __syncwarp();
+        if (g >= 0 && lane == __ffs(same) - 1) moff[g] = base + __popc(same);
+        __syncwarp();
+        if (b < B) rank[b] = (uint16_t)(base + __popc(same & ((1u << lane) - 1)));
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   auto tiles_of = [](int tokens) { return (uint32_t)(tokens + kTile - 1) / kTile; };
   // kv heads x pairs of row tiles x tiles of tokens
   auto prefix_visits = [&](int g) {
@@ -859,15 +989,19 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   const int nv = hi - lo;
   SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, lo, hi};
   __syncthreads();
-  if (tid < min(nv, kVisits)) describe_visit(p, plan, lo + tid, visits + 2 * tid);
+  if (tid < min(nv, kVisits)) describe_visit<TREE>(p, plan, lo + tid, visits + 2 * tid);
   plan.lens = plan.skip = plan.gp = nullptr;
   fence_proxy_async_smem();   // the ring, so far the plan's, is the copies' from here on
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
+  auto records = [&]() {
+    if constexpr (TREE) place_tree_records(p, plan, FEW);
+    else place_records(p, plan, FEW);
+  };
   if (nv <= 0) {   // uniform over the block
-    if (warp == 8) place_records(p, plan, FEW);
+    if (warp == 8) records();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
@@ -900,7 +1034,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
   };
   auto gather_q = [&](const Visit& s, int u, int qs, int w, int warps) {
-    gather_queries<D>(p, s, members, u, smem_u32(smem + lay.q) + (uint32_t)qs * G::OPERAND, w, warps);
+    gather_queries<D, TREE>(p, s, members, u, smem_u32(smem + lay.q) + (uint32_t)qs * G::OPERAND, w, warps);
   };
   auto sum_q = [&](const Visit& s, int u, int qs, int slot) {
     sum_queries<D, BF>(smem + lay.q + (size_t)qs * G::OPERAND,
@@ -1170,7 +1304,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         ok = wait_warp(kBarPassed + h, (v / kVisits - 1) & 1);
         if (!ok) break;
         for (int i = v + lane; i < min(nv, v + kVisits / 2); i += 32)
-          describe_visit(p, plan, lo + i, visits + 2 * (i & (kVisits - 1)));
+          describe_visit<TREE>(p, plan, lo + i, visits + 2 * (i & (kVisits - 1)));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarVisits + h));
       }
@@ -1181,7 +1315,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       for (int u = 0; u < tiles && ok; ++u, ++qc) {
         const int qs = qc & 1;
         if (qc >= 2 && !placed) {   // both tiles are in use: time for this
-          place_records(p, plan, FEW);
+          records();
           placed = true;
         }
         if (qc >= 2) ok = wait_warp(kBarQEmpty + qs, ((qc >> 1) - 1) & 1);
@@ -1194,7 +1328,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
       }
     }
-    if (!placed) place_records(p, plan, FEW);
+    if (!placed) records();
   } else if (warp >= 12) {
     // ============================ converters: K (12-15) and V (16-19)
     if constexpr (QUANT) {
@@ -1215,8 +1349,21 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           // scales of token t, with the middle code's part in the zero points
           const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
           const bool valid = t < hd.x && (hd.y >> (t >> 4) & 1);
-          const float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)slot * G::RAW_SCALES +
-                                                            (KV == KV_I8G ? t >> 6 : t) * 16);
+          float4 z = *reinterpret_cast<const float4*>(smem + lay.raw + (size_t)slot * G::RAW_SCALES +
+                                                      (KV == KV_I8G ? t >> 6 : t) * 16);
+          bool counts = valid;   // among the values' sizes
+          if constexpr (TREE) {
+            // A draft whose values are no numbers must not reach the rows that do not attend to
+            // it: its values are taken out here, and the merge gives them to the rows that do.
+            bool bad = false;
+            if (visits[2 * (v & (kVisits - 1))].y & kDrafts) {
+              bad = valid && !(fabsf(fmaf(255.f, z.z, z.w)) < INFINITY && fabsf(z.z) < INFINITY && fabsf(z.w) < INFINITY);
+              if (bad) z.z = z.w = 0.f;
+              counts = valid && !bad;
+            }
+            const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) reinterpret_cast<uint32_t*>(smem + lay.bad)[(v % kHdrs) * 4 + (warp - 12)] = bads;
+          }
           float* sc = reinterpret_cast<float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
           // (scores come out in the log2 domain; one without a token is -inf, see the softmax)
           const float vz = fmaf(G::CENTRE, z.z, z.w);
@@ -1227,7 +1374,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           sc[2 * kTile + 2] = valid ? vz : 0.f;
           // the largest of the values' sizes, and the smallest
           const float size = value_size(z.z, vz);
-          const float most = warp_max(valid ? size : 0.f), least = -warp_max(valid ? -size : -INFINITY);
+          const float most = warp_max(counts ? size : 0.f), least = -warp_max(counts ? -size : -INFINITY);
           if (lane == 0) {
             float* vm = reinterpret_cast<float*>(smem + lay.vmax + (v % kScaleSlots) * 32) + (warp - 12);
             vm[0] = most;
@@ -1249,7 +1396,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm_s(st) + lanes, to = tm_o(st) + lanes;
-    const size_t whole = (size_t)2 * B * p.num_q_heads;   // record rows of segments by stream
+    const size_t whole = (size_t)(TREE ? 1 : 2) * p.batch * p.num_q_heads;   // record rows of segments by stream
     int qc = 0, v = 0;
     uint32_t n_ev = 0, n_seg = 0, n_pair = 0, n_x = 0;   // events, segments, meetings so far
     auto meet = [&](int b, uint32_t& n) -> bool {   // two warps of the same rows
@@ -1269,6 +1416,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     const float* sc = nullptr;
     float lv = 0.f;
     bool even = true;
+    // trees of drafts: whether the tile has some, and which of its tokens' values are no numbers
+    [[maybe_unused]] bool drafts = false;
+    [[maybe_unused]] uint32_t bads[4] = {0, 0, 0, 0};
     auto begin = [&]() -> bool {
       if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
       if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
@@ -1276,13 +1426,20 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       ntok = hd.x;
       mask = hd.y;
       valid = row < ntok && (mask >> (row >> 4) & 1);
+      if constexpr (TREE) drafts = flags_of(v) & kDrafts;
+      if constexpr (TREE && QUANT) {
+        if (drafts) {
+          const uint4 b = *reinterpret_cast<const uint4*>(smem + lay.bad + (v % kHdrs) * 16);
+          bads[0] = b.x, bads[1] = b.y, bads[2] = b.z, bads[3] = b.w;
+        }
+      }
       if constexpr (QUANT) {
         sc = reinterpret_cast<const float*>(smem + lay.scales + (v % kScaleSlots) * G::SCALES);
         const float4* vm = reinterpret_cast<const float4*>(smem + lay.vmax + (v % kScaleSlots) * 32);
         const int most = size_exponent(fmaxf(fmaxf(vm[0].x, vm[0].y), fmaxf(vm[0].z, vm[0].w)));
         even = most - size_exponent(fminf(fminf(vm[1].x, vm[1].y), fminf(vm[1].z, vm[1].w))) <= kEvenBits;
         lv = (float)most;
-      } else if (ntok < kTile || mask != 0xFF) {
+      } else if (ntok < kTile || mask != 0xFF || (TREE && drafts)) {
         // rows of V that hold no token of this segment may hold anything, NaN
         // too, and a weight of 0 would not clear it
         const int slot = v % S;
@@ -1295,6 +1452,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 #pragma unroll 4
           for (int i = 0; i < G::HALVES * 8; ++i)
             *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        if constexpr (TREE) {
+          if (drafts) {   // (see the converters)
+            int* marks = reinterpret_cast<int*>(smem + lay.bad) + (v % kBadSlots) * kTile;
+            if (valid) clear_no_numbers<G::HALVES, BF>(smem + lay.ring + (size_t)(S + slot) * G::ENTRY, row, marks + row, v);
+            if (!meet_all()) return false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bads[i] = __ballot_sync(0xffffffffu, *(volatile int*)(marks + 32 * i + lane) == v);
+          }
         }
       }
       tc_after();
@@ -1329,6 +1495,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         float* xch = reinterpret_cast<float*>(smem + lay.xch) + st * (2 * 4 * 32);
         uint8_t* pt = smem + lay.pt + st * G::PT;
         const bool wide = s.rows > 8;
+        [[maybe_unused]] uint32_t poison = 0;   // rows that attend to values that are no numbers
         float r = -INFINITY, l[FEW];
         [[maybe_unused]] float zs[FEW];
         int flags = s.flags;
@@ -1344,6 +1511,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               }
             }
             float a[FEW];
+            [[maybe_unused]] uint32_t sees = 0;   // rows that attend to the thread's token
+            if constexpr (TREE) {
+              sees = !valid ? 0u : drafts ? tree_rows(p, s, visits[2 * (v & (kVisits - 1))].x + row) : 0xffffffffu;
+              if (drafts && (bads[quad] >> lane & 1)) poison |= sees;
+            }
             const int at = (row >> 1) * 4 + (row & 1);
             const float ks = QUANT ? sc[at] : p.scale;
             const float kz = QUANT ? sc[at + 2] : 0.f, vs = QUANT ? sc[2 * kTile + at] : 1.f;
@@ -1364,7 +1536,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 a[e + j] = QUANT ? fmaf(ks, a[e + j], kz * reinterpret_cast<const float*>(q4)[j]) : a[e + j] * ks;
-                if (!valid) a[e + j] = -INFINITY;
+                if (TREE ? !(sees >> (e + j) & 1) : !valid) a[e + j] = -INFINITY;
                 const float w = warp_max(QUANT ? a[e + j] + lt : a[e + j]);
                 if (lane == e + j) keep = w;
               }
@@ -1447,11 +1619,18 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           xb[quad * 32 + e + j] = ls;
           if constexpr (QUANT) xb[quad * 32 + FEW + e + j] = scatter_sum8(zs + e, lane, j);
         }
+        if constexpr (TREE) xb[quad * 32 + 31] = __uint_as_float(__reduce_or_sync(0xffffffffu, poison));
         ok = meet_all();
         if (!ok) break;
         auto total = [&](int i) { return (xb[i] + xb[32 + i]) + (xb[64 + i] + xb[96 + i]); };
         if (row < s.rows) {
-          p.ws_ml[rec0 + row] = make_float2(r, total(row));
+          float ls = total(row);
+          if constexpr (TREE) {   // a sum with a sign: values were left out, see the merge
+            const uint32_t rows = __float_as_uint(xb[31]) | __float_as_uint(xb[63]) | __float_as_uint(xb[95]) |
+                                  __float_as_uint(xb[127]);
+            if (rows >> row & 1) ls = -ls;
+          }
+          p.ws_ml[rec0 + row] = make_float2(r, ls);
           if (!s.is(kMany)) {   // a part of one visit: the other stream has nothing
             const size_t other = s.is(kContinued) ? rec0 + (st ? -kTile : kTile) : st ? s.rec : whole + s.rec;
             p.ws_ml[other + row] = make_float2(-INFINITY, 0.f);
@@ -1489,6 +1668,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       const bool active = quad * 32 < my_rows;   // this warp has query rows
       float r = -INFINITY, l = 0.f;
       [[maybe_unused]] float zs = 0.f, qs = 0.f;
+      [[maybe_unused]] bool poison = false;   // the row attends to values that are no numbers
       for (;;) {
         if (two || (v & 1) == st) {
           ok = begin();
@@ -1496,17 +1676,29 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (active) {
             if (QUANT && !have) qs = qsum[row];
             const uint64_t qs2 = pack2f(qs, qs), scale2 = pack2f(p.scale, p.scale);
-            if (ntok < kTile || mask != 0xFF) {   // columns without a token
+            [[maybe_unused]] uint4 sees = make_uint4(~0u, ~0u, ~0u, ~0u);   // tokens that the row attends to
+            auto sees32 = [&](int c) { return c < 64 ? (c < 32 ? sees.x : sees.y) : (c < 96 ? sees.z : sees.w); };
+            if constexpr (TREE) {
+              if (drafts && row < my_rows) {
+                sees = tree_window(p, s.row, (s.q0 + (two ? st * kTile : 0) + row) / Gq, visits[2 * (v & (kVisits - 1))].x);
+                poison |= (sees.x & bads[0]) | (sees.y & bads[1]) | (sees.z & bads[2]) | (sees.w & bads[3]);
+              }
+              __syncwarp();
+            }
+            // (quantised caches: drafts are left out where scores are scaled, below)
+            if (ntok < kTile || mask != 0xFF || (TREE && !QUANT && drafts)) {   // columns without a token
 #pragma unroll 1
               for (int c = 0; c < kTile; c += 16) {
                 const int left = mask >> (c >> 4) & 1 ? ntok - c : 0;
-                if (left >= 16) continue;
+                uint32_t on = 0xFFFFu;
+                if constexpr (TREE && !QUANT) on = sees32(c) >> (c & 16) & 0xFFFFu;
+                if (left >= 16 && (!TREE || QUANT || __all_sync(0xffffffffu, on == 0xFFFFu))) continue;
                 float a[16];
                 tmem_ld<16>(ts + c, reinterpret_cast<uint32_t*>(a));
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                  if (j >= left) a[j] = -INFINITY;
+                  if (j >= left || (TREE && !QUANT && !(on >> j & 1))) a[j] = -INFINITY;
                 tmem_st<16>(ts + c, reinterpret_cast<uint32_t*>(a));
               }
               tc_wait_st();
@@ -1523,6 +1715,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 for (int j = 0; j < COLS; j += 2) {
                   const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * (c + j));
                   unpack2f(ffma2(pack2f(a[j], a[j + 1]), k2.x, fmul2(k2.y, qs2)), a[j], a[j + 1]);
+                }
+                if constexpr (TREE) {
+                  if (drafts) {
+                    const uint32_t on = sees32(c);
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j)
+                      if (!(on >> j & 1)) a[j] = -INFINITY;
+                  }
                 }
                 tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
               }
@@ -1642,7 +1842,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         int from = 0, to_c = D;
         if (both) {
           float4* mls = reinterpret_cast<float4*>(smem + lay.ml);
-          mls[st * kTile + row] = make_float4(r, l, z, 0.f);
+          mls[st * kTile + row] = make_float4(r, l, z, TREE && poison ? 1.f : 0.f);
           tc_before();
           ok = meet(kBarPair + quad, n_pair);
           if (!ok) break;
@@ -1654,9 +1854,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           f1 = fast_exp2(other.x - Rr);
           L = fmaf(l, f0, other.y * f1);
           z = fmaf(z, f0, other.z * f1);
+          if constexpr (TREE) poison |= other.w != 0.f;
           from = st * (D / 2);
           to_c = from + D / 2;
         }
+        if constexpr (TREE) L = poison ? -L : L;
         if (row < my_rows && from == 0) p.ws_ml[rec0 + tile_row] = make_float2(R, L);
         // CHUNK channels at a time through shared memory (the stream's place for transposed
         // weights), so that a row's 64 (32) bytes are written together
@@ -1719,7 +1921,34 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 // kernel is short, as its code is fetched anew by every call.
 constexpr int kMergeThreads = 128;
 
-template <int D, int WPW>
+// The attention kernel takes infinities and NaNs out of the drafts' values (0 times one of them would be
+// one, in rows that do not attend to it) and marks the records of the rows that do attend to them:
+// the sum of those of a row's four channels, for its output.
+static __device__ __noinline__ float4 no_numbers(const SharedParams& p, int b, int t, int h, int ch, int D) {
+  const TreePlan r = tree_plan(p, b);
+  const uint64_t* words = tree_words(p, b, t);
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int j = 0; j < r.drafts; ++j) {
+    if (!(tree_bits(p, words, t, j) & 1)) continue;
+    const int tok = r.len - r.drafts + j, page = p.block_table[(size_t)b * p.max_pages + tok / p.page_size];
+    if (page < 0 || page >= p.num_pages) continue;
+    const size_t row = ((size_t)page * p.num_kv_heads + h) * p.page_size + tok % p.page_size;
+    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.kv_kind >= KV_I8T) z = *reinterpret_cast<const float4*>(p.kv_sz + (p.kv_kind == KV_I8G ? row / 64 : row) * 4);
+    for (int i = 0; i < 4; ++i) {
+      const size_t at = row * D + ch + i;
+      const float v = p.kv_kind == KV_F16    ? __half2float(reinterpret_cast<const __half*>(p.v_pages)[at])
+                      : p.kv_kind == KV_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v_pages)[at])
+                      : p.kv_kind == KV_U4T  ? fmaf((float)(p.v_pages[at / 2] >> (at & 1) * 4 & 15), z.z, z.w)
+                                             : fmaf((float)p.v_pages[at], z.z, z.w);
+      if (!(fabsf(v) < INFINITY)) x[i] += v;
+    }
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+template <int D, int WPW, bool TREE>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __grid_constant__ SharedParams p) {
   constexpr int BATCH = 4;
   __shared__ float4 part_a[WPW > 1 ? WPW : 1][32];
@@ -1729,13 +1958,29 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   const int item = at / D;   // row and query head
   pdl_wait();
   if (at >= p.batch * p.num_q_heads * D) return;
-  const int kvi = item / p.group, gq = item - kvi * p.group;   // row and kv head
-  const int4 own = __ldcg(p.ws_info + 3 * kvi);
-  int4 pre = __ldcg(p.ws_info + 3 * kvi + 1);
-  const int4 pre2 = __ldcg(p.ws_info + 3 * kvi + 2);
-  if (gq >= pre.w >> 1) pre = pre2;   // in the next pair of row tiles
-  pre.w &= 1;
-  const int ch = at % D, whole = 2 * p.batch * p.num_q_heads;
+  const int kvi = item / p.group;   // row and kv head
+  int gq = item - kvi * p.group;
+  int4 own = make_int4(0, 0, 0, 0), pre;
+  [[maybe_unused]] int seq = 0, draft = 0, head = 0;
+  [[maybe_unused]] bool marked = false;   // some of its records leave values out
+  if constexpr (TREE) {
+    const int b = kvi / p.num_kv_heads;
+    head = kvi - b * p.num_kv_heads;
+    seq = b / p.drafts;
+    draft = b - seq * p.drafts;
+    const int R = draft * p.group + gq, pair = R / (2 * kTile);   // among the sequence's query rows of this kv head
+    pre = __ldcg(p.ws_info + ((size_t)seq * p.num_kv_heads + head) * p.pairs + pair);
+    gq = R - pair * 2 * kTile;
+    if (gq >= pre.z >> 16) pre.z = gq = 0;   // no draft of the sequence
+    pre.z &= 0xFFFF;
+  } else {
+    own = __ldcg(p.ws_info + 3 * kvi);
+    pre = __ldcg(p.ws_info + 3 * kvi + 1);
+    const int4 pre2 = __ldcg(p.ws_info + 3 * kvi + 2);
+    if (gq >= pre.w >> 1) pre = pre2;   // in the next pair of row tiles
+    pre.w &= 1;
+  }
+  const int ch = at % D, whole = (TREE ? 1 : 2) * p.batch * p.num_q_heads;
   const int n0 = pre.z << pre.w, n1 = own.z << own.w;
   float M = -INFINITY, L = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1759,6 +2004,10 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
       r = on ? r + gq : 0;
       ml[i] = __ldcg(p.ws_ml + r);
       if (!on) ml[i] = make_float2(-INFINITY, 0.f);
+      if constexpr (TREE) {
+        marked |= signbit(ml[i].y);
+        ml[i].y = fabsf(ml[i].y);
+      }
       a[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (size_t)r * D + ch));
     }
     float Mn = M;
@@ -1780,13 +2029,17 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   }
   if constexpr (WPW > 1) {
     part_a[w][lane] = A;
-    part_ml[w][lane] = make_float2(M, L);
+    part_ml[w][lane] = make_float2(M, TREE && marked ? -L : L);
     __syncthreads();
     if (w != 0) return;
 #pragma unroll 1
     for (int o = 1; o < WPW; ++o) {
-      const float2 ml = part_ml[o][lane];
+      float2 ml = part_ml[o][lane];
       const float4 a = part_a[o][lane];
+      if constexpr (TREE) {
+        marked |= signbit(ml.y);
+        ml.y = fabsf(ml.y);
+      }
       const float Mn = fmaxf(M, ml.x), Mr = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M - Mr), f2 = fast_exp2(ml.x - Mr);
       L = L * f + ml.y * f2;
       A = make_float4(A.x * f + a.x * f2, A.y * f + a.y * f2, A.z * f + a.z * f2, A.w * f + a.w * f2);
@@ -1795,7 +2048,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   }
   // no token at all: zeros (L is 0 only then, or where every score is -inf; a NaN stays one)
   const float r = L == 0.f ? 0.f : 1.f / L;
-  const float4 f = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
+  float4 f = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
+  if constexpr (TREE) {
+    if (marked) {
+      const float4 x = no_numbers(p, seq, draft, head, ch, D);
+      f = make_float4(f.x + x.x, f.y + x.y, f.z + x.z, f.w + x.w);
+    }
+  }
   if (p.out_dtype == PKV_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = f;
   } else {

@@ -1,16 +1,19 @@
 """Build libpkv.so in-tree with nvcc for sm_103a (no torch extension machinery).
 
 Each translation unit compiles in parallel; the shared library is relinked only
-when a source or header is newer than it.
+when a source or header is newer than it. Beside it, where torch is installed with its
+headers: _pkv_torch.so, host code that makes some calls from torch tensors without Python.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
+TORCH_SRC = os.path.join(CSRC, "torch", "torch_calls.cpp")
+TORCH_LIB = os.path.join(OUT_DIR, "_pkv_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,6 +49,22 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_job(cuda: str):
+    """The command that builds TORCH_LIB; None where torch or the headers are not there."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    home, python = spec.submodule_search_locations[0], sysconfig.get_paths()["include"]
+    include, libs = os.path.join(home, "include"), os.path.join(home, "lib")
+    if not (os.path.exists(os.path.join(python, "Python.h")) and
+            os.path.exists(os.path.join(include, "torch", "csrc", "autograd", "python_variable.h")) and shutil.which("g++")):
+        return None
+    paths = [INCLUDE, include, os.path.join(include, "torch", "csrc", "api", "include"), python, os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for p in paths for x in ("-I", p)] + \
+        [TORCH_SRC, "-o", TORCH_LIB + ".tmp", "-L", libs] + \
+        ["-l" + n for n in ("torch_python", "torch", "torch_cuda", "torch_cpu", "c10_cuda", "c10")]
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     """Compile every source under csrc/ and link _lib/libpkv.so; return its path."""
     nvcc = _nvcc()
@@ -64,6 +85,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 cmd = [nvcc] + common + ["-c", src, "-o", obj]
             jobs.append(cmd)
 
+    torch_job = None
+    if force or _stale(TORCH_LIB, [TORCH_SRC] + headers):
+        torch_job = _torch_job(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))))
+    tool_jobs = len(jobs)
+    if torch_job:
+        jobs.append(torch_job)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -75,8 +103,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 if verbose or r.returncode != 0:
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed on {cmd[-3]}")
-    if force or jobs or _stale(LIB, objs):
+                    raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd[-3:])}")
+    if torch_job:
+        os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    if force or tool_jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -8,6 +8,7 @@ unloadable library raises, there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from ctypes import POINTER, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import Optional
@@ -56,6 +57,7 @@ class PkvCache(ctypes.Structure):
 
 
 _lib: Optional[ctypes.CDLL] = None
+_torch_calls = None
 
 
 def library_path() -> str:
@@ -117,6 +119,23 @@ def lib() -> ctypes.CDLL:
         fn.argtypes = args
     _lib = L
     return L
+
+
+def torch_calls():
+    """The module of csrc/torch, its calls bound to this library's; None where it is not built."""
+    global _torch_calls
+    if _torch_calls is None:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "_pkv_torch.so")
+        _torch_calls = False
+        if os.path.exists(path):
+            spec = importlib.util.spec_from_file_location("_pkv_torch", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            L = lib()
+            module.bind(*(ctypes.cast(f, c_void_p).value
+                          for f in (L.pkv_rotary_append, L.pkv_tree_attention, L.pkv_keep_tokens)))
+            _torch_calls = module
+    return _torch_calls or None
 
 
 def _check(status: int, where: str) -> None:

@@ -199,6 +199,11 @@ class PagedKVCache:
         self._shared_fit: Dict[Tuple[int, int, int, int, int], torch.Tensor] = {}   # the same, by stream and shape
         self._shared_lent: Dict[int, torch.Tensor] = {}   # by address
         self._shared_lock = threading.Lock()
+        # the calls for drafted tokens without Python in between (None: they go the way of the others)
+        self._calls = B.torch_calls() if self.device.type == "cuda" else None
+        self._native = None if self._calls is None else self._calls.handle(
+            ctypes.addressof(self._desc), self.device.index, self._shared_fit, self._shared_lock.acquire,
+            self._shared_lock.release)
 
     @classmethod
     def from_pools(cls, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_dtype: str = "bf16",
@@ -516,6 +521,11 @@ class PagedKVCache:
         stand in it, by default at their positions in the sequence. interleaved: pairs of
         neighbouring channels instead of the rotated part's two halves. q_out may be q itself.
         Behind this call an attention call has no fresh_rows to promise: the queries are new."""
+        if stream is None and self._native is not None:
+            got = self._calls.rotary_append(self._native, q, k_new, v_new, cos_sin, block_table, positions, rotary_positions,
+                                            new_lens, interleaved, q_out, dev_status)
+            if got is not NotImplemented:
+                return got
         if stream is not None:
             with torch.cuda.stream(stream):   # q_out is allocated on it
                 return self.rotary_append(q, k_new, v_new, cos_sin, block_table, positions, rotary_positions, new_lens,
@@ -573,6 +583,11 @@ class PagedKVCache:
         before the drafts and to those drafts that mask, int64 [B][T][ceil(T / 64)] or [T][ceil(T / 64)],
         has a bit for (tree_mask makes one; None: all up to itself). Rows beyond draft_lens are zeros.
         workspace, stream: as for shared_attention."""
+        if stream is None and workspace is None and self._native is not None:
+            got = self._calls.tree_attention(self._native, q, block_table, seq_lens, mask, draft_lens, sm_scale, out,
+                                             _TORCH_TO_PKV.get(out_dtype), num_splits, dev_status)
+            if got is not NotImplemented:
+                return got
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.tree_attention(q, block_table, seq_lens, mask, draft_lens, sm_scale, out, out_dtype,
@@ -622,6 +637,9 @@ class PagedKVCache:
         """Token first[b] + keep[b][j] of row b becomes token first[b] + j, for j < keep_lens[b] (by default
         all of keep [B][K], strictly ascending): of the drafts from first[b] on the accepted
         path stays. Not for per-group caches: append the accepted tokens anew at first[b]."""
+        if stream is None and self._native is not None and \
+                self._calls.keep_tokens(self._native, keep, keep_lens, block_table, first, dev_status) is not NotImplemented:
+            return
         if keep.dim() != 2 or block_table.dim() != 2:
             raise ValueError("keep must be [batch][tokens], block_table [batch][pages]")
         Bsz, K = keep.shape

@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     __syncthreads();
   } else {
     const int lens32 = lane < NG ? p.prefix_lens[lane] : 0;   // of the first 32 groups
-  #pragma unroll 1
+#pragma unroll 1
     for (int b0 = warp * 32; b0 < B; b0 += NT) {
       const int b = b0 + lane;
       const RowPlan r = row_plan(p, b < B ? p.seq_lens[b] : 0, b < B ? p.prefix_group[b] : -1, [&](int g) {
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       skip[b] = r.skip;
       rowg[b] = (int16_t)r.group;
     }
-  #pragma unroll 1
+#pragma unroll 1
     for (int g = tid; g < NG; g += NT) {
       const int P = g < 32 ? lens32 : p.prefix_lens[g];
       if (P < 0 && blockIdx.x == 0) flag_status(p.dev_status, PKV_DEV_BAD_GROUP);
@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
     __syncthreads();
     if (warp == 0 && NG > 0) {   // each row's place among its group's rows
-  #pragma unroll 1
+#pragma unroll 1
       for (int b0 = 0; b0 < B; b0 += 32) {
         const int b = b0 + lane, g = b < B ? rowg[b] : -1;
         const unsigned same = __match_any_sync(0xffffffffu, g);
@@ -1180,6 +1180,66 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (!ok) break;
           rows = uni(d.rows);
           flags = uni(d.flags);
+          if constexpr (TREE) {
+          // Whole tiles within a segment of two row tiles: the order of the passes below, S of one stream
+          // and P V of the other, without what the ends of segments need. (The warp's instructions, fetched
+          // anew between those of the softmax, set the pace of such segments.)
+          constexpr int kMiddle = kFirst | kLast | kTwo | 0xFF;
+          if (pend.on && !p.two_terms && (flags & kMiddle) == (kTwo | kTile)) {
+            const uint32_t hi_k = (uint32_t)(kmajor >> 32), hi_v = (uint32_t)(vmajor >> 32), lo_v = (uint32_t)vmajor;
+            constexpr uint32_t is = kType | (uint32_t)(kTile / 8) << 17, io = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
+            auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+            uint32_t vlo = lo_v | (QUANT ? vop : ring + (uint32_t)(S + pend.at.slot) * G::ENTRY) >> 4;
+            int vslot = pend.at.slot;
+            uint32_t acc = !pend.fresh;   // of the first P V to come
+            pend.fresh = false;
+            do {
+              ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + pos.slot, pos.phase);
+              if (!ok) break;
+              const uint32_t klo = (uint32_t)kmajor | (QUANT ? kop : ring + (uint32_t)pos.slot * G::ENTRY) >> 4;
+#pragma unroll 1
+              for (u = 0; u < 2; ++u) {
+                const uint32_t qlo = (uint32_t)kmajor | (qb + (uint32_t)((qc + u) & 1) * G::OPERAND) >> 4;
+                tc_after();
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(tm_s(u), desc(qlo + (k >> 2) * 1024 + (k & 3) * 2, hi_k), desc(klo + (k >> 2) * 1024 + (k & 3) * 2, hi_k),
+                         is, k > 0, on);
+                tc_commit(bar(kBarS + u), on);
+                if (u == 1) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + pos.slot), on);
+                const int o = u ^ 1;
+                ok = wait_warp(kBarP + o, ~(odd >> o) & 1);
+                if (!ok) break;
+                if (u == 1) {   // P V of this visit
+                  vslot = pos.slot;
+                  if constexpr (!QUANT) vlo = lo_v | (ring + (uint32_t)(S + vslot) * G::ENTRY) >> 4;
+                  ok = QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + vslot, pos.phase);
+                  if (!ok) break;
+                }
+                tc_after();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  mma_ts(tm_o(o), tm_s(o) + 32 * (j >> 1) + 8 * (j & 1), desc(vlo + j * 128, hi_v), io, j > 0 ? 1 : acc, on);
+                acc = 1;
+                if (u == 0) {
+                  tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarVEmpty + vslot), on);
+                  vop_phase ^= 1;
+                }
+                odd ^= 1u << u;
+              }
+              if (!ok) break;
+              u = 0;
+              pend.at = pos;
+              passed(v);
+              ++v;
+              pos.next(S);
+              ok = described(v);
+              if (!ok) break;
+              flags = uni(flags_of(v));
+            } while ((flags & kMiddle) == (kTwo | kTile));
+            if (!ok) break;
+          }
+          }
           ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + pos.slot, pos.phase);
           if (!ok) break;
           begun = true;
@@ -1462,12 +1522,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             for (int i = 0; i < 4; ++i) bads[i] = __ballot_sync(0xffffffffu, *(volatile int*)(marks + 32 * i + lane) == v);
           }
         }
+        fence_proxy_async_smem();   // before the products read them
       }
       tc_after();
       return true;
     };
     auto end_event = [&]() {   // the weights are written
-      fence_proxy_async_smem();
       tc_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarP + st));
@@ -1599,6 +1659,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               *reinterpret_cast<uint4*>(pt + e * 256 + row * 16) = make_uint4(hi16[0], hi16[1], hi16[2], hi16[3]);
               *reinterpret_cast<uint4*>(pt + (FEW + e) * 256 + row * 16) = make_uint4(lo16[0], lo16[1], lo16[2], lo16[3]);
             }
+            fence_proxy_async_smem();
             have = true;
             end_event();
           }

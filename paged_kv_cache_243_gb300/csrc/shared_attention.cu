@@ -2,6 +2,7 @@
 // shared_kernel.cuh.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 #include <set>
 #include <utility>
@@ -119,6 +120,17 @@ bool pool_map(void* base, uint64_t rows, int d, bool bf, CUtensorMap& m) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [rows][heads][d] in boxes of 64 channels x a group's heads x `drafts` rows.
+bool query_map(const void* q, uint64_t rows, int heads, int group, int d, int drafts, bool bf, CUtensorMap& m) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, rows}, strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)drafts}, step[3] = {1, 1, 1};
+  return enc(&m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q), dims,
+             strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int kind_of(const pkv_cache* c) {
   return c->kv_dtype == PKV_F16 ? KV_F16 : c->kv_dtype == PKV_BF16 ? KV_BF16 : c->kv_dtype == PKV_U4 ? KV_U4T
          : c->quant == PKV_QUANT_PER_TOKEN ? KV_I8T : KV_I8G;
@@ -161,10 +173,17 @@ pkv_status cache_params(const pkv_cache* c, const Device& dev, const void* fn, i
   return PKV_OK;
 }
 
-template <int D, bool TREE>
+template <int D>
 const void* merge_kernel(int warps) {
-  return warps == 4 ? reinterpret_cast<const void*>(&shared_merge_kernel<D, 4, TREE>)
-                    : reinterpret_cast<const void*>(&shared_merge_kernel<D, 1, TREE>);
+  return warps == 4 ? reinterpret_cast<const void*>(&shared_merge_kernel<D, 4>)
+                    : reinterpret_cast<const void*>(&shared_merge_kernel<D, 1>);
+}
+
+template <int D>
+const void* tree_merge(int warps, int lrows) {
+  return warps == 4   ? reinterpret_cast<const void*>(&tree_merge_kernel<D, 4, 1>)
+         : lrows == 1 ? reinterpret_cast<const void*>(&tree_merge_kernel<D, 1, 1>)
+                      : reinterpret_cast<const void*>(&tree_merge_kernel<D, 1, 2>);
 }
 
 }  // namespace
@@ -236,7 +255,7 @@ pkv_status launch_shared(const SharedArgs& a) {
   // 16K, 4-bit) 45.6 and 42.5, 1024 (32 rows x 2K) 23.3 and 25.1, 2048 (64 rows x 16K) 49.4 and 48.1,
   // (64 rows x 8K, INT8) 58.1 and 59.9, 3904 (5 groups x 5K) 46.6 and 57.6, 8192 (256 rows x 8K) 83 and 104.
   const int wpw = units < 6 * dev.sms ? 4 : 1;
-  const void* merge = D == 64 ? merge_kernel<64, false>(wpw) : merge_kernel<128, false>(wpw);
+  const void* merge = D == 64 ? merge_kernel<64>(wpw) : merge_kernel<128>(wpw);
   const int per = 4 / wpw;
   return launch_pdl(merge, dim3((unsigned)((units + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
              ? PKV_OK
@@ -307,13 +326,21 @@ pkv_status launch_tree(const TreeArgs& a) {
   p.mask_words = (a.drafts + 63) / 64;
   p.mask_stride = a.mask_shared ? 0 : (long long)a.drafts * p.mask_words;
   p.pairs = pairs;
+  // Row tiles that end between two drafts are copied as boxes; the others are gathered. (24 x 8K, 64 drafts of 4 heads:
+  // a segment's 256 rows by one warp took 8 us, which nothing hides.)
+  p.q_box = kTile % group != 0 ? 0 : std::min(a.drafts, kTile / group);
+  if (p.q_box && !query_map(a.q, (uint64_t)rows, a.num_q_heads, group, D, p.q_box, bf, p.tmap_q)) return PKV_ERR_CUDA;
   void* args[] = {&p};
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
-  const long long outs = (long long)rows * a.num_q_heads * D, units = (outs + 127) / 128;
+  const long long units = ((long long)rows * a.num_q_heads * D + 127) / 128;
   const int wpw = units < 6 * dev.sms ? 4 : 1;   // (see above)
-  const void* merge = D == 64 ? merge_kernel<64, true>(wpw) : merge_kernel<128, true>(wpw);
+  // Two rows a lane where the merge alone would be several waves; one against two (and four), us a call: 4096 units
+  // (8 x 4K) 31.5, 32.5 (34.4), 12288 (16 x 8K INT8) 128, 124 (125), 49152 (24 x 8K of 64) 191, 164 (163).
+  const int lrows = units >= 48 * dev.sms ? 2 : 1, each = lrows * 128 / D;
+  const long long items = (long long)a.batch * c->num_kv_heads * ((a.drafts * group + each - 1) / each);
+  const void* merge = D == 64 ? tree_merge<64>(wpw, lrows) : tree_merge<128>(wpw, lrows);
   const int per = 4 / wpw;
-  return launch_pdl(merge, dim3((unsigned)((units + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
+  return launch_pdl(merge, dim3((unsigned)((items + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

@@ -121,6 +121,7 @@ struct SharedLayout {
 };
 struct SharedParams {
   CUtensorMap tmap_k, tmap_v;   // 16-bit pools as [rows][d], boxes of 16 rows x 64 channels
+  CUtensorMap tmap_q;           // trees: the queries as [drafts][heads][d], see q_box
   const uint8_t* k_pages;
   const uint8_t* v_pages;
   const float* kv_sz;
@@ -142,6 +143,7 @@ struct SharedParams {
   const int32_t* draft_lens;   // drafts of each sequence, or NULL: `drafts` of each
   const uint64_t* tree_mask;   // [sequences][drafts][mask_words], or NULL: each after the one before
   int drafts, mask_words, pairs, kv_kind;
+  int q_box;   // drafts of a box of queries (64 channels of a group's heads of each), 0: they are gathered
   long long mask_stride;       // words from one sequence's masks to the next's (0: the same)
   SharedLayout lay;
 };
@@ -170,7 +172,7 @@ enum SharedBars {   // mbarriers, 8 bytes each
   kBarHdr = 4 * kMaxEntries, kBarQFull = kBarHdr + kHdrs, kBarQEmpty = kBarQFull + 2, kBarS = kBarQEmpty + 2,
   kBarP = kBarS + 2, kBarO = kBarP + 2, kBarKop = kBarO + 2, kBarVop = kBarKop + 2,
   kBarPair = kBarVop + 2, kBarVisits = kBarPair + 4, kBarPassed = kBarVisits + 2, kBarEnd = kBarPassed + 2,
-  kBarCount = kBarEnd + 1
+  kBarQLoad = kBarEnd + 1 /* copied queries whose sums are still to be taken */, kBarCount = kBarQLoad + 2
 };
 
 template <class G>
@@ -203,12 +205,13 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.lpre = put((groups + 1) * 4);
   o.moff = put((groups + 1) * 4);
   o.members = put(batch * 2);
+  if (tree) o.gp = put(groups * 4);
   o.total = at;
   // the plan's other arrays are needed only while the ring is still empty
   at = o.ring;
   o.lens = put(batch * 4);
   o.skip = put(batch * 4);
-  o.gp = put(groups * 4);
+  if (!tree) o.gp = put(groups * 4);
   o.rank = put(batch * 2);
   o.rowg = put(batch * 2);
   if (at > o.total) o.total = at;
@@ -356,7 +359,7 @@ struct SharedPlan {
   const int *gpre, *lpre, *bpre;   // visits before each group's prefix (heavy, other), each row's own tokens
   const int* moff;                 // members before each group
   const uint16_t* members;
-  const int *lens, *skip, *gp;     // shared memory (while planning), or NULL: from the inputs again
+  const int *lens, *skip, *gp;     // shared memory (while planning), or NULL: from the inputs again (trees: gp stays)
   int lo, hi;                      // the block's visits
 };
 
@@ -448,19 +451,15 @@ __device__ __forceinline__ const uint64_t* tree_words(const SharedParams& p, int
   return p.tree_mask ? p.tree_mask + g * p.mask_stride + (size_t)t * p.mask_words : nullptr;
 }
 
-// The four words of a tile's 128 tokens for draft t of sequence g.
-static __device__ __noinline__ uint4 tree_window(const SharedParams& p, int g, int t, int tok0) {
-  const TreePlan r = tree_plan(p, g);
-  const int j0 = tok0 - (r.len - r.drafts);
+// The four words of a tile's 128 tokens for draft t of sequence g; the tile's first token is draft j0.
+static __device__ __noinline__ uint4 tree_window(const SharedParams& p, int g, int t, int j0) {
   const uint64_t* w = tree_words(p, g, t);
   return make_uint4(tree_bits(p, w, t, j0), tree_bits(p, w, t, j0 + 32), tree_bits(p, w, t, j0 + 64),
                     tree_bits(p, w, t, j0 + 96));
 }
 
-// Which of a segment's few query rows attend to token `tok` of the sequence.
-static __device__ __noinline__ uint32_t tree_rows(const SharedParams& p, const Visit& s, int tok) {
-  const TreePlan r = tree_plan(p, s.row);
-  const int j = tok - (r.len - r.drafts);
+// Which of a segment's few query rows attend to draft j of the sequence (below 0: a token before the drafts).
+static __device__ __noinline__ uint32_t tree_rows(const SharedParams& p, const Visit& s, int j) {
   if (j < 0) return 0xffffffffu;
   uint32_t rows = 0;
 #pragma unroll 4
@@ -480,9 +479,8 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
     const int* pre = x < pl.gpre[p.num_groups] ? pl.gpre : pl.lpre;
     const int g = upper(pre, p.num_groups, x);
     if constexpr (TREE) {
-      const TreePlan r = tree_plan(p, g);
-      end_tok = r.len;
-      drafts = r.drafts;
+      end_tok = pl.gp[g];
+      drafts = pl.moff[g + 1] - pl.moff[g];
     } else {
       end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] & -p.round_to;
     }
@@ -810,9 +808,8 @@ static __device__ __noinline__ void place_tree_records(const SharedParams& p, co
 #pragma unroll 1
   for (int i = blockIdx.x + gridDim.x * lane; i < p.num_groups * p.num_kv_heads * p.pairs; i += gridDim.x * 32) {
     const int gh = i / p.pairs, pair = i - gh * p.pairs, g = gh / p.num_kv_heads, h = gh - g * p.num_kv_heads;
-    const TreePlan r = tree_plan(p, g);
-    const int rows = r.drafts * p.group, pairs = (rows + 2 * kTile - 1) / (2 * kTile);
-    const int n = (int)((uint32_t)(r.len + kTile - 1) / kTile), mine = min(2 * kTile, rows - pair * 2 * kTile);
+    const int rows = (pl.moff[g + 1] - pl.moff[g]) * p.group, pairs = (rows + 2 * kTile - 1) / (2 * kTile);
+    const int n = (int)((uint32_t)(pl.gp[g] + kTile - 1) / kTile), mine = min(2 * kTile, rows - pair * 2 * kTile);
     int4 info = make_int4(0, 0, 0, 0);
     if (mine > 0) {
       const int x = (rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, c = shares.block_of(x);
@@ -863,6 +860,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarQFull + i), 1);
       mbar_init(bar(kBarQEmpty + i), 1);
+      mbar_init(bar(kBarQLoad + i), 1);
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), 4);
       mbar_init(bar(kBarO + i), 1);
@@ -990,7 +988,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, lo, hi};
   __syncthreads();
   if (tid < min(nv, kVisits)) describe_visit<TREE>(p, plan, lo + tid, visits + 2 * tid);
-  plan.lens = plan.skip = plan.gp = nullptr;
+  plan.lens = plan.skip = nullptr;
+  if constexpr (!TREE) plan.gp = nullptr;
   fence_proxy_async_smem();   // the ring, so far the plan's, is the copies' from here on
   tc_before();
   __syncthreads();
@@ -1045,7 +1044,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   Visit first;
   visit(0, first);
   const int first_tiles = first.rows > kTile ? 2 : 1;
-  if (warp < 8) {
+  const bool copied_q = TREE && p.q_box;   // queries come by tensor copies, issued by warp 10
+  if (copied_q) {
+  } else if (warp < 8) {
     for (int u = 0; u < first_tiles; ++u) gather_q(first, u, u, warp, 8);
     fence_proxy_async_smem();
     named_bar_sync(1, 288);
@@ -1354,10 +1355,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ============================== Q gather, from the second segment on
-    int qc = first_tiles;
+    // ============================== Q gather, from the second segment on (copies: from the first)
+    int qc = copied_q ? 0 : first_tiles;
     bool ok = true, placed = false;
-    for (int v = 1; v < nv && ok; ++v) {
+    for (int v = copied_q ? 0 : 1; v < nv && ok; ++v) {
       if (v >= kVisits && (v & (kVisits / 2 - 1)) == 0) {
         // the next half of the visits' descriptions, once the last use of their place is over
         const int h = v / (kVisits / 2) & 1;
@@ -1380,6 +1381,23 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         }
         if (qc >= 2) ok = wait_warp(kBarQEmpty + qs, ((qc >> 1) - 1) & 1);
         if (!ok) break;
+        if (copied_q) {
+          const uint32_t full = bar((QUANT ? kBarQLoad : kBarQFull) + qs);
+          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(G::HALVES * 128 * Gq) * (uint32_t)p.q_box);
+          __syncwarp();
+          if (lane < G::HALVES)
+            tma_load_3d(smem_u32(smem + lay.q) + (uint32_t)qs * G::OPERAND + (uint32_t)lane * 16384u, &p.tmap_q, lane * 64,
+                        s.head * Gq, s.row * p.drafts + (s.q0 + u * kTile) / Gq, full);
+          __syncwarp();
+          if constexpr (QUANT) {
+            ok = wait_warp(kBarQLoad + qs, (qc >> 1) & 1);
+            if (!ok) break;
+            sum_q(s, u, qs, qc % kQSums);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
+          }
+          continue;
+        }
         gather_q(s, u, qs, 0, 1);
         __syncwarp();
         if constexpr (QUANT) sum_q(s, u, qs, qc % kQSums);
@@ -1388,6 +1406,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(kBarQFull + qs));
       }
     }
+    // every issued copy lands before the block can end
+    if (copied_q && lane == 0)
+      for (int e = qc > 2 ? qc - 2 : 0; e < qc; ++e)
+        if (!mbar_wait_bounded(bar((QUANT ? kBarQLoad : kBarQFull) + (e & 1)), (e >> 1) & 1)) break;
+    __syncwarp();
     if (!placed) records();
   } else if (warp >= 12) {
     // ============================ converters: K (12-15) and V (16-19)
@@ -1470,6 +1493,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       named_bar_sync(2 + st, 128);
       return misc[1] == 0;
     };
+    // trees: the tokens of sequence g before its drafts
+    [[maybe_unused]] auto before = [&](int g) { return gp[g] - (moff[g + 1] - moff[g]); };
     // the stream's next event: the scores of visit v are there
     int ntok = 0, mask = 0;
     bool valid = false;   // token `row` of the tile
@@ -1481,7 +1506,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     [[maybe_unused]] uint32_t bads[4] = {0, 0, 0, 0};
     auto begin = [&]() -> bool {
       if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
-      if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
+      if constexpr (!TREE || QUANT) {
+        if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
+      }
       const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
       ntok = hd.x;
       mask = hd.y;
@@ -1524,6 +1551,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         }
         fence_proxy_async_smem();   // before the products read them
       }
+      if constexpr (TREE && !QUANT) {   // (values are looked at while the scores are on their way)
+        if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
+      }
       tc_after();
       return true;
     };
@@ -1561,6 +1591,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         int flags = s.flags;
         for (;;) {
           if ((v & 1) == st) {
+            [[maybe_unused]] uint32_t sees = 0xffffffffu;   // rows that attend to the thread's token
+            if constexpr (TREE) {   // (known before the scores are there)
+              if (flags & kDrafts) sees = tree_rows(p, s, visits[2 * (v & (kVisits - 1))].x + row - before(s.row));
+            }
             ok = begin();
             if (!ok) break;
             if (!have) {
@@ -1571,9 +1605,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               }
             }
             float a[FEW];
-            [[maybe_unused]] uint32_t sees = 0;   // rows that attend to the thread's token
             if constexpr (TREE) {
-              sees = !valid ? 0u : drafts ? tree_rows(p, s, visits[2 * (v & (kVisits - 1))].x + row) : 0xffffffffu;
+              if (!valid) sees = 0;
               if (drafts && (bads[quad] >> lane & 1)) poison |= sees;
             }
             const int at = (row >> 1) * 4 + (row & 1);
@@ -1732,19 +1765,22 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       [[maybe_unused]] bool poison = false;   // the row attends to values that are no numbers
       for (;;) {
         if (two || (v & 1) == st) {
+          [[maybe_unused]] uint4 sees = make_uint4(~0u, ~0u, ~0u, ~0u);   // tokens that the row attends to
+          if constexpr (TREE) {
+            if (s.is(kDrafts) && row < my_rows)
+              sees = tree_window(p, s.row, (s.q0 + (two ? st * kTile : 0) + row) / Gq,
+                                 visits[2 * (v & (kVisits - 1))].x - before(s.row));
+            __syncwarp();
+          }
           ok = begin();
           if (!ok) break;
           if (active) {
             if (QUANT && !have) qs = qsum[row];
             const uint64_t qs2 = pack2f(qs, qs), scale2 = pack2f(p.scale, p.scale);
-            [[maybe_unused]] uint4 sees = make_uint4(~0u, ~0u, ~0u, ~0u);   // tokens that the row attends to
             auto sees32 = [&](int c) { return c < 64 ? (c < 32 ? sees.x : sees.y) : (c < 96 ? sees.z : sees.w); };
             if constexpr (TREE) {
-              if (drafts && row < my_rows) {
-                sees = tree_window(p, s.row, (s.q0 + (two ? st * kTile : 0) + row) / Gq, visits[2 * (v & (kVisits - 1))].x);
+              if (drafts && row < my_rows)
                 poison |= (sees.x & bads[0]) | (sees.y & bads[1]) | (sees.z & bads[2]) | (sees.w & bads[3]);
-              }
-              __syncwarp();
             }
             // (quantised caches: drafts are left out where scores are scaled, below)
             if (ntok < kTile || mask != 0xFF || (TREE && !QUANT && drafts)) {   // columns without a token
@@ -1982,6 +2018,17 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 // kernel is short, as its code is fetched anew by every call.
 constexpr int kMergeThreads = 128;
 
+// Four outputs, rounded once.
+__device__ __forceinline__ void store_out4(const SharedParams& p, size_t at, float4 f) {
+  if (p.out_dtype == PKV_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = f;
+  } else {
+    const uint2 v = p.out_dtype == PKV_BF16 ? make_uint2(pack16<true>(f.x, f.y), pack16<true>(f.z, f.w))
+                                            : make_uint2(pack16<false>(f.x, f.y), pack16<false>(f.z, f.w));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = v;
+  }
+}
+
 // The attention kernel takes infinities and NaNs out of the drafts' values (0 times one of them would be
 // one, in rows that do not attend to it) and marks the records of the rows that do attend to them:
 // the sum of those of a row's four channels, for its output.
@@ -2009,7 +2056,7 @@ static __device__ __noinline__ float4 no_numbers(const SharedParams& p, int b, i
   return make_float4(x[0], x[1], x[2], x[3]);
 }
 
-template <int D, int WPW, bool TREE>
+template <int D, int WPW>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __grid_constant__ SharedParams p) {
   constexpr int BATCH = 4;
   __shared__ float4 part_a[WPW > 1 ? WPW : 1][32];
@@ -2019,29 +2066,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   const int item = at / D;   // row and query head
   pdl_wait();
   if (at >= p.batch * p.num_q_heads * D) return;
-  const int kvi = item / p.group;   // row and kv head
-  int gq = item - kvi * p.group;
-  int4 own = make_int4(0, 0, 0, 0), pre;
-  [[maybe_unused]] int seq = 0, draft = 0, head = 0;
-  [[maybe_unused]] bool marked = false;   // some of its records leave values out
-  if constexpr (TREE) {
-    const int b = kvi / p.num_kv_heads;
-    head = kvi - b * p.num_kv_heads;
-    seq = b / p.drafts;
-    draft = b - seq * p.drafts;
-    const int R = draft * p.group + gq, pair = R / (2 * kTile);   // among the sequence's query rows of this kv head
-    pre = __ldcg(p.ws_info + ((size_t)seq * p.num_kv_heads + head) * p.pairs + pair);
-    gq = R - pair * 2 * kTile;
-    if (gq >= pre.z >> 16) pre.z = gq = 0;   // no draft of the sequence
-    pre.z &= 0xFFFF;
-  } else {
-    own = __ldcg(p.ws_info + 3 * kvi);
-    pre = __ldcg(p.ws_info + 3 * kvi + 1);
-    const int4 pre2 = __ldcg(p.ws_info + 3 * kvi + 2);
-    if (gq >= pre.w >> 1) pre = pre2;   // in the next pair of row tiles
-    pre.w &= 1;
-  }
-  const int ch = at % D, whole = (TREE ? 1 : 2) * p.batch * p.num_q_heads;
+  const int kvi = item / p.group, gq = item - kvi * p.group;   // row and kv head
+  const int4 own = __ldcg(p.ws_info + 3 * kvi);
+  int4 pre = __ldcg(p.ws_info + 3 * kvi + 1);
+  const int4 pre2 = __ldcg(p.ws_info + 3 * kvi + 2);
+  if (gq >= pre.w >> 1) pre = pre2;   // in the next pair of row tiles
+  pre.w &= 1;
+  const int ch = at % D, whole = 2 * p.batch * p.num_q_heads;
   const int n0 = pre.z << pre.w, n1 = own.z << own.w;
   float M = -INFINITY, L = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -2065,10 +2096,6 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
       r = on ? r + gq : 0;
       ml[i] = __ldcg(p.ws_ml + r);
       if (!on) ml[i] = make_float2(-INFINITY, 0.f);
-      if constexpr (TREE) {
-        marked |= signbit(ml[i].y);
-        ml[i].y = fabsf(ml[i].y);
-      }
       a[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (size_t)r * D + ch));
     }
     float Mn = M;
@@ -2090,17 +2117,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   }
   if constexpr (WPW > 1) {
     part_a[w][lane] = A;
-    part_ml[w][lane] = make_float2(M, TREE && marked ? -L : L);
+    part_ml[w][lane] = make_float2(M, L);
     __syncthreads();
     if (w != 0) return;
 #pragma unroll 1
     for (int o = 1; o < WPW; ++o) {
-      float2 ml = part_ml[o][lane];
+      const float2 ml = part_ml[o][lane];
       const float4 a = part_a[o][lane];
-      if constexpr (TREE) {
-        marked |= signbit(ml.y);
-        ml.y = fabsf(ml.y);
-      }
       const float Mn = fmaxf(M, ml.x), Mr = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M - Mr), f2 = fast_exp2(ml.x - Mr);
       L = L * f + ml.y * f2;
       A = make_float4(A.x * f + a.x * f2, A.y * f + a.y * f2, A.z * f + a.z * f2, A.w * f + a.w * f2);
@@ -2109,19 +2132,106 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   }
   // no token at all: zeros (L is 0 only then, or where every score is -inf; a NaN stays one)
   const float r = L == 0.f ? 0.f : 1.f / L;
-  float4 f = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
-  if constexpr (TREE) {
-    if (marked) {
-      const float4 x = no_numbers(p, seq, draft, head, ch, D);
-      f = make_float4(f.x + x.x, f.y + x.y, f.z + x.z, f.w + x.w);
+  const float4 f = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
+  store_out4(p, at, f);
+}
+
+// The same for trees. WPW = 1: a warp has LROWS x 128 / d consecutive query rows of a segment, whose records
+// lie together and are as many for each: with their loads in flight at once the merge of many
+// rows is no longer a chain of latencies for each of them.
+template <int D, int WPW, int LROWS>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ SharedParams p) {
+  constexpr int SIDE = 128 / D, ROWS = LROWS * SIDE;   // rows beside each other in a warp, rows of a warp
+  constexpr int BATCH = LROWS > 1 ? 2 : 4;             // records of a row in flight
+  __shared__ float4 part_a[WPW > 1 ? WPW : 1][32];
+  __shared__ float2 part_ml[WPW > 1 ? WPW : 1][32];
+  const int lane = threadIdx.x & 31, w = WPW > 1 ? threadIdx.x >> 5 : 0;
+  const int item = (int)blockIdx.x * (4 / WPW) + (WPW > 1 ? 0 : (int)threadIdx.x >> 5);
+  const int each = p.drafts * p.group, chunks = (each + ROWS - 1) / ROWS;   // of a sequence's kv head
+  const int sh = item / chunks, r0 = (item - sh * chunks) * ROWS + lane / (32 / SIDE);   // the lane's first row
+  pdl_wait();
+  if (sh >= p.num_groups * p.num_kv_heads) return;
+  const int pair = r0 / (2 * kTile), whole = p.batch * p.num_q_heads, ch = lane % (32 / SIDE) * 4;
+  const int4 seg = __ldcg(p.ws_info + (size_t)sh * p.pairs + pair);
+  const int first = r0 - pair * 2 * kTile, live = (seg.z >> 16) - first;   // (a row of the segment where live is above it)
+  const int n = live > 0 ? (seg.z & 0xFFFF) << seg.w : 0;
+  float M[LROWS], L[LROWS];
+  float4 A[LROWS];
+  uint32_t marked = 0;   // rows of which some records leave values out
+#pragma unroll
+  for (int k = 0; k < LROWS; ++k) {
+    M[k] = -INFINITY;
+    L[k] = 0.f;
+    A[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 1
+  for (int j0 = w; j0 < n; j0 += WPW * BATCH) {
+    float2 ml[BATCH][LROWS];
+    float4 a[BATCH][LROWS];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int j = j0 + i * WPW;
+      // stream and part; a block's first part, where it continues the segment, has its place by block
+      const int st = j & seg.w, part = j >> seg.w;
+      const int rec = (part == 0 ? seg.x + st * whole : seg.y + (part - 1) * 2 * kTile + st * kTile) + first;
+#pragma unroll
+      for (int k = 0; k < LROWS; ++k) {
+        const bool on = j < n && k * SIDE < live;
+        const int r = on ? rec + k * SIDE : 0;
+        ml[i][k] = __ldcg(p.ws_ml + r);
+        a[i][k] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (size_t)r * D + ch));
+        if (!on) ml[i][k] = make_float2(-INFINITY, 0.f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < LROWS; ++k) {
+      float Mn = M[k];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i][k].x);
+      const float Mr = Mn == -INFINITY ? 0.f : Mn, f0 = fast_exp2(M[k] - Mr);
+      M[k] = Mn;
+      L[k] *= f0;
+      A[k] = make_float4(A[k].x * f0, A[k].y * f0, A[k].z * f0, A[k].w * f0);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (signbit(ml[i][k].y)) marked |= 1u << k;
+        const float l = fabsf(ml[i][k].y);
+        if (ml[i][k].x == -INFINITY && l == 0.f) continue;   // no token (see above)
+        const float f = fast_exp2(ml[i][k].x - Mr);
+        L[k] = fmaf(f, l, L[k]);
+        A[k] = make_float4(fmaf(f, a[i][k].x, A[k].x), fmaf(f, a[i][k].y, A[k].y), fmaf(f, a[i][k].z, A[k].z),
+                           fmaf(f, a[i][k].w, A[k].w));
+      }
     }
   }
-  if (p.out_dtype == PKV_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = f;
-  } else {
-    const uint2 v = p.out_dtype == PKV_BF16 ? make_uint2(pack16<true>(f.x, f.y), pack16<true>(f.z, f.w))
-                                            : make_uint2(pack16<false>(f.x, f.y), pack16<false>(f.z, f.w));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = v;
+  if constexpr (WPW > 1) {
+    part_a[w][lane] = A[0];
+    part_ml[w][lane] = make_float2(M[0], marked ? -L[0] : L[0]);
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll 1
+    for (int o = 1; o < WPW; ++o) {
+      const float2 ml = part_ml[o][lane];
+      const float4 a = part_a[o][lane];
+      if (signbit(ml.y)) marked = 1;
+      const float Mn = fmaxf(M[0], ml.x), Mr = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M[0] - Mr), f2 = fast_exp2(ml.x - Mr);
+      L[0] = L[0] * f + fabsf(ml.y) * f2;
+      A[0] = make_float4(A[0].x * f + a.x * f2, A[0].y * f + a.y * f2, A[0].z * f + a.z * f2, A[0].w * f + a.w * f2);
+      M[0] = Mn;
+    }
+  }
+  const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
+#pragma unroll
+  for (int k = 0; k < LROWS; ++k) {
+    const int R = r0 + k * SIDE, t = R / p.group;
+    if (R >= each) break;
+    const float r = L[k] == 0.f ? 0.f : 1.f / L[k];
+    float4 f = make_float4(A[k].x * r, A[k].y * r, A[k].z * r, A[k].w * r);
+    if (marked >> k & 1) {
+      const float4 x = no_numbers(p, seq, t, head, ch, D);
+      f = make_float4(f.x + x.x, f.y + x.y, f.z + x.z, f.w + x.w);
+    }
+    store_out4(p, (((size_t)seq * p.drafts + t) * p.num_q_heads + head * p.group + (R - t * p.group)) * D + ch, f);
   }
 }
 

@@ -83,12 +83,13 @@ Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
   return w;
 }
 
-// For trees: each pair of row tiles' place, and one record row per query row and stream besides the
-// blocks' 256.
-Work tree_layout(const pkv_cache* c, int rows, int sequences, int pairs, int hq, int ctas) {
-  const size_t recs = 2 * (size_t)rows * hq + (size_t)ctas * 2 * kTile;
+// For trees: each pair of row tiles' place, and one record row per query row (of each sequence's kv head, rounded
+// up to 32) and stream besides the blocks' 256.
+Work tree_layout(const pkv_cache* c, int sequences, int drafts, int group, int ctas) {
+  const size_t rows = (size_t)(drafts * group + 31) / 32 * 32, heads = (size_t)sequences * c->num_kv_heads;
+  const size_t recs = 2 * heads * rows + (size_t)(ctas + 1) * 2 * kTile, pairs = (drafts * group + 2 * kTile - 1) / (2 * kTile);
   Work w;
-  w.ml = align256((size_t)sequences * c->num_kv_heads * pairs * sizeof(int4));
+  w.ml = align256(heads * pairs * sizeof(int4));
   w.acc = w.ml + align256(recs * sizeof(float2));
   w.total = w.acc + align256(recs * c->head_dim * sizeof(float)) + 256;
   return w;
@@ -180,10 +181,9 @@ const void* merge_kernel(int warps) {
 }
 
 template <int D>
-const void* tree_merge(int warps, int lrows) {
-  return warps == 4   ? reinterpret_cast<const void*>(&tree_merge_kernel<D, 4, 1>)
-         : lrows == 1 ? reinterpret_cast<const void*>(&tree_merge_kernel<D, 1, 1>)
-                      : reinterpret_cast<const void*>(&tree_merge_kernel<D, 1, 2>);
+const void* tree_merge(int warps) {
+  return warps == 4 ? reinterpret_cast<const void*>(&tree_merge_kernel<D, 4>)
+                    : reinterpret_cast<const void*>(&tree_merge_kernel<D, 1>);
 }
 
 }  // namespace
@@ -269,9 +269,7 @@ pkv_status tree_workspace_bytes(const pkv_cache* c, int batch, int drafts, int n
     const pkv_status st = device(dev);
     if (st != PKV_OK) return st;
   }
-  bytes = tree_layout(c, batch * drafts, batch, tree_pairs(drafts, num_q_heads / c->num_kv_heads), num_q_heads,
-                      num_splits ? num_splits : dev.sms)
-              .total;
+  bytes = tree_layout(c, batch, drafts, num_q_heads / c->num_kv_heads, num_splits ? num_splits : dev.sms).total;
   return PKV_OK;
 }
 
@@ -286,9 +284,9 @@ pkv_status launch_tree(const TreeArgs& a) {
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
   if (2 * tiles >= (1ll << 31) / ((long long)c->num_kv_heads * a.batch * pairs) ||
-      (2ll * rows * a.num_q_heads + 512ll * ctas) * D >= (1ll << 31))
+      (2ll * a.batch * c->num_kv_heads * (a.drafts * group + 31) + 256ll * ctas + 512) * D >= (1ll << 31))
     return PKV_ERR_UNSUPPORTED;
-  const Work w = tree_layout(c, rows, a.batch, pairs, a.num_q_heads, ctas);
+  const Work w = tree_layout(c, a.batch, a.drafts, group, ctas);
   if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < w.total)
     return PKV_ERR_WORKSPACE;
   SharedParams p = {};
@@ -326,20 +324,19 @@ pkv_status launch_tree(const TreeArgs& a) {
   p.mask_words = (a.drafts + 63) / 64;
   p.mask_stride = a.mask_shared ? 0 : (long long)a.drafts * p.mask_words;
   p.pairs = pairs;
+  p.rec_rows = (a.drafts * group + 31) / 32 * 32;
   // Row tiles that end between two drafts are copied as boxes; the others are gathered. (24 x 8K, 64 drafts of 4 heads:
   // a segment's 256 rows by one warp took 8 us, which nothing hides.)
   p.q_box = kTile % group != 0 ? 0 : std::min(a.drafts, kTile / group);
   if (p.q_box && !query_map(a.q, (uint64_t)rows, a.num_q_heads, group, D, p.q_box, bf, p.tmap_q)) return PKV_ERR_CUDA;
   void* args[] = {&p};
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
-  const long long units = ((long long)rows * a.num_q_heads * D + 127) / 128;
-  const int wpw = units < 6 * dev.sms ? 4 : 1;   // (see above)
-  // Two rows a lane where the merge alone would be several waves; one against two (and four), us a call: 4096 units
-  // (8 x 4K) 31.5, 32.5 (34.4), 12288 (16 x 8K INT8) 128, 124 (125), 49152 (24 x 8K of 64) 191, 164 (163).
-  const int lrows = units >= 48 * dev.sms ? 2 : 1, each = lrows * 128 / D;
-  const long long items = (long long)a.batch * c->num_kv_heads * ((a.drafts * group + each - 1) / each);
-  const void* merge = D == 64 ? tree_merge<64>(wpw, lrows) : tree_merge<128>(wpw, lrows);
-  const int per = 4 / wpw;
+  const long long items = (long long)a.batch * c->num_kv_heads * (p.rec_rows / 32) * (D / 16);
+#ifndef V_W4
+#define V_W4 8
+#endif
+  const int wpw = items < V_W4 * dev.sms ? 4 : 1, per = 4 / wpw;
+  const void* merge = D == 64 ? tree_merge<64>(wpw) : tree_merge<128>(wpw);
   return launch_pdl(merge, dim3((unsigned)((items + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;

@@ -143,6 +143,7 @@ struct SharedParams {
   const int32_t* draft_lens;   // drafts of each sequence, or NULL: `drafts` of each
   const uint64_t* tree_mask;   // [sequences][drafts][mask_words], or NULL: each after the one before
   int drafts, mask_words, pairs, kv_kind;
+  int rec_rows;   // record rows of a sequence's kv head: its query rows, rounded up to 32
   int q_box;   // drafts of a box of queries (64 channels of a group's heads of each), 0: they are gathered
   long long mask_stride;       // words from one sequence's masks to the next's (0: the same)
   SharedLayout lay;
@@ -495,7 +496,8 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
     s.rows = min(2 * kTile, total - s.q0);
     s.mem0 = pl.moff[g];
     s.row = TREE ? g : pl.members[s.mem0];
-    s.rec = s.head * p.batch * p.group + s.mem0 * p.group + s.q0;
+    s.rec = TREE ? (g * p.num_kv_heads + s.head) * p.rec_rows + s.q0
+                 : s.head * p.batch * p.group + s.mem0 * p.group + s.q0;
   } else {
     const int b = upper(pl.bpre, p.batch, x);
     if (pl.lens) {
@@ -742,16 +744,30 @@ static __device__ __noinline__ void sum_queries(const uint8_t* src, float* qsum,
 template <int HALVES, bool BF>
 static __device__ __noinline__ void clear_no_numbers(uint8_t* tile, int row, volatile int* mark, int v) {
   constexpr uint32_t E = BF ? 0x7F80u : 0x7C00u;
+  constexpr int HELD = 8;
+  auto piece = [&](int i) {
+    return reinterpret_cast<uint4*>(tile + (i >> 3) * 16384 + row * 128 + ((i & 7) ^ (row & 7)) * 16);
+  };
+  auto none = [](uint32_t w) { return ((w & E) == E ? 0xFFFFu : 0u) | ((w >> 16 & E) == E ? 0xFFFF0000u : 0u); };
 #pragma unroll 1
-  for (int i = 0; i < HALVES * 8; ++i) {
-    uint4* at = reinterpret_cast<uint4*>(tile + (i >> 3) * 16384 + row * 128 + ((i & 7) ^ (row & 7)) * 16);
-    uint4 x = *at;
-    auto none = [](uint32_t w) { return ((w & E) == E ? 0xFFFFu : 0u) | ((w >> 16 & E) == E ? 0xFFFF0000u : 0u); };
-    const uint4 m = make_uint4(none(x.x), none(x.y), none(x.z), none(x.w));
-    if (m.x | m.y | m.z | m.w) {
-      *mark = v;
-      __threadfence_block();
-      *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+  for (int i = 0; i < HALVES * 8; i += HELD) {
+    uint4 x[HELD];
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) x[j] = *piece(i + j);
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {   // (carries out of the exponents' places: those of none but ones)
+      auto some = [](uint32_t w) { return (((w & 0x7FFF7FFFu) + ((0x8000u - E) * 0x10001u)) & 0x80008000u) != 0; };
+      found |= some(x[j].x) || some(x[j].y) || some(x[j].z) || some(x[j].w);
+    }
+    if (!found) continue;
+    *mark = v;
+    __threadfence_block();
+#pragma unroll 1
+    for (int j = 0; j < HELD; ++j) {
+      uint4* at = piece(i + j);
+      const uint4 y = *at;
+      *at = make_uint4(y.x & ~none(y.x), y.y & ~none(y.y), y.z & ~none(y.z), y.w & ~none(y.w));
     }
   }
   __threadfence_block();
@@ -800,10 +816,16 @@ static __device__ __noinline__ void place_records(const SharedParams& p, const S
   }
 }
 
+// Trees: record rows of one stream, in all sequences. An accumulator's place is [32 rows][channel][row], so that
+// 32 lanes that have a row each write and read a channel together.
+__host__ __device__ __forceinline__ int tree_records(const SharedParams& p) {
+  return p.num_groups * p.num_kv_heads * p.rec_rows;
+}
+
 // The same for trees of drafts: for each sequence, kv head and pair of row tiles its record rows (of the
 // first block, of those that continue it), parts and query rows, and whether both streams have a record.
 static __device__ __noinline__ void place_tree_records(const SharedParams& p, const SharedPlan& pl, int few_max) {
-  const int lane = threadIdx.x & 31, whole = p.batch * p.num_q_heads;
+  const int lane = threadIdx.x & 31, whole = tree_records(p);
   const Shares shares(pl.gpre[p.num_groups], pl.lpre[p.num_groups], p.num_ctas);
 #pragma unroll 1
   for (int i = blockIdx.x + gridDim.x * lane; i < p.num_groups * p.num_kv_heads * p.pairs; i += gridDim.x * 32) {
@@ -813,7 +835,7 @@ static __device__ __noinline__ void place_tree_records(const SharedParams& p, co
     int4 info = make_int4(0, 0, 0, 0);
     if (mine > 0) {
       const int x = (rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, c = shares.block_of(x);
-      info = make_int4(h * p.batch * p.group + pl.moff[g] * p.group + pair * 2 * kTile, 2 * whole + (c + 1) * 2 * kTile,
+      info = make_int4(gh * p.rec_rows + pair * 2 * kTile, 2 * whole + (c + 1) * 2 * kTile,
                        (shares.block_of(x + n - 1) - c + 1) | mine << 16, mine <= few_max);
     }
     p.ws_info[i] = info;
@@ -825,7 +847,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
   using G = SharedGeom<D, KV, BF>;
   constexpr bool QUANT = G::QUANT;
-  constexpr int NT = G::THREADS, COLS = QUANT ? 32 : 64;   // columns of a pass over the scores
+  constexpr int NT = G::THREADS, COLS = QUANT || TREE ? 32 : 64;   // columns of a pass over the scores
   constexpr int FEW = G::FEW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -1479,7 +1501,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm_s(st) + lanes, to = tm_o(st) + lanes;
-    const size_t whole = (size_t)(TREE ? 1 : 2) * p.batch * p.num_q_heads;   // record rows of segments by stream
+    const size_t whole = TREE ? tree_records(p) : (size_t)2 * p.batch * p.num_q_heads;   // record rows of segments by stream
     int qc = 0, v = 0;
     uint32_t n_ev = 0, n_seg = 0, n_pair = 0, n_x = 0;   // events, segments, meetings so far
     auto meet = [&](int b, uint32_t& n) -> bool {   // two warps of the same rows
@@ -1543,7 +1565,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         if constexpr (TREE) {
           if (drafts) {   // (see the converters)
             int* marks = reinterpret_cast<int*>(smem + lay.bad) + (v % kBadSlots) * kTile;
-            if (valid) clear_no_numbers<G::HALVES, BF>(smem + lay.ring + (size_t)(S + slot) * G::ENTRY, row, marks + row, v);
+            const Visit& d = *reinterpret_cast<const Visit*>(visits + 2 * (v & (kVisits - 1)));
+            if (valid && d.tok0 + row >= before(d.row))
+              clear_no_numbers<G::HALVES, BF>(smem + lay.ring + (size_t)(S + slot) * G::ENTRY, row, marks + row, v);
             if (!meet_all()) return false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) bads[i] = __ballot_sync(0xffffffffu, *(volatile int*)(marks + 32 * i + lane) == v);
@@ -1740,6 +1764,18 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             tmem_ld<8>(to + e, o);
             tmem_ld<8>(to + FEW + e, o + 8);
             tc_wait_ld();
+            if constexpr (TREE) {   // (rows up to the next multiple of 32 are the record's own)
+              float f[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                f[k] = __uint_as_float(o[k]) + __uint_as_float(o[8 + k]);
+                if constexpr (QUANT) f[k] += total(FEW + e + k);
+              }
+              float4* at = reinterpret_cast<float4*>(p.ws_acc + rec0 * D + row * 32 + e);
+              at[0] = make_float4(f[0], f[1], f[2], f[3]);
+              at[1] = make_float4(f[4], f[5], f[6], f[7]);
+              continue;
+            }
             float* acc = p.ws_acc + (rec0 + e) * D + row;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -1777,25 +1813,29 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (active) {
             if (QUANT && !have) qs = qsum[row];
             const uint64_t qs2 = pack2f(qs, qs), scale2 = pack2f(p.scale, p.scale);
-            auto sees32 = [&](int c) { return c < 64 ? (c < 32 ? sees.x : sees.y) : (c < 96 ? sees.z : sees.w); };
+            const bool partial = ntok < kTile || mask != 0xFF;
             if constexpr (TREE) {
               if (drafts && row < my_rows)
                 poison |= (sees.x & bads[0]) | (sees.y & bads[1]) | (sees.z & bads[2]) | (sees.w & bads[3]);
             }
-            // (quantised caches: drafts are left out where scores are scaled, below)
-            if (ntok < kTile || mask != 0xFF || (TREE && !QUANT && drafts)) {   // columns without a token
+            // tokens [c, c + 32) of the tile that the row attends to
+            [[maybe_unused]] auto sees32 = [&](int c) {
+              uint32_t on = c < 64 ? (c < 32 ? sees.x : sees.y) : (c < 96 ? sees.z : sees.w);
+              if (ntok - c < 32) on &= (1u << (ntok - c)) - 1u;
+              const int pieces = mask >> (c >> 4);
+              return on & ((pieces & 1 ? 0xFFFFu : 0u) | (pieces & 2 ? 0xFFFF0000u : 0u));
+            };
+            if (!TREE && partial) {   // columns without a token (trees: left out in the pass below)
 #pragma unroll 1
               for (int c = 0; c < kTile; c += 16) {
                 const int left = mask >> (c >> 4) & 1 ? ntok - c : 0;
-                uint32_t on = 0xFFFFu;
-                if constexpr (TREE && !QUANT) on = sees32(c) >> (c & 16) & 0xFFFFu;
-                if (left >= 16 && (!TREE || QUANT || __all_sync(0xffffffffu, on == 0xFFFFu))) continue;
+                if (left >= 16) continue;
                 float a[16];
                 tmem_ld<16>(ts + c, reinterpret_cast<uint32_t*>(a));
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                  if (j >= left || (TREE && !QUANT && !(on >> j & 1))) a[j] = -INFINITY;
+                  if (j >= left) a[j] = -INFINITY;
                 tmem_st<16>(ts + c, reinterpret_cast<uint32_t*>(a));
               }
               tc_wait_st();
@@ -1813,22 +1853,23 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                   const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * (c + j));
                   unpack2f(ffma2(pack2f(a[j], a[j + 1]), k2.x, fmul2(k2.y, qs2)), a[j], a[j + 1]);
                 }
-                if constexpr (TREE) {
-                  if (drafts) {
-                    const uint32_t on = sees32(c);
-#pragma unroll
-                    for (int j = 0; j < COLS; ++j)
-                      if (!(on >> j & 1)) a[j] = -INFINITY;
-                  }
-                }
-                tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
               }
+              if constexpr (TREE) {
+                if (drafts || partial) {
+                  const uint32_t on = sees32(c);
+#pragma unroll
+                  for (int j = 0; j < COLS; ++j)
+                    if (!(on >> j & 1)) a[j] = -INFINITY;
+                  if constexpr (!QUANT) tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+                }
+              }
+              if constexpr (QUANT) tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
               float m4[4] = {mx, a[0], a[1], a[2]};
 #pragma unroll
               for (int j = 3; j < COLS - 1; j += 2) m4[j >> 1 & 3] = max3(m4[j >> 1 & 3], a[j], a[j + 1]);
               mx = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), a[COLS - 1]);
             }
-            if constexpr (QUANT) tc_wait_st();
+            if constexpr (QUANT || TREE) tc_wait_st();
             if constexpr (QUANT) {
               if (!even) {   // uniform over the block
                 mx = -INFINITY;
@@ -1960,6 +2001,24 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         // CHUNK channels at a time through shared memory (the stream's place for transposed
         // weights), so that a row's 64 (32) bytes are written together
         const uint32_t to2 = tm_o(st ^ 1) + lanes;
+        if constexpr (TREE) {
+          constexpr int PASS = QUANT ? 16 : 32;
+          float* out = p.ws_acc + (rec0 + tile_row - lane) * D + lane;
+#pragma unroll 1
+          for (int c = from; c < to_c; c += PASS) {
+            uint32_t o[PASS], o2[PASS];
+            tmem_ld<PASS>(to + c, o);
+            if (both) tmem_ld<PASS>(to2 + c, o2);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < PASS; ++j) {
+              float f = __uint_as_float(o[j]);
+              if (both) f = fmaf(__uint_as_float(o2[j]), f1, f * f0);
+              if constexpr (QUANT) f += z;
+              out[(c + j) * 32] = f;
+            }
+          }
+        } else {
         constexpr int CHUNK = G::PT / 512, PARTS4 = CHUNK / 4;   // 16 or 8
         uint8_t* stage = smem + lay.pt + st * G::PT + quad * (32 * CHUNK * 4);
         const int live = min(32, my_rows - quad * 32);   // the warp's query rows
@@ -1991,6 +2050,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             if (q < live) *reinterpret_cast<float4*>(out + (size_t)q * D + c) = f;
           }
           __syncwarp();
+        }
         }
         if (both) {   // neither accumulator is overwritten before both are read
           tc_before();
@@ -2136,102 +2196,80 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const __gri
   store_out4(p, at, f);
 }
 
-// The same for trees. WPW = 1: a warp has LROWS x 128 / d consecutive query rows of a segment, whose records
-// lie together and are as many for each: with their loads in flight at once the merge of many
-// rows is no longer a chain of latencies for each of them.
-template <int D, int WPW, int LROWS>
+// The same for trees: a warp (WPW of them, each every WPW-th record) has 16 channels of 32 query rows of a
+// segment, a row a lane. The rows' records lie together, so each load brings a channel of all 32, and
+// a record's 16 loads, and the next one's, are in flight at once.
+template <int D, int WPW>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int SIDE = 128 / D, ROWS = LROWS * SIDE;   // rows beside each other in a warp, rows of a warp
-  constexpr int BATCH = LROWS > 1 ? 2 : 4;             // records of a row in flight
-  __shared__ float4 part_a[WPW > 1 ? WPW : 1][32];
-  __shared__ float2 part_ml[WPW > 1 ? WPW : 1][32];
+  constexpr int CH = 16, SLICES = D / CH;
+  __shared__ float part[WPW > 1 ? WPW - 1 : 1][CH + 2][32];
   const int lane = threadIdx.x & 31, w = WPW > 1 ? threadIdx.x >> 5 : 0;
   const int item = (int)blockIdx.x * (4 / WPW) + (WPW > 1 ? 0 : (int)threadIdx.x >> 5);
-  const int each = p.drafts * p.group, chunks = (each + ROWS - 1) / ROWS;   // of a sequence's kv head
-  const int sh = item / chunks, r0 = (item - sh * chunks) * ROWS + lane / (32 / SIDE);   // the lane's first row
+  const int each = p.drafts * p.group, blocks = (each + 31) / 32;   // query rows of a sequence's kv head
+  const int sb = item / SLICES, slice = item - sb * SLICES, sh = sb / blocks, r0 = (sb - sh * blocks) * 32, pair = r0 / (2 * kTile);
   pdl_wait();
   if (sh >= p.num_groups * p.num_kv_heads) return;
-  const int pair = r0 / (2 * kTile), whole = p.batch * p.num_q_heads, ch = lane % (32 / SIDE) * 4;
   const int4 seg = __ldcg(p.ws_info + (size_t)sh * p.pairs + pair);
-  const int first = r0 - pair * 2 * kTile, live = (seg.z >> 16) - first;   // (a row of the segment where live is above it)
-  const int n = live > 0 ? (seg.z & 0xFFFF) << seg.w : 0;
-  float M[LROWS], L[LROWS];
-  float4 A[LROWS];
-  uint32_t marked = 0;   // rows of which some records leave values out
+  const int first = r0 - pair * 2 * kTile, live = (seg.z >> 16) - first;   // the segment's rows from r0 on
+  const int n = live > 0 ? (seg.z & 0xFFFF) << seg.w : 0, whole = tree_records(p);
+  float M = -INFINITY, L = 0.f, A[CH];
+  bool marked = false;   // some of the row's records leave values out
 #pragma unroll
-  for (int k = 0; k < LROWS; ++k) {
-    M[k] = -INFINITY;
-    L[k] = 0.f;
-    A[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-#pragma unroll 1
-  for (int j0 = w; j0 < n; j0 += WPW * BATCH) {
-    float2 ml[BATCH][LROWS];
-    float4 a[BATCH][LROWS];
+  for (int c = 0; c < CH; ++c) A[c] = 0.f;
+  auto join = [&](float2 ml, const float* a) {
+    marked |= signbit(ml.y);
+    const float l = fabsf(ml.y), Mn = fmaxf(M, ml.x), Mr = Mn == -INFINITY ? 0.f : Mn, f0 = fast_exp2(M - Mr);
+    // no token: its accumulator means nothing (see above)
+    const bool none = ml.x == -INFINITY && l == 0.f;
+    const float f = fast_exp2(ml.x - Mr);
+    M = Mn;
+    L = none ? L * f0 : fmaf(f, l, L * f0);
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int j = j0 + i * WPW;
-      // stream and part; a block's first part, where it continues the segment, has its place by block
-      const int st = j & seg.w, part = j >> seg.w;
-      const int rec = (part == 0 ? seg.x + st * whole : seg.y + (part - 1) * 2 * kTile + st * kTile) + first;
+    for (int c = 0; c < CH; ++c) A[c] = none ? A[c] * f0 : fmaf(f, a[c], A[c] * f0);
+  };
+#pragma unroll 2
+  for (int j = w; j < n; j += WPW) {
+    // stream and part; a block's first part, where it continues the segment, has its place by block
+    const int st = j & seg.w, k = j >> seg.w;
+    const size_t rec = (size_t)(k == 0 ? seg.x + st * whole : seg.y + (k - 1) * 2 * kTile + st * kTile) + first;
+    const float* acc = p.ws_acc + rec * D + slice * CH * 32 + lane;
+    float a[CH];
+    float2 ml = __ldcg(p.ws_ml + rec + min(lane, live - 1));
 #pragma unroll
-      for (int k = 0; k < LROWS; ++k) {
-        const bool on = j < n && k * SIDE < live;
-        const int r = on ? rec + k * SIDE : 0;
-        ml[i][k] = __ldcg(p.ws_ml + r);
-        a[i][k] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (size_t)r * D + ch));
-        if (!on) ml[i][k] = make_float2(-INFINITY, 0.f);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < LROWS; ++k) {
-      float Mn = M[k];
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i][k].x);
-      const float Mr = Mn == -INFINITY ? 0.f : Mn, f0 = fast_exp2(M[k] - Mr);
-      M[k] = Mn;
-      L[k] *= f0;
-      A[k] = make_float4(A[k].x * f0, A[k].y * f0, A[k].z * f0, A[k].w * f0);
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        if (signbit(ml[i][k].y)) marked |= 1u << k;
-        const float l = fabsf(ml[i][k].y);
-        if (ml[i][k].x == -INFINITY && l == 0.f) continue;   // no token (see above)
-        const float f = fast_exp2(ml[i][k].x - Mr);
-        L[k] = fmaf(f, l, L[k]);
-        A[k] = make_float4(fmaf(f, a[i][k].x, A[k].x), fmaf(f, a[i][k].y, A[k].y), fmaf(f, a[i][k].z, A[k].z),
-                           fmaf(f, a[i][k].w, A[k].w));
-      }
-    }
+    for (int c = 0; c < CH; ++c) a[c] = __ldcg(acc + c * 32);
+    join(ml, a);
   }
   if constexpr (WPW > 1) {
-    part_a[w][lane] = A[0];
-    part_ml[w][lane] = make_float2(M[0], marked ? -L[0] : L[0]);
+    if (w > 0) {
+      part[w - 1][0][lane] = M;
+      part[w - 1][1][lane] = marked ? -L : L;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) part[w - 1][2 + c][lane] = A[c];
+    }
     __syncthreads();
     if (w != 0) return;
 #pragma unroll 1
-    for (int o = 1; o < WPW; ++o) {
-      const float2 ml = part_ml[o][lane];
-      const float4 a = part_a[o][lane];
-      if (signbit(ml.y)) marked = 1;
-      const float Mn = fmaxf(M[0], ml.x), Mr = Mn == -INFINITY ? 0.f : Mn, f = fast_exp2(M[0] - Mr), f2 = fast_exp2(ml.x - Mr);
-      L[0] = L[0] * f + fabsf(ml.y) * f2;
-      A[0] = make_float4(A[0].x * f + a.x * f2, A[0].y * f + a.y * f2, A[0].z * f + a.z * f2, A[0].w * f + a.w * f2);
-      M[0] = Mn;
+    for (int o = 0; o < WPW - 1; ++o) {
+      float a[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) a[c] = part[o][2 + c][lane];
+      join(make_float2(part[o][0][lane], part[o][1][lane]), a);
     }
   }
-  const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
+  const int R = r0 + lane, seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads, t = R / p.group;
+  if (R >= each) return;
+  // no token at all: zeros (L is 0 only then, or where every score is -inf; a NaN stays one)
+  const float r = lane >= live || L == 0.f ? 0.f : 1.f / L;
+  const size_t at = (((size_t)seq * p.drafts + t) * p.num_q_heads + head * p.group + (R - t * p.group)) * D + slice * CH;
 #pragma unroll
-  for (int k = 0; k < LROWS; ++k) {
-    const int R = r0 + k * SIDE, t = R / p.group;
-    if (R >= each) break;
-    const float r = L[k] == 0.f ? 0.f : 1.f / L[k];
-    float4 f = make_float4(A[k].x * r, A[k].y * r, A[k].z * r, A[k].w * r);
-    if (marked >> k & 1) {
-      const float4 x = no_numbers(p, seq, t, head, ch, D);
+  for (int c = 0; c < CH; c += 4) {
+    float4 f = make_float4(A[c] * r, A[c + 1] * r, A[c + 2] * r, A[c + 3] * r);
+    if (lane >= live) f = make_float4(0.f, 0.f, 0.f, 0.f);
+    else if (marked) {
+      const float4 x = no_numbers(p, seq, t, head, slice * CH + c, D);
       f = make_float4(f.x + x.x, f.y + x.y, f.z + x.z, f.w + x.w);
     }
-    store_out4(p, (((size_t)seq * p.drafts + t) * p.num_q_heads + head * p.group + (R - t * p.group)) * D + ch, f);
+    store_out4(p, at + c, f);
   }
 }
 

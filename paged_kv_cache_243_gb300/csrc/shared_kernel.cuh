@@ -1204,64 +1204,81 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           rows = uni(d.rows);
           flags = uni(d.flags);
           if constexpr (TREE) {
-          // Whole tiles within a segment of two row tiles: the order of the passes below, S of one stream
-          // and P V of the other, without what the ends of segments need. (The warp's instructions, fetched
-          // anew between those of the softmax, set the pace of such segments.)
-          constexpr int kMiddle = kFirst | kLast | kTwo | 0xFF;
-          if (pend.on && !p.two_terms && (flags & kMiddle) == (kTwo | kTile)) {
-            const uint32_t hi_k = (uint32_t)(kmajor >> 32), hi_v = (uint32_t)(vmajor >> 32), lo_v = (uint32_t)vmajor;
-            constexpr uint32_t is = kType | (uint32_t)(kTile / 8) << 17, io = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
-            auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
-            uint32_t vlo = lo_v | (QUANT ? vop : ring + (uint32_t)(S + pend.at.slot) * G::ENTRY) >> 4;
-            int vslot = pend.at.slot;
-            uint32_t acc = !pend.fresh;   // of the first P V to come
-            pend.fresh = false;
-            do {
-              ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + pos.slot, pos.phase);
-              if (!ok) break;
-              const uint32_t klo = (uint32_t)kmajor | (QUANT ? kop : ring + (uint32_t)pos.slot * G::ENTRY) >> 4;
-#pragma unroll 1
-              for (u = 0; u < 2; ++u) {
-                const uint32_t qlo = (uint32_t)kmajor | (qb + (uint32_t)((qc + u) & 1) * G::OPERAND) >> 4;
-                tc_after();
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  mma_ss(tm_s(u), desc(qlo + (k >> 2) * 1024 + (k & 3) * 2, hi_k), desc(klo + (k >> 2) * 1024 + (k & 3) * 2, hi_k),
-                         is, k > 0, on);
-                tc_commit(bar(kBarS + u), on);
-                if (u == 1) tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + pos.slot), on);
-                const int o = u ^ 1;
-                ok = wait_warp(kBarP + o, ~(odd >> o) & 1);
-                if (!ok) break;
-                if (u == 1) {   // P V of this visit
-                  vslot = pos.slot;
-                  if constexpr (!QUANT) vlo = lo_v | (ring + (uint32_t)(S + vslot) * G::ENTRY) >> 4;
-                  ok = QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + vslot, pos.phase);
+            // Whole tiles within a segment, without what its ends need. The order is that of the passes below, but
+            // a pass is P V of an event and S of the stream's next one: between the weights' arrival and the next
+            // scores lie just these products, everything else is done behind them or while the weights
+            // are being made. (This warp's instructions are slow, fetched anew between those of the softmax.)
+            const bool two = rows > kTile;
+            const int inside = (two ? kFirst | kLast : kEarly | kLate) | 0xFF;
+            if (pend.on && !p.two_terms && rows > FEW && (flags & inside) == kTile) {
+              const uint32_t hi_k = (uint32_t)(kmajor >> 32), hi_v = (uint32_t)(vmajor >> 32), lo_v = (uint32_t)vmajor;
+              constexpr uint32_t is = kType | (uint32_t)(kTile / 8) << 17, io = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
+              auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+              auto k_there = [&]() { return QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + pos.slot, pos.phase); };
+              uint32_t acc = !pend.fresh;                // of the first P V to come
+              RingPos last = pend.at, before_last = {};  // of the visits before v
+              bool pv = false, more = true;
+              ok = k_there();
+              while (ok) {
+                const int ms = two ? u : v & 1;
+                if (pv) {
+                  const RingPos at = two ? last : before_last;
+                  ok = wait_warp(kBarP + ms, ~(odd >> ms) & 1);
                   if (!ok) break;
-                }
-                tc_after();
+                  if (!two || ms == 0) {   // (otherwise V is known to be there)
+                    ok = QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + at.slot, at.phase);
+                    if (!ok) break;
+                  }
+                  const uint32_t vlo = lo_v | (QUANT ? vop : ring + (uint32_t)(S + at.slot) * G::ENTRY) >> 4;
+                  tc_after();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  mma_ts(tm_o(o), tm_s(o) + 32 * (j >> 1) + 8 * (j & 1), desc(vlo + j * 128, hi_v), io, j > 0 ? 1 : acc, on);
-                acc = 1;
-                if (u == 0) {
-                  tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarVEmpty + vslot), on);
+                  for (int j = 0; j < 8; ++j)
+                    mma_ts(tm_o(ms), tm_s(ms) + 32 * (j >> 1) + 8 * (j & 1), desc(vlo + j * 128, hi_v), io, j > 0 ? 1 : acc, on);
+                  acc = 1;
+                }
+                if (more) {
+                  if (QUANT && u == 0 && pv) {   // (the next K is converted once the last S is done: not before P V)
+                    ok = k_there();
+                    if (!ok) break;
+                  }
+                  const uint32_t klo = (uint32_t)kmajor | (QUANT ? kop : ring + (uint32_t)pos.slot * G::ENTRY) >> 4;
+                  const uint32_t qlo = (uint32_t)kmajor | (qb + (uint32_t)((qc + u) & 1) * G::OPERAND) >> 4;
+                  tc_after();
+#pragma unroll
+                  for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tm_s(ms), desc(qlo + (k >> 2) * 1024 + (k & 3) * 2, hi_k),
+                           desc(klo + (k >> 2) * 1024 + (k & 3) * 2, hi_k), is, k > 0, on);
+                  tc_commit(bar(kBarS + ms), on);
+                }
+                if (pv && (!two || ms == 1)) {
+                  tc_commit(QUANT ? bar(kBarVop + 1) : bar(kBarVEmpty + (two ? last : before_last).slot), on);
                   vop_phase ^= 1;
                 }
-                odd ^= 1u << u;
+                if (!more) break;
+                pv = true;
+                odd ^= 1u << ms;
+                if (two && u == 0) {
+                  u = 1;
+                  continue;
+                }
+                tc_commit(QUANT ? bar(kBarKop + 1) : bar(kBarKEmpty + pos.slot), on);
+                u = 0;
+                before_last = last;
+                last = pos;
+                passed(v);
+                ++v;
+                pos.next(S);
+                ok = described(v);
+                if (!ok) break;
+                flags = uni(flags_of(v));
+                more = (flags & inside) == kTile;
+                if (more && !QUANT) ok = k_there();
               }
               if (!ok) break;
-              u = 0;
-              pend.at = pos;
-              passed(v);
-              ++v;
-              pos.next(S);
-              ok = described(v);
-              if (!ok) break;
-              flags = uni(flags_of(v));
-            } while ((flags & kMiddle) == (kTwo | kTile));
-            if (!ok) break;
-          }
+              pend.st = two ? 1 : (v - 1) & 1;
+              pend.at = last;
+              pend.fresh = false;
+            }
           }
           ok = QUANT ? wait_warp(kBarKop, v & 1) : wait_warp(kBarKFull + pos.slot, pos.phase);
           if (!ok) break;
@@ -1841,6 +1858,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               tc_wait_st();
             }
             float mx = -INFINITY;
+            // Scales of 8 tokens are loaded while the scores, or those before, are on their way. (16 x 8K INT8 with 24 drafts:
+            // 4, 8, 16 tokens ahead, none: 123, 112, 121, 123 us; more of them do not fit 96 registers.)
+            constexpr int PRE = 4;
+            [[maybe_unused]] ulonglong2 k2[PRE];
+            [[maybe_unused]] auto scales = [&](int at) {
+#pragma unroll
+              for (int j = 0; j < PRE; ++j) k2[j] = *reinterpret_cast<const ulonglong2*>(sc + 2 * at + 4 * j);
+            };
+            if constexpr (QUANT) scales(0);
 #pragma unroll 1
             for (int c = 0; c < ntok; c += COLS) {
               float a[COLS];
@@ -1849,9 +1875,12 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               tc_wait_ld();
               if constexpr (QUANT) {
 #pragma unroll
-                for (int j = 0; j < COLS; j += 2) {
-                  const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * (c + j));
-                  unpack2f(ffma2(pack2f(a[j], a[j + 1]), k2.x, fmul2(k2.y, qs2)), a[j], a[j + 1]);
+                for (int h = 0; h < COLS; h += 2 * PRE) {
+#pragma unroll
+                  for (int j = 0; j < 2 * PRE; j += 2)
+                    unpack2f(ffma2(pack2f(a[h + j], a[h + j + 1]), k2[j / 2].x, fmul2(k2[j / 2].y, qs2)), a[h + j],
+                             a[h + j + 1]);
+                  scales(min(c + h + 2 * PRE, kTile - 2 * PRE));
                 }
               }
               if constexpr (TREE) {
@@ -1913,6 +1942,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             const float ref = r == -INFINITY ? 0.f : r;
             const uint64_t ref2 = pack2f(-ref, -ref);
             uint64_t ls0 = 0, ls1 = 0, z2 = 0;
+            if constexpr (QUANT) scales(kTile);
 #pragma unroll 1
             for (int c = 0; c < ntok; c += COLS) {
               float a[COLS];
@@ -1931,9 +1961,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 const uint64_t w2 = pack2f(a[j], a[j + 1]);
                 (j & 2 ? ls1 : ls0) = fadd2(j & 2 ? ls1 : ls0, w2);
                 if constexpr (QUANT) {
-                  const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + 2 * (c + j));
+                  const ulonglong2 v2 = k2[j / 2 % PRE];
                   z2 = ffma2(w2, v2.y, z2);
                   unpack2f(fmul2(w2, v2.x), a[j], a[j + 1]);
+                  if (j % (2 * PRE) == 2 * PRE - 2) scales(kTile + min(c + j + 2, kTile - 2 * PRE));
                 }
               }
               // The weights' one rounding to the operand type. They take the

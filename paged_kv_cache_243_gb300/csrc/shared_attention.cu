@@ -16,11 +16,11 @@ const void* shared_kernel_bf16(int D);
 const void* shared_kernel_i8t(int D, bool bf);
 const void* shared_kernel_i8g(int D, bool bf);
 const void* shared_kernel_u4t(int D, bool bf);
-const void* tree_kernel_f16(int D);
-const void* tree_kernel_bf16(int D);
-const void* tree_kernel_i8t(int D, bool bf);
-const void* tree_kernel_i8g(int D, bool bf);
-const void* tree_kernel_u4t(int D, bool bf);
+const void* tree_kernel_f16(int D, bool few);
+const void* tree_kernel_bf16(int D, bool few);
+const void* tree_kernel_i8t(int D, bool bf, bool few);
+const void* tree_kernel_i8g(int D, bool bf, bool few);
+const void* tree_kernel_u4t(int D, bool bf, bool few);
 
 namespace {
 
@@ -291,11 +291,13 @@ pkv_status launch_tree(const TreeArgs& a) {
     return PKV_ERR_WORKSPACE;
   SharedParams p = {};
   const bool bf = a.q_dtype == PKV_BF16;
-  const void* fn = kind == KV_F16    ? tree_kernel_f16(D)
-                   : kind == KV_BF16 ? tree_kernel_bf16(D)
-                   : kind == KV_I8T  ? tree_kernel_i8t(D, bf)
-                   : kind == KV_I8G  ? tree_kernel_i8g(D, bf)
-                                     : tree_kernel_u4t(D, bf);
+  const bool few = a.drafts * group <= (kind == KV_F16 || kind == KV_BF16 ? SharedGeom<64, KV_F16, false>::FEW
+                                                                         : SharedGeom<64, KV_I8T, false>::FEW);
+  const void* fn = kind == KV_F16    ? tree_kernel_f16(D, few)
+                   : kind == KV_BF16 ? tree_kernel_bf16(D, few)
+                   : kind == KV_I8T  ? tree_kernel_i8t(D, bf, few)
+                   : kind == KV_I8G  ? tree_kernel_i8g(D, bf, few)
+                                     : tree_kernel_u4t(D, bf, few);
   int threads = 0, smem = 0;
   st = cache_params(c, dev, fn, 0, a.batch, true, p, threads, smem);
   if (st != PKV_OK) return st;

@@ -4,8 +4,8 @@
 namespace pkv {
 
 const void* shared_kernel_f16(int D) {
-  return D == 64 ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_F16, false, false>)
-                 : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_F16, false, false>);
+  return D == 64 ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_F16, false, kPrefixes>)
+                 : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_F16, false, kPrefixes>);
 }
 
 }  // namespace pkv

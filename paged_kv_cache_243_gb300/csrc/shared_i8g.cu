@@ -5,10 +5,10 @@ namespace pkv {
 
 const void* shared_kernel_i8g(int D, bool bf) {
   if (D == 64)
-    return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8G, true, false>)
-              : reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8G, false, false>);
-  return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8G, true, false>)
-            : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8G, false, false>);
+    return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8G, true, kPrefixes>)
+              : reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8G, false, kPrefixes>);
+  return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8G, true, kPrefixes>)
+            : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8G, false, kPrefixes>);
 }
 
 }  // namespace pkv

@@ -5,10 +5,10 @@ namespace pkv {
 
 const void* shared_kernel_i8t(int D, bool bf) {
   if (D == 64)
-    return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8T, true, false>)
-              : reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8T, false, false>);
-  return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8T, true, false>)
-            : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8T, false, false>);
+    return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8T, true, kPrefixes>)
+              : reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8T, false, kPrefixes>);
+  return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8T, true, kPrefixes>)
+            : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8T, false, kPrefixes>);
 }
 
 }  // namespace pkv

@@ -824,7 +824,7 @@ __host__ __device__ __forceinline__ int tree_records(const SharedParams& p) {
 
 // The same for trees of drafts: for each sequence, kv head and pair of row tiles its record rows (of the
 // first block, of those that continue it), parts and query rows, and whether both streams have a record.
-static __device__ __noinline__ void place_tree_records(const SharedParams& p, const SharedPlan& pl, int few_max) {
+static __device__ __noinline__ void place_tree_records(const SharedParams& p, const SharedPlan& pl, bool few) {
   const int lane = threadIdx.x & 31, whole = tree_records(p);
   const Shares shares(pl.gpre[p.num_groups], pl.lpre[p.num_groups], p.num_ctas);
 #pragma unroll 1
@@ -836,19 +836,26 @@ static __device__ __noinline__ void place_tree_records(const SharedParams& p, co
     if (mine > 0) {
       const int x = (rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, c = shares.block_of(x);
       info = make_int4(gh * p.rec_rows + pair * 2 * kTile, 2 * whole + (c + 1) * 2 * kTile,
-                       (shares.block_of(x + n - 1) - c + 1) | mine << 16, mine <= few_max);
+                       (shares.block_of(x + n - 1) - c + 1) | mine << 16, few);
     }
     p.ws_info[i] = info;
   }
 }
 
-template <int D, int KV, bool BF, bool TREE>
+// What a kernel serves. Trees have one for calls of few query rows, where a segment's rows never exceed FEW, and
+// one for the others: half the code and fewer registers (16 x 8K INT8 with 24 drafts: V_MEASURED us).
+enum SharedMode { kPrefixes = 0, kFewDrafts = 1, kDraftRows = 2 };
+
+template <int D, int KV, bool BF, int MODE>
 __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
   using G = SharedGeom<D, KV, BF>;
-  constexpr bool QUANT = G::QUANT;
+  constexpr bool QUANT = G::QUANT, TREE = MODE != kPrefixes;
   constexpr int NT = G::THREADS, COLS = QUANT || TREE ? 32 : 64;   // columns of a pass over the scores
   constexpr int FEW = G::FEW;
+  // whether a segment of so many rows runs transposed, and whether it has two row tiles
+  auto is_few = [](int rows) { return MODE == kFewDrafts || (MODE == kPrefixes && rows <= FEW); };
+  auto is_two = [](int rows) { return MODE != kFewDrafts && rows > kTile; };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const SharedLayout& lay = p.lay;
@@ -1018,7 +1025,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   tc_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
   auto records = [&]() {
-    if constexpr (TREE) place_tree_records(p, plan, FEW);
+    if constexpr (TREE) place_tree_records(p, plan, MODE == kFewDrafts);
     else place_records(p, plan, FEW);
   };
   if (nv <= 0) {   // uniform over the block
@@ -1203,14 +1210,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (!ok) break;
           rows = uni(d.rows);
           flags = uni(d.flags);
-          if constexpr (TREE) {
+          if constexpr (MODE == kDraftRows) {
             // Whole tiles within a segment, without what its ends need. The order is that of the passes below, but
             // a pass is P V of an event and S of the stream's next one: between the weights' arrival and the next
             // scores lie just these products, everything else is done behind them or while the weights
             // are being made. (This warp's instructions are slow, fetched anew between those of the softmax.)
-            const bool two = rows > kTile;
+            const bool two = is_two(rows);
             const int inside = (two ? kFirst | kLast : kEarly | kLate) | 0xFF;
-            if (pend.on && !p.two_terms && rows > FEW && (flags & inside) == kTile) {
+            if (pend.on && !p.two_terms && (flags & inside) == kTile) {
               const uint32_t hi_k = (uint32_t)(kmajor >> 32), hi_v = (uint32_t)(vmajor >> 32), lo_v = (uint32_t)vmajor;
               constexpr uint32_t is = kType | (uint32_t)(kTile / 8) << 17, io = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
               auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
@@ -1284,14 +1291,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           if (!ok) break;
           begun = true;
         }
-        const bool two = rows > kTile;
+        const bool two = is_two(rows);
         const int st = two ? u : v & 1;
         const int qt = qc + (two ? u : 0), qs = qt & 1;
         // queries still on their way hold up no product that could go ahead
         const bool scores =
             v < end && !(pend.on && (pend.st == st || (flags & kFirst &&
                                                        !__all_sync(0xffffffffu, mbar_test(bar(kBarQFull + qs), (qt >> 1) & 1)))));
-        const bool few = rows <= FEW;
+        const bool few = is_few(rows);
         const bool last_s = !two || u == 1;
         if (scores) {
           if (flags & kFirst) ok = wait_warp(kBarQFull + qs, (qt >> 1) & 1);
@@ -1319,7 +1326,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
           const uint64_t vd = at(vmajor, QUANT ? vop : ring + (uint32_t)(S + slot) * G::ENTRY);
           const uint32_t o = tm_o(ps);
           uint32_t acc = !pend.fresh;
-          if (pend.few) {
+          if (MODE == kFewDrafts || (MODE == kPrefixes && pend.few)) {
             // O^T (+)= V^T [P1^T | P2^T]: channels x rows, first and second terms of
             // the weights side by side
             constexpr uint32_t idesc = kType | 1u << 15 | 1u << 16 | (uint32_t)(2 * FEW / 8) << 17;
@@ -1613,7 +1620,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       Visit s;
       ok = visit(v, s);
       if (!ok) break;
-      const bool two = s.is(kTwo), few = s.rows <= FEW;
+      const bool two = MODE != kFewDrafts && s.is(kTwo), few = is_few(s.rows);
       const size_t rec0 = s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
                                            : (few ? st * whole : 0) + s.rec;
       const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + ((qc + (two ? st : 0)) % kQSums) * kTile;
@@ -2033,7 +2040,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         // weights), so that a row's 64 (32) bytes are written together
         const uint32_t to2 = tm_o(st ^ 1) + lanes;
         if constexpr (TREE) {
-          constexpr int PASS = QUANT ? 16 : 32;
+          constexpr int PASS = QUANT ? 8 : 32;
           float* out = p.ws_acc + (rec0 + tile_row - lane) * D + lane;
 #pragma unroll 1
           for (int c = from; c < to_c; c += PASS) {

@@ -3,9 +3,12 @@
 
 namespace pkv {
 
-const void* tree_kernel_bf16(int D) {
-  return D == 64 ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_BF16, true, true>)
-                 : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_BF16, true, true>);
+template <int D>
+static const void* of(bool few) {
+  return few ? reinterpret_cast<const void*>(&shared_attention_kernel<D, KV_BF16, true, kFewDrafts>)
+             : reinterpret_cast<const void*>(&shared_attention_kernel<D, KV_BF16, true, kDraftRows>);
 }
+
+const void* tree_kernel_bf16(int D, bool few) { return D == 64 ? of<64>(few) : of<128>(few); }
 
 }  // namespace pkv

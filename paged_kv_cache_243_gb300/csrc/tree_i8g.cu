@@ -3,12 +3,14 @@
 
 namespace pkv {
 
-const void* tree_kernel_i8g(int D, bool bf) {
-  if (D == 64)
-    return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8G, true, true>)
-              : reinterpret_cast<const void*>(&shared_attention_kernel<64, KV_I8G, false, true>);
-  return bf ? reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8G, true, true>)
-            : reinterpret_cast<const void*>(&shared_attention_kernel<128, KV_I8G, false, true>);
+template <int D, bool BF>
+static const void* of(bool few) {
+  return few ? reinterpret_cast<const void*>(&shared_attention_kernel<D, KV_I8G, BF, kFewDrafts>)
+             : reinterpret_cast<const void*>(&shared_attention_kernel<D, KV_I8G, BF, kDraftRows>);
+}
+
+const void* tree_kernel_i8g(int D, bool bf, bool few) {
+  return D == 64 ? (bf ? of<64, true>(few) : of<64, false>(few)) : (bf ? of<128, true>(few) : of<128, false>(few));
 }
 
 }  // namespace pkv

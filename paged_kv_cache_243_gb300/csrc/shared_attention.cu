@@ -283,7 +283,7 @@ pkv_status launch_tree(const TreeArgs& a) {
   // visits, two units each at most, and values of records are counted in 32 bits
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
-  if (2 * tiles >= (1ll << 31) / ((long long)c->num_kv_heads * a.batch * pairs) ||
+  if (2 * (tiles + 4) >= (1ll << 31) / ((long long)c->num_kv_heads * a.batch * pairs) ||
       (2ll * a.batch * c->num_kv_heads * (a.drafts * group + 31) + 256ll * ctas + 512) * D >= (1ll << 31))
     return PKV_ERR_UNSUPPORTED;
   const Work w = tree_layout(c, a.batch, a.drafts, group, ctas);

@@ -116,7 +116,7 @@ constexpr int kBadSlots = 4;
 
 // Shared memory by offset from a 1024-byte boundary.
 struct SharedLayout {
-  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, bad, misc, visits, bpre, gpre, lpre, moff, members, lens, skip, gp, rank, rowg;
+  int q, kop, vop, ring, raw, pt, xch, scales, bars, hdr, ml, qsum, vmax, bad, misc, visits, bpre, gpre, lpre, moff, hseg, lseg, members, lens, skip, gp, rank, rowg;
   int total;
 };
 struct SharedParams {
@@ -206,7 +206,11 @@ __host__ __device__ inline SharedLayout shared_layout(int entries, int batch, in
   o.lpre = put((groups + 1) * 4);
   o.moff = put((groups + 1) * 4);
   o.members = put(batch * 2);
-  if (tree) o.gp = put(groups * 4);
+  if (tree) {
+    o.gp = put(groups * 4);
+    o.hseg = put((groups + 1) * 4);
+    o.lseg = put((groups + 1) * 4);
+  }
   o.total = at;
   // the plan's other arrays are needed only while the ring is still empty
   at = o.ring;
@@ -362,6 +366,8 @@ struct SharedPlan {
   const uint16_t* members;
   const int *lens, *skip, *gp;     // shared memory (while planning), or NULL: from the inputs again (trees: gp stays)
   int lo, hi;                      // the block's visits
+  // trees: moff has each sequence's drafts, and the segments before each, of two row tiles and of fewer rows
+  const int *hseg, *lseg;
 };
 
 // One visit: a tile of a segment.
@@ -419,6 +425,13 @@ __device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int L, int g,
   r.skip = g >= 0 ? P & -p.round_to : 0;
   return r;
 }
+
+// Trees: a sequence's kv head has segments of two row tiles, and one of what is left where that is one tile. The end
+// of a segment costs a block as much as some visits: in the shares every segment has that many more. (24 x 8K of 64 drafts with
+// 0, 1, 2, 3, 4 of two row tiles: 150, 149, 148, 146, 149 us; 8 x 4K with 0, 2, 3, 4 of fewer rows: 32.0, 29.3, 29.6, 29.9.)
+constexpr int kEndHeavy = 3, kEndLight = 2;
+__host__ __device__ __forceinline__ int heavy_pairs(int rows) { return (rows + kTile - 1) / (2 * kTile); }
+__host__ __device__ __forceinline__ int light_pairs(int rows) { return (rows + 2 * kTile - 1) / (2 * kTile) - heavy_pairs(rows); }
 
 // Trees of drafts: the tokens of sequence g within the table, the last `drafts` of which are drafts.
 struct TreePlan {
@@ -481,20 +494,21 @@ static __device__ __noinline__ void describe_visit(const SharedParams& p, const 
     const int g = upper(pre, p.num_groups, x);
     if constexpr (TREE) {
       end_tok = pl.gp[g];
-      drafts = pl.moff[g + 1] - pl.moff[g];
+      drafts = pl.moff[g];
     } else {
       end_tok = pl.gp ? pl.gp[g] : p.prefix_lens[g] & -p.round_to;
     }
     first_tok = 0;
     tiles = (end_tok + kTile - 1) / kTile;
-    const int total = (pl.moff[g + 1] - pl.moff[g]) * p.group;
-    const int pairs = (total + 2 * kTile - 1) / (2 * kTile);
+    const int total = (TREE ? drafts : pl.moff[g + 1] - pl.moff[g]) * p.group;
+    const int before = TREE && pre == pl.lpre ? heavy_pairs(total) : 0;   // pairs that are numbered elsewhere
+    const int pairs = TREE ? (before || pre == pl.lpre ? 1 : heavy_pairs(total)) : (total + 2 * kTile - 1) / (2 * kTile);
     const int rem = x - pre[g], hp = rem / tiles;
     tile = rem - hp * tiles;
     s.head = hp / pairs;
-    s.q0 = (hp - s.head * pairs) * 2 * kTile;
+    s.q0 = (hp - s.head * pairs + before) * 2 * kTile;
     s.rows = min(2 * kTile, total - s.q0);
-    s.mem0 = pl.moff[g];
+    s.mem0 = TREE ? 0 : pl.moff[g];
     s.row = TREE ? g : pl.members[s.mem0];
     s.rec = TREE ? (g * p.num_kv_heads + s.head) * p.rec_rows + s.q0
                  : s.head * p.batch * p.group + s.mem0 * p.group + s.q0;
@@ -822,19 +836,28 @@ __host__ __device__ __forceinline__ int tree_records(const SharedParams& p) {
   return p.num_groups * p.num_kv_heads * p.rec_rows;
 }
 
+// Their shares: visits and segments' ends.
+__device__ __forceinline__ Shares tree_shares(const SharedPlan& pl, int NG, int ctas) {
+  const int heavy = pl.gpre[NG] + kEndHeavy * pl.hseg[NG];
+  return Shares(heavy, heavy + pl.lpre[NG] - pl.gpre[NG] + kEndLight * pl.lseg[NG], ctas);
+}
+
 // The same for trees of drafts: for each sequence, kv head and pair of row tiles its record rows (of the
 // first block, of those that continue it), parts and query rows, and whether both streams have a record.
 static __device__ __noinline__ void place_tree_records(const SharedParams& p, const SharedPlan& pl, bool few) {
-  const int lane = threadIdx.x & 31, whole = tree_records(p);
-  const Shares shares(pl.gpre[p.num_groups], pl.lpre[p.num_groups], p.num_ctas);
+  const int lane = threadIdx.x & 31, whole = tree_records(p), NG = p.num_groups;
+  const Shares shares = tree_shares(pl, NG, p.num_ctas);
 #pragma unroll 1
-  for (int i = blockIdx.x + gridDim.x * lane; i < p.num_groups * p.num_kv_heads * p.pairs; i += gridDim.x * 32) {
+  for (int i = blockIdx.x + gridDim.x * lane; i < NG * p.num_kv_heads * p.pairs; i += gridDim.x * 32) {
     const int gh = i / p.pairs, pair = i - gh * p.pairs, g = gh / p.num_kv_heads, h = gh - g * p.num_kv_heads;
-    const int rows = (pl.moff[g + 1] - pl.moff[g]) * p.group, pairs = (rows + 2 * kTile - 1) / (2 * kTile);
+    const int rows = pl.moff[g] * p.group, heavy = heavy_pairs(rows);
     const int n = (int)((uint32_t)(pl.gp[g] + kTile - 1) / kTile), mine = min(2 * kTile, rows - pair * 2 * kTile);
     int4 info = make_int4(0, 0, 0, 0);
     if (mine > 0) {
-      const int x = (rows > kTile ? pl.gpre : pl.lpre)[g] + (h * pairs + pair) * n, c = shares.block_of(x);
+      // the segment's first visit, counted with the segments' ends
+      const int x = pair < heavy ? pl.gpre[g] + kEndHeavy * pl.hseg[g] + (h * heavy + pair) * (n + kEndHeavy)
+                                 : pl.lpre[g] + kEndHeavy * pl.hseg[NG] + kEndLight * pl.lseg[g] + h * (n + kEndLight);
+      const int c = shares.block_of(x);
       info = make_int4(gh * p.rec_rows + pair * 2 * kTile, 2 * whole + (c + 1) * 2 * kTile,
                        (shares.block_of(x + n - 1) - c + 1) | mine << 16, few);
     }
@@ -851,7 +874,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     shared_attention_kernel(const __grid_constant__ SharedParams p) {
   using G = SharedGeom<D, KV, BF>;
   constexpr bool QUANT = G::QUANT, TREE = MODE != kPrefixes;
-  constexpr int NT = G::THREADS, COLS = QUANT || TREE ? 32 : 64;   // columns of a pass over the scores
+  constexpr int NT = G::THREADS, COLS = QUANT ? 32 : 64;   // columns of a pass over the scores
   constexpr int FEW = G::FEW;
   // whether a segment of so many rows runs transposed, and whether it has two row tiles
   auto is_few = [](int rows) { return MODE == kFewDrafts || (MODE == kPrefixes && rows <= FEW); };
@@ -873,6 +896,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   int* moff = reinterpret_cast<int*>(smem + lay.moff);
   uint16_t* members = reinterpret_cast<uint16_t*>(smem + lay.members);
   int* lpre = reinterpret_cast<int*>(smem + lay.lpre);
+  [[maybe_unused]] int* hseg = reinterpret_cast<int*>(smem + lay.hseg);   // trees
+  [[maybe_unused]] int* lseg = reinterpret_cast<int*>(smem + lay.lseg);
   uint16_t* rank = reinterpret_cast<uint16_t*>(smem + lay.rank);
   int16_t* rowg = reinterpret_cast<int16_t*>(smem + lay.rowg);
   // (trees of drafts: the groups are all there is)
@@ -976,9 +1001,19 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   // prefix visits, visits of the rows' own tokens
   const int per_g = (NG + NT - 1) / NT, per_b = (B + NT - 1) / NT;
   const int ga = min(NG, tid * per_g), ge = min(NG, ga + per_g), ba = min(B, tid * per_b), be = min(B, ba + per_b);
+  // (trees: segments of fewer rows, heavy visits, other visits, segments of two row tiles)
   int4 run = make_int4(0, 0, 0, 0);
+  [[maybe_unused]] auto count_tree = [&](int g) {
+    const int rows = moff[g] * Gq, tiles = tiles_of(gp[g]);
+    const int h = tiles ? p.num_kv_heads * heavy_pairs(rows) : 0, l = tiles ? p.num_kv_heads * light_pairs(rows) : 0;
+    run = make_int4(run.x + l, run.y + h * tiles, run.z + l * tiles, run.w + h);
+  };
 #pragma unroll 1
   for (int g = ga; g < ge; ++g) {
+    if constexpr (TREE) {
+      count_tree(g);
+      continue;
+    }
     const int n = prefix_visits(g);
     run.x += moff[g];
     (moff[g] * Gq > kTile ? run.y : run.z) += n;
@@ -988,9 +1023,15 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   const int4 all = block_scan4(run, NT, scratch);
 #pragma unroll 1
   for (int g = ga; g < ge; ++g) {
-    const int n = prefix_visits(g), c = moff[g];
     gpre[g] = run.y;
     lpre[g] = all.y + run.z;
+    if constexpr (TREE) {
+      hseg[g] = run.w;
+      lseg[g] = run.x;
+      count_tree(g);
+      continue;
+    }
+    const int n = prefix_visits(g), c = moff[g];
     moff[g] = run.x;
     run.x += c;
     (c * Gq > kTile ? run.y : run.z) += n;
@@ -1001,20 +1042,49 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     run.w += p.num_kv_heads * tiles_of(lens[b] - skip[b]);
   }
   if (tid == 0) {
-    moff[NG] = all.x;
     gpre[NG] = all.y;
     lpre[NG] = all.y + all.z;
-    bpre[B] = all.y + all.z + all.w;
+    if constexpr (TREE) {
+      hseg[NG] = all.w;
+      lseg[NG] = all.x;
+    } else {
+      moff[NG] = all.x;
+      bpre[B] = all.y + all.z + all.w;
+    }
   }
   __syncthreads();
-  const Shares shares(all.y, all.y + all.z + all.w, p.num_ctas);
+  SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, 0, 0, hseg, lseg};
+  const int total = all.y + all.z + (TREE ? 0 : all.w);   // visits
+  const Shares shares = TREE ? tree_shares(plan, NG, p.num_ctas) : Shares(all.y, total, p.num_ctas);
 #pragma unroll 1
   for (int b = tid; b < B; b += NT)
     if (rowg[b] >= 0) members[moff[rowg[b]] + rank[b]] = (uint16_t)b;
-  const bool idle = (int)blockIdx.x >= shares.blocks || all.y + all.z + all.w == 0;
-  const int lo = idle ? 0 : shares.first(blockIdx.x), hi = idle ? 0 : shares.first(blockIdx.x + 1);
+  const bool idle = (int)blockIdx.x >= shares.blocks || total == 0;
+  int lo = idle ? 0 : shares.first(blockIdx.x), hi = idle ? 0 : shares.first(blockIdx.x + 1);
+  if constexpr (TREE) {
+    // from the count with the segments' ends to that of the visits: the sequence within which a border lies finds it
+    volatile int* range = reinterpret_cast<volatile int*>(scratch);
+    if (tid < 2) range[tid] = idle ? 0 : total;   // (where no sequence does)
+    __syncthreads();
+#pragma unroll 1
+    for (int g = tid; g < NG; g += NT) {
+      const int tiles = tiles_of(gp[g]), hl = hseg[NG] * kEndHeavy;
+#pragma unroll 1
+      for (int i = 0; i < 4 && !idle && tiles; ++i) {
+        const bool light = i & 1;
+        const int end = light ? kEndLight : kEndHeavy, seg = light ? lseg[g] : hseg[g];
+        const int n = (light ? lseg[g + 1] : hseg[g + 1]) - seg, real = light ? lpre[g] : gpre[g];
+        const int at = (i < 2 ? lo : hi) - (real + (light ? hl : 0) + end * seg);
+        if (at >= 0 && at < n * (tiles + end)) range[i >> 1] = real + at / (tiles + end) * tiles + min(at % (tiles + end), tiles);
+      }
+    }
+    __syncthreads();
+    lo = range[0];
+    hi = range[1];
+  }
   const int nv = hi - lo;
-  SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, lo, hi};
+  plan.lo = lo;
+  plan.hi = hi;
   __syncthreads();
   if (tid < min(nv, kVisits)) describe_visit<TREE>(p, plan, lo + tid, visits + 2 * tid);
   plan.lens = plan.skip = nullptr;
@@ -1540,7 +1610,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       return misc[1] == 0;
     };
     // trees: the tokens of sequence g before its drafts
-    [[maybe_unused]] auto before = [&](int g) { return gp[g] - (moff[g + 1] - moff[g]); };
+    [[maybe_unused]] auto before = [&](int g) { return gp[g] - moff[g]; };
     // the stream's next event: the scores of visit v are there
     int ntok = 0, mask = 0;
     bool valid = false;   // token `row` of the tile
@@ -1845,7 +1915,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             // tokens [c, c + 32) of the tile that the row attends to
             [[maybe_unused]] auto sees32 = [&](int c) {
               uint32_t on = c < 64 ? (c < 32 ? sees.x : sees.y) : (c < 96 ? sees.z : sees.w);
-              if (ntok - c < 32) on &= (1u << (ntok - c)) - 1u;
+              if (ntok - c < 32) on &= (1u << max(ntok - c, 0)) - 1u;
               const int pieces = mask >> (c >> 4);
               return on & ((pieces & 1 ? 0xFFFFu : 0u) | (pieces & 2 ? 0xFFFF0000u : 0u));
             };
@@ -1892,11 +1962,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               }
               if constexpr (TREE) {
                 if (drafts || partial) {
-                  const uint32_t on = sees32(c);
 #pragma unroll
-                  for (int j = 0; j < COLS; ++j)
-                    if (!(on >> j & 1)) a[j] = -INFINITY;
-                  if constexpr (!QUANT) tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));
+                  for (int h = 0; h < COLS; h += 32) {
+                    const uint32_t on = sees32(c + h);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                      if (!(on >> j & 1)) a[h + j] = -INFINITY;
+                    if constexpr (!QUANT) tmem_st<32>(ts + c + h, reinterpret_cast<uint32_t*>(a + h));
+                  }
                 }
               }
               if constexpr (QUANT) tmem_st<32>(ts + c, reinterpret_cast<uint32_t*>(a));

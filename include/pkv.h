@@ -584,6 +584,7 @@ size_t pkv_tree_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t t
  * Pages that it writes are the sequence's own (pkv_alloc_unshare). PER_GROUP64 is
  * PKV_ERR_UNSUPPORTED: codes of another group's scale cannot be moved; append the accepted tokens
  * anew with pkv_kv_append at first[b], which goes on from the originals of the open group.
+ * Pools of 2^31 rows (num_pages * num_kv_heads * page_size) or more are PKV_ERR_UNSUPPORTED.
  * One launch. An attention call right behind this one may not promise fresh_rows, nor a
  * scoring call early_start.
  * Device errors: PKV_DEV_BAD_POSITION (a list or a length as above, or beyond the table: the row stays

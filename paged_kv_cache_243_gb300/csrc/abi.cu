@@ -945,6 +945,7 @@ pkv_status pkv_keep_tokens(const pkv_cache* cache, int32_t batch, int32_t max_ke
   if (cache->quant == PKV_QUANT_PER_GROUP64) return PKV_ERR_UNSUPPORTED;
   if (batch < 0 || max_keep < 0 || max_pages <= 0) return PKV_ERR_INVALID_ARG;
   if (max_keep > 256 || (long long)batch * cache->num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if ((long long)cache->num_pages * cache->num_kv_heads * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if ((max_keep > 0 && !keep) || !block_table || !first) return PKV_ERR_INVALID_ARG;
   KeepParams p = {};

@@ -943,6 +943,69 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
 
   // ---- plan: lengths, who shares, visits before each segment. (Its loops stay
   // loops: this code is fetched anew by every call.)
+  SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, 0, 0, hseg, lseg};
+  auto tiles_of = [](int tokens) { return (uint32_t)(tokens + kTile - 1) / kTile; };
+  int lo = 0, hi = 0;
+  // trees: a sequence's segments of fewer rows, visits of two row tiles, other visits, segments of two row tiles
+  [[maybe_unused]] auto tree_counts = [&](int rows, int tiles) {
+    const int h = tiles ? p.num_kv_heads * heavy_pairs(rows) : 0, l = tiles ? p.num_kv_heads * light_pairs(rows) : 0;
+    return make_int4(l, h * tiles, l * tiles, h);
+  };
+  // the visit at a border of the shares that lies among `n` segments, `at` from their first; -1: it lies elsewhere
+  [[maybe_unused]] auto visit_at = [](int at, int n, int tiles, int end, int first) {
+    return at >= 0 && at < n * (tiles + end) ? first + at / (tiles + end) * tiles + min(at % (tiles + end), tiles) : -1;
+  };
+  if constexpr (TREE && !QUANT) {   // no visit's marks
+    for (int i = tid; i < kBadSlots * kTile; i += NT) reinterpret_cast<int*>(smem + lay.bad)[i] = -1;
+  }
+  if (TREE && NG <= 32) {
+    // few sequences: a lane each, in every warp, without a wait in between
+    TreePlan r = {0, 0, 0};
+    if (lane < NG) r = tree_plan(p, lane);
+    const int tiles = tiles_of(r.len);
+    const int4 mine = tree_counts(r.drafts * Gq, tiles);
+    int4 e = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int4 y = make_int4(__shfl_up_sync(0xffffffffu, e.x, off), __shfl_up_sync(0xffffffffu, e.y, off),
+                               __shfl_up_sync(0xffffffffu, e.z, off), __shfl_up_sync(0xffffffffu, e.w, off));
+      if (lane >= off) e = make_int4(e.x + y.x, e.y + y.y, e.z + y.z, e.w + y.w);
+    }
+    const int4 all = make_int4(__shfl_sync(0xffffffffu, e.x, 31), __shfl_sync(0xffffffffu, e.y, 31),
+                               __shfl_sync(0xffffffffu, e.z, 31), __shfl_sync(0xffffffffu, e.w, 31));
+    e = make_int4(e.x - mine.x, e.y - mine.y, e.z - mine.z, e.w - mine.w);
+    if (warp == 0) {
+      if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
+      if (lane < NG) {
+        moff[lane] = r.drafts;
+        gp[lane] = r.len;
+        gpre[lane] = e.y;
+        lpre[lane] = all.y + e.z;
+        hseg[lane] = e.w;
+        lseg[lane] = e.x;
+      }
+      if (lane == 0) {
+        gpre[NG] = all.y;
+        lpre[NG] = all.y + all.z;
+        hseg[NG] = all.w;
+        lseg[NG] = all.x;
+      }
+    }
+    const int heavy = all.y + kEndHeavy * all.w, total = all.y + all.z;
+    const Shares shares(heavy, heavy + all.z + kEndLight * all.x, p.num_ctas);
+    auto border = [&](int c) {
+      const int x = shares.first(c);
+      const int v = __reduce_max_sync(0xffffffffu, max(visit_at(x - e.y - kEndHeavy * e.w, mine.w, tiles, kEndHeavy, e.y),
+                                                       visit_at(x - heavy - e.z - kEndLight * e.x, mine.x, tiles, kEndLight,
+                                                                all.y + e.z)));
+      return v < 0 ? total : v;
+    };
+    if ((int)blockIdx.x < shares.blocks && total > 0) {
+      lo = border(blockIdx.x);
+      hi = border(blockIdx.x + 1);
+    }
+    __syncthreads();
+  } else {
   if constexpr (TREE) {
 #pragma unroll 1
     for (int g = tid; g < NG; g += NT) {
@@ -950,9 +1013,6 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       if (r.bad && blockIdx.x == 0) flag_status(p.dev_status, r.bad);
       moff[g] = r.drafts;
       gp[g] = r.len;
-    }
-    if constexpr (!QUANT) {   // no visit's marks
-      for (int i = tid; i < kBadSlots * kTile; i += NT) reinterpret_cast<int*>(smem + lay.bad)[i] = -1;
     }
     __syncthreads();
   } else {
@@ -992,7 +1052,6 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
     __syncthreads();
   }
-  auto tiles_of = [](int tokens) { return (uint32_t)(tokens + kTile - 1) / kTile; };
   // kv heads x pairs of row tiles x tiles of tokens
   auto prefix_visits = [&](int g) {
     return moff[g] == 0 ? 0 : (int)(p.num_kv_heads * ((uint32_t)(moff[g] * Gq + 2 * kTile - 1) / (2 * kTile)) * tiles_of(gp[g]));
@@ -1001,12 +1060,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
   // prefix visits, visits of the rows' own tokens
   const int per_g = (NG + NT - 1) / NT, per_b = (B + NT - 1) / NT;
   const int ga = min(NG, tid * per_g), ge = min(NG, ga + per_g), ba = min(B, tid * per_b), be = min(B, ba + per_b);
-  // (trees: segments of fewer rows, heavy visits, other visits, segments of two row tiles)
   int4 run = make_int4(0, 0, 0, 0);
   [[maybe_unused]] auto count_tree = [&](int g) {
-    const int rows = moff[g] * Gq, tiles = tiles_of(gp[g]);
-    const int h = tiles ? p.num_kv_heads * heavy_pairs(rows) : 0, l = tiles ? p.num_kv_heads * light_pairs(rows) : 0;
-    run = make_int4(run.x + l, run.y + h * tiles, run.z + l * tiles, run.w + h);
+    const int4 n = tree_counts(moff[g] * Gq, tiles_of(gp[g]));
+    run = make_int4(run.x + n.x, run.y + n.y, run.z + n.z, run.w + n.w);
   };
 #pragma unroll 1
   for (int g = ga; g < ge; ++g) {
@@ -1053,14 +1110,14 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     }
   }
   __syncthreads();
-  SharedPlan plan = {gpre, lpre, bpre, moff, members, lens, skip, gp, 0, 0, hseg, lseg};
   const int total = all.y + all.z + (TREE ? 0 : all.w);   // visits
   const Shares shares = TREE ? tree_shares(plan, NG, p.num_ctas) : Shares(all.y, total, p.num_ctas);
 #pragma unroll 1
   for (int b = tid; b < B; b += NT)
     if (rowg[b] >= 0) members[moff[rowg[b]] + rank[b]] = (uint16_t)b;
   const bool idle = (int)blockIdx.x >= shares.blocks || total == 0;
-  int lo = idle ? 0 : shares.first(blockIdx.x), hi = idle ? 0 : shares.first(blockIdx.x + 1);
+  lo = idle ? 0 : shares.first(blockIdx.x);
+  hi = idle ? 0 : shares.first(blockIdx.x + 1);
   if constexpr (TREE) {
     // from the count with the segments' ends to that of the visits: the sequence within which a border lies finds it
     volatile int* range = reinterpret_cast<volatile int*>(scratch);
@@ -1074,18 +1131,19 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         const bool light = i & 1;
         const int end = light ? kEndLight : kEndHeavy, seg = light ? lseg[g] : hseg[g];
         const int n = (light ? lseg[g + 1] : hseg[g + 1]) - seg, real = light ? lpre[g] : gpre[g];
-        const int at = (i < 2 ? lo : hi) - (real + (light ? hl : 0) + end * seg);
-        if (at >= 0 && at < n * (tiles + end)) range[i >> 1] = real + at / (tiles + end) * tiles + min(at % (tiles + end), tiles);
+        const int v = visit_at((i < 2 ? lo : hi) - (real + (light ? hl : 0) + end * seg), n, tiles, end, real);
+        if (v >= 0) range[i >> 1] = v;
       }
     }
     __syncthreads();
     lo = range[0];
     hi = range[1];
   }
+  __syncthreads();
+  }
   const int nv = hi - lo;
   plan.lo = lo;
   plan.hi = hi;
-  __syncthreads();
   if (tid < min(nv, kVisits)) describe_visit<TREE>(p, plan, lo + tid, visits + 2 * tid);
   plan.lens = plan.skip = nullptr;
   if constexpr (!TREE) plan.gp = nullptr;

@@ -1680,9 +1680,10 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
     [[maybe_unused]] uint32_t bads[4] = {0, 0, 0, 0};
     auto begin = [&]() -> bool {
       if (!wait_warp(kBarHdr + v % kHdrs, (v / kHdrs) & 1)) return false;
-      if constexpr (!TREE || QUANT) {
-        if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
-      }
+      // Trees look at a tile's drafts while its scores are on their way, but only in the ring's first round: the scores
+      // of v are the sign that V of v - S is done with, without which the parity of V's barrier says nothing.
+      const bool early = TREE && !QUANT && v < S;
+      if (!early && !wait_warp(kBarS + st, n_ev++ & 1)) return false;
       const int2 hd = *reinterpret_cast<const int2*>(smem + lay.hdr + (v % kHdrs) * 8);
       ntok = hd.x;
       mask = hd.y;
@@ -1727,9 +1728,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         }
         fence_proxy_async_smem();   // before the products read them
       }
-      if constexpr (TREE && !QUANT) {   // (values are looked at while the scores are on their way)
-        if (!wait_warp(kBarS + st, n_ev++ & 1)) return false;
-      }
+      if (early && !wait_warp(kBarS + st, n_ev++ & 1)) return false;
       tc_after();
       return true;
     };

@@ -67,6 +67,48 @@ def test_many_visits_per_block(kind, T, g):
     assert int(tb.status.item()) == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "i8t"])
+@pytest.mark.parametrize("T,g", [(3, 3), (13, 4), (30, 4), (64, 4), (100, 4)])
+@pytest.mark.parametrize("last", [1, 64, 77, 113, 128])
+def test_long_parts_end_in_drafts(kind, T, g, last):
+    # blocks whose part of a segment is long and ends with the drafts' tile, part of a tile or all of it: transposed, one
+    # and two row tiles, in either output type; and the same bits every time
+    lens = [128 * 40 + last, 128 * 23 + last, 128 * 9 + last]
+    tb = TreeBatch(kind, 1, 128, 16, lens, T, seed=T + last)
+    q, qf = tb.tree_queries(g)
+    for dt in (TORCH[tb.src], torch.float32):
+        for splits in (0, 3, 7):
+            ref = tb.tree_run(q, dt, num_splits=splits)
+            tb.tree_check(ref, qf, g)
+            for _ in range(5):
+                assert torch.equal(tb.tree_run(q, dt, num_splits=splits), ref)
+
+
+def test_every_call_of_a_large_batch_gives_the_same_bits():
+    for kind, T, g, n in (("bf16", 16, 4, 8), ("f16", 40, 7, 6), ("i8t", 24, 4, 8), ("bf16", 3, 4, 16)):
+        rng = np.random.default_rng(T)
+        tb = TreeBatch(kind, 4, 128, 16, rng.integers(1500, 4000, n), T, seed=T)
+        q, qf = tb.tree_queries(g)
+        dt = TORCH[tb.src]
+        tb.cache.k_pages.add_(0)      # (the pools are not in the cache of the first call)
+        ref = tb.tree_run(q, dt)
+        tb.tree_check(ref, qf, g)
+        junk = torch.empty(64 << 20, dtype=torch.float32, device="cuda")
+        for i in range(20):
+            if i % 2:
+                junk.zero_()          # K and V come from memory again
+            assert torch.equal(tb.tree_run(q, dt), ref)
+
+
+def test_forty_sequences():
+    # more than a warp plans by itself, of one and of two row tiles
+    rng = np.random.default_rng(5)
+    for T, g in ((70, 4), (9, 2)):
+        tb = TreeBatch("bf16", 2, 64, 32, rng.integers(0, 700, 40), T, drafts=rng.integers(0, T + 1, 40), seed=T)
+        q, qf = tb.tree_queries(g)
+        tb.tree_check(tb.tree_run(q, torch.bfloat16), qf, g)
+
+
 def test_long_contexts():
     tb = TreeBatch("bf16", 2, 128, 16, [20000, 3001, 129], 24, seed=8)
     q, qf = tb.tree_queries(4)

@@ -5,7 +5,9 @@
  * with GQA head grouping, fp16/bf16 or INT8 (per-token or per-64-token-group
  * scale/zero-point) keys and values dequantised inside the kernels, and a
  * query-aware sparse mode that scores pages by a per-page channel bounding box
- * and attends only over the top-K pages.
+ * and attends only over the top-K pages. Beside it stand calls for sequences that share
+ * pages, and for steps with several drafted tokens (rotary appends, attention for a tree of
+ * drafts, keeping those that were accepted).
  *
  * Sources, cited by short name and section:
  *   [Gemini page]      "GPU显存占用直降63%！Gemini KV Cache优化实战：FlashAttention-3适配全链路拆解"
@@ -14,8 +16,9 @@
  *   [TinyServe page]   "LLM推理中的KV缓存优化技术与TinyServe实践"
  *
  * Conventions (every call):
- *   - Pointers named *_pages, q, out, k_new, v_new, block_table, seq_lens,
- *     positions, new_lens, sel_*, scores_out, workspace, dev_status and the
+ *   - Pointers named *_pages, q, q_out, out, k_new, v_new, block_table, seq_lens,
+ *     positions, new_lens, sel_*, scores_out, cos_sin, rotary_positions, draft_lens,
+ *     tree_mask, keep, keep_lens, first, workspace, dev_status and the
  *     pointer members of pkv_cache are DEVICE pointers owned by the caller.
  *     The library allocates no device memory and keeps no pointer after a call
  *     returns. `stream` is a cudaStream_t passed as void* (NULL = legacy stream).

@@ -1,7 +1,7 @@
 """GB300 (sm_103a) paged KV-cache decode attention.
 
-The compute lives in libpkv.so (include/pkv.h): kv_append, page_score_topk and
-paged_decode_attention as hand-written CUDA kernels. `binding` marshals
+The compute lives in libpkv.so (include/pkv.h): kv_append, page_score_topk,
+paged_decode_attention and their like as hand-written CUDA kernels. `binding` marshals
 arguments to the C ABI; `cache` wraps device tensors for PyTorch users.
 """
 from . import binding  # noqa: F401

@@ -1630,8 +1630,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             // A draft whose values are no numbers must not reach the rows that do not attend to
             // it: its values are taken out here, and the merge gives them to the rows that do.
             bool bad = false;
-            if (visits[2 * (v & (kVisits - 1))].y & kDrafts) {
-              bad = valid && !(fabsf(fmaf(255.f, z.z, z.w)) < INFINITY && fabsf(z.z) < INFINITY && fabsf(z.w) < INFINITY);
+            const int4 d = visits[2 * (v & (kVisits - 1))];   // first token, flags, sequence
+            if (d.y & kDrafts && d.x + t >= gp[d.z] - moff[d.z]) {
+              bad = valid && !(fabsf(z.z) < INFINITY && fabsf(fmaf(G::CENTRE, z.z, z.w)) < INFINITY);
               if (bad) z.z = z.w = 0.f;
               counts = valid && !bad;
             }

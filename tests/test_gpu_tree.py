@@ -250,6 +250,23 @@ def test_no_number_reaches_rows_that_do_not_attend_to_it(kind, T, g, value, spli
     assert int(tb.status.item()) == 0
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16", "i8t", "u4t"])
+@pytest.mark.parametrize("T,g", [(3, 2), (20, 2), (50, 4)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_no_numbers_before_the_drafts_reach_every_row(kind, T, g, value):
+    # a value in the tile of the drafts, but not one of them; and one in a tile before it
+    for back in (1, 9, 200):
+        tb = TreeBatch(kind, 2, 64, 16, [T + 300, T + 64], T, seed=T)
+        q, _ = tb.tree_queries(g)
+        ref = tb.tree_run(q)
+        b = int(np.argmax(tb.lens))
+        spoil(tb, b, int(tb.lens[b]) - T - back, 1, "v", value)
+        out = tb.tree_run(q)
+        got = out[b, :, g:] if tb.cache.kv_sz is not None else out[b, :, g:, 5]
+        assert not bool(torch.isfinite(got).any())
+        assert torch.equal(out[b, :, :g], ref[b, :, :g]) and torch.equal(out[1 - b], ref[1 - b])
+
+
 def test_huge_values_cost_rows_that_do_not_attend_to_them_nothing():
     tb = TreeBatch("f16", 2, 64, 16, [200, 60], 20, seed=21)
     q, qf = tb.tree_queries(2)

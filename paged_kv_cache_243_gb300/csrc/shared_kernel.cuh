@@ -1375,13 +1375,13 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
                 const int ms = two ? u : v & 1;
                 if (pv) {
                   const RingPos at = two ? last : before_last;
-                  ok = wait_warp(kBarP + ms, ~(odd >> ms) & 1);
-                  if (!ok) break;
                   if (!two || ms == 0) {   // (otherwise V is known to be there)
                     ok = QUANT ? wait_warp(kBarVop, vop_phase) : wait_warp(kBarVFull + at.slot, at.phase);
                     if (!ok) break;
                   }
                   const uint32_t vlo = lo_v | (QUANT ? vop : ring + (uint32_t)(S + at.slot) * G::ENTRY) >> 4;
+                  ok = wait_warp(kBarP + ms, ~(odd >> ms) & 1);
+                  if (!ok) break;
                   tc_after();
 #pragma unroll
                   for (int j = 0; j < 8; ++j)

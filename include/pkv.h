@@ -521,6 +521,7 @@ pkv_status pkv_rotary_table(float* cos_sin, int32_t positions, int32_t rot_dim, 
  *   q_out            : [batch][t_new][num_q_heads][head_dim] of src_dtype. May be q itself where q_stride
  *                      is num_q_heads * head_dim. Rows of tokens beyond new_lens[b], or of a batch row
  *                      with a bad position, are left as they were.
+ * Tables of 2^31 tokens (max_pages * page_size) or more are PKV_ERR_UNSUPPORTED.
  * One launch; PER_GROUP64 two or three, and one more with boxes. An attention call right behind this
  * one may not promise fresh_rows, nor a scoring call early_start: this call writes queries.
  * Device errors: those of pkv_kv_append, and PKV_DEV_BAD_POSITION for a row beyond the table (the
@@ -587,7 +588,8 @@ size_t pkv_tree_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t t
  * Pages that it writes are the sequence's own (pkv_alloc_unshare). PER_GROUP64 is
  * PKV_ERR_UNSUPPORTED: codes of another group's scale cannot be moved; append the accepted tokens
  * anew with pkv_kv_append at first[b], which goes on from the originals of the open group.
- * Pools of 2^31 rows (num_pages * num_kv_heads * page_size) or more are PKV_ERR_UNSUPPORTED.
+ * Pools of 2^31 rows (num_pages * num_kv_heads * page_size) or more, and tables of 2^31 tokens
+ * (max_pages * page_size), are PKV_ERR_UNSUPPORTED.
  * One launch. An attention call right behind this one may not promise fresh_rows, nor a
  * scoring call early_start.
  * Device errors: PKV_DEV_BAD_POSITION (a list or a length as above, or beyond the table: the row stays

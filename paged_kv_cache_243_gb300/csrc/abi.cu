@@ -918,6 +918,7 @@ pkv_status pkv_rotary_append(const pkv_cache* cache, int32_t batch, int32_t t_ne
   if (cache->quant == PKV_QUANT_PER_GROUP64 && (!cache->tail || !aligned16(cache->tail) || cache->tail_rows < batch))
     return PKV_ERR_INVALID_ARG;
   if ((long long)t_new > (long long)max_pages * cache->page_size) return PKV_ERR_INVALID_ARG;
+  if ((long long)max_pages * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;   // token positions
   if (batch > 65535 || cache->num_kv_heads > 32767) return PKV_ERR_UNSUPPORTED;   // grid y / z limits
   if ((long long)batch * t_new > INT32_MAX / 2 || (long long)num_q_heads + 2 * cache->num_kv_heads > 65535)
     return PKV_ERR_UNSUPPORTED;
@@ -946,6 +947,7 @@ pkv_status pkv_keep_tokens(const pkv_cache* cache, int32_t batch, int32_t max_ke
   if (batch < 0 || max_keep < 0 || max_pages <= 0) return PKV_ERR_INVALID_ARG;
   if (max_keep > 256 || (long long)batch * cache->num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if ((long long)cache->num_pages * cache->num_kv_heads * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if ((long long)max_pages * cache->page_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;   // token positions
   if (batch == 0) return PKV_OK;
   if ((max_keep > 0 && !keep) || !block_table || !first) return PKV_ERR_INVALID_ARG;
   KeepParams p = {};

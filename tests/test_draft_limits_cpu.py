@@ -247,3 +247,10 @@ def test_strided_tokens(cache):
     assert _token_stride(x[1:2, 2:4], "x", (1, 2, 8, 64), -1) == 512
     with pytest.raises(ValueError):      # rows that do not go on where the one before ends
         _token_stride(x[:, :4], "x", (3, 4, 8, 64), -1)
+
+
+def test_tables_of_2_31_tokens_are_refused():
+    # (token positions are 32-bit on the device)
+    for call in (rotary, keep):
+        refused(call(max_pages=1 << 27), B.ERR_UNSUPPORTED)
+        call(batch=0, max_pages=(1 << 27) - 1)()

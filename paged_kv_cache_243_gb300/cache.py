@@ -546,6 +546,8 @@ class PagedKVCache:
         width = block_table.shape[1]
         self._ints((block_table, "block_table", (Bsz, width)), (positions, "positions", (Bsz,)),
                    (rotary_positions, "rotary_positions", (Bsz, T)), (new_lens, "new_lens", (Bsz,)))
+        if dev_status is not None:
+            _need(dev_status, "dev_status", torch.int32, self.device)
         Hq = qs = qp = op = 0
         if q is not None:
             Hq = q.shape[2]
@@ -603,6 +605,8 @@ class PagedKVCache:
         width = block_table.shape[1]
         self._ints((block_table, "block_table", (Bsz, width)), (seq_lens, "seq_lens", (Bsz,)),
                    (draft_lens, "draft_lens", (Bsz,)))
+        if dev_status is not None:
+            _need(dev_status, "dev_status", torch.int32, self.device)
         if mask is not None:
             if mask.get_device() != index or mask.dtype is not torch.int64 or not mask.is_contiguous():
                 _need(mask, "mask", torch.int64, self.device)
@@ -646,6 +650,8 @@ class PagedKVCache:
         width = block_table.shape[1]
         self._ints((keep, "keep", (Bsz, K)), (keep_lens, "keep_lens", (Bsz,)), (block_table, "block_table", (Bsz, width)),
                    (first, "first", (Bsz,)))
+        if dev_status is not None:
+            _need(dev_status, "dev_status", torch.int32, self.device)
         with self._on_device():
             B.keep_tokens(self._desc, Bsz, K, keep.data_ptr(), _ptr(keep_lens), block_table.data_ptr(), width,
                           first.data_ptr(), _ptr(dev_status), self._launch_stream(stream))

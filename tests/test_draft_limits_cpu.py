@@ -254,3 +254,16 @@ def test_tables_of_2_31_tokens_are_refused():
     for call in (rotary, keep):
         refused(call(max_pages=1 << 27), B.ERR_UNSUPPORTED)
         call(batch=0, max_pages=(1 << 27) - 1)()
+
+
+def test_status_words_are_checked(cache):
+    # what the kernels write to is a word on the cache's device
+    table, pos, word = i32(3, 4), i32(3), torch.zeros(1, dtype=torch.int64)
+    k = f16(3, 5, 2, 64)
+    for call in (lambda w: cache.rotary_append(None, k, k, torch.zeros(50, 64), table, pos, dev_status=w),
+                 lambda w: cache.tree_attention(f16(3, 5, 4, 64), table, pos, dev_status=w),
+                 lambda w: cache.keep_tokens(i32(3, 5), None, table, pos, dev_status=w)):
+        with pytest.raises(TypeError):
+            call(word)
+        with pytest.raises(ValueError):
+            call(torch.zeros(1, dtype=torch.int32, device="meta"))

@@ -145,3 +145,15 @@ def test_threads_take_turns_on_a_workspace():
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_status_words_elsewhere_are_refused():
+    # (the kernels would write to the host's memory)
+    s = Step("bf16", 2, 3, 64, 16, 3, 4, 32, True, 7)
+    table, pos = int_dev(s.table), int_dev(s.pos)
+    for word, error in ((torch.zeros(1, dtype=torch.int32), ValueError), (torch.zeros(1, dtype=torch.int64, device="cuda"), TypeError)):
+        for call in (lambda: s.cache.rotary_append(s.q, s.k, s.v, s.cs_dev, table, pos, dev_status=word),
+                     lambda: s.cache.tree_attention(s.q.contiguous(), table, pos, dev_status=word),
+                     lambda: s.cache.keep_tokens(int_dev([[0]] * 3), None, table, pos, dev_status=word)):
+            with pytest.raises(error):
+                call()

@@ -133,7 +133,7 @@ def torch_calls():
             spec.loader.exec_module(module)
             L = lib()
             module.bind(*(ctypes.cast(f, c_void_p).value
-                          for f in (L.pkv_rotary_append, L.pkv_tree_attention, L.pkv_keep_tokens)))
+                          for f in (L.pkv_rotary_append, L.pkv_tree_attention, L.pkv_keep_tokens)), PkvError)
             _torch_calls = module
     return _torch_calls or None
 

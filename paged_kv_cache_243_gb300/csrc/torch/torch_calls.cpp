@@ -23,6 +23,7 @@ namespace {
 decltype(&pkv_rotary_append) rotary_append_fn = nullptr;
 decltype(&pkv_tree_attention) tree_attention_fn = nullptr;
 decltype(&pkv_keep_tokens) keep_tokens_fn = nullptr;
+PyObject* error_type = nullptr;   // error_type(status, where)
 
 // What a cache keeps for these calls.
 struct Handle {
@@ -93,9 +94,12 @@ int64_t token_stride(const at::Tensor& t, int64_t rows, int64_t tokens, int64_t 
 }
 
 // A call that failed on the way to the device cannot be made again as if it had not begun.
-PyObject* not_ok(pkv_status st) {
+PyObject* not_ok(pkv_status st, const char* where) {
   if (st != PKV_ERR_CUDA) return decline();
-  PyErr_SetString(PyExc_RuntimeError, "a CUDA call or launch failed");
+  PyObject* e = PyObject_CallFunction(error_type, "is", (int)st, where);
+  if (!e) return nullptr;
+  PyErr_SetObject(error_type, e);
+  Py_DECREF(e);
   return nullptr;
 }
 
@@ -137,7 +141,7 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         data<float>(cs), (int32_t)cs->size(0), (int32_t)cs->size(1), a[9] == Py_True, data<int32_t>(turns),
         data<int32_t>(table), (int32_t)tab[1], data<int32_t>(pos), data<int32_t>(lens), data<void>(out),
         data<int32_t>(status), c10::cuda::getCurrentCUDAStream(h->device).stream());
-    if (st != PKV_OK) return not_ok(st);
+    if (st != PKV_OK) return not_ok(st, "rotary_append");
     if (!made.defined()) return Py_NewRef(a[10]);
     return THPVariable_Wrap(made);
   } catch (...) {
@@ -193,6 +197,15 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                     c10::Device(c10::kCUDA, h->device), std::nullopt);
       out = &made;
     }
+    // (nothing that could throw while the lock is held)
+    const void* const q_at = data<void>(q);
+    const int32_t *const table_at = data<int32_t>(table), *const lens_at = data<int32_t>(lens),
+                  *const drafts_at = data<int32_t>(drafts);
+    const int64_t* const mask_at = data<int64_t>(mask);
+    void *const out_at = data<void>(out), *const ws_at = ws.data_ptr();
+    int32_t* const status_at = data<int32_t>(status);
+    const size_t ws_bytes = ws.nbytes();
+    const int one_mask = mask && mask->dim() == 2;
     // threads take turns: a call's two launches follow one another on the stream
     PyObject* got = PyObject_CallOneArg(h->acquire, Py_False);
     if (!got) return nullptr;
@@ -200,13 +213,12 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_DECREF(got);
     if (!mine) return decline();
     const pkv_status st = tree_attention_fn(
-        h->cache, (int32_t)B, (int32_t)T, (int32_t)Hq, data<void>(q), qt, (float)scale, data<int32_t>(table), (int32_t)tab[1],
-        data<int32_t>(lens), data<int32_t>(drafts), data<int64_t>(mask), mask && mask->dim() == 2, data<void>(out), ot,
-        (int32_t)splits, ws.data_ptr(), (size_t)ws.nbytes(), data<int32_t>(status), stream);
+        h->cache, (int32_t)B, (int32_t)T, (int32_t)Hq, q_at, qt, (float)scale, table_at, (int32_t)tab[1], lens_at, drafts_at,
+        mask_at, one_mask, out_at, ot, (int32_t)splits, ws_at, ws_bytes, status_at, stream);
     PyObject* done = PyObject_CallNoArgs(h->release);
     if (!done) return nullptr;
     Py_DECREF(done);
-    if (st != PKV_OK) return not_ok(st);
+    if (st != PKV_OK) return not_ok(st, "tree_attention");
     if (!made.defined()) return Py_NewRef(a[7]);
     return THPVariable_Wrap(made);
   } catch (...) {
@@ -234,7 +246,7 @@ PyObject* keep_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const pkv_status st = keep_tokens_fn(h->cache, (int32_t)B, (int32_t)K, data<int32_t>(keep), data<int32_t>(lens),
                                          data<int32_t>(table), (int32_t)tab[1], data<int32_t>(first), data<int32_t>(status),
                                          c10::cuda::getCurrentCUDAStream(h->device).stream());
-    if (st != PKV_OK) return not_ok(st);
+    if (st != PKV_OK) return not_ok(st, "keep_tokens");
     Py_RETURN_NONE;
   } catch (...) {
     PyErr_Clear();
@@ -258,16 +270,18 @@ PyObject* handle(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return c;
 }
 
-// addresses of the library's entry points, in the order below
+// addresses of the library's entry points, in the order below, and the type of its errors
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 3) {
-    PyErr_SetString(PyExc_TypeError, "bind(rotary_append, tree_attention, keep_tokens)");
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "bind(rotary_append, tree_attention, keep_tokens, error)");
     return nullptr;
   }
   rotary_append_fn = reinterpret_cast<decltype(rotary_append_fn)>(PyLong_AsVoidPtr(a[0]));
   tree_attention_fn = reinterpret_cast<decltype(tree_attention_fn)>(PyLong_AsVoidPtr(a[1]));
   keep_tokens_fn = reinterpret_cast<decltype(keep_tokens_fn)>(PyLong_AsVoidPtr(a[2]));
   if (PyErr_Occurred()) return nullptr;
+  Py_XDECREF(error_type);
+  error_type = Py_NewRef(a[3]);
   Py_RETURN_NONE;
 }
 

@@ -157,3 +157,29 @@ def test_status_words_elsewhere_are_refused():
                      lambda: s.cache.keep_tokens(int_dev([[0]] * 3), None, table, pos, dev_status=word)):
             with pytest.raises(error):
                 call()
+
+
+def test_a_failed_launch_is_an_error_of_the_library():
+    # the entry points' place is taken by one that reports a failed launch
+    import ctypes
+    from paged_kv_cache_243_gb300 import binding as B
+    s = Step("bf16", 2, 3, 64, 16, 3, 4, 32, True, 7)
+    table, pos = int_dev(s.table), int_dev(s.pos)
+    L, calls = B.lib(), s.cache._calls
+    q = s.q.contiguous()
+    s.cache.tree_attention(q, table, pos + 4)      # (makes the workspace)
+    fails = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: 4)
+    at = [ctypes.cast(f, ctypes.c_void_p).value for f in (L.pkv_rotary_append, L.pkv_tree_attention, L.pkv_keep_tokens)]
+    torch.cuda.synchronize()
+    calls.bind(*[ctypes.cast(fails, ctypes.c_void_p).value] * 3, B.PkvError)
+    try:
+        for call, name in ((lambda: s.cache.rotary_append(s.q, s.k, s.v, s.cs_dev, table, pos), "rotary_append"),
+                           (lambda: s.cache.tree_attention(q, table, pos + 4), "tree_attention"),
+                           (lambda: s.cache.keep_tokens(int_dev([[0]] * 3), None, table, pos), "keep_tokens")):
+            with pytest.raises(B.PkvError) as e:
+                call()
+            assert e.value.status == 4 and str(e.value).startswith(name)
+    finally:
+        calls.bind(*at, B.PkvError)
+    s.cache.tree_attention(q, table, pos + 4)      # (no lock was kept)
+    torch.cuda.synchronize()

@@ -131,3 +131,35 @@ def test_steps_on_a_per_group_cache():
             assert np.array_equal(int8_codes(got), c)
             sz = s.cache.kv_sz.cpu().numpy()[s.table[b, :sc.shape[0]], :, 0]
             assert np.array_equal(sz[..., 0], sc) and np.array_equal(sz[..., 1], z)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "i8t"])
+def test_pools_beyond_32_bits(kind):
+    # the last pages of pools of more than 4 GiB (and 2^31 values) hold the same as a small pool's
+    from paged_kv_cache_243_gb300 import rotary_table
+    from paged_kv_cache_243_gb300.cache import PagedKVCache
+    kv_dtype, quant, src = KINDS[kind]
+    B, T, hkv, g, d, ps, width = 2, 12, 8, 4, 128, 16, 20
+    pages = (4 << 30) // (hkv * ps * d * (1 if quant != "none" else 2)) + 500
+    rng = np.random.default_rng(86)
+    draw = lambda n, h: to_dev(synth.round_to_dtype(rng.standard_normal((B, n, h, d)).astype(np.float32), src)[0], src)
+    prompt, drafts = [draw(200, h) for h in (hkv * g, hkv, hkv)], [draw(T, h) for h in (hkv * g, hkv, hkv)]
+    table = rng.permutation(B * width).reshape(B, width)
+    cs, base, keep = rotary_table(ps * width, d), int_dev([200, 200]), int_dev([[1, 2, 6, 11]] * B)
+    got = []
+    for n in (B * width, pages):
+        cache = PagedKVCache(n, ps, hkv, d, kv_dtype=kv_dtype, quant=quant, with_meta=True)
+        rows = int_dev(table + n - B * width)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        cache.rotary_append(*prompt, cs, rows, base - 200, dev_status=status)
+        q = cache.rotary_append(*drafts, cs, rows, base, dev_status=status)
+        out = cache.tree_attention(q, rows, base + T, dev_status=status)
+        cache.keep_tokens(keep, None, rows, base, dev_status=status)
+        after = cache.tree_attention(q[:, :4].contiguous(), rows, base + 4, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        got.append((q, out, after, cache.page_meta[rows.long()][:, :204 // ps].clone()))
+        del cache
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    torch.cuda.empty_cache()

@@ -80,9 +80,11 @@
 //   Records are laid out for 32 rows at a time, channel by channel, so that a thread that has a row writes, and the
 //     merge reads, 128 bytes together.
 //   Measured (both launches, d = 128, back to back): 4 x 32K, 13 drafts, 32 kv heads, f16 262 us, 6.7 TB/s; 24 x 8K,
-//     64 drafts of 32 heads over 8, bf16 148 to 155 us, 1.0 PFLOP/s; 8 x 4K, 16 drafts 29 us; 16 x 8K, 24 drafts, INT8
-//     100 us. A visit of two row tiles takes 3700 cycles, of which the products are 2180: the chain of an event is
-//     maximum 530, reference 150, weights 1130, then P V and S of 1090 and 700 of hand-over.
+//     64 drafts of 32 heads over 8, bf16 149 to 157 us, 1.0 PFLOP/s; 8 x 4K, 16 drafts 29.7 us; 16 x 8K, 24 drafts, INT8
+//     100 us. A visit of two row tiles takes 3970 cycles, of which the products are 2050: the chain of an event is
+//     maximum 500, reference 150, weights 1070, then P V and S and their hand-over 1470 to 2000. Shared memory is wanted for
+//     2050 as well: S takes 128 bytes a cycle of operands, all there is, P V half as much, and copies 64 KB. INT8's
+//     event: 2740, 240 and 2540, the latency of the scales' loads (1024 of shared memory's 3700 cycles a visit).
 //
 // Code size is a cost of its own: the two SMs of a pair share an instruction cache, and
 // 155 KB of code took 16 rows x 32K from 97 to 117 us. So loops stay loops, waits and plans
@@ -2010,8 +2012,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               tc_wait_st();
             }
             float mx = -INFINITY;
-            // Scales of 8 tokens are loaded while the scores, or those before, are on their way. (16 x 8K INT8 with 24 drafts:
-            // 4, 8, 16 tokens ahead, none: 123, 112, 121, 123 us; more of them do not fit 96 registers.)
+            // Scales of 8 tokens are loaded while the scores, or those before, are on their way. (A step of 16 x 8K INT8 with 24
+            // drafts, 4, 8, 16 tokens ahead: 116, 105, 106 us; more of them do not fit 96 registers.)
             constexpr int PRE = 4;
             [[maybe_unused]] ulonglong2 k2[PRE];
             [[maybe_unused]] auto scales = [&](int at) {

@@ -116,6 +116,37 @@ def test_long_contexts():
     tb.tree_check(tb.tree_run(q), qf, 4)
 
 
+@pytest.mark.parametrize("kind,T,g", [("bf16", 5, 2), ("i8t", 5, 2), ("bf16", 40, 4), ("u4t", 40, 4)])
+def test_more_tokens_than_a_float_counts(kind, T, g):
+    # 2^24 tokens and more, 64 pages of context over and over; each of its tokens weighs as often as it comes
+    times, ps, d, pages, tail = 16500, 16, 64, 64, 77
+    tb = TreeBatch(kind, 1, d, ps, [pages * ps + tail], T, seed=T)
+    L = pages * ps * times + tail
+    assert L > 1 << 24
+    table = int_dev(np.concatenate([np.tile(tb.table[0, :pages], times), tb.table[0, pages:]])[None])
+    q, qf = tb.tree_queries(g)
+    out = tb.cache.tree_attention(q, table, int_dev([L]), tb.mask, dev_status=tb.status)
+    torch.cuda.synchronize()
+    assert int(tb.status.item()) == 0
+    n, k, v, on = pages * ps, tb.k[0][:, 0], tb.v[0][:, 0], tb.attends(0)
+    often = np.where(np.arange(n + tail) < n, float(times), 1.0)
+    got = out.cpu().numpy().astype(np.float64)[0]
+    sm, half = 1.0 / np.sqrt(d), torch.finfo(TORCH[tb.src]).eps / 2
+    for h in range(g):
+        qq = qf[0, :, h].astype(np.float64)
+        w = np.where(on, np.exp(sm * (qq @ k.T)), 0.0) * often
+        w /= w.sum(1, keepdims=True)
+        want, mass = w @ v, w @ np.abs(v) + tb.vmid[0]
+        # the bound of TreeBatch.tree_expected, but for the sums: a block, of a hundred at least, adds up
+        # its own tokens, 16 at a time
+        most = (np.abs(qq) @ np.abs(k).T).max(1) + 2 * np.abs(qq).sum(1) * tb.kmid[0]
+        rel = 2 * np.expm1(sm * (d + 8) * 2.0 ** -23 * most) + 2.0 ** -20 + (L / 1600 + 64) * 2.0 ** -23 + half * half
+        if tb.src == "f16":
+            rel = rel + 2.0 ** -24      # fp16's smallest step beside weights of 2^7 and more
+        err = np.abs(got[:, h] - want)
+        assert (err <= rel[:, None] * mass).all(), (err.max(), (rel[:, None] * mass).min())
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(3)
     lens = rng.integers(0, 60, 1024)

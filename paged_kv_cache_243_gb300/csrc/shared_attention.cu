@@ -335,7 +335,7 @@ pkv_status launch_tree(const TreeArgs& a) {
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
   const long long items = (long long)a.batch * c->num_kv_heads * (p.rec_rows / 32) * (D / 16);
   // Where the warps are few, a block's four share an item's records, which come from memory one after the other. (Four and
-  // one: 8 x 4K with 24 drafts of 4 heads 29.9 and 33.8 us, 4 x 32K with 8 drafts of 32 kv heads 263 and 266; with more items than that
+  // one: 8 x 4K with 16 drafts of 4 heads 29.9 and 33.8 us, 4 x 32K with 13 drafts of 32 kv heads 263 and 266; with more items than that
   // they only wait for one another: 24 x 8K with 64 drafts 159.6 and 149.9.)
   const int wpw = items < 8ll * dev.sms ? 4 : 1, per = 4 / wpw;
   const void* merge = D == 64 ? tree_merge<64>(wpw) : tree_merge<128>(wpw);

@@ -101,15 +101,16 @@ typedef enum {
  *                      Restoration: x = u * scale + zero, u the stored byte
  *                      (I8: u = code + 128 in [0, 255]; U4: u in [0, 15]).
  *   tail             : PER_GROUP64 only, fp32
- *                      [tail_rows][num_kv_heads][2 (K, V)][2 (group parity)][64][head_dim]:
- *                      original values of each sequence's open (partially filled)
- *                      64-token group, kept so that every append re-quantises
- *                      the open group from its members. Row b belongs to batch
+ *                      [tail_rows][num_kv_heads][2 (K, V)][2 places][64][head_dim]:
+ *                      original values of two groups of each sequence: the open
+ *                      (partially filled) one, kept so that every append re-quantises
+ *                      the open group from its members, and the tokens before the last
+ *                      append of the group that it began in. Row b belongs to batch
  *                      row b of kv_append. Contents are managed by kv_append; a
  *                      new row is zero-filled, or begins with a sequence's token 0.
- *                      Place 63 never holds originals (a full group is closed):
+ *                      The last of the 64 is never an original (a full group is closed):
  *                      its first 4 bytes are the int32 position at which the
- *                      originals kept in that parity end (0: none).
+ *                      originals kept in that place end (0: none), which tells the group.
  *   page_meta        : optional (NULL = no sparse metadata), fp32
  *                      [num_pages][num_kv_heads][2][head_dim]: per channel, the
  *                      minimum (row 0) and maximum (row 1) of the page's valid
@@ -162,9 +163,11 @@ void pkv_tuning_reload(void);
  * F16/BF16 caches store the values (converted to kv_dtype). INT8 caches
  * quantise: per token over head_dim values; per group over the group's
  * members, re-quantising the open group from the originals kept in `tail`
- * (closed groups never change). Where a sequence goes on inside a group whose
- * originals its row does not hold (forked inside a closed group, cut back by more
- * than a group), the earlier members are what their stored codes say, at the
+ * (closed groups never change). A sequence may be cut back to where its last append
+ * began, or further within that group, however many tokens that append had: the
+ * originals are there. Where it goes on inside a group whose originals its row does
+ * not hold (forked inside a closed group, cut back by several appends and more than
+ * a group), the earlier members are what their stored codes say, at the
  * cost of one more rounding. If page_meta is set, the bounding box of every
  * page the append touched is recomputed from the stored keys.
  * Quantiser (bit-exact definition, fp32 ops, ties to even):
@@ -587,7 +590,9 @@ size_t pkv_tree_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t t
  *   first     : int32 [batch], the tokens before the drafts.
  * Pages that it writes are the sequence's own (pkv_alloc_unshare). PER_GROUP64 is
  * PKV_ERR_UNSUPPORTED: codes of another group's scale cannot be moved; append the accepted tokens
- * anew with pkv_kv_append at first[b], which goes on from the originals of the open group.
+ * anew (the same call that appended the drafts, with new_lens) at first[b]. Where one append brought
+ * all the drafts, of any number, it goes on from the originals of the group that first[b] is in; drafts
+ * of several appends may reach no further than the group behind that one.
  * Pools of 2^31 rows (num_pages * num_kv_heads * page_size) or more, and tables of 2^31 tokens
  * (max_pages * page_size), are PKV_ERR_UNSUPPORTED.
  * One launch. An attention call right behind this one may not promise fresh_rows, nor a

@@ -640,7 +640,8 @@ class PagedKVCache:
                     stream: Optional[torch.cuda.Stream] = None) -> None:
         """Token first[b] + keep[b][j] of row b becomes token first[b] + j, for j < keep_lens[b] (by default
         all of keep [B][K], strictly ascending): of the drafts from first[b] on the accepted
-        path stays. Not for per-group caches: append the accepted tokens anew at first[b]."""
+        path stays. Not for per-group caches: append the accepted tokens anew at first[b] (drafts that one
+        append brought leave nothing behind there, see pkv_keep_tokens in include/pkv.h)."""
         if stream is None and self._native is not None and \
                 self._calls.keep_tokens(self._native, keep, keep_lens, block_table, first, dev_status) is not NotImplemented:
             return

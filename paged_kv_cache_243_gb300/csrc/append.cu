@@ -234,16 +234,33 @@ __global__ void __launch_bounds__(256) append_per_token_kernel(const AppendParam
   }
 }
 
-__device__ __forceinline__ float* tail_row(const AppendParams& p, int b, int g, int kv, int parity) {
-  return p.tail + ((((size_t)b * p.num_kv_heads + g) * 2 + kv) * 2 + parity) * 64 * p.head_dim;
+__device__ __forceinline__ float* tail_row(const AppendParams& p, int b, int g, int kv, int place) {
+  return p.tail + ((((size_t)b * p.num_kv_heads + g) * 2 + kv) * 2 + place) * 64 * p.head_dim;
 }
 
-// Which tokens' originals a row holds: the last of a group's 64 places is never needed (a group of
-// 64 is closed), so its first word holds the position at which they end; they begin where that
-// position's group does. 0: none. It shows when a sequence goes on inside a group whose originals
-// the row does not have, as after a fork inside a closed group.
-__device__ __forceinline__ int32_t* tail_end(const AppendParams& p, int b, int g, int kv, int parity) {
-  return reinterpret_cast<int32_t*>(tail_row(p, b, g, kv, parity) + 63 * p.head_dim);
+// Which tokens' originals one of a row's two places holds: the last of a group's 64 tokens is never
+// needed (a group of 64 is closed), so its first word holds the position at which they end; they
+// begin where that position's group does. 0: none. It shows when a sequence goes on inside a group whose
+// originals the row does not have, as after a fork inside a closed group.
+__device__ __forceinline__ int32_t* tail_end(const AppendParams& p, int b, int g, int kv, int place) {
+  return reinterpret_cast<int32_t*>(tail_row(p, b, g, kv, place) + 63 * p.head_dim);
+}
+
+// A group's place is that of its parity, but for one: an append that begins inside a group leaves that
+// group's earlier tokens where they are, as the sequence may be cut back to where the append began
+// (drafts that are rejected), and the group that it leaves open goes to the other place.
+__device__ __forceinline__ bool ends_in(int end, int gi) { return end > gi * 64 && end < gi * 64 + 64; }
+// Whether group gi, in which an append begins behind earlier tokens, has them in the place of the other parity, where `own`
+// is the end in its parity's place. (Both ends loaded at once, whatever the first one says: one token for each of 64 rows x 8
+// heads 6.6 -> 7.3 us.)
+__device__ __forceinline__ bool is_moved(int gi, int own, const int32_t* other) {
+  return !ends_in(own, gi) && ends_in(__ldcg(other), gi);
+}
+// Group gi has no originals in this place any more. (Another block may have given the place to
+// another group since.)
+__device__ __forceinline__ void forget_group(int32_t* at, int gi) {
+  const int end = *at;
+  if (ends_in(end, gi)) atomicCAS(at, end, 0);
 }
 
 // Per-64-token-group INT8. grid (group slot, kv head * 2 + kv, row); one block
@@ -273,8 +290,11 @@ __global__ void __launch_bounds__(kGroupThreads, ROTATED ? 2 : 4) append_per_gro
   const int t_end = min(t0 + 64, pos + n);
   const int nf = (t_end - t0) * D / 4;      // float4s of the group
   const void* sp = kv ? p.v_new : p.k_new;
+  // (where earlier tokens are but for the rarest of cases: loaded before it is known)
   const float* tl = tail_row(p, b, g, kv, gi & 1);
-  const int had = pos > t0 ? *tail_end(p, b, g, kv, gi & 1) : pos;
+  const int g0 = pos / 64;
+  const bool inside = pos % 64 != 0;
+  const int own = inside ? *tail_end(p, b, g, kv, g0 & 1) : 0;
   float4 x[kGroupVec4];
 #pragma unroll
   for (int k = 0; k < kGroupVec4; ++k) {
@@ -288,7 +308,18 @@ __global__ void __launch_bounds__(kGroupThreads, ROTATED ? 2 : 4) append_per_gro
   }
   if (threadIdx.x == 0) ok_s = page_of(p, b, page_div(p, t0));
   const int off0 = page_mod(p, t0);
-  const bool lost = had < pos || had > t0 + 63;   // uniform over the block
+  // (uniform over the block)
+  const bool moved = inside && is_moved(g0, own, tail_end(p, b, g, kv, ~g0 & 1));
+  bool lost = pos > t0 && (own < pos || own > t0 + 63);
+  if (moved && pos > t0) {
+    lost = __ldcg(tail_end(p, b, g, kv, ~gi & 1)) < pos;
+    tl = tail_row(p, b, g, kv, ~gi & 1);
+#pragma unroll
+    for (int k = 0; k < kGroupVec4; ++k) {
+      const int f = threadIdx.x + k * kGroupThreads;
+      if (f < (pos - t0) * D / 4) x[k] = __ldcg(reinterpret_cast<const float4*>(tl + 4 * f));   // (not to be merged with the loads above)
+    }
+  }
   if (lost) {
     const int phys = p.block_table[(size_t)b * p.max_pages + page_div(p, t0)];
     if (phys >= 0 && phys < p.num_pages) {
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(kGroupThreads, ROTATED ? 2 : 4) append_per_gro
         if (f < (pos - t0) * D / 4) {
           const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + 4 * f);
           x[k] = make_float4(value(w, 0), value(w, 1), value(w, 2), value(w, 3));
-          *reinterpret_cast<float4*>(tail_row(p, b, g, kv, gi & 1) + 4 * f) = x[k];
+          *reinterpret_cast<float4*>(tail_row(p, b, g, kv, (gi & 1) ^ moved) + 4 * f) = x[k];
         }
       }
     }
@@ -339,8 +370,10 @@ __global__ void __launch_bounds__(kGroupThreads, ROTATED ? 2 : 4) append_per_gro
   const float rs = quant_recip(s);
   uint8_t* dst = reinterpret_cast<uint8_t*>(kv ? p.v_pages : p.k_pages) +
                 (((size_t)phys * H + g) * p.page_size + off0) * D;
-  float* tw = tail_row(p, b, g, kv, gi & 1);
   const bool keep = write_tail && t_end - t0 < 64;
+  // (with write_tail there is one group behind the first at most, of the other parity)
+  const int place = (gi & 1) ^ moved;
+  float* tw = tail_row(p, b, g, kv, place);
 #pragma unroll
   for (int k = 0; k < kGroupVec4; ++k) {
     const int f = threadIdx.x + k * kGroupThreads;
@@ -359,11 +392,11 @@ __global__ void __launch_bounds__(kGroupThreads, ROTATED ? 2 : 4) append_per_gro
     szp[kv * 2 + 1] = z;
     // (without write_tail the tail kernel has the last word on a group that stays open; originals
     // of another group that this one did not overwrite stay)
-    int32_t* const ends = tail_end(p, b, g, kv, gi & 1);
-    if (keep || pos > t0)
-      *ends = keep ? t_end : pos;
-    else if (*ends > t0 && *ends < t0 + 64)
-      *ends = 0;
+    if (keep || pos > t0) *tail_end(p, b, g, kv, place) = keep ? t_end : pos;
+    if (!keep) {   // nothing is left of what the group had before
+      if (pos <= t0) forget_group(tail_end(p, b, g, kv, place), gi);
+      forget_group(tail_end(p, b, g, kv, 1 - place), gi);
+    }
   }
 }
 
@@ -392,8 +425,6 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_group_bulk_kernel(con
   const uint16_t* ks = reinterpret_cast<const uint16_t*>(p.k_new);
   const uint16_t* vs = reinterpret_cast<const uint16_t*>(p.v_new);
   uint2 kr[NV], vr[NV];
-  int32_t* const ends = threadIdx.x < 2 ? tail_end(p, b, g, threadIdx.x, gi & 1) : nullptr;
-  const int had = ends ? *ends : 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int f = threadIdx.x + k * kGroupThreads;
@@ -465,7 +496,7 @@ __global__ void __launch_bounds__(kGroupThreads, 4) append_group_bulk_kernel(con
     *reinterpret_cast<float4*>(szp) = make_float4(sk, kmn, sv, vmn);
   }
   // originals of this group's earlier contents (the open group's are kept by the tail kernel, after this one)
-  if (had > t0 && had < t0 + 64) *ends = 0;
+  if (threadIdx.x < 4) forget_group(tail_end(p, b, g, threadIdx.x >> 1, threadIdx.x & 1), gi);
 }
 
 // Keeps the new members of each row's open group (appends longer than one
@@ -484,8 +515,13 @@ __global__ void append_tail_kernel(const AppendParams p) {
   const int gi = (end - 1) / 64, t0 = gi * 64;
   const int first = max(t0, pos);
   const void* sp = kv ? p.v_new : p.k_new;
-  float* tw = tail_row(p, b, g, kv, gi & 1);
-  if (threadIdx.x == 0) *tail_end(p, b, g, kv, gi & 1) = end;
+  const int g0 = pos / 64;
+  const bool inside = pos % 64 != 0;
+  const bool moved = inside && is_moved(g0, *tail_end(p, b, g, kv, g0 & 1), tail_end(p, b, g, kv, ~g0 & 1));
+  const int place = (inside && gi != g0 ? ~g0 & 1 : gi & 1) ^ moved;   // see above
+  float* tw = tail_row(p, b, g, kv, place);
+  __syncthreads();   // every thread has read the ends
+  if (threadIdx.x == 0) *tail_end(p, b, g, kv, place) = end;
   if constexpr (ROTATED) {
     for (int i = 4 * threadIdx.x; i < (end - first) * D; i += 4 * blockDim.x) {
       const int tt = i / D, e = i - tt * D, tok = first + tt;

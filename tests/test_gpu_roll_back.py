@@ -1,0 +1,131 @@
+"""Per-group INT8 caches: drafts stored by one append, however many, and the accepted ones appended anew
+where they began. What the sequence had before its drafts is quantised from its originals again: the
+rejected drafts leave nothing behind, codes and scales are those of the sequence written at once."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from helpers import int8_codes
+from shared_batch import int_dev, to_dev
+from test_gpu_rotary import rotated
+
+pytestmark = pytest.mark.gpu
+
+H, PS, WIDTH = 2, 64, 20
+
+
+class Sequences:
+    def __init__(self, d, rows, seed, rot=0):
+        from paged_kv_cache_243_gb300.cache import PagedKVCache, rotary_table
+        self.d, self.B, self.rot, self.rng = d, rows, rot, np.random.default_rng([94, seed])
+        self.cache = PagedKVCache(rows * WIDTH, PS, H, d, kv_dtype="int8", quant="per_group64", tail_rows=rows, poison=True)
+        self.table = self.rng.permutation(rows * WIDTH).reshape(rows, WIDTH).astype(np.int32)
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        if rot:
+            self.cs_dev = rotary_table(PS * WIDTH, rot)
+            self.cs = self.cs_dev.cpu().numpy()
+        self.held = [[np.zeros((0, H, d), np.float32)] * 2 for _ in range(rows)]   # K (rotated) and V
+
+    def tokens(self, n, scale=1.0):
+        """Bits and values [2][B][n][H][d]."""
+        return synth.round_to_dtype((scale * self.rng.standard_normal((2, self.B, n, H, self.d))).astype(np.float32), "f16")
+
+    def append(self, bits, val, pos, lens, keep=True):
+        """The first lens[b] of the tokens to row b at pos[b]; with keep they are what the row holds from there."""
+        k, v = (to_dev(x, "f16") for x in bits)
+        if self.rot:
+            self.cache.rotary_append(None, k, v, self.cs_dev, int_dev(self.table), int_dev(pos), new_lens=int_dev(lens),
+                                     dev_status=self.status)
+        else:
+            self.cache.append(k, v, int_dev(self.table), int_dev(pos), int_dev(lens), dev_status=self.status)
+        if keep:
+            kv = (rotated(val[0], self.cs[pos[:, None] + np.arange(val.shape[2])], False) if self.rot else val[0], val[1])
+            for b in range(self.B):
+                self.held[b] = [np.concatenate([h[:pos[b]], x[b, :lens[b]]]) for h, x in zip(self.held[b], kv)]
+
+    def check(self):
+        torch.cuda.synchronize()
+        assert int(self.status.item()) == 0
+        sz = self.cache.kv_sz.cpu().numpy()
+        for i, pool in enumerate((self.cache.k_pages.cpu().numpy(), self.cache.v_pages.cpu().numpy())):
+            for b in range(self.B):
+                x = self.held[b][i]
+                t = np.arange(len(x))
+                codes, scale, zero = oracle.quantize_per_group(x)
+                pages = self.table[b, :scale.shape[0]]
+                assert np.array_equal(sz[pages, :, 0, 2 * i], scale) and np.array_equal(sz[pages, :, 0, 2 * i + 1], zero), (i, b)
+                assert np.array_equal(int8_codes(pool[self.table[b, t // PS], :, t % PS]), codes), (i, b)
+
+
+@pytest.mark.parametrize("rot", [0, 64])
+@pytest.mark.parametrize("d,T", [(64, 66), (64, 100), (128, 129), (64, 200), (128, 256)])
+def test_rejected_drafts_leave_nothing(d, T, rot):
+    # rows that begin at every kind of place of a group, 255 drafts and more reaching the fifth group
+    s = Sequences(d, 6, T + rot, rot)
+    base = np.array([37, 63, 65, 64, 1, 127])
+    prompt = s.tokens(127)
+    s.append(*prompt, np.zeros(6, np.int64), base)
+    s.check()
+    for step, n in enumerate(([3, 1, 0, 20, 2, 5], [64, 30, 7, 66, 0, 1], [1] * 6)):
+        bits, val = s.tokens(T)
+        n = np.array(n)
+        loud = np.arange(T)[None] >= n[:, None]            # the drafts that will be rejected
+        bits, val = synth.round_to_dtype(val * np.where(loud, 60.0, 1.0).astype(np.float32)[None, :, :, None, None], "f16")
+        s.append(bits, val, base, np.full(6, T), keep=False)
+        s.append(bits, val, base, n)
+        base = base + n
+        if n.all():
+            s.check()
+    s.check()
+
+
+def test_drafts_again_and_again_before_anything_is_kept():
+    # the same place several times, with drafts of other lengths; and then from a place before it
+    s = Sequences(64, 3, 7)
+    base = np.array([50, 127, 70])
+    s.append(*s.tokens(127), np.zeros(3, np.int64), base)
+    for T in (150, 256, 3, 90, 129):
+        s.append(*s.tokens(T, 30.0), base, np.full(3, T), keep=False)
+    s.append(*s.tokens(10), base, np.full(3, 10))
+    s.check()
+    base = base + 10
+    s.append(*s.tokens(140, 30.0), base, np.full(3, 140), keep=False)
+    s.append(*s.tokens(9), base - 5, np.full(3, 9))
+    s.check()
+
+
+def test_random_appends_and_returns():
+    # appends of every length that go on at the end, where the last one began, or inside the first or last group
+    # that it touched: the originals of all of these are there
+    s = Sequences(64, 4, 8)
+    pos, end = np.zeros(4, np.int64), np.zeros(4, np.int64)
+    for step in range(60):
+        at = end.copy()
+        for b in range(4):
+            how = s.rng.integers(4)
+            if how == 1:
+                at[b] = pos[b]
+            elif how == 2:
+                at[b] = s.rng.integers(pos[b] // 64 * 64, pos[b] + 1)
+            elif how == 3:
+                at[b] = s.rng.integers(max(pos[b], end[b] // 64 * 64), end[b] + 1)
+            if at[b] > 900:
+                at[b] = 0                                    # another sequence
+        n = s.rng.integers(1, [2, 40, 70, 300][step % 4], 4)
+        s.append(*s.tokens(int(n.max()) + 5 * (step % 3)), at, n)
+        pos, end = at, at + n
+        if step % 6 == 5:
+            s.check()
+    s.check()
+
+
+def test_a_chunked_prompt_on_every_grid():
+    # nothing is cut back: a prompt in pieces has the codes of one in one piece, as ever
+    s = Sequences(128, 2, 9, 64)
+    at = np.zeros(2, np.int64)
+    for n in (30, 100, 64, 130, 1, 200, 65, 190, 77):
+        s.append(*s.tokens(n), at, np.full(2, n))
+        at = at + n
+        s.check()

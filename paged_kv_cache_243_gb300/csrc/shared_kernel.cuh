@@ -1362,9 +1362,11 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
             // a pass is P V of an event and S of the stream's next one: between the weights' arrival and the next
             // scores lie just these products, everything else is done behind them or while the weights
             // are being made. (This warp's instructions are slow, fetched anew between those of the softmax.)
+            // With one row tile the scores of v go out before V of v - 2 is given back, which a ring of a single entry does not
+            // allow: the softmax takes the scores of v as the sign that it is (see begin below).
             const bool two = is_two(rows);
             const int inside = (two ? kFirst | kLast : kEarly | kLate) | 0xFF;
-            if (pend.on && !p.two_terms && (flags & inside) == kTile) {
+            if ((QUANT || S > 1) && pend.on && !p.two_terms && (flags & inside) == kTile) {
               const uint32_t hi_k = (uint32_t)(kmajor >> 32), hi_v = (uint32_t)(vmajor >> 32), lo_v = (uint32_t)vmajor;
               constexpr uint32_t is = kType | (uint32_t)(kTile / 8) << 17, io = kType | 1u << 16 | (uint32_t)(D / 8) << 17;
               auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
@@ -1725,8 +1727,9 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
         // rows of V that hold no token of this segment may hold anything, NaN
         // too, and a weight of 0 would not clear it
         const int slot = v % S;
-        // (a slot's parity tells its last two uses apart, and V of v - 2 is done with: with a
-        // single slot, v - 1 has to be done with, too)
+        // (A slot's parity tells its last two uses apart. With two slots and more the scores of v were issued behind
+        // the products of V of v - S at the latest. With a single slot they were issued behind V of v - 2 was
+        // given back, and V of v - 1 has to be, too: that barrier's parity then means v - 1, not v - 3.)
         if (S == 1 && v > 0 && !wait_warp(kBarVEmpty, (v - 1) & 1)) return false;
         if (!wait_warp(kBarVFull + slot, (v / S) & 1)) return false;
         if (row < (ntok + 15) / 16 * 16 && !valid) {

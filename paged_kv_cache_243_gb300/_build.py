@@ -2,7 +2,7 @@
 
 Each translation unit compiles in parallel; the shared library is relinked only
 when a source or header is newer than it. Beside it, where torch is installed with its
-headers: _pkv_torch.so, host code that makes some calls from torch tensors without Python.
+headers and CUDA libraries: _pkv_torch.so, host code that makes some calls from torch tensors without Python.
 """
 from __future__ import annotations
 
@@ -49,20 +49,25 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+_TORCH_LINKS = ("torch_python", "torch", "torch_cuda", "torch_cpu", "c10_cuda", "c10")
+
+
 def _torch_job(cuda: str):
-    """The command that builds TORCH_LIB; None where torch or the headers are not there."""
+    """The command that builds TORCH_LIB; None where torch, its headers or its CUDA libraries are not there."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
         return None
     home, python = spec.submodule_search_locations[0], sysconfig.get_paths()["include"]
     include, libs = os.path.join(home, "include"), os.path.join(home, "lib")
-    if not (os.path.exists(os.path.join(python, "Python.h")) and
-            os.path.exists(os.path.join(include, "torch", "csrc", "autograd", "python_variable.h")) and shutil.which("g++")):
+    needed = [os.path.join(python, "Python.h"), os.path.join(include, "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(include, "c10", "cuda", "CUDAStream.h"), os.path.join(cuda, "include", "cuda_runtime_api.h")] + \
+        [os.path.join(libs, f"lib{n}.so") for n in _TORCH_LINKS]
+    if not (all(map(os.path.exists, needed)) and shutil.which("g++")):
         return None
     paths = [INCLUDE, include, os.path.join(include, "torch", "csrc", "api", "include"), python, os.path.join(cuda, "include")]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for p in paths for x in ("-I", p)] + \
         [TORCH_SRC, "-o", TORCH_LIB + ".tmp", "-L", libs] + \
-        ["-l" + n for n in ("torch_python", "torch", "torch_cuda", "torch_cpu", "c10_cuda", "c10")]
+        ["-l" + n for n in _TORCH_LINKS]
 
 
 def build(verbose: bool = False, force: bool = False) -> str:

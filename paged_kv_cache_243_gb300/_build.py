@@ -1,8 +1,8 @@
 """Build libpkv.so in-tree with nvcc for sm_103a (no torch extension machinery).
 
 Each translation unit compiles in parallel; the shared library is relinked only
-when a source or header is newer than it. Beside it, where torch is installed with its
-headers and CUDA libraries: _pkv_torch.so, host code that makes some calls from torch tensors without Python.
+when a source or header is newer than it. Beside it, where torch is installed with its headers
+and CUDA libraries: torch_library(), host code that makes some calls from torch tensors without Python.
 """
 from __future__ import annotations
 
@@ -10,6 +10,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,7 +23,6 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
 TORCH_SRC = os.path.join(CSRC, "torch", "torch_calls.cpp")
-TORCH_LIB = os.path.join(OUT_DIR, "_pkv_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,25 +49,35 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def torch_library(version: str) -> str:
+    """Where the module for this torch and this Python is: it has the layouts of both compiled in."""
+    return os.path.join(OUT_DIR, f"_pkv_torch.{version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
 _TORCH_LINKS = ("torch_python", "torch", "torch_cuda", "torch_cpu", "c10_cuda", "c10")
 
 
 def _torch_job(cuda: str):
-    """The command that builds TORCH_LIB; None where torch, its headers or its CUDA libraries are not there."""
+    """(the command that builds the module for the torch that is installed, with ".tmp" behind its name; that name). None
+    where torch, its headers or its CUDA libraries are not there."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
         return None
     home, python = spec.submodule_search_locations[0], sysconfig.get_paths()["include"]
     include, libs = os.path.join(home, "include"), os.path.join(home, "lib")
     needed = [os.path.join(python, "Python.h"), os.path.join(include, "torch", "csrc", "autograd", "python_variable.h"),
-              os.path.join(include, "c10", "cuda", "CUDAStream.h"), os.path.join(cuda, "include", "cuda_runtime_api.h")] + \
-        [os.path.join(libs, f"lib{n}.so") for n in _TORCH_LINKS]
+              os.path.join(include, "c10", "cuda", "CUDAStream.h"), os.path.join(cuda, "include", "cuda_runtime_api.h"),
+              os.path.join(home, "version.py")] + [os.path.join(libs, f"lib{n}.so") for n in _TORCH_LINKS]
     if not (all(map(os.path.exists, needed)) and shutil.which("g++")):
         return None
+    with open(os.path.join(home, "version.py")) as f:
+        version = re.search(r"^__version__ = ['\"]([^'\"]+)['\"]", f.read(), re.M)
+    if not version:
+        return None
     paths = [INCLUDE, include, os.path.join(include, "torch", "csrc", "api", "include"), python, os.path.join(cuda, "include")]
+    target = torch_library(version.group(1))
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for p in paths for x in ("-I", p)] + \
-        [TORCH_SRC, "-o", TORCH_LIB + ".tmp", "-L", libs] + \
-        ["-l" + n for n in _TORCH_LINKS]
+        [TORCH_SRC, "-o", target + ".tmp", "-L", libs] + ["-l" + n for n in _TORCH_LINKS], target
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -90,12 +100,12 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 cmd = [nvcc] + common + ["-c", src, "-o", obj]
             jobs.append(cmd)
 
-    torch_job = None
-    if force or _stale(TORCH_LIB, [TORCH_SRC] + headers):
-        torch_job = _torch_job(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))))
     tool_jobs = len(jobs)
-    if torch_job:
-        jobs.append(torch_job)
+    torch_cmd, torch_lib = _torch_job(os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))) or (None, None)
+    if torch_cmd and (force or _stale(torch_lib, [TORCH_SRC] + headers)):
+        jobs.append(torch_cmd)
+    else:
+        torch_cmd = None
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -109,8 +119,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
                 if r.returncode != 0:
                     raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd[-3:])}")
-    if torch_job:
-        os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    if torch_cmd:
+        os.replace(torch_lib + ".tmp", torch_lib)
     if force or tool_jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs

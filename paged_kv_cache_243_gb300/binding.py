@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import threading
 from ctypes import POINTER, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import Optional
 
@@ -58,6 +59,7 @@ class PkvCache(ctypes.Structure):
 
 _lib: Optional[ctypes.CDLL] = None
 _torch_calls = None
+_torch_lock = threading.Lock()
 
 
 def library_path() -> str:
@@ -122,12 +124,16 @@ def lib() -> ctypes.CDLL:
 
 
 def torch_calls():
-    """The module of csrc/torch, its calls bound to this library's; None where it is not built."""
+    """The module of csrc/torch, its calls bound to this library's; None where it is not built for this torch. One that
+    is there and does not load raises, every time."""
     global _torch_calls
-    if _torch_calls is None:
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "_pkv_torch.so")
-        _torch_calls = False
-        if os.path.exists(path):
+    with _torch_lock:
+        if _torch_calls is None:
+            import torch
+            from ._build import torch_library
+            path = torch_library(torch.__version__)
+            if not os.path.exists(path):
+                return None
             spec = importlib.util.spec_from_file_location("_pkv_torch", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
@@ -135,7 +141,7 @@ def torch_calls():
             module.bind(*(ctypes.cast(f, c_void_p).value
                           for f in (L.pkv_rotary_append, L.pkv_tree_attention, L.pkv_keep_tokens)), PkvError)
             _torch_calls = module
-    return _torch_calls or None
+        return _torch_calls
 
 
 def _check(status: int, where: str) -> None:

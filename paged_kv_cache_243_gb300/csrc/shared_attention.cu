@@ -83,11 +83,15 @@ Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
   return w;
 }
 
-// For trees: each pair of row tiles' place, and one record row per query row (of each sequence's kv head, rounded
-// up to 32) and stream besides the blocks' 256.
+// For trees: each pair of row tiles' place, and besides the blocks' 256 one record row per query row of each sequence's kv head,
+// rounded up to 32; where rows are few (16 at most) one of each stream. (Counted as the latter up to 64 rows: a workspace
+// for some drafts serves fewer, too.)
+size_t tree_record_rows(const pkv_cache* c, int sequences, int drafts, int group, int ctas) {
+  return (size_t)sequences * c->num_kv_heads * std::max(64, (drafts * group + 31) / 32 * 32) + (size_t)(ctas + 1) * 2 * kTile;
+}
 Work tree_layout(const pkv_cache* c, int sequences, int drafts, int group, int ctas) {
-  const size_t rows = (size_t)(drafts * group + 31) / 32 * 32, heads = (size_t)sequences * c->num_kv_heads;
-  const size_t recs = 2 * heads * rows + (size_t)(ctas + 1) * 2 * kTile, pairs = (drafts * group + 2 * kTile - 1) / (2 * kTile);
+  const size_t recs = tree_record_rows(c, sequences, drafts, group, ctas), heads = (size_t)sequences * c->num_kv_heads;
+  const size_t pairs = (drafts * group + 2 * kTile - 1) / (2 * kTile);
   Work w;
   w.ml = align256(heads * pairs * sizeof(int4));
   w.acc = w.ml + align256(recs * sizeof(float2));
@@ -281,10 +285,11 @@ pkv_status launch_tree(const TreeArgs& a) {
   const int D = c->head_dim, group = a.num_q_heads / c->num_kv_heads, kind = kind_of(c);
   const int rows = a.batch * a.drafts, pairs = tree_pairs(a.drafts, group);
   // visits, two units each at most, and values of records are counted in 32 bits
+  static_assert(SharedGeom<64, KV_F16, false>::FEW <= 32, "few rows: records of two streams within 64");
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
   if (2 * (tiles + 4) >= (1ll << 31) / ((long long)c->num_kv_heads * a.batch * pairs) ||
-      (2ll * a.batch * c->num_kv_heads * (a.drafts * group + 31) + 256ll * ctas + 512) * D >= (1ll << 31))
+      tree_record_rows(c, a.batch, a.drafts, group, ctas) * D >= (1ull << 31))
     return PKV_ERR_UNSUPPORTED;
   const Work w = tree_layout(c, a.batch, a.drafts, group, ctas);
   if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < w.total)

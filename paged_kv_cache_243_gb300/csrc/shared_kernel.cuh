@@ -848,7 +848,7 @@ static __device__ __noinline__ void place_records(const SharedParams& p, const S
   }
 }
 
-// Trees: record rows of one stream, in all sequences. An accumulator's place is [32 rows][channel][row], so that
+// Trees: record rows of one stream, in all sequences (only few rows have records of both). An accumulator's place is [32 rows][channel][row], so that
 // 32 lanes that have a row each write and read a channel together.
 __host__ __device__ __forceinline__ int tree_records(const SharedParams& p) {
   return p.num_groups * p.num_kv_heads * p.rec_rows;
@@ -863,7 +863,7 @@ __device__ __forceinline__ Shares tree_shares(const SharedPlan& pl, int NG, int 
 // The same for trees of drafts: for each sequence, kv head and pair of row tiles its record rows (of the
 // first block, of those that continue it), parts and query rows, and whether both streams have a record.
 static __device__ __noinline__ void place_tree_records(const SharedParams& p, const SharedPlan& pl, bool few) {
-  const int lane = threadIdx.x & 31, whole = tree_records(p), NG = p.num_groups;
+  const int lane = threadIdx.x & 31, whole = tree_records(p) << few, NG = p.num_groups;
   const Shares shares = tree_shares(pl, NG, p.num_ctas);
 #pragma unroll 1
   for (int i = blockIdx.x + gridDim.x * lane; i < NG * p.num_kv_heads * p.pairs; i += gridDim.x * 32) {
@@ -876,7 +876,7 @@ static __device__ __noinline__ void place_tree_records(const SharedParams& p, co
       const int x = pair < heavy ? pl.gpre[g] + kEndHeavy * pl.hseg[g] + (h * heavy + pair) * (n + kEndHeavy)
                                  : pl.lpre[g] + kEndHeavy * pl.hseg[NG] + kEndLight * pl.lseg[g] + h * (n + kEndLight);
       const int c = shares.block_of(x);
-      info = make_int4(gh * p.rec_rows + pair * 2 * kTile, 2 * whole + (c + 1) * 2 * kTile,
+      info = make_int4(gh * p.rec_rows + pair * 2 * kTile, whole + (c + 1) * 2 * kTile,
                        (shares.block_of(x + n - 1) - c + 1) | mine << 16, few);
     }
     p.ws_info[i] = info;
@@ -1771,7 +1771,8 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
       ok = visit(v, s);
       if (!ok) break;
       const bool two = MODE != kFewDrafts && s.is(kTwo), few = is_few(s.rows);
-      const size_t rec0 = s.is(kContinued) ? 2 * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
+      constexpr int STREAMS = MODE == kDraftRows ? 1 : 2;   // that write records of their own
+      const size_t rec0 = s.is(kContinued) ? STREAMS * whole + (size_t)blockIdx.x * 2 * kTile + (few ? st * kTile : 0)
                                            : (few ? st * whole : 0) + s.rec;
       const float* qsum = reinterpret_cast<const float*>(smem + lay.qsum) + ((qc + (two ? st : 0)) % kQSums) * kTile;
       qc += two ? 2 : 1;

@@ -498,7 +498,8 @@ pkv_status pkv_rotary_frequencies(int32_t rot_dim, double base, pkv_rotary_scali
  * rotary_table — cosines and sines for positions 0 .. positions - 1, worked out in 64 bits and
  * rounded once: row m holds rot_dim / 2 cosines of m w_i, then the sines, all times table_scale. A
  * program makes it once; any other fp32 table of this layout serves pkv_rotary_append as well.
- *   cos_sin  : fp32 [positions][rot_dim], DEVICE memory, 16-byte aligned.
+ *   cos_sin  : fp32 [positions][rot_dim], DEVICE memory, 16-byte aligned. 2^31 - 65535 positions and
+ *              more are PKV_ERR_UNSUPPORTED.
  *   inv_freq : HOST, rot_dim / 2 values w_i, read before the call returns.
  */
 pkv_status pkv_rotary_table(float* cos_sin, int32_t positions, int32_t rot_dim, const double* inv_freq,

@@ -107,6 +107,8 @@ def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, device: st
                  stream: Optional[torch.cuda.Stream] = None, **scaling) -> torch.Tensor:
     """The table [positions][rot_dim] of cosines and sines for PagedKVCache.rotary_append (one serves all
     layers). Further arguments: rotary_frequencies'."""
+    if not 0 <= positions < 1 << 31:
+        raise ValueError("positions are counted in 31 bits")
     w, scale = rotary_frequencies(rot_dim, base, **scaling)
     with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
         out = torch.empty((positions, rot_dim), dtype=torch.float32, device=device)

@@ -888,6 +888,7 @@ pkv_status pkv_rotary_table(float* cos_sin, int32_t positions, int32_t rot_dim, 
                             double table_scale, void* stream) {
   if (positions < 0 || rot_dim <= 0) return PKV_ERR_INVALID_ARG;
   if (rot_dim % 16 != 0 || rot_dim > 128) return PKV_ERR_UNSUPPORTED;
+  if (positions > INT32_MAX - 65535) return PKV_ERR_UNSUPPORTED;   // the kernel counts them in 32 bits, a grid at a time
   if (positions == 0) return PKV_OK;
   if (!cos_sin || !aligned16(cos_sin) || !inv_freq) return PKV_ERR_INVALID_ARG;
   return launch_rotary_table(cos_sin, positions, rot_dim, inv_freq, table_scale, static_cast<cudaStream_t>(stream));

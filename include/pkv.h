@@ -576,7 +576,7 @@ pkv_status pkv_tree_attention(const pkv_cache* cache, int32_t batch, int32_t t_d
                               void* stream);
 
 /* Workspace bytes of pkv_tree_attention for these shapes on the current device
- * (num_splits as in the call); 0 on bad input. */
+ * (num_splits as in the call); 0 on bad input, and for shapes whose query rows the call does not serve. */
 size_t pkv_tree_workspace_bytes(const pkv_cache* cache, int32_t batch, int32_t t_draft, int32_t num_q_heads,
                                 int32_t num_splits);
 

@@ -89,6 +89,10 @@ Work layout(const pkv_cache* c, int batch, int hq, int ctas) {
 size_t tree_record_rows(const pkv_cache* c, int sequences, int drafts, int group, int ctas) {
   return (size_t)sequences * c->num_kv_heads * std::max(64, (drafts * group + 31) / 32 * 32) + (size_t)(ctas + 1) * 2 * kTile;
 }
+// Their values are counted in 32 bits.
+bool tree_records_fit(const pkv_cache* c, int sequences, int drafts, int group, int ctas) {
+  return tree_record_rows(c, sequences, drafts, group, ctas) * c->head_dim < (1ull << 31);
+}
 Work tree_layout(const pkv_cache* c, int sequences, int drafts, int group, int ctas) {
   const size_t recs = tree_record_rows(c, sequences, drafts, group, ctas), heads = (size_t)sequences * c->num_kv_heads;
   const size_t pairs = (drafts * group + 2 * kTile - 1) / (2 * kTile);
@@ -273,7 +277,9 @@ pkv_status tree_workspace_bytes(const pkv_cache* c, int batch, int drafts, int n
     const pkv_status st = device(dev);
     if (st != PKV_OK) return st;
   }
-  bytes = tree_layout(c, batch, drafts, num_q_heads / c->num_kv_heads, num_splits ? num_splits : dev.sms).total;
+  const int group = num_q_heads / c->num_kv_heads, ctas = num_splits ? num_splits : dev.sms;
+  if (!tree_records_fit(c, batch, drafts, group, ctas)) return PKV_ERR_UNSUPPORTED;
+  bytes = tree_layout(c, batch, drafts, group, ctas).total;
   return PKV_OK;
 }
 
@@ -284,12 +290,12 @@ pkv_status launch_tree(const TreeArgs& a) {
   if (st != PKV_OK) return st;
   const int D = c->head_dim, group = a.num_q_heads / c->num_kv_heads, kind = kind_of(c);
   const int rows = a.batch * a.drafts, pairs = tree_pairs(a.drafts, group);
-  // visits, two units each at most, and values of records are counted in 32 bits
+  // visits, two units each at most, are counted in 32 bits
   static_assert(SharedGeom<64, KV_F16, false>::FEW <= 32, "few rows: records of two streams within 64");
   const long long tiles = ((long long)a.max_pages * c->page_size + kTile - 1) / kTile;
   const int ctas = a.num_splits ? a.num_splits : dev.sms;
   if (2 * (tiles + 4) >= (1ll << 31) / ((long long)c->num_kv_heads * a.batch * pairs) ||
-      tree_record_rows(c, a.batch, a.drafts, group, ctas) * D >= (1ull << 31))
+      !tree_records_fit(c, a.batch, a.drafts, group, ctas))
     return PKV_ERR_UNSUPPORTED;
   const Work w = tree_layout(c, a.batch, a.drafts, group, ctas);
   if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < w.total)

@@ -32,6 +32,6 @@ def test_no_workspace_for_a_call_that_is_refused():
     # (a caller, the wrapper among them, would make it first: 8 GB and more)
     ask = lambda batch, T: B.tree_workspace_bytes(desc(8, 128), batch, T, 64, 152)  # noqa: E731
     assert ask(1000, 128) > 1 << 31
-    for batch, T in ((1024, 256), (1024, 255), (1020, 256)):
+    for batch, T in ((1024, 256), (1024, 255), (1023, 256)):
         with pytest.raises(B.PkvError):
             ask(batch, T)

@@ -445,9 +445,11 @@ __device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int L, int g,
 }
 
 // Trees: a sequence's kv head has segments of two row tiles, and one of what is left where that is one tile. The end
-// of a segment costs a block as much as some visits: in the shares every segment has that many more. (24 x 8K of 64 drafts with
-// 0, 1, 2, 3, 4 of two row tiles: 150, 149, 148, 146, 149 us; 8 x 4K with 0, 2, 3, 4 of fewer rows: 32.0, 29.3, 29.6, 29.9.)
-constexpr int kEndHeavy = 3, kEndLight = 2;
+// of a segment costs a block as much as some visits: in the shares every segment has that many more. (Of two row tiles with 0, 1, 2, 3, 4:
+// 40 calls of 24 to 357 us drawn over types, heads and sizes take 1.008, 0.977, 0.980, 1, 1.016 times as long as with 3, by their geometric mean;
+// for a single call, where a border falls makes up to a tenth either way. Of fewer rows with 0, 2, 3, 4: 8 x 3K of 16 drafts 32.0, 29.3,
+// 29.6, 29.9 us.)
+constexpr int kEndHeavy = 1, kEndLight = 2;
 __host__ __device__ __forceinline__ int heavy_pairs(int rows) { return (rows + kTile - 1) / (2 * kTile); }
 __host__ __device__ __forceinline__ int light_pairs(int rows) { return (rows + 2 * kTile - 1) / (2 * kTile) - heavy_pairs(rows); }
 

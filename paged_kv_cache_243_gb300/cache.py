@@ -586,6 +586,8 @@ class PagedKVCache:
         seq_lens tokens in the cache (draft_lens [B] of them, by default T): each attends to the tokens
         before the drafts and to those drafts that mask, int64 [B][T][ceil(T / 64)] or [T][ceil(T / 64)],
         has a bit for (tree_mask makes one; None: all up to itself). Rows beyond draft_lens are zeros.
+        With a 16-bit out_dtype softmax weights may be rounded once to q's type; the default, fp32, keeps two terms of
+        them, which takes up to 1.4 times as long where query rows are many.
         workspace, stream: as for shared_attention."""
         if stream is None and workspace is None and self._native is not None:
             got = self._calls.tree_attention(self._native, q, block_table, seq_lens, mask, draft_lens, sm_scale, out,

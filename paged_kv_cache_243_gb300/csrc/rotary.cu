@@ -14,7 +14,9 @@
 // flight before the position is known.
 //
 // Measured (32 + 2 x 8 heads of 128, bf16): 4 x 8192 tokens 124 us, 6.6 TB/s, 0.99 of the copy rate; 4 tokens 2.1 us,
-// 61 x 11 tokens (28 + 2 x 4 heads of 64) 3.3 us.
+// 61 x 11 tokens (28 + 2 x 4 heads of 64) 3.1 us. Into per-token INT8 179, 3.2, 6.1 us, 4-bit 175, 3.2, 6.1: the quantisers'
+// arithmetic; per-group INT8 301, 4.9, 8.0: every group in 32 bits, each key read twice and the table for every head.
+// Boxes are one more launch, which reads the keys back: 2.5 to 3 us, 9 to 11 on 4 x 8192.
 #include <cmath>
 
 #include "pkv_internal.h"

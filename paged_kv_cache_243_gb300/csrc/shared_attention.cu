@@ -338,7 +338,7 @@ pkv_status launch_tree(const TreeArgs& a) {
   p.mask_stride = a.mask_shared ? 0 : (long long)a.drafts * p.mask_words;
   p.pairs = pairs;
   p.rec_rows = (a.drafts * group + 31) / 32 * 32;
-  // Row tiles that end between two drafts are copied as boxes; the others are gathered. (24 x 8K, 64 drafts of 4 heads:
+  // Row tiles that end between two drafts are copied as boxes; the others are gathered. (24 x ~6K, 64 drafts of 4 heads:
   // a segment's 256 rows by one warp took 8 us, which nothing hides.)
   p.q_box = kTile % group != 0 ? 0 : std::min(a.drafts, kTile / group);
   if (p.q_box && !query_map(a.q, (uint64_t)rows, a.num_q_heads, group, D, p.q_box, bf, p.tmap_q)) return PKV_ERR_CUDA;
@@ -346,8 +346,9 @@ pkv_status launch_tree(const TreeArgs& a) {
   if (launch_pdl(fn, dim3(ctas), dim3(threads), smem, a.stream, args) != cudaSuccess) return PKV_ERR_CUDA;
   const long long items = (long long)a.batch * c->num_kv_heads * (p.rec_rows / 32) * (D / 16);
   // Where the warps are few, a block's four share an item's records, which come from memory one after the other. (Four and
-  // one: 8 x 4K with 16 drafts of 4 heads 29.9 and 33.8 us, 4 x 32K with 13 drafts of 32 kv heads 263 and 266; with more items than that
-  // they only wait for one another: 24 x 8K with 64 drafts 159.6 and 149.9.)
+  // one, with 1024 items: 8 x ~3K with 16 drafts of 4 heads 30.8 and 34.5 us, 4 x ~27K with 13 drafts of 32 kv heads 265.6 and 268.9. With
+  // many more they only wait for one another: 12288, 24 x ~6K with 64 drafts, 162.0 and 151.8; 24576, 48 x ~770 with 64, 117.7 and
+  // 96.5. In between they are within 2 us: 1536 39.9 and 41.4, 2048 34.9 and 37.0, 3072 65.7 and 64.4, 4096 50.4 and 48.4.)
   const int wpw = items < 8ll * dev.sms ? 4 : 1, per = 4 / wpw;
   const void* merge = D == 64 ? tree_merge<64>(wpw) : tree_merge<128>(wpw);
   return launch_pdl(merge, dim3((unsigned)((items + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess

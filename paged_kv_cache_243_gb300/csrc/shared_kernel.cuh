@@ -79,11 +79,12 @@
 //   Queries come as boxes of a tensor map, where a group's heads divide 128.
 //   Records are laid out for 32 rows at a time, channel by channel, so that a thread that has a row writes, and the
 //     merge reads, 128 bytes together.
-//   Measured (both launches, d = 128, back to back): 4 x 32K, 13 drafts, 32 kv heads, f16 262 us, 6.7 TB/s; 24 x 8K,
-//     64 drafts of 32 heads over 8, bf16 149 to 157 us, 1.0 PFLOP/s; 8 x 4K, 16 drafts 29.7 us; 16 x 8K, 24 drafts, INT8
-//     100 us. A visit of two row tiles takes 3970 cycles, of which the products are 2050: the chain of an event is
-//     maximum 500, reference 150, weights 1070, then P V and S and their hand-over 1470 to 2000. Shared memory is wanted for
-//     2050 as well: S takes 128 bytes a cycle of operands, all there is, P V half as much, and copies 64 KB. INT8's
+//   Measured (both launches, d = 128, back to back, 16-bit outputs): 4 sequences of 20K to 32K, 13 drafts, 32 kv heads, f16
+//     262 to 267 us, 6.6 to 6.7 TB/s; 24 of 4K to 8K, 64 drafts of 32 heads over 8, bf16 152 to 156 us, 1.0 PFLOP/s; 8 of 2K to 4K,
+//     16 drafts 30 us; 16 x 8192, 24 drafts, bf16 95, INT8 133, 4-bit 127 us. With 32-bit outputs, whose weights are two terms and whose
+//     products are not issued in the inner loop, 262, 210, 33, 104, 158, 151 us. A visit of two row tiles takes 3970 cycles, of
+//     which the products are 2050: the chain of an event is maximum 500, reference 150, weights 1070, then P V and S and their
+//     hand-over 1470 to 2000. Shared memory is wanted for 2050 as well: S takes 128 bytes a cycle of operands, all there is, P V half as much, and copies 64 KB. INT8's
 //     event: 2740, 240 and 2540, the latency of the scales' loads (1024 of shared memory's 3700 cycles a visit).
 //
 // Code size is a cost of its own: the two SMs of a pair share an instruction cache, and
@@ -447,7 +448,7 @@ __device__ __forceinline__ RowPlan row_plan(const SharedParams& p, int L, int g,
 // Trees: a sequence's kv head has segments of two row tiles, and one of what is left where that is one tile. The end
 // of a segment costs a block as much as some visits: in the shares every segment has that many more. (Of two row tiles with 0, 1, 2, 3, 4:
 // 40 calls of 24 to 357 us drawn over types, heads and sizes take 1.008, 0.977, 0.980, 1, 1.016 times as long as with 3, by their geometric mean;
-// for a single call, where a border falls makes up to a tenth either way. Of fewer rows with 0, 2, 3, 4: 8 x 3K of 16 drafts 32.0, 29.3,
+// for a single call, where a border falls makes up to a tenth either way. Of fewer rows with 0, 2, 3, 4: 8 x ~3K of 16 drafts 32.0, 29.3,
 // 29.6, 29.9 us.)
 constexpr int kEndHeavy = 1, kEndLight = 2;
 __host__ __device__ __forceinline__ int heavy_pairs(int rows) { return (rows + kTile - 1) / (2 * kTile); }
@@ -886,8 +887,8 @@ static __device__ __noinline__ void place_tree_records(const SharedParams& p, co
 }
 
 // What a kernel serves. Trees have one for calls of few query rows, where a segment's rows never exceed FEW, and
-// one for the others: half the code and fewer registers (one for both: 8 x 4K 32 us, 24 x 8K of 64 drafts 157, 5 x 1K 4-bit
-// 16; two: 29, 152, 11).
+// one for the others: half the code and fewer registers (one for both: 8 x ~3K of 16 drafts 32 us, 24 x ~6K of 64 157, the tree of
+// 5 x ~800 in 4 bits 16; two: 29, 152, 11).
 enum SharedMode { kPrefixes = 0, kFewDrafts = 1, kDraftRows = 2 };
 
 template <int D, int KV, bool BF, int MODE>
@@ -2018,7 +2019,7 @@ __global__ void __launch_bounds__(SharedGeom<D, KV, BF>::THREADS, 1)
               tc_wait_st();
             }
             float mx = -INFINITY;
-            // Scales of 8 tokens are loaded while the scores, or those before, are on their way. (A step of 16 x 8K INT8 with 24
+            // Scales of 8 tokens are loaded while the scores, or those before, are on their way. (A step of 16 x ~6K INT8 with 24
             // drafts, 4, 8, 16 tokens ahead: 116, 105, 106 us; more of them do not fit 96 registers.)
             constexpr int PRE = 4;
             [[maybe_unused]] ulonglong2 k2[PRE];

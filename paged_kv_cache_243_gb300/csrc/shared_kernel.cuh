@@ -84,8 +84,9 @@
 //     16 drafts 30 us; 16 x 8192, 24 drafts, bf16 95, INT8 133, 4-bit 127 us. With 32-bit outputs, whose weights are two terms and whose
 //     products are not issued in the inner loop, 262, 210, 33, 104, 158, 151 us. A visit of two row tiles takes 3970 cycles, of
 //     which the products are 2050: the chain of an event is maximum 500, reference 150, weights 1070, then P V and S and their
-//     hand-over 1470 to 2000. Shared memory is wanted for 2050 as well: S takes 128 bytes a cycle of operands, all there is, P V half as much, and copies 64 KB. INT8's
-//     event: 2740, 240 and 2540, the latency of the scales' loads (1024 of shared memory's 3700 cycles a visit).
+//     hand-over 1470 to 2000. Shared memory is wanted for 2050 as well: S takes 128 bytes a cycle of operands, all there is, P V
+//     half as much, and copies 64 KB. INT8's event: 2740, 240 and 2540, the latency of the scales' loads (1024 of shared
+//     memory's 3700 cycles a visit).
 //
 // Code size is a cost of its own: the two SMs of a pair share an instruction cache, and
 // 155 KB of code took 16 rows x 32K from 97 to 117 us. So loops stay loops, waits and plans

@@ -8,8 +8,10 @@ import torch
 import oracle
 import synth
 from helpers import int8_codes
-from shared_batch import int_dev, to_dev
+from shared_batch import int_dev, restore, to_dev
+from test_gpu_draft_steps import Tokens
 from test_gpu_rotary import rotated
+from tree_batch import TreeBatch, pack, random_parents, seen_from_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +131,44 @@ def test_a_chunked_prompt_on_every_grid():
         s.append(*s.tokens(n), at, np.full(2, n))
         at = at + n
         s.check()
+
+
+@pytest.mark.parametrize("d,g,T", [(64, 2, 100), (128, 4, 70), (64, 3, 256)])
+def test_steps_with_trees_that_reach_the_third_group(d, g, T):
+    # attention for the drafts, by the definition over the sequence quantised at once; then the accepted path is
+    # appended anew, turned by its depth as before
+    B = 3
+    s = Tokens("i8g", 2, g, d, 64, B, T, d, False, T)
+    prompt = np.array([70, 1, 33])
+    _, _, kr, vf = s.append(np.zeros(B), np.broadcast_to(np.arange(70), (B, 70)), prompt)
+    for b in range(B):
+        s.k[b], s.v[b] = kr[b, :prompt[b]], vf[b, :prompt[b]]
+    base, tb = prompt.copy(), TreeBatch.__new__(TreeBatch)
+    for step in range(4):
+        seen = np.stack([seen_from_parents(random_parents(s.rng, T)) for _ in range(B)])
+        turns = base[:, None] + seen.sum(-1) - 1
+        (q, k, v), (qf, kf, vf) = s.draw(T)
+        q = s.cache.rotary_append(q, k, v, s.cs_dev, int_dev(s.table), int_dev(base), int_dev(turns), dev_status=s.status)
+        out = s.cache.tree_attention(q, int_dev(s.table), int_dev(base + T), pack(seen).cuda(), dev_status=s.status,
+                                     out_dtype=torch.float32 if step % 2 else q.dtype)
+        qr, kr = synth.round_to_dtype(rotated(qf, s.cs[turns], False), s.src)[1], rotated(kf, s.cs[turns], False)
+        tb.B, tb.T, tb.d, tb.src, tb.seen = B, T, d, s.src, seen
+        tb.lens, tb.drafts = (base + T).astype(np.int32), np.full(B, T)
+        tb.k, tb.v, tb.kmid, tb.vmid = [], [], [], []
+        for b in range(B):
+            for mine, mid, x in ((tb.k, tb.kmid, np.concatenate([s.k[b], kr[b]])), (tb.v, tb.vmid, np.concatenate([s.v[b], vf[b]]))):
+                val, m = restore("i8g", x)
+                mine.append(val)
+                mid.append(m)
+        tb.tree_check(out, qr, g)
+        paths = [np.flatnonzero(seen[b, s.rng.integers(0, T)]) for b in range(B)]
+        n = np.array([len(p) for p in paths])
+        at = np.stack([np.resize(p, n.max()) for p in paths])
+        rows = torch.arange(B, device="cuda")[:, None], torch.from_numpy(at).cuda()
+        s.cache.rotary_append(None, k[rows], v[rows], s.cs_dev, int_dev(s.table), int_dev(base),
+                              int_dev(np.take_along_axis(turns, at, 1)), new_lens=int_dev(n), dev_status=s.status)
+        for b, p in enumerate(paths):
+            s.k[b], s.v[b] = np.concatenate([s.k[b], kr[b, p]]), np.concatenate([s.v[b], vf[b, p]])
+        base = base + n
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0

@@ -133,6 +133,22 @@ def test_a_chunked_prompt_on_every_grid():
         s.check()
 
 
+@pytest.mark.parametrize("cut", [137, 130, 37, 20])
+@pytest.mark.parametrize("more", [1, 40, 200])
+def test_a_fork_behind_a_long_append(cut, more):
+    # the child's row says where the originals are as its parent's does: of the group that is open, and of the one
+    # in which the last append began
+    s = Sequences(64, 2, cut + more)
+    s.append(*s.tokens(37), np.zeros(2, np.int64), np.array([37, 0]))
+    s.append(*s.tokens(100), np.array([37, 0]), np.array([100, 0]))
+    s.cache.copy_pages(s.table[0], s.table[1], [0], [1])
+    s.held[1] = [x[:cut] for x in s.held[0]]
+    for _ in range(3):
+        at = np.array([len(s.held[b][0]) for b in range(2)])
+        s.append(*s.tokens(more), at, np.full(2, more))
+        s.check()
+
+
 @pytest.mark.parametrize("d,g,T", [(64, 2, 100), (128, 4, 70), (64, 3, 256)])
 def test_steps_with_trees_that_reach_the_third_group(d, g, T):
     # attention for the drafts, by the definition over the sequence quantised at once; then the accepted path is

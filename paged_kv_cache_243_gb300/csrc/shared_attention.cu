@@ -348,7 +348,7 @@ pkv_status launch_tree(const TreeArgs& a) {
   // Where the warps are few, a block's four share an item's records, which come from memory one after the other. (Four and
   // one, with 1024 items: 8 x ~3K with 16 drafts of 4 heads 30.8 and 34.5 us, 4 x ~27K with 13 drafts of 32 kv heads 265.6 and 268.9. With
   // many more they only wait for one another: 12288, 24 x ~6K with 64 drafts, 162.0 and 151.8; 24576, 48 x ~770 with 64, 117.7 and
-  // 96.5. In between they are within 2 us: 1536 39.9 and 41.4, 2048 34.9 and 37.0, 3072 65.7 and 64.4, 4096 50.4 and 48.4.)
+  // 96.5. In between they are within 2 us: 1536 39.9 and 41.4, 2048 34.9 and 37.0, 4096 50.4 and 48.4.)
   const int wpw = items < 8ll * dev.sms ? 4 : 1, per = 4 / wpw;
   const void* merge = D == 64 ? tree_merge<64>(wpw) : tree_merge<128>(wpw);
   return launch_pdl(merge, dim3((unsigned)((items + per - 1) / per)), dim3(kMergeThreads), 0, a.stream, args) == cudaSuccess

@@ -80,7 +80,7 @@
 //   Records are laid out for 32 rows at a time, channel by channel, so that a thread that has a row writes, and the
 //     merge reads, 128 bytes together.
 //   Measured (both launches, d = 128, back to back, 16-bit outputs): 4 sequences of 20K to 32K, 13 drafts, 32 kv heads, f16
-//     262 to 267 us, 6.6 to 6.7 TB/s; 24 of 4K to 8K, 64 drafts of 32 heads over 8, bf16 152 to 156 us, 1.0 PFLOP/s; 8 of 2K to 4K,
+//     262 to 267 us, 6.6 to 6.7 TB/s; 24 of 4K to 8K, 64 drafts of 32 heads over 8, bf16 152 to 160 us, 1.0 PFLOP/s; 8 of 2K to 4K,
 //     16 drafts 30 us; 16 x 8192, 24 drafts, bf16 95, INT8 133, 4-bit 127 us. With 32-bit outputs, whose weights are two terms and whose
 //     products are not issued in the inner loop, 262, 210, 33, 104, 158, 151 us. A visit of two row tiles takes 3970 cycles, of
 //     which the products are 2050: the chain of an event is maximum 500, reference 150, weights 1070, then P V and S and their
